@@ -469,6 +469,58 @@ int sdm_gen_inputs(unsigned long long seed, int B, int H, int T, int b_off, int 
 int sdm_gen_M0(unsigned long long seed, int H, long long N, int d_v, float scale, float* M0,
                void* stream);
 
+/* ---- Layers that stand beside the memory layer in a recurrent stack ----
+ *
+ * The tensors that a caller cuts out of wider projections (x, dt, z, B, C) are given with two
+ * strides in elements, between sequences (_bs) and between tokens (_ts); their innermost
+ * dimension is dense.  They need only be aligned to their elements (16-byte aligned rows are
+ * faster); outputs are dense.
+ *   lengths  int32 [B] on the device, or NULL: the tokens of each sequence that exist (clamped to
+ *            [0, T]).  Tokens past them are not read, y is 0 there, and the state is the one
+ *            after the last that exists.
+ *   slots    int32 [B] on the device, or NULL: the row of `state` and `state_out` that each
+ *            sequence's state lives in (NULL: row b).  A negative slot is a padding row: y is 0
+ *            and no state is touched.  A slot >= n_slots is treated as padding and reported as
+ *            SDM_DEV_INDEX_RANGE.  Live slots of one call are distinct.
+ *   state    read (NULL: zeros); state_out written (NULL: not kept); the same buffer updates it
+ *            in place.  n_slots: rows of either. */
+typedef enum { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1, SDM_ACT_GELU = 2 } sdm_activation;
+
+#define SDM_MAX_CONV 8    /* taps of the short convolution */
+#define SDM_MAX_SSM_N 128 /* states a channel of the selective scan */
+
+/* sdm_causal_conv - short causal depthwise convolution over T tokens (T = 1: one decode token):
+ *   y[b,t,d] = act(bias[d] + sum_{j<K} w[d,j] u[b, t-K+1+j, d])
+ * with u the K-1 inputs before token 0 (the state) followed by x.
+ *   x [B, T, D] dt;  w [D, K], bias [D] (or NULL) w_dt;  y [B, T, D] dt, dense.
+ *   state, state_out [n_slots, K-1, D] dt: the last K-1 inputs, oldest first.
+ *   act: SDM_ACT_NONE or SDM_ACT_SILU.  Requires 2 <= K <= SDM_MAX_CONV. */
+int sdm_causal_conv(const void* x, long long x_bstride, long long x_tstride, int dt, const void* w,
+                    const void* bias, int w_dt, int B, int T, int D, int K, int act,
+                    const void* state, void* state_out, int n_slots, const int32_t* lengths,
+                    const int32_t* slots, void* y, int* dev_err, void* stream);
+
+/* sdm_selective_scan - selective state space scan over T tokens (T = 1: one decode token):
+ *   delta = softplus(dt + dt_bias) (softplus 0: without it)
+ *   h_t[d,n] = exp(delta_t[d] A[d,n]) h_{t-1}[d,n] + delta_t[d] x_t[d] B_t[g,n]
+ *   y_t[d] = (sum_n C_t[g,n] h_t[d,n] + D[d] x_t[d]) silu(z_t[d]),  g = d / (Dm / G)
+ * Requires Dm % G == 0 and 1 <= N <= SDM_MAX_SSM_N.  States and sums are fp32. */
+typedef struct {
+  const void *x, *dt, *Bm, *Cm, *z; /* [B,T,Dm], [B,T,Dm], [B,T,G,N] (2x), [B,T,Dm] or NULL */
+  long long x_bs, x_ts, dt_bs, dt_ts, B_bs, B_ts, C_bs, C_ts, z_bs, z_ts;
+  const float *A, *D, *dt_bias;     /* [Dm,N], [Dm] or NULL, [Dm] or NULL */
+  const float* state;               /* [n_slots, Dm, N] or NULL */
+  float* state_out;                 /* [n_slots, Dm, N] or NULL */
+  const int32_t *lengths, *slots;
+  void* y;                          /* [B,T,Dm] dense */
+  int dtype;                        /* of x, dt, Bm, Cm, z and y */
+  int B, T, Dm, N, G, softplus, n_slots;
+} sdm_ssm_args;
+/* Bytes of device workspace for these sizes; 0 where none is needed. */
+size_t sdm_selective_scan_workspace_size(int B, int T, int Dm, int N, int G);
+int sdm_selective_scan(const sdm_ssm_args* args, void* workspace, size_t workspace_bytes,
+                       int* dev_err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,210 @@
+// Short causal depthwise convolution in front of a recurrent layer, over prompts and for single
+// tokens.
+//
+//   y[b,t,d] = act(bias[d] + sum_{j<K} w[d,j] u[b, t-K+1+j, d])
+//
+// where u is the K-1 inputs carried from before token 0 (the state) followed by x, and the new
+// state is the last K-1 inputs of each sequence.  2K flop for each element read and written
+// once: HBM bounds it, so each thread keeps its 16-byte piece of channels (8 bf16 or 4 fp32)
+// and walks a strip of tokens with the last K-1 inputs in registers: every input is read once,
+// except the K-1 tokens before a strip.  Loads of kAhead tokens are issued together.
+#include "sdm_layers.cuh"
+
+namespace sdm {
+namespace {
+
+constexpr int kConvThreads = 128;
+constexpr int kAhead = 8;  // tokens loaded together; strips are multiples of it, so K-1 < strip
+
+struct ConvArgs {
+  const void* x;
+  long long x_bs, x_ts;  // elements between sequences and between tokens
+  const void* w;
+  const void* bias;
+  int w_dt, B, T, D, act;
+  const void* state;
+  void* state_out;
+  int n_slots;
+  const int32_t* lengths;
+  const int32_t* slots;
+  void* y;
+  int* dev_err;
+  int strip, strips, pieces;  // tokens a thread, strips a sequence, pieces a row
+};
+
+__device__ __forceinline__ float weight_at(const void* p, int dt, size_t i) {
+  return dt == SDM_F32 ? static_cast<const float*>(p)[i]
+                       : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// V channels at p: one 16-byte load where V is a whole piece, else one element.
+template <typename T, int V>
+__device__ __forceinline__ void load_piece(const T* p, float (&v)[V]) {
+  if constexpr (V == 1)
+    v[0] = to_f32(*p);
+  else
+    Piece<T>::load(*reinterpret_cast<const uint4*>(p), v);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_piece(T* p, const float (&v)[V]) {
+  if constexpr (V == 1)
+    from_f32(v[0], p);
+  else
+    *reinterpret_cast<uint4*>(p) = Piece<T>::pack(v);
+}
+
+template <typename T, int K, int V>
+__global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
+  const long long id = (long long)blockIdx.x * kConvThreads + threadIdx.x;
+  const int piece = int(id % a.pieces);
+  const long long row = id / a.pieces;
+  const int strip = int(row % a.strips), b = int(row / a.strips);
+  if (b >= a.B) return;
+  const int d = piece * V;
+  const int slot = row_slot(a.slots, b, a.n_slots, a.dev_err);
+  const int len = slot < 0 ? 0 : row_length(a.lengths, b, a.T);
+  const int t0 = strip * a.strip, t1 = min(t0 + a.strip, a.T);
+  const T* x = static_cast<const T*>(a.x) + b * a.x_bs + d;
+  T* y = static_cast<T*>(a.y) + (size_t(b) * a.T) * a.D + d;
+
+  float w[K][V], bias[V], win[K - 1][V];
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[j][i] = weight_at(a.w, a.w_dt, size_t(d + i) * K + j);
+#pragma unroll
+  for (int i = 0; i < V; ++i) bias[i] = a.bias ? weight_at(a.bias, a.w_dt, d + i) : 0.f;
+
+  const size_t srow = size_t(max(slot, 0)) * (K - 1) * a.D + d;
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) {
+    const int t = t0 - (K - 1) + j;
+    if (t0 > 0 && t < len) {
+      load_piece<T, V>(x + t * a.x_ts, win[j]);
+    } else if (t0 == 0 && a.state && slot >= 0) {
+      load_piece<T, V>(static_cast<const T*>(a.state) + srow + size_t(j) * a.D, win[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) win[j][i] = 0.f;
+    }
+  }
+  if (t0 == 0 && slot >= 0 && a.state_out) {
+    // This thread alone reads its channels' old state (above) and writes the new one, so the
+    // state may be updated in place.
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      const int t = len - (K - 1) + j;
+      float v[V];
+      if (t >= 0) {
+        load_piece<T, V>(x + t * a.x_ts, v);
+      } else {  // a sequence shorter than the window keeps the end of the old state
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.f;
+#pragma unroll
+        for (int o = 0; o < K - 1; ++o)
+          if (o == t + K - 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = win[o][i];
+          }
+      }
+      store_piece<T, V>(static_cast<T*>(a.state_out) + srow + size_t(j) * a.D, v);
+    }
+  }
+
+  for (int t = t0; t < t1; t += kAhead) {
+    float in[kAhead][V];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (t + k < len) {
+        load_piece<T, V>(x + (t + k) * a.x_ts, in[k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) in[k][i] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (t + k >= t1) break;
+      float o[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float s = bias[i];
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) s = fmaf(w[j][i], win[j][i], s);
+        s = fmaf(w[K - 1][i], in[k][i], s);
+        o[i] = t + k < len ? (a.act ? silu(s) : s) : 0.f;
+#pragma unroll
+        for (int j = 0; j + 1 < K - 1; ++j) win[j][i] = win[j + 1][i];
+        win[K - 2][i] = in[k][i];
+      }
+      store_piece<T, V>(y + size_t(t + k) * a.D, o);
+    }
+  }
+}
+
+template <typename T, int K>
+int launch_k(const ConvArgs& a, bool vec, cudaStream_t s) {
+  const long long blocks =
+      ((long long)a.B * a.strips * a.pieces + kConvThreads - 1) / kConvThreads;
+  if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
+  if (vec)
+    conv_kernel<T, K, Piece<T>::n><<<unsigned(blocks), kConvThreads, 0, s>>>(a);
+  else
+    conv_kernel<T, K, 1><<<unsigned(blocks), kConvThreads, 0, s>>>(a);
+  return last_launch_status();
+}
+
+template <typename T>
+int launch_t(const ConvArgs& a, int K, bool vec, cudaStream_t s) {
+  switch (K) {
+    case 2: return launch_k<T, 2>(a, vec, s);
+    case 3: return launch_k<T, 3>(a, vec, s);
+    case 4: return launch_k<T, 4>(a, vec, s);
+    case 5: return launch_k<T, 5>(a, vec, s);
+    case 6: return launch_k<T, 6>(a, vec, s);
+    case 7: return launch_k<T, 7>(a, vec, s);
+    case 8: return launch_k<T, 8>(a, vec, s);
+    default: return SDM_EUNSUPPORTED;
+  }
+}
+
+}  // namespace
+}  // namespace sdm
+
+using namespace sdm;
+
+extern "C" int sdm_causal_conv(const void* x, long long x_bstride, long long x_tstride, int dt,
+                               const void* w, const void* bias, int w_dt, int B, int T, int D,
+                               int K, int act, const void* state, void* state_out, int n_slots,
+                               const int32_t* lengths, const int32_t* slots, void* y,
+                               int* dev_err, void* stream) {
+  if (B < 1 || T < 0 || D < 1 || K < 2 || bad_dtype(dt) || bad_dtype(w_dt)) return SDM_EINVAL;
+  if (act != SDM_ACT_NONE && act != SDM_ACT_SILU) return SDM_EINVAL;
+  if (K > SDM_MAX_CONV || (long long)B * T > 0x7FFFFFFFLL || D > 0x7FFFFFF) return SDM_EUNSUPPORTED;
+  if ((state || state_out || slots) && n_slots < (slots ? 1 : B)) return SDM_EINVAL;
+  const int es = dt == SDM_F32 ? 4 : 2;
+  const uintptr_t odd = uintptr_t(es - 1), wodd = uintptr_t(w_dt == SDM_F32 ? 3 : 1);
+  auto off = [](const void* p, uintptr_t m) { return (reinterpret_cast<uintptr_t>(p) & m) != 0; };
+  if (!w || off(w, wodd) || off(bias, wodd) || off(state, odd) || off(state_out, odd) ||
+      off(lengths, 3) || off(slots, 3) || off(dev_err, 3))
+    return SDM_EALIGN;
+  if (T > 0 && (!x || !y || off(x, odd) || off(y, odd))) return SDM_EALIGN;
+  if (T == 0 && (state == state_out || !state_out)) return SDM_OK;
+
+  const int V = 16 / es;
+  // 16-byte pieces where every row of every operand starts on 16 bytes, else single elements.
+  const bool vec = D % V == 0 && x_bstride % V == 0 && x_tstride % V == 0 && !off(x, 15) &&
+                   !off(y, 15) && !off(state, 15) && !off(state_out, 15);
+  ConvArgs a{x,     x_bstride, x_tstride, w,     bias, w_dt,    B, T, D,
+             act,   state,     state_out, n_slots, lengths, slots, y, dev_err, 0, 0, 0};
+  a.pieces = vec ? D / V : D;
+  // Strips of 32 tokens (the K-1 tokens read twice are then under a tenth), shorter ones where
+  // that leaves the card's threads short.
+  a.strip = 32;
+  while (a.strip > kAhead &&
+         (long long)B * ((T + a.strip - 1) / a.strip) * a.pieces < 152LL * 1024)
+    a.strip /= 2;
+  a.strips = T > 0 ? (T + a.strip - 1) / a.strip : 1;
+  return dt == SDM_F32 ? launch_t<float>(a, K, vec, as_stream(stream))
+                       : launch_t<__nv_bfloat16>(a, K, vec, as_stream(stream));
+}

@@ -1,0 +1,623 @@
+// Selective state space scan, over prompts and for single tokens.
+//
+//   delta_t[d] = softplus(dt_t[d] + dt_bias[d])            (softplus optional)
+//   h_t[d,n]   = exp(delta_t[d] A[d,n]) h_{t-1}[d,n] + delta_t[d] x_t[d] B_t[g,n]
+//   y_t[d]     = (sum_n C_t[g,n] h_t[d,n] + D[d] x_t[d]) silu(z_t[d])
+//
+// with channel d in group g = d / (Dm / G).  Everything is computed and held in fp32; inputs and
+// y are bf16 or fp32.
+//
+// Each (t, d, n) costs one exp2 and four fp32 operations (two products, two fused multiply-adds).
+// A GB300 SM does 32 exp2 and 31 such foursomes a clock (measured), so with N = 16 and bf16 the
+// arithmetic takes 1.5 times as long as HBM does for the 8 bytes of an element: the arithmetic is
+// what has to be kept fed.
+#include "sdm_layers.cuh"
+
+namespace sdm {
+namespace {
+
+constexpr int kS = 8;         // states a lane holds of each of its channels
+constexpr int kThreads = 128;
+constexpr int kTT = 16;       // tokens of a shared-memory tile
+
+struct ScanArgs {
+  sdm_ssm_args io;
+  int tiles_g, Dg;             // channel tiles of a group, channels of a group
+  int chunks, chunk;           // chunks of a sequence, tokens of a chunk (a multiple of kTT)
+  float* ws_h;                 // [chunks][B][Dm][N]: state before chunk 0, then each chunk's own end
+  float* ws_d;                 // [chunks][B][Dm]: sum of delta over each chunk
+  bool vec;                    // rows of x, dt, z and y in 16-byte pieces
+  bool vec_bc;                 // rows of B and C in 16-byte pieces (N a multiple of the piece)
+  int* dev_err;
+};
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A in units of exp2.  A finite A stays finite, so that a step of size 0 has the decay 1 (0 times
+// an infinite rate would have none).
+__device__ __forceinline__ float decay_rate(float A) {
+  const float r = A * kLog2e;
+  return isinf(r) && !isinf(A) ? copysignf(3.402823466e38f, A) : r;
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes to shared memory, zeros where !in.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
+  const int n = in ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// Passes over a sequence: one block takes all tokens (kWhole); or the sequence is cut in chunks,
+// every chunk but the last is reduced to its end state from zero and its sum of delta (kReduce), and
+// each chunk then starts from the given state carried through those before it (kJoin).  Chunks
+// share A, so a chunk decays the state by exp(A sum(delta)).  The first pass also copies the given
+// state, so that the second may write the new one in its place.
+enum Pass { kWhole = 0, kReduce = 1, kJoin = 2 };
+
+// L lanes share a channel (kS states each); a lane has 2 * P channels, in pairs.
+template <typename T, int L, int P>
+struct Tile {
+  static constexpr int V = Piece<T>::n;
+  static constexpr int groups = kThreads / L;       // lane groups, each with P pairs of channels
+  static constexpr int CH = 2 * P * groups;         // channels of a block
+  static constexpr int NP = L * kS;                 // padded number of states
+  static constexpr int RV = CH / V;                 // pieces of a tile row
+  static constexpr int pieces = kTT * RV;           // pieces of a tile
+  static constexpr int raw = kTT * CH * int(sizeof(T));
+  static constexpr int raw_bc = kTT * NP * int(sizeof(T));
+  static constexpr int stage = 3 * raw + 2 * raw_bc;        // x, dt, z, B, C as they come
+  static constexpr int off_dx = 2 * stage;                  // {delta, delta, delta x, delta x} by pair
+  static constexpr int off_b = off_dx + kTT * CH * 8;
+  static constexpr int off_c = off_b + kTT * NP * 4;
+  static constexpr int bytes = off_c + kTT * NP * 4;
+};
+
+template <typename T, int L, int P, int PASS>
+__global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ ScanArgs a) {
+  using S = Tile<T, L, P>;
+  constexpr int V = S::V;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const sdm_ssm_args& io = a.io;
+  const int tid = threadIdx.x;
+
+  // block -> (channel tile, sequence, chunk)
+  int id = blockIdx.x;
+  const int nct = a.tiles_g * io.G;
+  const int ct = id % nct;
+  id /= nct;
+  const int b = id % io.B;
+  const int chunk = PASS == kWhole ? 0 : id / io.B;
+  const int g = ct / a.tiles_g;
+  const int c0 = (ct - g * a.tiles_g) * S::CH;  // first channel of the tile in its group
+  const int d0 = g * a.Dg + c0;
+  const int nch = min(S::CH, a.Dg - c0);
+
+  const int slot = row_slot(io.slots, b, io.n_slots, a.dev_err);
+  const int len = slot < 0 ? 0 : row_length(io.lengths, b, io.T);
+  const int t_lo = PASS == kWhole ? 0 : chunk * a.chunk;
+  const int t_hi = PASS == kWhole ? io.T : min(t_lo + a.chunk, io.T);
+  const int t_end = min(len, t_hi);  // tokens of this block that exist: [t_lo, t_end)
+
+  const T* gx = static_cast<const T*>(io.x) + b * io.x_bs + d0;
+  const T* gdt = static_cast<const T*>(io.dt) + b * io.dt_bs + d0;
+  const T* gz = static_cast<const T*>(io.z) + (io.z ? b * io.z_bs + d0 : 0);
+  const T* gB = static_cast<const T*>(io.Bm) + b * io.B_bs + g * io.N;
+  const T* gC = static_cast<const T*>(io.Cm) + b * io.C_bs + g * io.N;
+  T* gy = static_cast<T*>(io.y) + (size_t(b) * io.T) * io.Dm + d0;
+
+  auto raw = [&](int st, int which) { return reinterpret_cast<T*>(smem + st * S::stage + which * S::raw); };
+  auto raw_bc = [&](int st, int which) {
+    return reinterpret_cast<T*>(smem + st * S::stage + 3 * S::raw + which * S::raw_bc);
+  };
+  float4* dx = reinterpret_cast<float4*>(smem + S::off_dx);
+  float* sB = reinterpret_cast<float*>(smem + S::off_b);
+  float* sC = reinterpret_cast<float*>(smem + S::off_c);
+
+  auto load_tile = [&](int st, int t0) {
+    const int nt = min(kTT, t_end - t0);
+    if (a.vec) {
+      for (int v = tid; v < S::pieces; v += kThreads) {
+        const int t = v / S::RV, c = (v % S::RV) * V;
+        const bool in = t < nt && c < nch;
+        const long long tt = in ? t0 + t : 0;
+        const int cc = in ? c : 0;
+        copy16(raw(st, 0) + v * V, gx + tt * io.x_ts + cc, in);
+        copy16(raw(st, 1) + v * V, gdt + tt * io.dt_ts + cc, in);
+        if (PASS != kReduce && io.z) copy16(raw(st, 2) + v * V, gz + tt * io.z_ts + cc, in);
+      }
+    } else {
+      for (int e = tid; e < kTT * S::CH; e += kThreads) {
+        const int t = e / S::CH, c = e % S::CH;
+        const bool in = t < nt && c < nch;
+        const long long tt = t0 + t;
+        raw(st, 0)[e] = in ? gx[tt * io.x_ts + c] : T(0.f);
+        raw(st, 1)[e] = in ? gdt[tt * io.dt_ts + c] : T(0.f);
+        if (PASS != kReduce && io.z) raw(st, 2)[e] = in ? gz[tt * io.z_ts + c] : T(0.f);
+      }
+    }
+    if (a.vec_bc) {
+      for (int v = tid; v < kTT * S::NP / V; v += kThreads) {
+        const int t = v / (S::NP / V), n = (v % (S::NP / V)) * V;
+        const bool in = t < nt && n < io.N;
+        const long long tt = in ? t0 + t : 0;
+        const int nn = in ? n : 0;
+        copy16(raw_bc(st, 0) + v * V, gB + tt * io.B_ts + nn, in);
+        if (PASS != kReduce) copy16(raw_bc(st, 1) + v * V, gC + tt * io.C_ts + nn, in);
+      }
+    } else {
+      for (int e = tid; e < kTT * S::NP; e += kThreads) {
+        const int t = e / S::NP, n = e % S::NP;
+        const bool in = t < nt && n < io.N;
+        const long long tt = t0 + t;
+        raw_bc(st, 0)[e] = in ? gB[tt * io.B_ts + n] : T(0.f);
+        if (PASS != kReduce) raw_bc(st, 1)[e] = in ? gC[tt * io.C_ts + n] : T(0.f);
+      }
+    }
+    copies_commit();
+  };
+
+  // kThreads is a multiple of RV, so a thread's pieces all hold the same channels: their constants
+  // stay in registers.
+  static_assert(kThreads % S::RV == 0, "a thread's pieces share their channels");
+  const int pr = tid % S::RV, pc = pr * V;
+  float bias[V], skip[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    bias[i] = io.dt_bias && pc + i < nch ? io.dt_bias[d0 + pc + i] : 0.f;
+    skip[i] = PASS != kReduce && io.D && pc + i < nch ? io.D[d0 + pc + i] : 0.f;
+  }
+
+  // Piece v of a tile holds channels c .. c+V-1 of token t; its pairs i go to plane i, so that the
+  // pieces of a warp write and its lane groups read consecutive 16-byte words.
+  auto prepare_tile = [&](int st) {
+    for (int v = tid; v < S::pieces; v += kThreads) {
+      const int t = v / S::RV;
+      float x[V], d[V];
+      Piece<T>::load(*reinterpret_cast<const uint4*>(raw(st, 0) + v * V), x);
+      Piece<T>::load(*reinterpret_cast<const uint4*>(raw(st, 1) + v * V), d);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        d[i] += bias[i];
+        if (io.softplus) d[i] = softplus(d[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i)
+        dx[t * (S::CH / 2) + i * S::RV + pr] =
+            make_float4(d[2 * i], d[2 * i + 1], d[2 * i] * x[2 * i], d[2 * i + 1] * x[2 * i + 1]);
+    }
+    for (int e = tid; e < kTT * S::NP; e += kThreads) {
+      sB[e] = to_f32(raw_bc(st, 0)[e]);
+      if (PASS != kReduce) sC[e] = to_f32(raw_bc(st, 1)[e]);
+    }
+  };
+
+  auto store_tile = [&](int st, int t0) {  // y of the tile out of dx
+    const int nt = min(kTT, t_end - t0);
+    for (int v = tid; v < S::pieces; v += kThreads) {
+      const int t = v / S::RV;
+      if (t >= nt || pc >= nch) continue;
+      float x[V], o[V];
+      Piece<T>::load(*reinterpret_cast<const uint4*>(raw(st, 0) + v * V), x);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const float2 p = *reinterpret_cast<const float2*>(&dx[t * (S::CH / 2) + i * S::RV + pr]);
+        o[2 * i] = p.x;
+        o[2 * i + 1] = p.y;
+      }
+      if (io.D) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = fmaf(skip[i], x[i], o[i]);
+      }
+      if (io.z) {
+        float z[V];
+        Piece<T>::load(*reinterpret_cast<const uint4*>(raw(st, 2) + v * V), z);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] *= silu(z[i]);
+      }
+      T* p = gy + size_t(t0 + t) * io.Dm + pc;
+      if (a.vec) {
+        *reinterpret_cast<uint4*>(p) = Piece<T>::pack(o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (pc + i < nch) from_f32(o[i], p + i);
+      }
+    }
+  };
+
+  // This lane's channels and states.
+  const int sub = tid % L, grp = tid / L;
+  int ch[P];  // first channel of pair p in the tile
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int q = grp + p * S::groups;
+    ch[p] = (q % S::RV) * V + 2 * (q / S::RV);
+  }
+  uint64_t A[P][2][kS / 2], h[P][2][kS / 2];
+  float dsum[P][2];
+  const size_t bd = size_t(b) * io.Dm + d0;
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = ch[p] + k;
+      dsum[p][k] = 0.f;
+#pragma unroll
+      for (int j = 0; j < kS / 2; ++j) {
+        float av[2], hv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int n = sub * kS + 2 * j + e;
+          const bool in = c < nch && n < io.N;
+          av[e] = in ? decay_rate(io.A[size_t(d0 + c) * io.N + n]) : 0.f;
+          hv[e] = 0.f;
+          if (in && slot >= 0) {
+            if (PASS == kWhole || (PASS == kReduce && chunk == 0)) {
+              const float v = io.state ? io.state[(size_t(slot) * io.Dm + d0 + c) * io.N + n] : 0.f;
+              if (PASS == kReduce)
+                a.ws_h[(bd + c) * io.N + n] = v;
+              else
+                hv[e] = v;
+            } else if (PASS == kJoin) {
+              hv[e] = a.ws_h[(bd + c) * io.N + n];
+            }
+          }
+        }
+        A[p][k][j] = pack2(av[0], av[1]);
+        h[p][k][j] = pack2(hv[0], hv[1]);
+      }
+    }
+  if (PASS == kJoin && slot >= 0) {
+    const size_t per = size_t(io.B) * io.Dm;
+    for (int q = 0; q < chunk; ++q) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = ch[p] + k;
+          if (c >= nch) continue;
+          const float s = a.ws_d[q * per + bd + c];
+#pragma unroll
+          for (int j = 0; j < kS / 2; ++j) {
+            float e0, e1, n0 = 0.f, n1 = 0.f;
+            const int n = sub * kS + 2 * j;
+            const float* e = a.ws_h + ((q + 1) * per + bd + c) * io.N + n;
+            if (n < io.N) n0 = e[0];
+            if (n + 1 < io.N) n1 = e[1];
+            unpack2(mul2(pack2(s, s), A[p][k][j]), e0, e1);
+            h[p][k][j] = fma2(pack2(exp2_fast(e0), exp2_fast(e1)), h[p][k][j], pack2(n0, n1));
+          }
+        }
+    }
+  }
+
+  if (t_lo < t_end) {
+    load_tile(0, t_lo);
+    copies_wait();
+    __syncthreads();
+    prepare_tile(0);
+    if (t_lo + kTT < t_end) load_tile(1, t_lo + kTT);
+    __syncthreads();
+    int st = 0;
+    for (int t0 = t_lo; t0 < t_end; t0 += kTT, st ^= 1) {
+      const int nt = min(kTT, t_end - t0);
+#pragma unroll 2
+      for (int t = 0; t < nt; ++t) {
+        const ulonglong2* pB = reinterpret_cast<const ulonglong2*>(sB + t * S::NP + sub * kS);
+        const ulonglong2* pC = reinterpret_cast<const ulonglong2*>(sC + t * S::NP + sub * kS);
+        uint64_t vB[kS / 2], vC[kS / 2];
+#pragma unroll
+        for (int j = 0; j < kS / 4; ++j) {
+          const ulonglong2 w = pB[j];
+          vB[2 * j] = w.x, vB[2 * j + 1] = w.y;
+          if (PASS != kReduce) {
+            const ulonglong2 u = pC[j];
+            vC[2 * j] = u.x, vC[2 * j + 1] = u.y;
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          float4& word = dx[t * (S::CH / 2) + grp + p * S::groups];
+          const float4 w = word;
+          float y[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float dl = k ? w.y : w.x, dlx = k ? w.w : w.z;
+            const uint64_t dl2 = pack2(dl, dl), dlx2 = pack2(dlx, dlx);
+            uint64_t acc = 0;
+#pragma unroll
+            for (int j = 0; j < kS / 2; ++j) {
+              float e0, e1;
+              unpack2(mul2(dl2, A[p][k][j]), e0, e1);
+              h[p][k][j] = fma2(pack2(exp2_fast(e0), exp2_fast(e1)), h[p][k][j], mul2(dlx2, vB[j]));
+              if (PASS != kReduce) acc = j ? fma2(h[p][k][j], vC[j], acc) : mul2(h[p][k][j], vC[j]);
+            }
+            if (PASS == kReduce) {
+              dsum[p][k] += dl;
+            } else {
+              float y0, y1;
+              unpack2(acc, y0, y1);
+              y[k] = y0 + y1;
+            }
+          }
+          if (PASS != kReduce) {
+            // Sum over the channel's lanes; the result replaces the pair's delta words.
+            float* out = reinterpret_cast<float*>(&word);
+            if (L == 1) {
+              out[0] = y[0];
+              out[1] = y[1];
+            } else {
+              // neighbours swap channels: an even lane sums channel 0, an odd one channel 1
+              const float give = sub & 1 ? y[0] : y[1], keep = sub & 1 ? y[1] : y[0];
+              float s = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+#pragma unroll
+              for (int o = 2; o < L; o *= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+              if (sub < 2) out[sub] = s;
+            }
+          }
+        }
+      }
+      copies_wait();
+      __syncthreads();
+      if (PASS != kReduce) store_tile(st, t0);
+      if (t0 + kTT < t_end) prepare_tile(st ^ 1);
+      __syncthreads();
+      if (t0 + 2 * kTT < t_end) load_tile(st, t0 + 2 * kTT);
+    }
+  }
+
+  if (PASS != kReduce) {  // tokens past the sequence's length
+    const int z0 = max(t_end, t_lo);
+    const long long cells = (long long)(t_hi - z0) * nch;
+    for (long long e = tid; e < cells; e += kThreads)
+      from_f32(0.f, gy + size_t(z0 + e / nch) * io.Dm + int(e % nch));
+  }
+  const bool last = PASS == kWhole || (PASS == kJoin && chunk == a.chunks - 1);
+  if (slot >= 0 && (PASS == kReduce || (last && io.state_out))) {
+    const size_t per = size_t(io.B) * io.Dm;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int c = ch[p] + k;
+        if (c >= nch) continue;
+        float* dst = PASS == kReduce ? a.ws_h + ((chunk + 1) * per + bd + c) * io.N
+                                     : io.state_out + (size_t(slot) * io.Dm + d0 + c) * io.N;
+#pragma unroll
+        for (int j = 0; j < kS / 2; ++j) {
+          float h0, h1;
+          unpack2(h[p][k][j], h0, h1);
+          const int n = sub * kS + 2 * j;
+          if (n < io.N) dst[n] = h0;
+          if (n + 1 < io.N) dst[n + 1] = h1;
+        }
+        if (PASS == kReduce && sub == 0) a.ws_d[chunk * per + bd + c] = dsum[p][k];
+      }
+  }
+}
+
+// One token: a lane has four states of a channel (16 bytes in, 16 bytes out), L lanes a channel.
+// HBM bounds it: the state read and written once.
+template <typename T, int L>
+__global__ void __launch_bounds__(256) token_kernel(const __grid_constant__ ScanArgs a) {
+  const sdm_ssm_args& io = a.io;
+  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int sub = int(id % L);
+  const long long cell = id / L;
+  const int d = int(cell % io.Dm);
+  const long long row = cell / io.Dm;
+  const bool live = row < io.B;
+  const int b = live ? int(row) : 0;
+  const int slot = live ? row_slot(io.slots, b, io.n_slots, sub == 0 && d == 0 ? a.dev_err : nullptr) : -1;
+  const int len = slot < 0 ? 0 : row_length(io.lengths, b, 1);
+  float y = 0.f, x = 0.f;
+  if (slot >= 0) {
+    const int n0 = sub * 4;
+    const int g = d / a.Dg;
+    const float* A = io.A + size_t(d) * io.N + n0;
+    const float* hs = io.state ? io.state + (size_t(slot) * io.Dm + d) * io.N + n0 : nullptr;
+    float h[4] = {0.f, 0.f, 0.f, 0.f}, av[4], bv[4], cv[4];
+    const bool vec = a.vec_bc;  // N % 4 == 0 and states on 16 bytes
+    if (vec && n0 < io.N) {
+      if (hs) *reinterpret_cast<float4*>(h) = *reinterpret_cast<const float4*>(hs);
+      *reinterpret_cast<float4*>(av) = *reinterpret_cast<const float4*>(A);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        av[j] = n0 + j < io.N ? A[j] : 0.f;
+        if (hs && n0 + j < io.N) h[j] = hs[j];
+      }
+    }
+    if (len > 0) {
+      const T* gB = static_cast<const T*>(io.Bm) + b * io.B_bs + g * io.N + n0;
+      const T* gC = static_cast<const T*>(io.Cm) + b * io.C_bs + g * io.N + n0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bv[j] = n0 + j < io.N ? to_f32(gB[j]) : 0.f;
+        cv[j] = n0 + j < io.N ? to_f32(gC[j]) : 0.f;
+      }
+      x = to_f32(static_cast<const T*>(io.x)[b * io.x_bs + d]);
+      float dl = to_f32(static_cast<const T*>(io.dt)[b * io.dt_bs + d]);
+      if (io.dt_bias) dl += io.dt_bias[d];
+      if (io.softplus) dl = softplus(dl);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[j] = fmaf(exp2_fast(dl * decay_rate(av[j])), h[j], dl * x * bv[j]);
+        y = fmaf(h[j], cv[j], y);
+      }
+    }
+    if (io.state_out) {
+      float* ho = io.state_out + (size_t(slot) * io.Dm + d) * io.N + n0;
+      if (vec && n0 < io.N) {
+        *reinterpret_cast<float4*>(ho) = *reinterpret_cast<const float4*>(h);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n0 + j < io.N) ho[j] = h[j];
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < L; o *= 2) y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
+  if (live && sub == 0) {
+    if (len > 0) {
+      if (io.D) y = fmaf(io.D[d], x, y);
+      if (io.z) y *= silu(to_f32(static_cast<const T*>(io.z)[b * io.z_bs + d]));
+    }
+    from_f32(y, static_cast<T*>(io.y) + size_t(b) * io.Dm + d);
+  }
+}
+
+int lanes_for(int N, int per) {
+  int l = 1;
+  while (l * per < N) l *= 2;
+  return l;
+}
+
+template <typename T, int L, int P, int PASS>
+int launch_pass(const ScanArgs& a, int chunks, cudaStream_t s) {
+  using S = Tile<T, L, P>;
+  auto fn = scan_kernel<T, L, P, PASS>;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes) != cudaSuccess)
+    return SDM_ECUDA;
+  const long long blocks = (long long)a.tiles_g * a.io.G * a.io.B * chunks;
+  if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
+  fn<<<unsigned(blocks), kThreads, S::bytes, s>>>(a);
+  return last_launch_status();
+}
+
+template <typename T, int L>
+int launch_scan_l(ScanArgs& a, cudaStream_t s) {
+  constexpr int P = 1;
+  a.tiles_g = (a.Dg + Tile<T, L, P>::CH - 1) / Tile<T, L, P>::CH;
+  if (a.chunks <= 1) return launch_pass<T, L, P, kWhole>(a, 1, s);
+  const int st = launch_pass<T, L, P, kReduce>(a, a.chunks - 1, s);
+  return st != SDM_OK ? st : launch_pass<T, L, P, kJoin>(a, a.chunks, s);
+}
+
+template <typename T>
+int launch_scan(ScanArgs& a, cudaStream_t s) {
+  switch (lanes_for(a.io.N, kS)) {
+    case 1: return launch_scan_l<T, 1>(a, s);
+    case 2: return launch_scan_l<T, 2>(a, s);
+    case 4: return launch_scan_l<T, 4>(a, s);
+    case 8: return launch_scan_l<T, 8>(a, s);
+    case 16: return launch_scan_l<T, 16>(a, s);
+    default: return SDM_EUNSUPPORTED;
+  }
+}
+
+template <typename T>
+int launch_token(const ScanArgs& a, cudaStream_t s) {
+  const int L = lanes_for(a.io.N, 4);
+  const long long blocks = ((long long)a.io.B * a.io.Dm * L + 255) / 256;
+  if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
+  switch (L) {
+    case 1: token_kernel<T, 1><<<unsigned(blocks), 256, 0, s>>>(a); break;
+    case 2: token_kernel<T, 2><<<unsigned(blocks), 256, 0, s>>>(a); break;
+    case 4: token_kernel<T, 4><<<unsigned(blocks), 256, 0, s>>>(a); break;
+    case 8: token_kernel<T, 8><<<unsigned(blocks), 256, 0, s>>>(a); break;
+    case 16: token_kernel<T, 16><<<unsigned(blocks), 256, 0, s>>>(a); break;
+    case 32: token_kernel<T, 32><<<unsigned(blocks), 256, 0, s>>>(a); break;
+    default: return SDM_EUNSUPPORTED;
+  }
+  return last_launch_status();
+}
+
+// Chunks of a sequence and tokens of a chunk: one chunk where the channels alone give the card
+// enough blocks, else as many as bring it there, of 128 tokens at least.
+void cut(int B, int T, int Dm, int N, int G, int* chunks, int* chunk) {
+  const int L = lanes_for(N, kS), CH = 2 * kThreads / L;
+  const long long blocks = (long long)B * G * ((Dm / G + CH - 1) / CH);
+  long long n = blocks >= 304 ? 1 : (608 + blocks - 1) / blocks;
+  n = n < T / 128 ? n : T / 128;
+  if (n < 1) n = 1;
+  const int per = int(((T + n - 1) / n + kTT - 1) / kTT) * kTT;
+  *chunk = per;
+  *chunks = T > 0 ? (T + per - 1) / per : 1;
+}
+
+bool sizes_ok(int B, int T, int Dm, int N, int G) {
+  return B >= 1 && T >= 0 && Dm >= 1 && N >= 1 && G >= 1 && Dm % G == 0;
+}
+
+}  // namespace
+}  // namespace sdm
+
+using namespace sdm;
+
+extern "C" size_t sdm_selective_scan_workspace_size(int B, int T, int Dm, int N, int G) {
+  if (!sizes_ok(B, T, Dm, N, G) || N > SDM_MAX_SSM_N) return 0;
+  int chunks, chunk;
+  cut(B, T, Dm, N, G, &chunks, &chunk);
+  if (chunks <= 1) return 0;
+  return size_t(chunks) * B * Dm * (N + 1) * 4;
+}
+
+extern "C" int sdm_selective_scan(const sdm_ssm_args* args, void* workspace, size_t workspace_bytes,
+                                  int* dev_err, void* stream) {
+  if (!args) return SDM_EINVAL;
+  const sdm_ssm_args& io = *args;
+  if (!sizes_ok(io.B, io.T, io.Dm, io.N, io.G) || bad_dtype(io.dtype)) return SDM_EINVAL;
+  if (io.N > SDM_MAX_SSM_N || (long long)io.B * io.T > 0x7FFFFFFFLL || io.Dm > 0x3FFFFFF)
+    return SDM_EUNSUPPORTED;
+  if ((io.state || io.state_out || io.slots) && io.n_slots < (io.slots ? 1 : io.B)) return SDM_EINVAL;
+  const uintptr_t odd = io.dtype == SDM_F32 ? 3 : 1;
+  auto off = [](const void* p, uintptr_t m) { return (reinterpret_cast<uintptr_t>(p) & m) != 0; };
+  if (!io.A || off(io.A, 3) || off(io.D, 3) || off(io.dt_bias, 3) || off(io.state, 3) ||
+      off(io.state_out, 3) || off(io.lengths, 3) || off(io.slots, 3) || off(dev_err, 3))
+    return SDM_EALIGN;
+  if (io.T > 0 && (!io.x || !io.dt || !io.Bm || !io.Cm || !io.y || off(io.x, odd) || off(io.dt, odd) ||
+                   off(io.Bm, odd) || off(io.Cm, odd) || off(io.z, odd) || off(io.y, odd)))
+    return SDM_EALIGN;
+  if (io.T == 0 && (io.state == io.state_out || !io.state_out)) return SDM_OK;
+
+  ScanArgs a = {};
+  a.io = io;
+  a.Dg = io.Dm / io.G;
+  a.dev_err = dev_err;
+  cudaStream_t s = as_stream(stream);
+  if (io.T == 1) {
+    a.vec_bc = io.N % 4 == 0 && !off(io.A, 15) && !off(io.state, 15) && !off(io.state_out, 15);
+    return io.dtype == SDM_F32 ? launch_token<float>(a, s) : launch_token<__nv_bfloat16>(a, s);
+  }
+  const size_t need = sdm_selective_scan_workspace_size(io.B, io.T, io.Dm, io.N, io.G);
+  cut(io.B, io.T, io.Dm, io.N, io.G, &a.chunks, &a.chunk);
+  if (need) {
+    if (!aligned16(workspace)) return SDM_EALIGN;
+    if (workspace_bytes < need) return SDM_ENOSPACE;
+    a.ws_h = static_cast<float*>(workspace);
+    a.ws_d = a.ws_h + size_t(a.chunks) * io.B * io.Dm * io.N;
+  }
+  const int V = io.dtype == SDM_F32 ? 4 : 8;
+  auto rows16 = [&](const void* p, long long bs, long long ts) {
+    return !p || (!off(p, 15) && bs % V == 0 && ts % V == 0);
+  };
+  a.vec = a.Dg % V == 0 && rows16(io.x, io.x_bs, io.x_ts) && rows16(io.dt, io.dt_bs, io.dt_ts) &&
+          rows16(io.z, io.z_bs, io.z_ts) && !off(io.y, 15);
+  a.vec_bc = io.N % V == 0 && rows16(io.Bm, io.B_bs, io.B_ts) && rows16(io.Cm, io.C_bs, io.C_ts);
+  return io.dtype == SDM_F32 ? launch_scan<float>(a, s) : launch_scan<__nv_bfloat16>(a, s);
+}
