@@ -521,6 +521,25 @@ size_t sdm_selective_scan_workspace_size(int B, int T, int Dm, int N, int G);
 int sdm_selective_scan(const sdm_ssm_args* args, void* workspace, size_t workspace_bytes,
                        int* dev_err, void* stream);
 
+/* sdm_project_gated - gated feed-forward projections, both and the activation and the product in
+ * one kernel:  h = act(x Wg^T) * (x Wu^T).
+ *   x [M, D] bf16;  w [2F, D] bf16, one row per output column: Wg's F rows, then Wu's;
+ *   h [M, F] bf16;  act: SDM_ACT_SILU or SDM_ACT_GELU (the exact one, g Phi(g)).
+ * fp32 accumulation, one rounding.  Requires D % 8 == 0 and F % 8 == 0 (SDM_EUNSUPPORTED). */
+int sdm_project_gated(const void* x, const void* w, long long M, int D, int F, int act, void* h,
+                      int* dev_err, void* stream);
+
+/* sdm_project_gated_backward - its gradient for a given dh [M, F] bf16:
+ *   dg = dh * u * act'(g), du = dh * act(g);  dx = dg Wg + du Wu;  dw = [dg^T x; du^T x].
+ * g and u are recomputed from x and w.  dx [M, D], dw [2F, D] bf16, summed in fp32; dg and du are
+ * rounded to bf16 between the products.  M = 0 writes dw = 0.  The workspace holds [dg | du] and
+ * the partial sums of products that are split over their reduction; results do not depend on
+ * timing. */
+size_t sdm_project_gated_backward_workspace_size(long long M, int D, int F);
+int sdm_project_gated_backward(const void* x, const void* w, const void* dh, long long M, int D,
+                               int F, int act, void* dx, void* dw, void* workspace,
+                               size_t workspace_bytes, int* dev_err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,549 @@
+// Gated feed-forward projections and their gradient, on the tcgen05 tensor cores.
+//
+//   g = x Wg^T,  u = x Wu^T,  h = act(g) * u                     (w = [Wg; Wu], [2F, D])
+//   dg = dh * u * act'(g),  du = dh * act(g)
+//   dx = dg Wg + du Wu = [dg | du] w,   dw = [dg | du]^T x
+//
+// Four products of one shape run on one kernel, a persistent pair of CTAs (cta_group::2) that
+// forms 256 x 256 tiles with fp32 accumulators in TMEM, double-buffered, TMA feeding a ring of
+// stages (the roles of the projection kernel in sdm_project.cu):
+//   kForward   the pair's two halves of the column tile are 128 columns of Wg and the same 128 of
+//              Wu, so one thread of the epilogue holds g and u of an element and h leaves the chip
+//              once: neither g nor u is ever written.
+//   kSlope     the same product again in the backward pass (g and u were not kept: 4F bytes a token
+//              less to hold between the passes, for a third of the backward's flops); its epilogue
+//              reads dh and writes dg and du, rounded to bf16 for the two products that follow.
+//   kInput     dx = [dg | du] w: w's rows are the reduction here, so its tile is read MN-major.
+//   kWeight    dw = [dg | du]^T x: the tokens are the reduction, both operands MN-major.
+// No operand is transposed in memory: TMA boxes of 64 x 64 in the 128-byte swizzle serve as either
+// major, and only the descriptors differ.  Sums are fp32; dg and du are the only rounding between
+// inputs and outputs.
+#include "sdm_layers.cuh"
+#include "sdm_tcgen05.cuh"
+
+namespace sdm {
+namespace {
+
+enum Mode { kForward = 0, kSlope = 1, kInput = 2, kWeight = 3 };
+
+constexpr int kHalf = 128;                       // rows (and columns) of a tile each CTA stages
+constexpr int kOperand = kHalf * kTileK * 2;     // 16 KB
+constexpr int kStage = 2 * kOperand;
+constexpr int kStages = 6;
+constexpr int kRoles = 192;                      // copy warp, MMA warp, four epilogue warps
+constexpr int kBars = 2 * kStages + 5;           // full[], empty[], acc_full[2], acc_empty[2], drain
+constexpr int kSmem = kStages * kStage + 1024 + 256;
+constexpr uint32_t kColumns = 512;
+constexpr int kRowGroup = 32;                    // row tiles of a group of the tile order
+
+struct GatedArgs {
+  int rows, cols;       // of the output, in elements (kForward, kSlope: tokens and F)
+  int row_tiles, col_tiles, splits;
+  int kblocks, per_split;  // K steps in all, and of each split
+  int F, act;
+  __nv_bfloat16* out;      // h, dx or dw; [dg | du] for kSlope
+  const __nv_bfloat16* dh;
+  float* partial;          // [splits][rows][cols] where splits > 1
+  int* dev_err;
+};
+
+// D fp32, A and B bf16, M 256, N 256; bits 15 and 16: A, B MN-major.
+constexpr uint32_t idesc(bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         (uint32_t(256 >> 3) << 17) | (uint32_t(256 >> 4) << 24);
+}
+
+// MN-major operand of boxes of 64 (MN) x 64 (K): a box is 64 K rows of 128 bytes, 8-row atoms of
+// 1,024 bytes stacked along K (stride byte offset), the next 64 along MN one box further (leading
+// byte offset 8,192).  A K step of 16 is two atoms: 2,048 bytes.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(8192 >> 4) << 16) |
+         (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate,
+                                     uint32_t id) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(accumulate), "r"(id)
+      : "memory");
+}
+
+// g Phi(g), the exact gelu.
+__device__ __forceinline__ float gelu_cdf(float g) {
+  return 0.5f * erfcf(-0.70710678118654752f * g);
+}
+// Sigmoid; 0 where the exponential is inf.
+__device__ __forceinline__ float sigmoid(float g) {
+  return __fdividef(1.0f, 1.0f + exp2_fast(-kLog2e * g));
+}
+template <int ACT>
+__device__ __forceinline__ float gate(float g) {
+  return ACT == SDM_ACT_SILU ? silu(g) : g * gelu_cdf(g);
+}
+// act(g) and act'(g).
+template <int ACT>
+__device__ __forceinline__ void gate_slope(float g, float& a, float& s) {
+  if (ACT == SDM_ACT_SILU) {
+    const float p = sigmoid(g);
+    a = g * p;
+    s = fmaf(a, 1.0f - p, p);
+  } else {
+    const float p = gelu_cdf(g);
+    a = g * p;
+    s = fmaf(g * 0.39894228040143268f, exp2_fast(-0.5f * kLog2e * g * g), p);
+  }
+}
+
+// Work unit -> row tile, column tile, split: groups of kRowGroup row tiles, row tiles fastest, so
+// that units running at once share a few rows of A and a few column tiles of B in L2.
+struct Unit {
+  int row, col, split;
+};
+__device__ __forceinline__ Unit unit_at(int u, const GatedArgs& a) {
+  const int tiles = a.row_tiles * a.col_tiles;
+  Unit r;
+  r.split = u / tiles;
+  u -= r.split * tiles;
+  const int g = u / (kRowGroup * a.col_tiles), w = u - g * kRowGroup * a.col_tiles;
+  const int gm = min(kRowGroup, a.row_tiles - g * kRowGroup);
+  r.col = w / gm;
+  r.row = g * kRowGroup + (w - r.col * gm);
+  return r;
+}
+
+template <int MODE, int ACT>
+__device__ __forceinline__ void epilogue(const GatedArgs& a, const Unit& un, int rank, int row,
+                                         uint32_t taddr) {
+  const int m = (un.row * 2 + rank) * kHalf + row;
+  if constexpr (MODE == kForward || MODE == kSlope) {
+    const int f0 = un.col * kHalf;
+#pragma unroll 1
+    for (int c = 0; c < kHalf; c += 32) {
+      uint32_t g[32], u[32];
+      tmem_load32(taddr + uint32_t(c), g);
+      tmem_load32(taddr + uint32_t(kHalf + c), u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // F % 8 == 0: a 16-byte piece is in or out
+        const int f = f0 + c + 8 * j;
+        if (m >= a.rows || f >= a.F) break;
+        float o[8];
+        if constexpr (MODE == kForward) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            o[i] = gate<ACT>(__uint_as_float(g[8 * j + i])) * __uint_as_float(u[8 * j + i]);
+          *reinterpret_cast<uint4*>(a.out + size_t(m) * a.F + f) = Piece<__nv_bfloat16>::pack(o);
+        } else {
+          float d[8], o2[8];
+          Piece<__nv_bfloat16>::load(
+              __ldcs(reinterpret_cast<const uint4*>(a.dh + size_t(m) * a.F + f)), d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float v, s;
+            gate_slope<ACT>(__uint_as_float(g[8 * j + i]), v, s);
+            o[i] = d[i] * __uint_as_float(u[8 * j + i]) * s;
+            o2[i] = d[i] * v;
+          }
+          __nv_bfloat16* p = a.out + size_t(m) * (2 * size_t(a.F)) + f;
+          *reinterpret_cast<uint4*>(p) = Piece<__nv_bfloat16>::pack(o);
+          *reinterpret_cast<uint4*>(p + a.F) = Piece<__nv_bfloat16>::pack(o2);
+        }
+      }
+      __syncwarp();  // tcgen05.ld takes the whole warp
+    }
+  } else {
+    const int n0 = un.col * 2 * kHalf;
+#pragma unroll 1
+    for (int c = 0; c < 2 * kHalf; c += 32) {
+      uint32_t r[32];
+      tmem_load32(taddr + uint32_t(c), r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = n0 + c + 8 * j;
+        if (m >= a.rows || n >= a.cols) break;
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(r[8 * j + i]);
+        if (a.splits > 1) {
+          float* p = a.partial + (size_t(un.split) * a.rows + m) * a.cols + n;
+          *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<float4*>(p + 4) = make_float4(o[4], o[5], o[6], o[7]);
+        } else {
+          *reinterpret_cast<uint4*>(a.out + size_t(m) * a.cols + n) = Piece<__nv_bfloat16>::pack(o);
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// Every wait is bounded; a wait that runs out stops both CTAs, which drain the copies and MMAs in
+// flight, free TMEM and report SDM_DEV_TIMEOUT.
+template <int MODE, int ACT>
+__global__ void __launch_bounds__(kRoles, 1)
+    gated_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ GatedArgs a) {
+  constexpr bool kAMN = MODE == kWeight, kBMN = MODE == kInput || MODE == kWeight;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t ring = (raw + 1023u) & ~1023u;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (ring - raw) + kStages * kStage);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
+  volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* issued = tmem_slot + 2;  // copies issued per stage, read by the leader after a stop
+  const int FULL = 0, EMPTY = kStages, ACC_FULL = 2 * kStages, ACC_EMPTY = 2 * kStages + 2,
+            DRAIN = 2 * kStages + 4;
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const uint32_t peer_stop = cluster_addr(smem_u32(const_cast<int*>(stop)), rank ^ 1u);
+  const int cid = blockIdx.x / 2, ncl = gridDim.x / 2;
+  const int units = a.row_tiles * a.col_tiles * a.splits;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(FULL + s), 1);   // the leader's expect_tx; both CTAs' bytes
+      mbar_init(bar(EMPTY + s), 1);  // the leader's commit
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(ACC_FULL + i), 1);
+      mbar_init(bar(ACC_EMPTY + i), 8);  // the 4 epilogue warps of each CTA
+    }
+    mbar_init(bar(DRAIN), 1);
+    *stop = 0;
+    for (int s = 0; s < kStages; ++s) issued[s] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- copies (both CTAs) ----
+      const CUtensorMap* mapB = (MODE == kForward || MODE == kSlope) && rank ? &tmB2 : &tmB;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = cid; ok && u < units; u += ncl) {
+        const Unit un = unit_at(u, a);
+        const int m0 = (un.row * 2 + int(rank)) * kHalf;
+        const int n0 = kBMN ? un.col * 2 * kHalf + int(rank) * kHalf : un.col * kHalf;
+        const int k_lo = un.split * a.per_split, k_hi = min(a.kblocks, k_lo + a.per_split);
+        for (int kb = k_lo; kb < k_hi; ++kb) {
+          if (!mbar_wait_cluster(bar(EMPTY + stage), phase ^ 1u, stop, peer_stop, kWaitNs)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = ring + uint32_t(stage) * kStage, sb = sa + kOperand;
+          const uint32_t full = cluster_addr(bar(FULL + stage), 0);
+          if (leader) mbar_expect_tx(bar(FULL + stage), 2 * kStage);
+          if (kAMN) {
+            tma_load_2d_pair(sa, &tmA, m0, kb * kTileK, full);
+            tma_load_2d_pair(sa + kOperand / 2, &tmA, m0 + kHalf / 2, kb * kTileK, full);
+          } else {
+            tma_load_2d_pair(sa, &tmA, kb * kTileK, m0, full);
+          }
+          if (kBMN) {
+            tma_load_2d_pair(sb, mapB, n0, kb * kTileK, full);
+            tma_load_2d_pair(sb + kOperand / 2, mapB, n0 + kHalf / 2, kb * kTileK, full);
+          } else {
+            tma_load_2d_pair(sb, mapB, kb * kTileK, n0, full);
+          }
+          issued[stage] = issued[stage] + 1u;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ---- MMAs (leader only) ----
+      constexpr uint32_t id = idesc(kAMN, kBMN);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int it = 0;
+      for (int u = cid; ok && u < units; u += ncl, ++it) {
+        const Unit un = unit_at(u, a);
+        const int k_lo = un.split * a.per_split, k_hi = min(a.kblocks, k_lo + a.per_split);
+        const int acc = it & 1;
+        const uint32_t acc_par = uint32_t(it >> 1) & 1u;
+        if (!mbar_wait_cluster(bar(ACC_EMPTY + acc), acc_par ^ 1u, stop, peer_stop, kWaitNs)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + uint32_t(acc * 256);
+        for (int kb = k_lo; kb < k_hi; ++kb) {
+          if (!mbar_wait_cluster(bar(FULL + stage), phase, stop, peer_stop, kWaitNs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = ring + uint32_t(stage) * kStage, sb = sa + kOperand;
+#pragma unroll
+          for (int kk = 0; kk < kTileK / 16; ++kk)
+            mma2(d, kAMN ? mn_desc(sa + kk * 2048) : sw128_desc(sa + kk * 32),
+                 kBMN ? mn_desc(sb + kk * 2048) : sw128_desc(sb + kk * 32), kb > k_lo || kk > 0, id);
+          mma2_commit_both(bar(EMPTY + stage));
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) mma2_commit_both(bar(ACC_FULL + acc));
+      }
+      mma2_commit_local(bar(DRAIN));
+      mbar_wait_teardown(bar(DRAIN), 0);
+    }
+  } else {
+    // ---- epilogue (both CTAs): warp w reads TMEM lanes 32 * (w % 4) .. + 31 ----
+    const int quad = warp & 3;
+    int it = 0;
+    for (int u = cid; u < units; u += ncl, ++it) {
+      const int acc = it & 1;
+      const uint32_t acc_par = uint32_t(it >> 1) & 1u;
+      if (!__all_sync(0xFFFFFFFFu,
+                      mbar_wait_cluster(bar(ACC_FULL + acc), acc_par, stop, peer_stop, kWaitNs)))
+        break;
+      tc_fence_after();
+      epilogue<MODE, ACT>(a, unit_at(u, a), int(rank), quad * 32 + lane,
+                          tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * 256));
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(bar(ACC_EMPTY + acc), 0));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(kColumns)
+                 : "memory");
+  if (leader && warp == 0 && lane == 0 && *stop) {
+    // After a stop, every copy either CTA issued lands before the pair's shared memory goes away:
+    // per stage the two issued the same number of copies or one more than the other; the leader
+    // arms a phase only its peer issued with the peer's bytes, counts the peer's missing bytes of
+    // a phase only it issued as done, and waits for the last phase of each stage.
+    const uint32_t peer_issued = cluster_addr(smem_u32(const_cast<uint32_t*>(issued)), 1u);
+    for (int s = 0; s < kStages; ++s) {
+      const uint32_t lc = issued[s], pc = ld_cluster_u32(peer_issued + 4u * uint32_t(s));
+      if (pc == lc + 1u) {
+        mbar_expect_tx(bar(FULL + s), kStage);
+        mbar_wait_teardown(bar(FULL + s), lc & 1u);
+      } else if (lc == pc + 1u) {
+        mbar_complete_tx(bar(FULL + s), kStage);
+        mbar_wait_teardown(bar(FULL + s), (lc - 1u) & 1u);
+      } else if (lc == pc && lc > 0u) {
+        mbar_wait_teardown(bar(FULL + s), (lc - 1u) & 1u);
+      }
+    }
+  }
+  if (threadIdx.x == 0 && *stop && a.dev_err) atomicOr(a.dev_err, SDM_DEV_TIMEOUT);
+  cluster_sync_all();  // the peer's shared memory outlives the leader's drain
+}
+
+// Sums the splits' partial results in their order and rounds once.
+__global__ void __launch_bounds__(256) join_kernel(const float* partial, __nv_bfloat16* out,
+                                                   size_t n, int splits) {
+  const size_t i = (size_t(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  float o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = 0.f;
+  for (int s = 0; s < splits; ++s) {
+    const float4* p = reinterpret_cast<const float4*>(partial + size_t(s) * n + i);
+    const float4 v = __ldcs(p), w = __ldcs(p + 1);
+    o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
+    o[4] += w.x, o[5] += w.y, o[6] += w.z, o[7] += w.w;
+  }
+  *reinterpret_cast<uint4*>(out + i) = Piece<__nv_bfloat16>::pack(o);
+}
+
+int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
+
+// Splits of the reduction (K steps of 64) so that the 76 pairs of SMs are busy: the number s of
+// least time where a unit takes its K steps and about 8 more for its start and its epilogue, and
+// joining moves the partials twice (a K step is 512 clocks of a pair; HBM moves about 2 MB in it).
+int splits_for(long long tiles, int kblocks, double out_elems) {
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= 16 && s <= kblocks; ++s) {
+    const int per = ceil_div(kblocks, s);
+    if (ceil_div(kblocks, per) != s) continue;
+    const double t = double(ceil_div(tiles * s, 76)) * (per + 8) +
+                     (s > 1 ? out_elems * (8.0 * s + 2.0) / 1.8e6 + 10 : 0);
+    if (s == 1 || t < least) {
+      best = s;
+      least = t;
+    }
+  }
+  return best;
+}
+
+struct Plan {
+  int row_tiles, col_tiles, splits, kblocks;
+};
+Plan plan(int mode, int M, int D, int F) {
+  Plan p;
+  const int rows = mode == kWeight ? 2 * F : M;
+  p.row_tiles = ceil_div(rows, 2 * kHalf);
+  p.col_tiles = mode == kForward || mode == kSlope ? ceil_div(F, kHalf) : ceil_div(D, 2 * kHalf);
+  p.kblocks = ceil_div(mode == kInput ? 2LL * F : mode == kWeight ? M : D, kTileK);
+  p.splits = mode == kForward || mode == kSlope
+                 ? 1
+                 : splits_for((long long)p.row_tiles * p.col_tiles, p.kblocks, double(rows) * D);
+  return p;
+}
+
+// Row-major bf16 [rows, cols] in boxes of box_rows x 64.
+bool tile_map(CUtensorMap* map, const void* base, int rows, int cols, int box_rows) {
+  return bf16_tile_map(map, base, rows, cols, box_rows);
+}
+
+template <int MODE, int ACT>
+int launch_mode(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& B2, GatedArgs a,
+                const Plan& p, cudaStream_t s) {
+  a.row_tiles = p.row_tiles;
+  a.col_tiles = p.col_tiles;
+  a.splits = p.splits;
+  a.kblocks = p.kblocks;
+  a.per_split = ceil_div(p.kblocks, p.splits);
+  const long long units = (long long)p.row_tiles * p.col_tiles * p.splits;
+  if (units > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
+  auto fn = gated_kernel<MODE, ACT>;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    return SDM_ECUDA;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int sms = sm_count();
+  if (sms < 2) return SDM_ECUDA;
+  long long pairs = sms / 2;
+  cfg.gridDim = dim3(unsigned(pairs * 2));
+  cfg.blockDim = dim3(kRoles);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int active = 0;
+  if (cudaOccupancyMaxActiveClusters(&active, fn, &cfg) != cudaSuccess || active <= 0) return SDM_ECUDA;
+  if (active < pairs) pairs = active;
+  if (units < pairs) pairs = units;
+  cfg.gridDim = dim3(unsigned(pairs * 2));
+  if (cudaLaunchKernelEx(&cfg, fn, A, B, B2, a) != cudaSuccess) return SDM_ECUDA;
+  if (a.splits > 1) {
+    const size_t n = size_t(a.rows) * a.cols;
+    join_kernel<<<unsigned((n / 8 + 255) / 256), 256, 0, s>>>(a.partial, a.out, n, a.splits);
+  }
+  return last_launch_status();
+}
+
+template <int MODE>
+int launch_act(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& B2, const GatedArgs& a,
+               const Plan& p, cudaStream_t s) {
+  return a.act == SDM_ACT_SILU ? launch_mode<MODE, SDM_ACT_SILU>(A, B, B2, a, p, s)
+                               : launch_mode<MODE, SDM_ACT_GELU>(A, B, B2, a, p, s);
+}
+
+int check_gated(const void* x, const void* w, long long M, int D, int F, int act) {
+  if (M < 0 || D < 1 || F < 1 || (act != SDM_ACT_SILU && act != SDM_ACT_GELU)) return SDM_EINVAL;
+  if (D % 8 || F % 8 || M > 0x7FFFFFFFLL - 256 || D > 0x3FFFFFF || F > 0x3FFFFFF) return SDM_EUNSUPPORTED;
+  if (!aligned16(w) || (M > 0 && !aligned16(x))) return SDM_EALIGN;
+  return SDM_OK;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace sdm
+
+using namespace sdm;
+
+extern "C" int sdm_project_gated(const void* x, const void* w, long long M, int D, int F, int act,
+                                 void* h, int* dev_err, void* stream) {
+  const int st = check_gated(x, w, M, D, F, act);
+  if (st != SDM_OK) return st;
+  if (M == 0) return SDM_OK;
+  if (!aligned16(h)) return SDM_EALIGN;
+  CUtensorMap tx, tg, tu;
+  if (!tile_map(&tx, x, int(M), D, kHalf) || !tile_map(&tg, w, F, D, kHalf) ||
+      !tile_map(&tu, static_cast<const __nv_bfloat16*>(w) + size_t(F) * D, F, D, kHalf))
+    return SDM_ECUDA;
+  GatedArgs a = {};
+  a.rows = int(M);
+  a.cols = a.F = F;
+  a.act = act;
+  a.out = static_cast<__nv_bfloat16*>(h);
+  a.dev_err = dev_err;
+  return launch_act<kForward>(tx, tg, tu, a, plan(kForward, int(M), D, F), as_stream(stream));
+}
+
+extern "C" size_t sdm_project_gated_backward_workspace_size(long long M, int D, int F) {
+  if (M < 1 || D < 1 || F < 1 || M > 0x7FFFFFFFLL - 256) return 0;
+  const Plan pi = plan(kInput, int(M), D, F), pw = plan(kWeight, int(M), D, F);
+  size_t part = 0;
+  if (pi.splits > 1) part = size_t(pi.splits) * M * D * 4;
+  if (pw.splits > 1) {
+    const size_t n = size_t(pw.splits) * 2 * F * D * 4;
+    part = n > part ? n : part;
+  }
+  return round256(size_t(M) * 2 * F * 2) + part;
+}
+
+extern "C" int sdm_project_gated_backward(const void* x, const void* w, const void* dh, long long M,
+                                          int D, int F, int act, void* dx, void* dw, void* workspace,
+                                          size_t workspace_bytes, int* dev_err, void* stream) {
+  int st = check_gated(x, w, M, D, F, act);
+  if (st != SDM_OK) return st;
+  if (!aligned16(dw) || (M > 0 && (!aligned16(dh) || !aligned16(dx)))) return SDM_EALIGN;
+  cudaStream_t s = as_stream(stream);
+  if (M == 0)
+    return cudaMemsetAsync(dw, 0, size_t(2) * F * D * 2, s) == cudaSuccess ? SDM_OK : SDM_ECUDA;
+  if (!aligned16(workspace)) return SDM_EALIGN;
+  if (workspace_bytes < sdm_project_gated_backward_workspace_size(M, D, F)) return SDM_ENOSPACE;
+  __nv_bfloat16* slope = static_cast<__nv_bfloat16*>(workspace);
+  CUtensorMap tx, tg, tu, ts, tw, tst, txt;
+  if (!tile_map(&tx, x, int(M), D, kHalf) || !tile_map(&tg, w, F, D, kHalf) ||
+      !tile_map(&tu, static_cast<const __nv_bfloat16*>(w) + size_t(F) * D, F, D, kHalf) ||
+      !tile_map(&ts, slope, int(M), 2 * F, kHalf) || !tile_map(&tw, w, 2 * F, D, kTileK) ||
+      !tile_map(&tst, slope, int(M), 2 * F, kTileK) || !tile_map(&txt, x, int(M), D, kTileK))
+    return SDM_ECUDA;
+  GatedArgs a = {};
+  a.rows = int(M);
+  a.cols = a.F = F;
+  a.act = act;
+  a.out = slope;
+  a.dh = static_cast<const __nv_bfloat16*>(dh);
+  a.dev_err = dev_err;
+  st = launch_act<kSlope>(tx, tg, tu, a, plan(kSlope, int(M), D, F), s);
+  if (st != SDM_OK) return st;
+  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + round256(size_t(M) * 2 * F * 2));
+  a.cols = D;
+  a.out = static_cast<__nv_bfloat16*>(dx);
+  st = launch_mode<kInput, 0>(ts, tw, tw, a, plan(kInput, int(M), D, F), s);
+  if (st != SDM_OK) return st;
+  a.rows = 2 * F;
+  a.out = static_cast<__nv_bfloat16*>(dw);
+  return launch_mode<kWeight, 0>(tst, txt, txt, a, plan(kWeight, int(M), D, F), s);
+}

@@ -41,6 +41,9 @@ def _fn(name):
             "sdm_causal_conv": ([p, ll, ll, i, p, p, i, i, i, i, i, i, p, p, i, p, p, p, p, p], i),
             "sdm_selective_scan": ([_c.POINTER(_ScanArgs), p, sz, p, p], i),
             "sdm_selective_scan_workspace_size": ([i, i, i, i, i], sz),
+            "sdm_project_gated": ([p, p, ll, i, i, i, p, p, p], i),
+            "sdm_project_gated_backward": ([p, p, p, ll, i, i, i, p, p, p, sz, p, p], i),
+            "sdm_project_gated_backward_workspace_size": ([ll, i, i], sz),
         }[name]
         _fns[name] = f
     return f
@@ -240,3 +243,68 @@ def selective_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, *, state, state
                                 None if z is None else z.unsqueeze(1), dt_bias, state, state_out, dt_softplus, None,
                                 slots, None if out is None else out.unsqueeze(1), None, dev_err)
     return (y.squeeze(1) if out is None else out), written
+
+
+def _gated_args(x, w, index):
+    """(tokens, D, F, address of x, address of w) of the gated projections' operands."""
+    bf16 = torch.bfloat16
+    if x.dim() < 1 or not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[0] % 2:
+        raise ValueError("x must be [..., D] and w [2 * F, D]")
+    D = x.shape[-1]
+    return (x.numel() // D if D else 0, D, w.shape[0] // 2, _dense(x, "x", bf16, x.shape, index),
+            _dense(w, "w", bf16, (w.shape[0], D), index))
+
+
+def project_gated(x, w, activation="silu", out=None, dev_err=None):
+    """Gated feed-forward projections in one kernel: h = act(x Wg^T) * (x Wu^T) (sdm_project_gated).
+
+    x: [..., D] bf16; w: [2*F, D] bf16, one row per output column, Wg's F rows and then Wu's; D and F multiples of
+    8.  activation: "silu" or "gelu" (the exact one).  Returns h [..., F] bf16."""
+    index = _cuda_index(x, "x")
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return project_gated(x, w, activation, out, dev_err)
+    act = _activation(activation, ("silu", "gelu"))
+    M, D, F, px, pw = _gated_args(x, w, index)
+    shape = (*x.shape[:-1], F)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    st = _fn("sdm_project_gated")(px, pw, M, D, F, act, _dense(out, "out", torch.bfloat16, shape, index),
+                                  _dense(dev_err, "dev_err", torch.int32, (1,), index), _stream(index))
+    if st != 0:
+        raise SDMError("sdm_project_gated", st)
+    return out
+
+
+def project_gated_backward_workspace_size(M: int, D: int, F: int) -> int:
+    """Bytes of workspace project_gated_backward needs for M tokens."""
+    return int(_fn("sdm_project_gated_backward_workspace_size")(M, D, F))
+
+
+def project_gated_backward(x, w, dh, activation="silu", dx=None, dw=None, workspace=None, dev_err=None):
+    """Gradient of project_gated: (dx [..., D], dw [2*F, D]) for dh [..., F], all bf16
+    (sdm_project_gated_backward).  The forward pass keeps nothing but its inputs: the projections are recomputed."""
+    index = _cuda_index(x, "x")
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return project_gated_backward(x, w, dh, activation, dx, dw, workspace, dev_err)
+    act = _activation(activation, ("silu", "gelu"))
+    bf16 = torch.bfloat16
+    M, D, F, px, pw = _gated_args(x, w, index)
+    ph = _dense(dh, "dh", bf16, (*x.shape[:-1], F), index)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=bf16, device=x.device)
+    if dw is None:
+        dw = torch.empty(w.shape, dtype=bf16, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(max(16, project_gated_backward_workspace_size(M, D, F)), dtype=torch.uint8,
+                                device=x.device)
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+        _refuse(workspace, "workspace", torch.uint8, None, index)
+    st = _fn("sdm_project_gated_backward")(
+        px, pw, ph, M, D, F, act, _dense(dx, "dx", bf16, x.shape, index), _dense(dw, "dw", bf16, w.shape, index),
+        workspace.data_ptr(), workspace.numel(), _dense(dev_err, "dev_err", torch.int32, (1,), index),
+        _stream(index))
+    if st != 0:
+        raise SDMError("sdm_project_gated_backward", st)
+    return dx, dw

@@ -95,3 +95,29 @@ def act_and_slope(g, act):
         return g * p, p * (1 + g * (1 - p))
     p = 0.5 * np.vectorize(math.erfc)(-g / math.sqrt(2.0))
     return g * p, p + g * np.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
+
+
+def gated(x, w, act):
+    """(h, g, u, bound of h's error before its rounding, bounds of g's and u's).  D exact products, summed in fp32 in
+    any order: within 4 D U of the sum of their sizes."""
+    F, D = w.shape[0] // 2, x.shape[1]
+    g, u = x @ w[:F].T, x @ w[F:].T
+    eg, eu = 4 * D * U * (np.abs(x) @ np.abs(w[:F]).T), 4 * D * U * (np.abs(x) @ np.abs(w[F:]).T)
+    a, slope = act_and_slope(g, act)
+    ea = (np.abs(slope) + eg) * eg + (16 + 8 * np.abs(g)) * U * np.abs(a)  # |act''| <= 1
+    return a * u, g, u, (np.abs(u) + eu) * ea + np.abs(a) * eu + 2 * U * np.abs(a * u), eg, eu
+
+
+def gated_grad(x, w, dh, act):
+    """(dx, dw, bounds of their errors before the last rounding): dg and du are rounded to bf16 on the way."""
+    F = w.shape[0] // 2
+    _, g, u, _, eg, eu = gated(x, w, act)
+    a, s = act_and_slope(g, act)
+    ea = (np.abs(s) + eg) * eg + (16 + 8 * np.abs(g)) * U * np.abs(a)
+    es = eg + (32 + 16 * np.abs(g)) * U * (1 + np.abs(g))
+    d = np.concatenate([dh * u * s, dh * a], axis=1)
+    e = np.concatenate([np.abs(dh) * ((np.abs(u) + eu) * es + np.abs(s) * eu), np.abs(dh) * ea], axis=1)
+    e = e + (2.0 ** -8 + 4 * U) * (np.abs(d) + e)
+    n = 4 * U * (np.abs(d) + e)
+    dx, dw = d @ w, d.T @ x
+    return dx, dw, (e + 2 * F * n) @ np.abs(w), (e + x.shape[0] * n).T @ np.abs(x)
