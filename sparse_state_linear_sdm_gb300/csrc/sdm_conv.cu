@@ -7,14 +7,16 @@
 // state is the last K-1 inputs of each sequence.  2K flop for each element read and written
 // once: HBM bounds it, so each thread keeps its 16-byte piece of channels (8 bf16 or 4 fp32)
 // and walks a strip of tokens with the last K-1 inputs in registers: every input is read once,
-// except the K-1 tokens before a strip.  Loads of kAhead tokens are issued together.
+// except the K-1 tokens before a strip.  The next kAhead tokens are always under way, as raw words:
+// few registers, so many warps.
 #include "sdm_layers.cuh"
 
 namespace sdm {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kAhead = 8;  // tokens loaded together; strips are multiples of it, so K-1 < strip
+constexpr int kAhead = 4;  // tokens loaded while the ones before are computed
+constexpr int kMinStrip = 8;  // shortest strip: longer than the window
 
 struct ConvArgs {
   const void* x;
@@ -30,31 +32,59 @@ struct ConvArgs {
   void* y;
   int* dev_err;
   int strip, strips, pieces;  // tokens a thread, strips a sequence, pieces a row
+  bool w_vec;                 // w and bias start on 8 bytes
 };
 
-__device__ __forceinline__ float weight_at(const void* p, int dt, size_t i) {
-  return dt == SDM_F32 ? static_cast<const float*>(p)[i]
-                       : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+// N weights from element i on; 8 bytes at a time where `vec` says that they start there.
+template <int N, int V>
+__device__ __forceinline__ void load_weights(const void* p, int dt, size_t i, bool vec, float (&w)[N]) {
+  if (V > 1 && vec) {
+    if (dt == SDM_F32) {
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) {
+        const float2 v = reinterpret_cast<const float2*>(static_cast<const float*>(p) + i)[k];
+        w[2 * k] = v.x, w[2 * k + 1] = v.y;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+        const uint2 v = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i)[k];
+        w[4 * k] = __uint_as_float(v.x << 16), w[4 * k + 1] = __uint_as_float(v.x & 0xFFFF0000u);
+        w[4 * k + 2] = __uint_as_float(v.y << 16), w[4 * k + 3] = __uint_as_float(v.y & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      w[k] = dt == SDM_F32 ? static_cast<const float*>(p)[i + k]
+                           : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i + k]);
+  }
 }
 
-// V channels at p: one 16-byte load where V is a whole piece, else one element.
+// V channels as they lie in memory: one 16-byte word where V is a whole piece, else one element.
 template <typename T, int V>
-__device__ __forceinline__ void load_piece(const T* p, float (&v)[V]) {
-  if constexpr (V == 1)
-    v[0] = to_f32(*p);
-  else
-    Piece<T>::load(*reinterpret_cast<const uint4*>(p), v);
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_piece(T* p, const float (&v)[V]) {
-  if constexpr (V == 1)
-    from_f32(v[0], p);
-  else
-    *reinterpret_cast<uint4*>(p) = Piece<T>::pack(v);
-}
+struct Word {
+  using type = uint4;
+  __device__ static type zero() { return make_uint4(0, 0, 0, 0); }
+  __device__ static void load(const type& w, float (&v)[V]) { Piece<T>::load(w, v); }
+  __device__ static type pack(const float (&v)[V]) { return Piece<T>::pack(v); }
+};
+template <typename T>
+struct Word<T, 1> {
+  using type = T;
+  __device__ static type zero() { return T(0.f); }
+  __device__ static void load(const type& w, float (&v)[1]) { v[0] = to_f32(w); }
+  __device__ static type pack(const float (&v)[1]) {
+    T r;
+    from_f32(v[0], &r);
+    return r;
+  }
+};
 
 template <typename T, int K, int V>
-__global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads) conv_kernel(const __grid_constant__ ConvArgs a) {
+  using W = Word<T, V>;
+  using word = typename W::type;
   const long long id = (long long)blockIdx.x * kConvThreads + threadIdx.x;
   const int piece = int(id % a.pieces);
   const long long row = id / a.pieces;
@@ -66,27 +96,30 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
   const int t0 = strip * a.strip, t1 = min(t0 + a.strip, a.T);
   const T* x = static_cast<const T*>(a.x) + b * a.x_bs + d;
   T* y = static_cast<T*>(a.y) + (size_t(b) * a.T) * a.D + d;
+  auto token = [&](int t) {  // zero past the sequence
+    return t < len ? *reinterpret_cast<const word*>(x + t * a.x_ts) : W::zero();
+  };
 
-  float w[K][V], bias[V], win[K - 1][V];
+  word next[kAhead];
 #pragma unroll
-  for (int j = 0; j < K; ++j)
+  for (int k = 0; k < kAhead; ++k) next[k] = token(t0 + k);
+
+  float w[K * V], bias[V];
+  load_weights<K * V, V>(a.w, a.w_dt, size_t(d) * K, a.w_vec, w);  // w[i * K + j]: channel i, tap j
 #pragma unroll
-    for (int i = 0; i < V; ++i) w[j][i] = weight_at(a.w, a.w_dt, size_t(d + i) * K + j);
-#pragma unroll
-  for (int i = 0; i < V; ++i) bias[i] = a.bias ? weight_at(a.bias, a.w_dt, d + i) : 0.f;
+  for (int i = 0; i < V; ++i) bias[i] = 0.f;
+  if (a.bias) load_weights<V, V>(a.bias, a.w_dt, d, a.w_vec, bias);
 
   const size_t srow = size_t(max(slot, 0)) * (K - 1) * a.D + d;
+  word old[K - 1];
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
-    const int t = t0 - (K - 1) + j;
-    if (t0 > 0 && t < len) {
-      load_piece<T, V>(x + t * a.x_ts, win[j]);
-    } else if (t0 == 0 && a.state && slot >= 0) {
-      load_piece<T, V>(static_cast<const T*>(a.state) + srow + size_t(j) * a.D, win[j]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) win[j][i] = 0.f;
-    }
+    if (t0 > 0)
+      old[j] = token(t0 - (K - 1) + j);
+    else
+      old[j] = a.state && slot >= 0
+                   ? *reinterpret_cast<const word*>(static_cast<const T*>(a.state) + srow + size_t(j) * a.D)
+                   : W::zero();
   }
   if (t0 == 0 && slot >= 0 && a.state_out) {
     // This thread alone reads its channels' old state (above) and writes the new one, so the
@@ -94,50 +127,46 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(ConvArgs a) {
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
       const int t = len - (K - 1) + j;
-      float v[V];
+      word v = W::zero();
       if (t >= 0) {
-        load_piece<T, V>(x + t * a.x_ts, v);
+        v = token(t);
       } else {  // a sequence shorter than the window keeps the end of the old state
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 0.f;
-#pragma unroll
         for (int o = 0; o < K - 1; ++o)
-          if (o == t + K - 1) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = win[o][i];
-          }
+          if (o == t + K - 1) v = old[o];
       }
-      store_piece<T, V>(static_cast<T*>(a.state_out) + srow + size_t(j) * a.D, v);
+      *reinterpret_cast<word*>(static_cast<T*>(a.state_out) + srow + size_t(j) * a.D) = v;
     }
   }
+  float win[K - 1][V];
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) W::load(old[j], win[j]);
 
   for (int t = t0; t < t1; t += kAhead) {
-    float in[kAhead][V];
+    word now[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (t + k < len) {
-        load_piece<T, V>(x + (t + k) * a.x_ts, in[k]);
-      } else {
+    for (int k = 0; k < kAhead; ++k) now[k] = next[k];
+    if (t + kAhead < t1) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) in[k][i] = 0.f;
-      }
+      for (int k = 0; k < kAhead; ++k) next[k] = token(t + kAhead + k);
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       if (t + k >= t1) break;
-      float o[V];
+      float in[V], o[V];
+      W::load(now[k], in);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         float s = bias[i];
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) s = fmaf(w[j][i], win[j][i], s);
-        s = fmaf(w[K - 1][i], in[k][i], s);
+        for (int j = 0; j < K - 1; ++j) s = fmaf(w[i * K + j], win[j][i], s);
+        s = fmaf(w[i * K + K - 1], in[i], s);
         o[i] = t + k < len ? (a.act ? silu(s) : s) : 0.f;
 #pragma unroll
         for (int j = 0; j + 1 < K - 1; ++j) win[j][i] = win[j + 1][i];
-        win[K - 2][i] = in[k][i];
+        win[K - 2][i] = in[i];
       }
-      store_piece<T, V>(y + size_t(t + k) * a.D, o);
+      *reinterpret_cast<word*>(y + size_t(t + k) * a.D) = W::pack(o);
     }
   }
 }
@@ -196,12 +225,13 @@ extern "C" int sdm_causal_conv(const void* x, long long x_bstride, long long x_t
   const bool vec = D % V == 0 && x_bstride % V == 0 && x_tstride % V == 0 && !off(x, 15) &&
                    !off(y, 15) && !off(state, 15) && !off(state_out, 15);
   ConvArgs a{x,     x_bstride, x_tstride, w,     bias, w_dt,    B, T, D,
-             act,   state,     state_out, n_slots, lengths, slots, y, dev_err, 0, 0, 0};
+             act,   state,     state_out, n_slots, lengths, slots, y, dev_err, 0, 0, 0, false};
   a.pieces = vec ? D / V : D;
-  // Strips of 32 tokens (the K-1 tokens read twice are then under a tenth), shorter ones where
-  // that leaves the card's threads short.
-  a.strip = 32;
-  while (a.strip > kAhead &&
+  a.w_vec = !off(w, 7) && !off(bias, 7);
+  // Strips of 128 tokens (the K-1 tokens read twice and the weights are then a small part),
+  // shorter ones where that leaves the card's threads short.
+  a.strip = 128;
+  while (a.strip > kMinStrip &&
          (long long)B * ((T + a.strip - 1) / a.strip) * a.pieces < 152LL * 1024)
     a.strip /= 2;
   a.strips = T > 0 ? (T + a.strip - 1) / a.strip : 1;

@@ -63,22 +63,55 @@ __device__ __forceinline__ float silu(float x) {
   return __fdividef(x, 1.0f + exp2_fast(-kLog2e * x));
 }
 
-// log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1].  log(1 + e) = 2 artanh(s) with
-// s = e / (2 + e) <= 1/3, summed as the series 2 s (1 + s^2/3 + s^4/5 + ...): every term is
-// positive, so the result keeps its relative precision where e is tiny (the logarithm of the
-// rounded 1 + e would not), and a step size of 1e-3 is as exact as one of 1.  Eight terms leave
-// a relative error below 2e-9 at s = 1/3.
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1], of two values.  log(1 + e) = e p(e)
+// keeps its relative precision where e is tiny (the logarithm of the rounded 1 + e would not), so a
+// step size of 1e-3 is as exact as one of 1.  p is the polynomial of degree 8 nearest to
+// log(1 + e) / e on [0, 1] in relative error (3e-8; 2e-7 with its roundings), by weighted least
+// squares on Chebyshev points, the weights moved until the error was level.
+__device__ __forceinline__ uint64_t softplus2(uint64_t x) {
+  float x0, x1;
+  unpack2(x, x0, x1);
+  const uint64_t e = pack2(exp2_fast(-kLog2e * fabsf(x0)), exp2_fast(-kLog2e * fabsf(x1)));
+  auto both = [](float v) { return pack2(v, v); };
+  uint64_t p = fma2(e, both(0.0052326880395412445f), both(-0.029505213722586632f));
+  p = fma2(e, p, both(0.07822591066360474f));
+  p = fma2(e, p, both(-0.13663242757320404f));
+  p = fma2(e, p, both(0.19106005132198334f));
+  p = fma2(e, p, both(-0.2484298199415207f));
+  p = fma2(e, p, both(0.3331909775733948f));
+  p = fma2(e, p, both(-0.4999949336051941f));
+  p = fma2(e, p, both(0.9999999403953552f));
+  return fma2(e, p, pack2(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f)));
+}
 __device__ __forceinline__ float softplus(float x) {
-  const float e = exp2_fast(-kLog2e * fabsf(x));
-  const float s = __fdividef(e, 2.0f + e);
-  const float q = s * s;
-  float p = fmaf(q, 1.0f / 15.0f, 1.0f / 13.0f);
-  p = fmaf(q, p, 1.0f / 11.0f);
-  p = fmaf(q, p, 1.0f / 9.0f);
-  p = fmaf(q, p, 1.0f / 7.0f);
-  p = fmaf(q, p, 1.0f / 5.0f);
-  p = fmaf(q, p, 1.0f / 3.0f);
-  return fmaxf(x, 0.0f) + 2.0f * fmaf(s * q, p, s);
+  float a, b;
+  unpack2(softplus2(pack2(x, x)), a, b);
+  return a;
 }
 
 // The sequence length of batch row b, clamped to [0, T] (T without lengths).

@@ -11,6 +11,8 @@
 // A GB300 SM does 32 exp2 and 31 such foursomes a clock (measured), so with N = 16 and bf16 the
 // arithmetic takes 1.5 times as long as HBM does for the 8 bytes of an element: the arithmetic is
 // what has to be kept fed.
+#include <type_traits>
+
 #include "sdm_layers.cuh"
 
 namespace sdm {
@@ -19,6 +21,7 @@ namespace {
 constexpr int kS = 8;         // states a lane holds of each of its channels
 constexpr int kThreads = 128;
 constexpr int kTT = 16;       // tokens of a shared-memory tile
+constexpr int kSteps = 4;     // tokens taken together by a lane
 
 struct ScanArgs {
   sdm_ssm_args io;
@@ -30,26 +33,6 @@ struct ScanArgs {
   bool vec_bc;                 // rows of B and C in 16-byte pieces (N a multiple of the piece)
   int* dev_err;
 };
-
-// Two fp32 operations an instruction.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 
 // A in units of exp2.  A finite A stays finite, so that a step of size 0 has the decay 1 (0 times
 // an infinite rate would have none).
@@ -183,11 +166,18 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
   // stay in registers.
   static_assert(kThreads % S::RV == 0, "a thread's pieces share their channels");
   const int pr = tid % S::RV, pc = pr * V;
-  float bias[V], skip[V];
+  uint64_t bias[V / 2], skip[V / 2];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bias[i] = io.dt_bias && pc + i < nch ? io.dt_bias[d0 + pc + i] : 0.f;
-    skip[i] = PASS != kReduce && io.D && pc + i < nch ? io.D[d0 + pc + i] : 0.f;
+  for (int i = 0; i < V / 2; ++i) {
+    float bv[2], sv[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = pc + 2 * i + k;
+      bv[k] = io.dt_bias && c < nch ? io.dt_bias[d0 + c] : 0.f;
+      sv[k] = PASS != kReduce && io.D && c < nch ? io.D[d0 + c] : 0.f;
+    }
+    bias[i] = pack2(bv[0], bv[1]);
+    skip[i] = pack2(sv[0], sv[1]);
   }
 
   // Piece v of a tile holds channels c .. c+V-1 of token t; its pairs i go to plane i, so that the
@@ -199,14 +189,12 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
       Piece<T>::load(*reinterpret_cast<const uint4*>(raw(st, 0) + v * V), x);
       Piece<T>::load(*reinterpret_cast<const uint4*>(raw(st, 1) + v * V), d);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        d[i] += bias[i];
-        if (io.softplus) d[i] = softplus(d[i]);
+      for (int i = 0; i < V / 2; ++i) {
+        uint64_t dl = add2(pack2(d[2 * i], d[2 * i + 1]), bias[i]);
+        if (io.softplus) dl = softplus2(dl);
+        *reinterpret_cast<ulonglong2*>(&dx[t * (S::CH / 2) + i * S::RV + pr]) =
+            make_ulonglong2(dl, mul2(dl, pack2(x[2 * i], x[2 * i + 1])));
       }
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i)
-        dx[t * (S::CH / 2) + i * S::RV + pr] =
-            make_float4(d[2 * i], d[2 * i + 1], d[2 * i] * x[2 * i], d[2 * i + 1] * x[2 * i + 1]);
     }
     for (int e = tid; e < kTT * S::NP; e += kThreads) {
       sB[e] = to_f32(raw_bc(st, 0)[e]);
@@ -219,23 +207,15 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
     for (int v = tid; v < S::pieces; v += kThreads) {
       const int t = v / S::RV;
       if (t >= nt || pc >= nch) continue;
-      float x[V], o[V];
+      float x[V], o[V], z[V];
       Piece<T>::load(*reinterpret_cast<const uint4*>(raw(st, 0) + v * V), x);
+      if (io.z) Piece<T>::load(*reinterpret_cast<const uint4*>(raw(st, 2) + v * V), z);
 #pragma unroll
       for (int i = 0; i < V / 2; ++i) {
-        const float2 p = *reinterpret_cast<const float2*>(&dx[t * (S::CH / 2) + i * S::RV + pr]);
-        o[2 * i] = p.x;
-        o[2 * i + 1] = p.y;
-      }
-      if (io.D) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = fmaf(skip[i], x[i], o[i]);
-      }
-      if (io.z) {
-        float z[V];
-        Piece<T>::load(*reinterpret_cast<const uint4*>(raw(st, 2) + v * V), z);
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] *= silu(z[i]);
+        uint64_t y = *reinterpret_cast<const uint64_t*>(&dx[t * (S::CH / 2) + i * S::RV + pr]);
+        y = fma2(skip[i], pack2(x[2 * i], x[2 * i + 1]), y);
+        if (io.z) y = mul2(y, pack2(silu(z[2 * i]), silu(z[2 * i + 1])));
+        unpack2(y, o[2 * i], o[2 * i + 1]);
       }
       T* p = gy + size_t(t0 + t) * io.Dm + pc;
       if (a.vec) {
@@ -314,6 +294,95 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
     }
   }
 
+  // G tokens from t of the prepared tile.  Their sums over the states are kept until the end and
+  // added over the channel's lanes together, so that no token waits for the one before it.
+  auto steps = [&](int t, auto count) {
+    constexpr int G = decltype(count)::value;
+    float y[P][G][2];
+#pragma unroll
+    for (int s = 0; s < G; ++s) {
+      const ulonglong2* pB = reinterpret_cast<const ulonglong2*>(sB + (t + s) * S::NP + sub * kS);
+      const ulonglong2* pC = reinterpret_cast<const ulonglong2*>(sC + (t + s) * S::NP + sub * kS);
+      uint64_t vB[kS / 2], vC[kS / 2];
+#pragma unroll
+      for (int j = 0; j < kS / 4; ++j) {
+        const ulonglong2 w = pB[j];
+        vB[2 * j] = w.x, vB[2 * j + 1] = w.y;
+        if (PASS != kReduce) {
+          const ulonglong2 u = pC[j];
+          vC[2 * j] = u.x, vC[2 * j + 1] = u.y;
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const float4 w = dx[(t + s) * (S::CH / 2) + grp + p * S::groups];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float dl = k ? w.y : w.x, dlx = k ? w.w : w.z;
+          const uint64_t dl2 = pack2(dl, dl), dlx2 = pack2(dlx, dlx);
+          uint64_t acc = 0;
+#pragma unroll
+          for (int j = 0; j < kS / 2; ++j) {
+            float e0, e1;
+            unpack2(mul2(dl2, A[p][k][j]), e0, e1);
+            h[p][k][j] = fma2(pack2(exp2_fast(e0), exp2_fast(e1)), h[p][k][j], mul2(dlx2, vB[j]));
+            if (PASS != kReduce) acc = j ? fma2(h[p][k][j], vC[j], acc) : mul2(h[p][k][j], vC[j]);
+          }
+          if (PASS == kReduce) {
+            dsum[p][k] += dl;
+          } else {
+            float y0, y1;
+            unpack2(acc, y0, y1);
+            y[p][s][k] = y0 + y1;
+          }
+        }
+      }
+    }
+    if constexpr (PASS != kReduce) {
+      // The sums replace the pairs' delta words, which the channel's lanes alone read.
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        float* out = reinterpret_cast<float*>(&dx[t * (S::CH / 2) + grp + p * S::groups]);
+        constexpr int row = 2 * S::CH;  // floats between tokens
+        if constexpr (L == 1) {
+#pragma unroll
+          for (int s = 0; s < G; ++s) *reinterpret_cast<float2*>(out + s * row) = make_float2(y[p][s][0], y[p][s][1]);
+        } else {
+          // neighbours swap channels: an even lane goes on with channel 0, an odd one with channel 1
+          float v[G];
+#pragma unroll
+          for (int s = 0; s < G; ++s) {
+            const float give = sub & 1 ? y[p][s][0] : y[p][s][1], keep = sub & 1 ? y[p][s][1] : y[p][s][0];
+            v[s] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+          }
+          // then, as far as they go, lanes halve the tokens between them; the rest add all they have
+          int n = G, first = 0;
+#pragma unroll
+          for (int o = 2; o < L; o *= 2) {
+            if (n > 1) {
+              n /= 2;
+              const bool up = (sub & o) != 0;
+#pragma unroll
+              for (int s = 0; s < G / 2; ++s)
+                if (s < n) {
+                  const float give = up ? v[s] : v[s + n], keep = up ? v[s + n] : v[s];
+                  v[s] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+                }
+              if (up) first += n;
+            } else {
+              v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+            }
+          }
+          if (sub < 2 * G || L <= 2 * G) {
+#pragma unroll
+            for (int s = 0; s < G; ++s)
+              if (s < n) out[(first + s) * row + (sub & 1)] = v[s];
+          }
+        }
+      }
+    }
+  };
+
   if (t_lo < t_end) {
     load_tile(0, t_lo);
     copies_wait();
@@ -324,62 +393,9 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
     int st = 0;
     for (int t0 = t_lo; t0 < t_end; t0 += kTT, st ^= 1) {
       const int nt = min(kTT, t_end - t0);
-#pragma unroll 2
-      for (int t = 0; t < nt; ++t) {
-        const ulonglong2* pB = reinterpret_cast<const ulonglong2*>(sB + t * S::NP + sub * kS);
-        const ulonglong2* pC = reinterpret_cast<const ulonglong2*>(sC + t * S::NP + sub * kS);
-        uint64_t vB[kS / 2], vC[kS / 2];
-#pragma unroll
-        for (int j = 0; j < kS / 4; ++j) {
-          const ulonglong2 w = pB[j];
-          vB[2 * j] = w.x, vB[2 * j + 1] = w.y;
-          if (PASS != kReduce) {
-            const ulonglong2 u = pC[j];
-            vC[2 * j] = u.x, vC[2 * j + 1] = u.y;
-          }
-        }
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          float4& word = dx[t * (S::CH / 2) + grp + p * S::groups];
-          const float4 w = word;
-          float y[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float dl = k ? w.y : w.x, dlx = k ? w.w : w.z;
-            const uint64_t dl2 = pack2(dl, dl), dlx2 = pack2(dlx, dlx);
-            uint64_t acc = 0;
-#pragma unroll
-            for (int j = 0; j < kS / 2; ++j) {
-              float e0, e1;
-              unpack2(mul2(dl2, A[p][k][j]), e0, e1);
-              h[p][k][j] = fma2(pack2(exp2_fast(e0), exp2_fast(e1)), h[p][k][j], mul2(dlx2, vB[j]));
-              if (PASS != kReduce) acc = j ? fma2(h[p][k][j], vC[j], acc) : mul2(h[p][k][j], vC[j]);
-            }
-            if (PASS == kReduce) {
-              dsum[p][k] += dl;
-            } else {
-              float y0, y1;
-              unpack2(acc, y0, y1);
-              y[k] = y0 + y1;
-            }
-          }
-          if (PASS != kReduce) {
-            // Sum over the channel's lanes; the result replaces the pair's delta words.
-            float* out = reinterpret_cast<float*>(&word);
-            if (L == 1) {
-              out[0] = y[0];
-              out[1] = y[1];
-            } else {
-              // neighbours swap channels: an even lane sums channel 0, an odd one channel 1
-              const float give = sub & 1 ? y[0] : y[1], keep = sub & 1 ? y[1] : y[0];
-              float s = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-#pragma unroll
-              for (int o = 2; o < L; o *= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-              if (sub < 2) out[sub] = s;
-            }
-          }
-        }
-      }
+      int t = 0;
+      for (; t + kSteps <= nt; t += kSteps) steps(t, std::integral_constant<int, kSteps>());
+      for (; t < nt; ++t) steps(t, std::integral_constant<int, 1>());
       copies_wait();
       __syncthreads();
       if (PASS != kReduce) store_tile(st, t0);
