@@ -18,8 +18,8 @@
 namespace sdm {
 namespace {
 
-constexpr int kS = 8;         // states a lane holds of each of its channels
 constexpr int kThreads = 128;
+constexpr int kLaneStates = 8;  // states a lane holds of each of its channels, at most
 constexpr int kTT = 16;       // tokens of a shared-memory tile
 constexpr int kSteps = 4;     // tokens taken together by a lane
 
@@ -60,13 +60,12 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 // state, so that the second may write the new one in its place.
 enum Pass { kWhole = 0, kReduce = 1, kJoin = 2 };
 
-// L lanes share a channel (kS states each); a lane has 2 * P channels, in pairs.
-template <typename T, int L, int P>
+// L lanes share a channel, N states each; a lane has a pair of channels.
+template <typename T, int L, int N>
 struct Tile {
   static constexpr int V = Piece<T>::n;
-  static constexpr int groups = kThreads / L;       // lane groups, each with P pairs of channels
-  static constexpr int CH = 2 * P * groups;         // channels of a block
-  static constexpr int NP = L * kS;                 // padded number of states
+  static constexpr int CH = 2 * kThreads / L;       // channels of a block
+  static constexpr int NP = L * N;                  // padded number of states
   static constexpr int RV = CH / V;                 // pieces of a tile row
   static constexpr int pieces = kTT * RV;           // pieces of a tile
   static constexpr int raw = kTT * CH * int(sizeof(T));
@@ -78,9 +77,9 @@ struct Tile {
   static constexpr int bytes = off_c + kTT * NP * 4;
 };
 
-template <typename T, int L, int P, int PASS>
+template <typename T, int L, int kS, int PASS>
 __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ ScanArgs a) {
-  using S = Tile<T, L, P>;
+  using S = Tile<T, L, kS>;
   constexpr int V = S::V;
   extern __shared__ __align__(16) uint8_t smem[];
   const sdm_ssm_args& io = a.io;
@@ -141,9 +140,12 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
         if (PASS != kReduce && io.z) raw(st, 2)[e] = in ? gz[tt * io.z_ts + c] : T(0.f);
       }
     }
-    if (a.vec_bc) {
-      for (int v = tid; v < kTT * S::NP / V; v += kThreads) {
-        const int t = v / (S::NP / V), n = (v % (S::NP / V)) * V;
+    constexpr int NV = S::NP / V;
+    bool rows = false;
+    if constexpr (NV > 0) rows = a.vec_bc;
+    if (rows) {
+      for (int v = tid; v < kTT * NV; v += kThreads) {
+        const int t = v / (NV ? NV : 1), n = (v % (NV ? NV : 1)) * V;
         const bool in = t < nt && n < io.N;
         const long long tt = in ? t0 + t : 0;
         const int nn = in ? n : 0;
@@ -229,68 +231,45 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
   };
 
   // This lane's channels and states.
-  const int sub = tid % L, grp = tid / L;
-  int ch[P];  // first channel of pair p in the tile
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int q = grp + p * S::groups;
-    ch[p] = (q % S::RV) * V + 2 * (q / S::RV);
-  }
-  uint64_t A[P][2][kS / 2], h[P][2][kS / 2];
-  float dsum[P][2];
+  const int sub = tid % L, pair = tid / L;
+  const int ch = (pair % S::RV) * V + 2 * (pair / S::RV);  // the pair's first channel in the tile
+  float A[2][kS], h[2][kS], dsum[2] = {0.f, 0.f};
   const size_t bd = size_t(b) * io.Dm + d0;
 #pragma unroll
-  for (int p = 0; p < P; ++p)
+  for (int k = 0; k < 2; ++k) {
+    const int c = ch + k;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = ch[p] + k;
-      dsum[p][k] = 0.f;
-#pragma unroll
-      for (int j = 0; j < kS / 2; ++j) {
-        float av[2], hv[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int n = sub * kS + 2 * j + e;
-          const bool in = c < nch && n < io.N;
-          av[e] = in ? decay_rate(io.A[size_t(d0 + c) * io.N + n]) : 0.f;
-          hv[e] = 0.f;
-          if (in && slot >= 0) {
-            if (PASS == kWhole || (PASS == kReduce && chunk == 0)) {
-              const float v = io.state ? io.state[(size_t(slot) * io.Dm + d0 + c) * io.N + n] : 0.f;
-              if (PASS == kReduce)
-                a.ws_h[(bd + c) * io.N + n] = v;
-              else
-                hv[e] = v;
-            } else if (PASS == kJoin) {
-              hv[e] = a.ws_h[(bd + c) * io.N + n];
-            }
-          }
+    for (int j = 0; j < kS; ++j) {
+      const int n = sub * kS + j;
+      const bool in = c < nch && n < io.N;
+      A[k][j] = in ? decay_rate(io.A[size_t(d0 + c) * io.N + n]) : 0.f;
+      h[k][j] = 0.f;
+      if (in && slot >= 0) {
+        if (PASS == kWhole || (PASS == kReduce && chunk == 0)) {
+          const float v = io.state ? io.state[(size_t(slot) * io.Dm + d0 + c) * io.N + n] : 0.f;
+          if (PASS == kReduce)
+            a.ws_h[(bd + c) * io.N + n] = v;
+          else
+            h[k][j] = v;
+        } else if (PASS == kJoin) {
+          h[k][j] = a.ws_h[(bd + c) * io.N + n];
         }
-        A[p][k][j] = pack2(av[0], av[1]);
-        h[p][k][j] = pack2(hv[0], hv[1]);
       }
     }
+  }
   if (PASS == kJoin && slot >= 0) {
     const size_t per = size_t(io.B) * io.Dm;
     for (int q = 0; q < chunk; ++q) {
 #pragma unroll
-      for (int p = 0; p < P; ++p)
+      for (int k = 0; k < 2; ++k) {
+        const int c = ch + k;
+        if (c >= nch) continue;
+        const float s = a.ws_d[q * per + bd + c];
+        const float* e = a.ws_h + ((q + 1) * per + bd + c) * io.N + sub * kS;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int c = ch[p] + k;
-          if (c >= nch) continue;
-          const float s = a.ws_d[q * per + bd + c];
-#pragma unroll
-          for (int j = 0; j < kS / 2; ++j) {
-            float e0, e1, n0 = 0.f, n1 = 0.f;
-            const int n = sub * kS + 2 * j;
-            const float* e = a.ws_h + ((q + 1) * per + bd + c) * io.N + n;
-            if (n < io.N) n0 = e[0];
-            if (n + 1 < io.N) n1 = e[1];
-            unpack2(mul2(pack2(s, s), A[p][k][j]), e0, e1);
-            h[p][k][j] = fma2(pack2(exp2_fast(e0), exp2_fast(e1)), h[p][k][j], pack2(n0, n1));
-          }
-        }
+        for (int j = 0; j < kS; ++j)
+          h[k][j] = fmaf(exp2_fast(s * A[k][j]), h[k][j], sub * kS + j < io.N ? e[j] : 0.f);
+      }
     }
   }
 
@@ -298,86 +277,85 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
   // added over the channel's lanes together, so that no token waits for the one before it.
   auto steps = [&](int t, auto count) {
     constexpr int G = decltype(count)::value;
-    float y[P][G][2];
+    float y[G][2];
 #pragma unroll
     for (int s = 0; s < G; ++s) {
       const ulonglong2* pB = reinterpret_cast<const ulonglong2*>(sB + (t + s) * S::NP + sub * kS);
       const ulonglong2* pC = reinterpret_cast<const ulonglong2*>(sC + (t + s) * S::NP + sub * kS);
-      uint64_t vB[kS / 2], vC[kS / 2];
+      const float4 w = dx[(t + s) * (S::CH / 2) + pair];
+      const float dl[2] = {w.x, w.y};
+      const uint64_t dlx[2] = {pack2(w.z, w.z), pack2(w.w, w.w)};
+      uint64_t acc[2][2];
 #pragma unroll
       for (int j = 0; j < kS / 4; ++j) {
-        const ulonglong2 w = pB[j];
-        vB[2 * j] = w.x, vB[2 * j + 1] = w.y;
-        if (PASS != kReduce) {
-          const ulonglong2 u = pC[j];
-          vC[2 * j] = u.x, vC[2 * j + 1] = u.y;
+        const ulonglong2 vB = pB[j];
+        ulonglong2 vC;
+        if (PASS != kReduce) vC = pC[j];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int q = 4 * j + 2 * i;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float x0, x1;
+            unpack2(mul2(dlx[k], i ? vB.y : vB.x), x0, x1);
+            h[k][q] = fmaf(exp2_fast(dl[k] * A[k][q]), h[k][q], x0);
+            h[k][q + 1] = fmaf(exp2_fast(dl[k] * A[k][q + 1]), h[k][q + 1], x1);
+            if (PASS != kReduce) {
+              const uint64_t hh = pack2(h[k][q], h[k][q + 1]), cc = i ? vC.y : vC.x;
+              acc[k][i] = j ? fma2(hh, cc, acc[k][i]) : mul2(hh, cc);
+            }
+          }
         }
       }
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const float4 w = dx[(t + s) * (S::CH / 2) + grp + p * S::groups];
+      if (PASS == kReduce) {
+        dsum[0] += w.x;
+        dsum[1] += w.y;
+      } else {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float dl = k ? w.y : w.x, dlx = k ? w.w : w.z;
-          const uint64_t dl2 = pack2(dl, dl), dlx2 = pack2(dlx, dlx);
-          uint64_t acc = 0;
-#pragma unroll
-          for (int j = 0; j < kS / 2; ++j) {
-            float e0, e1;
-            unpack2(mul2(dl2, A[p][k][j]), e0, e1);
-            h[p][k][j] = fma2(pack2(exp2_fast(e0), exp2_fast(e1)), h[p][k][j], mul2(dlx2, vB[j]));
-            if (PASS != kReduce) acc = j ? fma2(h[p][k][j], vC[j], acc) : mul2(h[p][k][j], vC[j]);
-          }
-          if (PASS == kReduce) {
-            dsum[p][k] += dl;
-          } else {
-            float y0, y1;
-            unpack2(acc, y0, y1);
-            y[p][s][k] = y0 + y1;
-          }
+          float y0, y1;
+          unpack2(add2(acc[k][0], acc[k][1]), y0, y1);
+          y[s][k] = y0 + y1;
         }
       }
     }
     if constexpr (PASS != kReduce) {
-      // The sums replace the pairs' delta words, which the channel's lanes alone read.
+      // The sums replace the pair's delta words, which the channel's lanes alone read.
+      float* out = reinterpret_cast<float*>(&dx[t * (S::CH / 2) + pair]);
+      constexpr int row = 2 * S::CH;  // floats between tokens
+      if constexpr (L == 1) {
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        float* out = reinterpret_cast<float*>(&dx[t * (S::CH / 2) + grp + p * S::groups]);
-        constexpr int row = 2 * S::CH;  // floats between tokens
-        if constexpr (L == 1) {
+        for (int s = 0; s < G; ++s) *reinterpret_cast<float2*>(out + s * row) = make_float2(y[s][0], y[s][1]);
+      } else {
+        // neighbours swap channels: an even lane goes on with channel 0, an odd one with channel 1
+        float v[G];
 #pragma unroll
-          for (int s = 0; s < G; ++s) *reinterpret_cast<float2*>(out + s * row) = make_float2(y[p][s][0], y[p][s][1]);
-        } else {
-          // neighbours swap channels: an even lane goes on with channel 0, an odd one with channel 1
-          float v[G];
+        for (int s = 0; s < G; ++s) {
+          const float give = sub & 1 ? y[s][0] : y[s][1], keep = sub & 1 ? y[s][1] : y[s][0];
+          v[s] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+        }
+        // then, as far as they go, lanes halve the tokens between them; the rest add all they have
+        int n = G, first = 0;
 #pragma unroll
-          for (int s = 0; s < G; ++s) {
-            const float give = sub & 1 ? y[p][s][0] : y[p][s][1], keep = sub & 1 ? y[p][s][1] : y[p][s][0];
-            v[s] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+        for (int o = 2; o < L; o *= 2) {
+          if (n > 1) {
+            n /= 2;
+            const bool up = (sub & o) != 0;
+#pragma unroll
+            for (int s = 0; s < G / 2; ++s)
+              if (s < n) {
+                const float give = up ? v[s] : v[s + n], keep = up ? v[s + n] : v[s];
+                v[s] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+              }
+            if (up) first += n;
+          } else {
+            v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
           }
-          // then, as far as they go, lanes halve the tokens between them; the rest add all they have
-          int n = G, first = 0;
+        }
+        if (L <= 2 * G || sub < 2 * G) {
 #pragma unroll
-          for (int o = 2; o < L; o *= 2) {
-            if (n > 1) {
-              n /= 2;
-              const bool up = (sub & o) != 0;
-#pragma unroll
-              for (int s = 0; s < G / 2; ++s)
-                if (s < n) {
-                  const float give = up ? v[s] : v[s + n], keep = up ? v[s + n] : v[s];
-                  v[s] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
-                }
-              if (up) first += n;
-            } else {
-              v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
-            }
-          }
-          if (sub < 2 * G || L <= 2 * G) {
-#pragma unroll
-            for (int s = 0; s < G; ++s)
-              if (s < n) out[(first + s) * row + (sub & 1)] = v[s];
-          }
+          for (int s = 0; s < G; ++s)
+            if (s < n) out[(first + s) * row + (sub & 1)] = v[s];
         }
       }
     }
@@ -415,23 +393,16 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
   if (slot >= 0 && (PASS == kReduce || (last && io.state_out))) {
     const size_t per = size_t(io.B) * io.Dm;
 #pragma unroll
-    for (int p = 0; p < P; ++p)
+    for (int k = 0; k < 2; ++k) {
+      const int c = ch + k;
+      if (c >= nch) continue;
+      float* dst = PASS == kReduce ? a.ws_h + ((chunk + 1) * per + bd + c) * io.N
+                                   : io.state_out + (size_t(slot) * io.Dm + d0 + c) * io.N;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int c = ch[p] + k;
-        if (c >= nch) continue;
-        float* dst = PASS == kReduce ? a.ws_h + ((chunk + 1) * per + bd + c) * io.N
-                                     : io.state_out + (size_t(slot) * io.Dm + d0 + c) * io.N;
-#pragma unroll
-        for (int j = 0; j < kS / 2; ++j) {
-          float h0, h1;
-          unpack2(h[p][k][j], h0, h1);
-          const int n = sub * kS + 2 * j;
-          if (n < io.N) dst[n] = h0;
-          if (n + 1 < io.N) dst[n + 1] = h1;
-        }
-        if (PASS == kReduce && sub == 0) a.ws_d[chunk * per + bd + c] = dsum[p][k];
-      }
+      for (int j = 0; j < kS; ++j)
+        if (sub * kS + j < io.N) dst[sub * kS + j] = h[k][j];
+      if (PASS == kReduce && sub == 0) a.ws_d[chunk * per + bd + c] = dsum[k];
+    }
   }
 }
 
@@ -513,35 +484,35 @@ int lanes_for(int N, int per) {
   return l;
 }
 
-template <typename T, int L, int P, int PASS>
+template <typename T, int L, int S, int PASS>
 int launch_pass(const ScanArgs& a, int chunks, cudaStream_t s) {
-  using S = Tile<T, L, P>;
-  auto fn = scan_kernel<T, L, P, PASS>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes) != cudaSuccess)
+  constexpr int bytes = Tile<T, L, S>::bytes;
+  auto fn = scan_kernel<T, L, S, PASS>;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return SDM_ECUDA;
   const long long blocks = (long long)a.tiles_g * a.io.G * a.io.B * chunks;
   if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
-  fn<<<unsigned(blocks), kThreads, S::bytes, s>>>(a);
+  fn<<<unsigned(blocks), kThreads, bytes, s>>>(a);
   return last_launch_status();
 }
 
-template <typename T, int L>
-int launch_scan_l(ScanArgs& a, cudaStream_t s) {
-  constexpr int P = 1;
-  a.tiles_g = (a.Dg + Tile<T, L, P>::CH - 1) / Tile<T, L, P>::CH;
-  if (a.chunks <= 1) return launch_pass<T, L, P, kWhole>(a, 1, s);
-  const int st = launch_pass<T, L, P, kReduce>(a, a.chunks - 1, s);
-  return st != SDM_OK ? st : launch_pass<T, L, P, kJoin>(a, a.chunks, s);
+template <typename T, int L, int S>
+int launch_passes(ScanArgs& a, cudaStream_t s) {
+  a.tiles_g = (a.Dg + Tile<T, L, S>::CH - 1) / Tile<T, L, S>::CH;
+  if (a.chunks <= 1) return launch_pass<T, L, S, kWhole>(a, 1, s);
+  const int st = launch_pass<T, L, S, kReduce>(a, a.chunks - 1, s);
+  return st != SDM_OK ? st : launch_pass<T, L, S, kJoin>(a, a.chunks, s);
 }
 
 template <typename T>
 int launch_scan(ScanArgs& a, cudaStream_t s) {
-  switch (lanes_for(a.io.N, kS)) {
-    case 1: return launch_scan_l<T, 1>(a, s);
-    case 2: return launch_scan_l<T, 2>(a, s);
-    case 4: return launch_scan_l<T, 4>(a, s);
-    case 8: return launch_scan_l<T, 8>(a, s);
-    case 16: return launch_scan_l<T, 16>(a, s);
+  if (a.io.N <= 4) return launch_passes<T, 1, 4>(a, s);
+  switch (lanes_for(a.io.N, kLaneStates)) {
+    case 1: return launch_passes<T, 1, kLaneStates>(a, s);
+    case 2: return launch_passes<T, 2, kLaneStates>(a, s);
+    case 4: return launch_passes<T, 4, kLaneStates>(a, s);
+    case 8: return launch_passes<T, 8, kLaneStates>(a, s);
+    case 16: return launch_passes<T, 16, kLaneStates>(a, s);
     default: return SDM_EUNSUPPORTED;
   }
 }
@@ -566,7 +537,7 @@ int launch_token(const ScanArgs& a, cudaStream_t s) {
 // Chunks of a sequence and tokens of a chunk: one chunk where the channels alone give the card
 // enough blocks, else as many as bring it there, of 128 tokens at least.
 void cut(int B, int T, int Dm, int N, int G, int* chunks, int* chunk) {
-  const int L = lanes_for(N, kS), CH = 2 * kThreads / L;
+  const int L = lanes_for(N, kLaneStates), CH = 2 * kThreads / L;
   const long long blocks = (long long)B * G * ((Dm / G + CH - 1) / CH);
   long long n = blocks >= 304 ? 1 : (608 + blocks - 1) / blocks;
   n = n < T / 128 ? n : T / 128;
