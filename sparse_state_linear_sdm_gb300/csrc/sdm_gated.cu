@@ -429,26 +429,28 @@ int launch_mode(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& B
   const long long units = (long long)p.row_tiles * p.col_tiles * p.splits;
   if (units > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
   auto fn = gated_kernel<MODE, ACT>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-    return SDM_ECUDA;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  const int sms = sm_count();
-  if (sms < 2) return SDM_ECUDA;
-  long long pairs = sms / 2;
-  cfg.gridDim = dim3(unsigned(pairs * 2));
   cfg.blockDim = dim3(kRoles);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int active = 0;
-  if (cudaOccupancyMaxActiveClusters(&active, fn, &cfg) != cudaSuccess || active <= 0) return SDM_ECUDA;
-  if (active < pairs) pairs = active;
+  // Pairs that can be resident at once: a larger persistent grid would run in two waves.
+  static PerDevice resident;
+  long long pairs = resident.get([&] {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return -1;
+    const int most = sm_count() / 2;
+    cfg.gridDim = dim3(unsigned(most > 0 ? most * 2 : 2));
+    int active = 0;
+    if (cudaOccupancyMaxActiveClusters(&active, fn, &cfg) != cudaSuccess || active <= 0) return -1;
+    return active < most ? active : most;
+  });
+  if (pairs <= 0) return SDM_ECUDA;
   if (units < pairs) pairs = units;
   cfg.gridDim = dim3(unsigned(pairs * 2));
   if (cudaLaunchKernelEx(&cfg, fn, A, B, B2, a) != cudaSuccess) return SDM_ECUDA;

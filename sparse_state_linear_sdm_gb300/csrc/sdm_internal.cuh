@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -18,6 +19,27 @@ inline bool aligned16(const void* p) {
 inline int last_launch_status() {
   return cudaGetLastError() == cudaSuccess ? SDM_OK : SDM_ECUDA;
 }
+
+// A value computed once for each device, e.g. a kernel's attribute set or a query's answer: `make`
+// returns it, negative where it failed (then it is tried again).  Racing first calls compute the
+// same value.
+struct PerDevice {
+  static constexpr int kDevices = 64;
+  std::atomic<int> value[kDevices] = {};  // 0: not yet, else the value + 1
+  template <typename Make>
+  int get(Make make) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+    if (dev >= kDevices) return make();
+    int v = value[dev].load(std::memory_order_acquire);
+    if (v == 0) {
+      v = make() + 1;
+      if (v <= 0) return v - 1;
+      value[dev].store(v, std::memory_order_release);
+    }
+    return v - 1;
+  }
+};
 
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 

@@ -488,7 +488,10 @@ template <typename T, int L, int S, int PASS>
 int launch_pass(const ScanArgs& a, int chunks, cudaStream_t s) {
   constexpr int bytes = Tile<T, L, S>::bytes;
   auto fn = scan_kernel<T, L, S, PASS>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+  static PerDevice ready;
+  if (ready.get([&] {
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess ? 0 : -1;
+      }) < 0)
     return SDM_ECUDA;
   const long long blocks = (long long)a.tiles_g * a.io.G * a.io.B * chunks;
   if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
