@@ -6,7 +6,8 @@
 //
 // Four products of one shape run on one kernel, a persistent pair of CTAs (cta_group::2) that
 // forms 256 x 256 tiles with fp32 accumulators in TMEM, double-buffered, TMA feeding a ring of
-// stages (the roles of the projection kernel in sdm_project.cu):
+// stages (the roles of the projection kernel in sdm_project.cu, with eight epilogue warps: with four,
+// kSlope's elementwise work was longer than its products):
 //   kForward   the pair's two halves of the column tile are 128 columns of Wg and the same 128 of
 //              Wu, so one thread of the epilogue holds g and u of an element and h leaves the chip
 //              once: neither g nor u is ever written.
@@ -30,7 +31,8 @@ constexpr int kHalf = 128;                       // rows (and columns) of a tile
 constexpr int kOperand = kHalf * kTileK * 2;     // 16 KB
 constexpr int kStage = 2 * kOperand;
 constexpr int kStages = 6;
-constexpr int kRoles = 192;                      // copy warp, MMA warp, four epilogue warps
+constexpr int kEpilogueWarps = 8;                // two for each quarter of the tile's rows
+constexpr int kRoles = 64 + 32 * kEpilogueWarps; // copy warp, MMA warp, epilogue warps
 constexpr int kBars = 2 * kStages + 5;           // full[], empty[], acc_full[2], acc_empty[2], drain
 constexpr int kSmem = kStages * kStage + 1024 + 256;
 constexpr uint32_t kColumns = 512;
@@ -113,70 +115,88 @@ __device__ __forceinline__ Unit unit_at(int u, const GatedArgs& a) {
   return r;
 }
 
+// The epilogue of one warp: 32 rows, and half of the tile's columns.
 template <int MODE, int ACT>
-__device__ __forceinline__ void epilogue(const GatedArgs& a, const Unit& un, int rank, int row,
-                                         uint32_t taddr) {
-  const int m = (un.row * 2 + rank) * kHalf + row;
-  if constexpr (MODE == kForward || MODE == kSlope) {
-    const int f0 = un.col * kHalf;
-#pragma unroll 1
-    for (int c = 0; c < kHalf; c += 32) {
-      uint32_t g[32], u[32];
-      tmem_load32(taddr + uint32_t(c), g);
-      tmem_load32(taddr + uint32_t(kHalf + c), u);
+struct Epilogue {
+  const GatedArgs& a;
+  int m, half;
+  uint4 dh[MODE == kSlope ? kHalf / 16 : 1];
+
+  __device__ Epilogue(const GatedArgs& args, const Unit& un, int rank, int row, int half_)
+      : a(args), m((un.row * 2 + rank) * kHalf + row), half(half_) {}
+
+  // What the epilogue reads of memory: asked for before the products are awaited.
+  __device__ void fetch(const Unit& un) {
+    if constexpr (MODE == kSlope) {
+      const int f0 = un.col * kHalf + half * (kHalf / 2);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {  // F % 8 == 0: a 16-byte piece is in or out
-        const int f = f0 + c + 8 * j;
-        if (m >= a.rows || f >= a.F) break;
-        float o[8];
-        if constexpr (MODE == kForward) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            o[i] = gate<ACT>(__uint_as_float(g[8 * j + i])) * __uint_as_float(u[8 * j + i]);
-          *reinterpret_cast<uint4*>(a.out + size_t(m) * a.F + f) = Piece<__nv_bfloat16>::pack(o);
-        } else {
-          float d[8], o2[8];
-          Piece<__nv_bfloat16>::load(
-              __ldcs(reinterpret_cast<const uint4*>(a.dh + size_t(m) * a.F + f)), d);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float v, s;
-            gate_slope<ACT>(__uint_as_float(g[8 * j + i]), v, s);
-            o[i] = d[i] * __uint_as_float(u[8 * j + i]) * s;
-            o2[i] = d[i] * v;
-          }
-          __nv_bfloat16* p = a.out + size_t(m) * (2 * size_t(a.F)) + f;
-          *reinterpret_cast<uint4*>(p) = Piece<__nv_bfloat16>::pack(o);
-          *reinterpret_cast<uint4*>(p + a.F) = Piece<__nv_bfloat16>::pack(o2);
-        }
-      }
-      __syncwarp();  // tcgen05.ld takes the whole warp
-    }
-  } else {
-    const int n0 = un.col * 2 * kHalf;
-#pragma unroll 1
-    for (int c = 0; c < 2 * kHalf; c += 32) {
-      uint32_t r[32];
-      tmem_load32(taddr + uint32_t(c), r);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + c + 8 * j;
-        if (m >= a.rows || n >= a.cols) break;
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(r[8 * j + i]);
-        if (a.splits > 1) {
-          float* p = a.partial + (size_t(un.split) * a.rows + m) * a.cols + n;
-          *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<float4*>(p + 4) = make_float4(o[4], o[5], o[6], o[7]);
-        } else {
-          *reinterpret_cast<uint4*>(a.out + size_t(m) * a.cols + n) = Piece<__nv_bfloat16>::pack(o);
-        }
-      }
-      __syncwarp();
+      for (int j = 0; j < kHalf / 16; ++j)
+        if (m < a.rows && f0 + 8 * j < a.F)
+          dh[j] = __ldcs(reinterpret_cast<const uint4*>(a.dh + size_t(m) * a.F + f0 + 8 * j));
     }
   }
-}
+
+  __device__ void run(const Unit& un, uint32_t taddr) {
+    if constexpr (MODE == kForward || MODE == kSlope) {
+      const int c0 = half * (kHalf / 2), f0 = un.col * kHalf + c0;
+#pragma unroll
+      for (int c = 0; c < kHalf / 2; c += 32) {
+        uint32_t g[32], u[32];
+        tmem_load32(taddr + uint32_t(c0 + c), g);
+        tmem_load32(taddr + uint32_t(kHalf + c0 + c), u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // F % 8 == 0: a 16-byte piece is in or out
+          const int f = f0 + c + 8 * j;
+          if (m >= a.rows || f >= a.F) break;
+          float o[8];
+          if constexpr (MODE == kForward) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              o[i] = gate<ACT>(__uint_as_float(g[8 * j + i])) * __uint_as_float(u[8 * j + i]);
+            *reinterpret_cast<uint4*>(a.out + size_t(m) * a.F + f) = Piece<__nv_bfloat16>::pack(o);
+          } else {
+            float d[8], o2[8];
+            Piece<__nv_bfloat16>::load(dh[c / 8 + j], d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float v, s;
+              gate_slope<ACT>(__uint_as_float(g[8 * j + i]), v, s);
+              o[i] = d[i] * __uint_as_float(u[8 * j + i]) * s;
+              o2[i] = d[i] * v;
+            }
+            __nv_bfloat16* p = a.out + size_t(m) * (2 * size_t(a.F)) + f;
+            *reinterpret_cast<uint4*>(p) = Piece<__nv_bfloat16>::pack(o);
+            *reinterpret_cast<uint4*>(p + a.F) = Piece<__nv_bfloat16>::pack(o2);
+          }
+        }
+        __syncwarp();  // tcgen05.ld takes the whole warp
+      }
+    } else {
+      const int c0 = half * kHalf, n0 = un.col * 2 * kHalf + c0;
+#pragma unroll 1
+      for (int c = 0; c < kHalf; c += 32) {
+        uint32_t r[32];
+        tmem_load32(taddr + uint32_t(c0 + c), r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = n0 + c + 8 * j;
+          if (m >= a.rows || n >= a.cols) break;
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(r[8 * j + i]);
+          if (a.splits > 1) {
+            float* p = a.partial + (size_t(un.split) * a.rows + m) * a.cols + n;
+            *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4*>(p + 4) = make_float4(o[4], o[5], o[6], o[7]);
+          } else {
+            *reinterpret_cast<uint4*>(a.out + size_t(m) * a.cols + n) = Piece<__nv_bfloat16>::pack(o);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+};
 
 // Every wait is bounded; a wait that runs out stops both CTAs, which drain the copies and MMAs in
 // flight, free TMEM and report SDM_DEV_TIMEOUT.
@@ -210,7 +230,7 @@ __global__ void __launch_bounds__(kRoles, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(ACC_FULL + i), 1);
-      mbar_init(bar(ACC_EMPTY + i), 8);  // the 4 epilogue warps of each CTA
+      mbar_init(bar(ACC_EMPTY + i), 2 * kEpilogueWarps);  // both CTAs' epilogue warps
     }
     mbar_init(bar(DRAIN), 1);
     *stop = 0;
@@ -317,12 +337,14 @@ __global__ void __launch_bounds__(kRoles, 1)
     for (int u = cid; u < units; u += ncl, ++it) {
       const int acc = it & 1;
       const uint32_t acc_par = uint32_t(it >> 1) & 1u;
+      const Unit un = unit_at(u, a);
+      Epilogue<MODE, ACT> e(a, un, int(rank), quad * 32 + lane, (warp - 2) >> 2);
+      e.fetch(un);
       if (!__all_sync(0xFFFFFFFFu,
                       mbar_wait_cluster(bar(ACC_FULL + acc), acc_par, stop, peer_stop, kWaitNs)))
         break;
       tc_fence_after();
-      epilogue<MODE, ACT>(a, unit_at(u, a), int(rank), quad * 32 + lane,
-                          tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * 256));
+      e.run(un, tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * 256));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cluster_addr(bar(ACC_EMPTY + acc), 0));
@@ -375,6 +397,107 @@ __global__ void __launch_bounds__(256) join_kernel(const float* partial, __nv_bf
     o[4] += w.x, o[5] += w.y, o[6] += w.z, o[7] += w.w;
   }
   *reinterpret_cast<uint4*>(out + i) = Piece<__nv_bfloat16>::pack(o);
+}
+
+// ---- few tokens ----
+//
+// A decode step's product reads all of w for a handful of tokens: HBM bounds it, and what counts is
+// that every SM reads its even share with enough loads under way.  A block takes 8 columns f: the 8
+// rows of Wg and the 8 of Wu are the 16 rows of one mma.m16n8k16, tokens its 8 columns, so that a lane
+// ends with g and u of the same elements.  The eight warps take K steps of 32 in turn, straight from
+// global memory in 16-byte words (a lane's 8 consecutive k stand for the two groups of four that it
+// holds of two MMAs; x is read the same way, so the order of k is the same on both sides), and their
+// sums meet in shared memory.
+constexpr int kFewThreads = 256;
+constexpr int kFewF = 8;
+constexpr int kFewTokens = 64;
+
+__device__ __forceinline__ uint4 load_stream(const void* p) {  // read once: past L1
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void mma16n8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+      " {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT groups of 8 tokens.
+template <int ACT, int NT>
+__global__ void __launch_bounds__(kFewThreads) few_kernel(const __nv_bfloat16* __restrict__ x,
+                                                          const __nv_bfloat16* __restrict__ w, int M,
+                                                          int D, int F, __nv_bfloat16* h) {
+  constexpr int kWarps = kFewThreads / 32, kAhead = NT <= 2 ? 4 : 2;
+  __shared__ float4 part[kWarps][NT][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int f = blockIdx.x * kFewF + g;  // F % 8 == 0
+  const __nv_bfloat16* wg = w + size_t(f) * D + c * 8;
+  const __nv_bfloat16* wu = wg + size_t(F) * D;
+  const __nv_bfloat16* xr = x + size_t(g) * D + c * 8;
+
+  float acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int k0 = warp * 32; k0 < D; k0 += kWarps * 32 * kAhead) {
+    uint4 vg[kAhead], vu[kAhead], vx[kAhead][NT];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = k0 + j * kWarps * 32;
+      const bool in = k + c * 8 < D;  // D % 8 == 0
+      vg[j] = in ? load_stream(wg + k) : zero;
+      vu[j] = in ? load_stream(wu + k) : zero;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        vx[j][t] = in && t * 8 + g < M ? *reinterpret_cast<const uint4*>(xr + size_t(t) * 8 * D + k) : zero;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma16n8(acc[t], vg[j].x, vu[j].x, vg[j].y, vu[j].y, vx[j][t].x, vx[j][t].y);
+        mma16n8(acc[t], vg[j].z, vu[j].z, vg[j].w, vu[j].w, vx[j][t].z, vx[j][t].w);
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) part[warp][t][lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+  __syncthreads();
+  for (int t = warp; t < NT; t += kWarps) {  // g of tokens 2c, 2c+1 in x, y; u in z, w
+    float4 s = part[0][t][lane];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) {
+      const float4 p = part[i][t][lane];
+      s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+    }
+    const int m = t * 8 + 2 * c;
+    if (m < M) h[size_t(m) * F + f] = __float2bfloat16_rn(gate<ACT>(s.x) * s.z);
+    if (m + 1 < M) h[size_t(m + 1) * F + f] = __float2bfloat16_rn(gate<ACT>(s.y) * s.w);
+  }
+}
+
+template <int ACT>
+int launch_few(const void* x, const void* w, int M, int D, int F, void* h, cudaStream_t s) {
+  const __nv_bfloat16* xp = static_cast<const __nv_bfloat16*>(x);
+  const __nv_bfloat16* wp = static_cast<const __nv_bfloat16*>(w);
+  __nv_bfloat16* hp = static_cast<__nv_bfloat16*>(h);
+  const unsigned blocks = unsigned(F / kFewF);
+  if (M <= 8)
+    few_kernel<ACT, 1><<<blocks, kFewThreads, 0, s>>>(xp, wp, M, D, F, hp);
+  else if (M <= 16)
+    few_kernel<ACT, 2><<<blocks, kFewThreads, 0, s>>>(xp, wp, M, D, F, hp);
+  else if (M <= 32)
+    few_kernel<ACT, 4><<<blocks, kFewThreads, 0, s>>>(xp, wp, M, D, F, hp);
+  else
+    few_kernel<ACT, 8><<<blocks, kFewThreads, 0, s>>>(xp, wp, M, D, F, hp);
+  return last_launch_status();
 }
 
 int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
@@ -488,6 +611,9 @@ extern "C" int sdm_project_gated(const void* x, const void* w, long long M, int 
   if (st != SDM_OK) return st;
   if (M == 0) return SDM_OK;
   if (!aligned16(h)) return SDM_EALIGN;
+  if (M <= kFewTokens)
+    return act == SDM_ACT_SILU ? launch_few<SDM_ACT_SILU>(x, w, int(M), D, F, h, as_stream(stream))
+                               : launch_few<SDM_ACT_GELU>(x, w, int(M), D, F, h, as_stream(stream));
   CUtensorMap tx, tg, tu;
   if (!tile_map(&tx, x, int(M), D, kHalf) || !tile_map(&tg, w, F, D, kHalf) ||
       !tile_map(&tu, static_cast<const __nv_bfloat16*>(w) + size_t(F) * D, F, D, kHalf))

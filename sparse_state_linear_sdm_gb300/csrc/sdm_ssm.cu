@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kLaneStates = 8;  // states a lane holds of each of its channels, at most
+constexpr int kTokenThreads = 128;
 constexpr int kTT = 16;       // tokens of a shared-memory tile
 constexpr int kSteps = 4;     // tokens taken together by a lane
 
@@ -29,8 +30,8 @@ struct ScanArgs {
   int chunks, chunk;           // chunks of a sequence, tokens of a chunk (a multiple of kTT)
   float* ws_h;                 // [chunks][B][Dm][N]: state before chunk 0, then each chunk's own end
   float* ws_d;                 // [chunks][B][Dm]: sum of delta over each chunk
-  bool vec;                    // rows of x, dt, z and y in 16-byte pieces
-  bool vec_bc;                 // rows of B and C in 16-byte pieces (N a multiple of the piece)
+  bool vec;                    // rows of x, dt, z and y in 16-byte pieces; one token: four states a word
+  bool vec_bc;                 // rows of B and C in 16-byte pieces; one token: four entries a word
   int* dev_err;
 };
 
@@ -406,75 +407,121 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
   }
 }
 
-// One token: a lane has four states of a channel (16 bytes in, 16 bytes out), L lanes a channel.
-// HBM bounds it: the state read and written once.
-template <typename T, int L>
-__global__ void __launch_bounds__(256) token_kernel(const __grid_constant__ ScanArgs a) {
-  const sdm_ssm_args& io = a.io;
-  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int sub = int(id % L);
-  const long long cell = id / L;
-  const int d = int(cell % io.Dm);
-  const long long row = cell / io.Dm;
-  const bool live = row < io.B;
-  const int b = live ? int(row) : 0;
-  const int slot = live ? row_slot(io.slots, b, io.n_slots, sub == 0 && d == 0 ? a.dev_err : nullptr) : -1;
-  const int len = slot < 0 ? 0 : row_length(io.lengths, b, 1);
-  float y = 0.f, x = 0.f;
-  if (slot >= 0) {
-    const int n0 = sub * 4;
-    const int g = d / a.Dg;
-    const float* A = io.A + size_t(d) * io.N + n0;
-    const float* hs = io.state ? io.state + (size_t(slot) * io.Dm + d) * io.N + n0 : nullptr;
-    float h[4] = {0.f, 0.f, 0.f, 0.f}, av[4], bv[4], cv[4];
-    const bool vec = a.vec_bc;  // N % 4 == 0 and states on 16 bytes
-    if (vec && n0 < io.N) {
-      if (hs) *reinterpret_cast<float4*>(h) = *reinterpret_cast<const float4*>(hs);
-      *reinterpret_cast<float4*>(av) = *reinterpret_cast<const float4*>(A);
+// Four elements from p on; one word of them where `vec` says that p is aligned to it, the first n
+// where a row ends.
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, int n, bool vec, float (&v)[4]) {
+  if (vec) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 w = *reinterpret_cast<const float4*>(p);
+      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
     } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+      v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = j < n ? to_f32(p[j]) : 0.f;
+  }
+}
+
+// One token: a lane has four states of a channel (16 bytes in, 16 bytes out) in each of R sequences,
+// L lanes a channel.  HBM bounds it, the states read and written once, so R states are under way in
+// every lane, and what a channel computes once (step size, gate) is done for each sequence by one of
+// its lanes: lane r < R for sequence r.
+template <typename T, int L>
+__global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_constant__ ScanArgs a) {
+  constexpr int R = L < 4 ? L : 4;
+  const sdm_ssm_args& io = a.io;
+  const long long id = (long long)blockIdx.x * kTokenThreads + threadIdx.x;
+  const int sub = int(id % L), own = sub % R;
+  const int d = int((id / L) % io.Dm);
+  const long long b0 = id / L / io.Dm * R;
+  const int n0 = sub * 4, left = io.N - n0, g = d / a.Dg;
+
+  int slot[R], len[R];
+  float h[R][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    slot[r] = -1;
+    len[r] = 0;
+    if (b0 + r < io.B) {
+      slot[r] = row_slot(io.slots, int(b0) + r, io.n_slots, d == 0 && sub == 0 ? a.dev_err : nullptr);
+      len[r] = slot[r] < 0 ? 0 : row_length(io.lengths, int(b0) + r, 1);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[r][j] = 0.f;
+    if (slot[r] >= 0 && io.state && left > 0)
+      load4(io.state + (size_t(slot[r]) * io.Dm + d) * io.N + n0, left, a.vec, h[r]);
+  }
+  float x = 0.f, dl = 0.f, z = 0.f;
+  bool mine = false;
+#pragma unroll
+  for (int r = 0; r < R; ++r) mine = mine || (own == r && len[r] > 0);
+  if (mine) {
+    const long long b = b0 + own;
+    x = to_f32(static_cast<const T*>(io.x)[b * io.x_bs + d]);
+    dl = to_f32(static_cast<const T*>(io.dt)[b * io.dt_bs + d]);
+    if (io.z) z = to_f32(static_cast<const T*>(io.z)[b * io.z_bs + d]);
+    if (io.dt_bias) dl += io.dt_bias[d];
+    if (io.softplus) dl = softplus(dl);
+  }
+  float A[4] = {0.f, 0.f, 0.f, 0.f};
+  if (left > 0) load4(io.A + size_t(d) * io.N + n0, left, a.vec, A);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) A[j] = decay_rate(A[j]);
+
+  float y[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float dr = __shfl_sync(0xFFFFFFFFu, dl, r, L), dx = __shfl_sync(0xFFFFFFFFu, dl * x, r, L);
+    y[r] = 0.f;
+    if (len[r] > 0 && left > 0) {
+      const long long b = b0 + r;
+      float B[4], C[4];
+      load4(static_cast<const T*>(io.Bm) + b * io.B_bs + g * io.N + n0, left, a.vec_bc, B);
+      load4(static_cast<const T*>(io.Cm) + b * io.C_bs + g * io.N + n0, left, a.vec_bc, C);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        av[j] = n0 + j < io.N ? A[j] : 0.f;
-        if (hs && n0 + j < io.N) h[j] = hs[j];
+        h[r][j] = fmaf(exp2_fast(dr * A[j]), h[r][j], dx * B[j]);
+        y[r] = fmaf(h[r][j], C[j], y[r]);
       }
     }
-    if (len > 0) {
-      const T* gB = static_cast<const T*>(io.Bm) + b * io.B_bs + g * io.N + n0;
-      const T* gC = static_cast<const T*>(io.Cm) + b * io.C_bs + g * io.N + n0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bv[j] = n0 + j < io.N ? to_f32(gB[j]) : 0.f;
-        cv[j] = n0 + j < io.N ? to_f32(gC[j]) : 0.f;
-      }
-      x = to_f32(static_cast<const T*>(io.x)[b * io.x_bs + d]);
-      float dl = to_f32(static_cast<const T*>(io.dt)[b * io.dt_bs + d]);
-      if (io.dt_bias) dl += io.dt_bias[d];
-      if (io.softplus) dl = softplus(dl);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[j] = fmaf(exp2_fast(dl * decay_rate(av[j])), h[j], dl * x * bv[j]);
-        y = fmaf(h[j], cv[j], y);
-      }
-    }
-    if (io.state_out) {
-      float* ho = io.state_out + (size_t(slot) * io.Dm + d) * io.N + n0;
-      if (vec && n0 < io.N) {
-        *reinterpret_cast<float4*>(ho) = *reinterpret_cast<const float4*>(h);
+    if (slot[r] >= 0 && io.state_out && left > 0) {
+      float* p = io.state_out + (size_t(slot[r]) * io.Dm + d) * io.N + n0;
+      if (a.vec) {
+        *reinterpret_cast<float4*>(p) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (n0 + j < io.N) ho[j] = h[j];
+          if (j < left) p[j] = h[r][j];
       }
     }
   }
+  // Sums over the channel's lanes; lane r keeps sequence r's.
+  if constexpr (R >= 2) {
+    const bool odd = sub & 1;
 #pragma unroll
-  for (int o = 1; o < L; o *= 2) y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
-  if (live && sub == 0) {
-    if (len > 0) {
-      if (io.D) y = fmaf(io.D[d], x, y);
-      if (io.z) y *= silu(to_f32(static_cast<const T*>(io.z)[b * io.z_bs + d]));
+    for (int r = 0; r < R; r += 2) {
+      const float give = odd ? y[r] : y[r + 1], keep = odd ? y[r + 1] : y[r];
+      y[r / 2] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
     }
-    from_f32(y, static_cast<T*>(io.y) + size_t(b) * io.Dm + d);
+  }
+  if constexpr (R == 4) {
+    const bool up = sub & 2;
+    const float give = up ? y[0] : y[1], keep = up ? y[1] : y[0];
+    y[0] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 2);
+#pragma unroll
+    for (int o = 4; o < L; o *= 2) y[0] += __shfl_xor_sync(0xFFFFFFFFu, y[0], o);
+  }
+  if (sub < R && b0 + own < io.B) {
+    float v = 0.f;
+    if (mine) {
+      v = io.D ? fmaf(io.D[d], x, y[0]) : y[0];
+      if (io.z) v *= silu(z);
+    }
+    from_f32(v, static_cast<T*>(io.y) + (b0 + own) * io.Dm + d);
   }
 }
 
@@ -520,21 +567,27 @@ int launch_scan(ScanArgs& a, cudaStream_t s) {
   }
 }
 
+template <typename T, int L>
+int launch_token_l(const ScanArgs& a, cudaStream_t s) {
+  constexpr int R = L < 4 ? L : 4;
+  const long long blocks =
+      ((long long)((a.io.B + R - 1) / R) * a.io.Dm * L + kTokenThreads - 1) / kTokenThreads;
+  if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
+  token_kernel<T, L><<<unsigned(blocks), kTokenThreads, 0, s>>>(a);
+  return last_launch_status();
+}
+
 template <typename T>
 int launch_token(const ScanArgs& a, cudaStream_t s) {
-  const int L = lanes_for(a.io.N, 4);
-  const long long blocks = ((long long)a.io.B * a.io.Dm * L + 255) / 256;
-  if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
-  switch (L) {
-    case 1: token_kernel<T, 1><<<unsigned(blocks), 256, 0, s>>>(a); break;
-    case 2: token_kernel<T, 2><<<unsigned(blocks), 256, 0, s>>>(a); break;
-    case 4: token_kernel<T, 4><<<unsigned(blocks), 256, 0, s>>>(a); break;
-    case 8: token_kernel<T, 8><<<unsigned(blocks), 256, 0, s>>>(a); break;
-    case 16: token_kernel<T, 16><<<unsigned(blocks), 256, 0, s>>>(a); break;
-    case 32: token_kernel<T, 32><<<unsigned(blocks), 256, 0, s>>>(a); break;
+  switch (lanes_for(a.io.N, 4)) {
+    case 1: return launch_token_l<T, 1>(a, s);
+    case 2: return launch_token_l<T, 2>(a, s);
+    case 4: return launch_token_l<T, 4>(a, s);
+    case 8: return launch_token_l<T, 8>(a, s);
+    case 16: return launch_token_l<T, 16>(a, s);
+    case 32: return launch_token_l<T, 32>(a, s);
     default: return SDM_EUNSUPPORTED;
   }
-  return last_launch_status();
 }
 
 // Chunks of a sequence and tokens of a chunk: one chunk where the channels alone give the card
@@ -591,7 +644,10 @@ extern "C" int sdm_selective_scan(const sdm_ssm_args* args, void* workspace, siz
   a.dev_err = dev_err;
   cudaStream_t s = as_stream(stream);
   if (io.T == 1) {
-    a.vec_bc = io.N % 4 == 0 && !off(io.A, 15) && !off(io.state, 15) && !off(io.state_out, 15);
+    // Four states a word, and four entries of B and C (8 bytes of bf16, 16 of fp32).
+    const uintptr_t word = io.dtype == SDM_F32 ? 15 : 7;
+    a.vec = io.N % 4 == 0 && !off(io.A, 15) && !off(io.state, 15) && !off(io.state_out, 15);
+    a.vec_bc = io.N % 4 == 0 && io.B_bs % 4 == 0 && io.C_bs % 4 == 0 && !off(io.Bm, word) && !off(io.Cm, word);
     return io.dtype == SDM_F32 ? launch_token<float>(a, s) : launch_token<__nv_bfloat16>(a, s);
   }
   const size_t need = sdm_selective_scan_workspace_size(io.B, io.T, io.Dm, io.N, io.G);
