@@ -61,125 +61,178 @@ __device__ __forceinline__ void load_weights(const void* p, int dt, size_t i, bo
   }
 }
 
-// V channels as they lie in memory: one 16-byte word where V is a whole piece, else one element.
+// V channels: as they lie in memory (one 16-byte word where V is a whole piece, else one element),
+// and as numbers (pairs, for two operations an instruction, or one).
 template <typename T, int V>
-struct Word {
-  using type = uint4;
-  __device__ static type zero() { return make_uint4(0, 0, 0, 0); }
-  __device__ static void load(const type& w, float (&v)[V]) { Piece<T>::load(w, v); }
-  __device__ static type pack(const float (&v)[V]) { return Piece<T>::pack(v); }
+struct Channels {
+  static constexpr int n = V / 2;
+  using word = uint4;
+  using num = uint64_t;
+  __device__ static word zero() { return make_uint4(0, 0, 0, 0); }
+  __device__ static void load(const word& w, num (&v)[n]) {
+    float f[V];
+    Piece<T>::load(w, f);
+    join(f, v);
+  }
+  __device__ static void join(const float (&f)[V], num (&v)[n]) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+  }
+  __device__ static num fma(num a, num b, num c) { return fma2(a, b, c); }
+  __device__ static num act(num v) {
+    float a, b;
+    unpack2(v, a, b);
+    return mul2(v, pack2(sigmoid(a), sigmoid(b)));
+  }
+  __device__ static word pack(const num (&v)[n]) {
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < n; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
+    return Piece<T>::pack(f);
+  }
 };
 template <typename T>
-struct Word<T, 1> {
-  using type = T;
-  __device__ static type zero() { return T(0.f); }
-  __device__ static void load(const type& w, float (&v)[1]) { v[0] = to_f32(w); }
-  __device__ static type pack(const float (&v)[1]) {
+struct Channels<T, 1> {
+  static constexpr int n = 1;
+  using word = T;
+  using num = float;
+  __device__ static word zero() { return T(0.f); }
+  __device__ static void load(const word& w, num (&v)[1]) { v[0] = to_f32(w); }
+  __device__ static void join(const float (&f)[1], num (&v)[1]) { v[0] = f[0]; }
+  __device__ static num fma(num a, num b, num c) { return fmaf(a, b, c); }
+  __device__ static num act(num v) { return silu(v); }
+  __device__ static word pack(const num (&v)[1]) {
     T r;
     from_f32(v[0], &r);
     return r;
   }
 };
 
-template <typename T, int K, int V>
+template <typename T, int K, int V, bool ACT>
 __global__ void __launch_bounds__(kConvThreads) conv_kernel(const __grid_constant__ ConvArgs a) {
-  using W = Word<T, V>;
-  using word = typename W::type;
-  const long long id = (long long)blockIdx.x * kConvThreads + threadIdx.x;
-  const int piece = int(id % a.pieces);
-  const long long row = id / a.pieces;
-  const int strip = int(row % a.strips), b = int(row / a.strips);
+  using C = Channels<T, V>;
+  using word = typename C::word;
+  using num = typename C::num;
+  const unsigned id = blockIdx.x * kConvThreads + threadIdx.x;  // under 2^32, see the launch
+  const unsigned row = id / unsigned(a.pieces);
+  const int piece = int(id - row * unsigned(a.pieces));
+  const int b = int(row / unsigned(a.strips)), strip = int(row - unsigned(b) * unsigned(a.strips));
   if (b >= a.B) return;
   const int d = piece * V;
   const int slot = row_slot(a.slots, b, a.n_slots, a.dev_err);
   const int len = slot < 0 ? 0 : row_length(a.lengths, b, a.T);
   const int t0 = strip * a.strip, t1 = min(t0 + a.strip, a.T);
+  const int end = min(t1, len);  // tokens of this strip that exist: [t0, end)
   const T* x = static_cast<const T*>(a.x) + b * a.x_bs + d;
-  T* y = static_cast<T*>(a.y) + (size_t(b) * a.T) * a.D + d;
   auto token = [&](int t) {  // zero past the sequence
-    return t < len ? *reinterpret_cast<const word*>(x + t * a.x_ts) : W::zero();
+    return t < len ? *reinterpret_cast<const word*>(x + t * a.x_ts) : C::zero();
   };
 
   word next[kAhead];
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k) next[k] = token(t0 + k);
+  for (int k = 0; k < kAhead; ++k) next[k] = t0 + k < end ? token(t0 + k) : C::zero();
 
-  float w[K * V], bias[V];
-  load_weights<K * V, V>(a.w, a.w_dt, size_t(d) * K, a.w_vec, w);  // w[i * K + j]: channel i, tap j
+  num w[K][C::n], bias[C::n];
+  {
+    float f[K * V], tap[V];
+    load_weights<K * V, V>(a.w, a.w_dt, size_t(d) * K, a.w_vec, f);  // channel i, tap j at i * K + j
 #pragma unroll
-  for (int i = 0; i < V; ++i) bias[i] = 0.f;
-  if (a.bias) load_weights<V, V>(a.bias, a.w_dt, d, a.w_vec, bias);
+    for (int j = 0; j < K; ++j) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) tap[i] = f[i * K + j];
+      C::join(tap, w[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) tap[i] = 0.f;
+    if (a.bias) load_weights<V, V>(a.bias, a.w_dt, d, a.w_vec, tap);
+    C::join(tap, bias);
+  }
 
   const size_t srow = size_t(max(slot, 0)) * (K - 1) * a.D + d;
-  word old[K - 1];
-#pragma unroll
-  for (int j = 0; j < K - 1; ++j) {
-    if (t0 > 0)
-      old[j] = token(t0 - (K - 1) + j);
-    else
-      old[j] = a.state && slot >= 0
-                   ? *reinterpret_cast<const word*>(static_cast<const T*>(a.state) + srow + size_t(j) * a.D)
-                   : W::zero();
-  }
-  if (t0 == 0 && slot >= 0 && a.state_out) {
-    // This thread alone reads its channels' old state (above) and writes the new one, so the
-    // state may be updated in place.
+  num win[K - 1][C::n];
+  {
+    word old[K - 1];
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
-      const int t = len - (K - 1) + j;
-      word v = W::zero();
-      if (t >= 0) {
-        v = token(t);
-      } else {  // a sequence shorter than the window keeps the end of the old state
+      if (t0 > 0)
+        old[j] = token(t0 - (K - 1) + j);
+      else
+        old[j] = a.state && slot >= 0
+                     ? *reinterpret_cast<const word*>(static_cast<const T*>(a.state) + srow + size_t(j) * a.D)
+                     : C::zero();
+      C::load(old[j], win[j]);
+    }
+    if (t0 == 0 && slot >= 0 && a.state_out) {
+      // This thread alone reads its channels' old state (above) and writes the new one, so the
+      // state may be updated in place.
 #pragma unroll
-        for (int o = 0; o < K - 1; ++o)
-          if (o == t + K - 1) v = old[o];
+      for (int j = 0; j < K - 1; ++j) {
+        const int t = len - (K - 1) + j;
+        word v = C::zero();
+        if (t >= 0) {
+          v = token(t);
+        } else {  // a sequence shorter than the window keeps the end of the old state
+#pragma unroll
+          for (int o = 0; o < K - 1; ++o)
+            if (o == t + K - 1) v = old[o];
+        }
+        *reinterpret_cast<word*>(static_cast<T*>(a.state_out) + srow + size_t(j) * a.D) = v;
       }
-      *reinterpret_cast<word*>(static_cast<T*>(a.state_out) + srow + size_t(j) * a.D) = v;
     }
   }
-  float win[K - 1][V];
-#pragma unroll
-  for (int j = 0; j < K - 1; ++j) W::load(old[j], win[j]);
 
-  for (int t = t0; t < t1; t += kAhead) {
+  T* y = static_cast<T*>(a.y) + (size_t(b) * a.T + t0) * a.D + d;
+  const T* ahead = x + (t0 + kAhead) * a.x_ts;
+  int t = t0;
+  for (; t < end; t += kAhead) {
     word now[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) now[k] = next[k];
-    if (t + kAhead < t1) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) next[k] = token(t + kAhead + k);
+    for (int k = 0; k < kAhead; ++k) {
+      if (t + kAhead + k < end) next[k] = *reinterpret_cast<const word*>(ahead);
+      ahead += a.x_ts;
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (t + k >= t1) break;
-      float in[V], o[V];
-      W::load(now[k], in);
+      num in[C::n], o[C::n];
+      C::load(now[k], in);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float s = bias[i];
+      for (int i = 0; i < C::n; ++i) {
+        num s = bias[i];
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) s = fmaf(w[i * K + j], win[j][i], s);
-        s = fmaf(w[i * K + K - 1], in[i], s);
-        o[i] = t + k < len ? (a.act ? silu(s) : s) : 0.f;
+        for (int j = 0; j < K - 1; ++j) s = C::fma(w[j][i], win[j][i], s);
+        s = C::fma(w[K - 1][i], in[i], s);
+        o[i] = ACT ? C::act(s) : s;
 #pragma unroll
         for (int j = 0; j + 1 < K - 1; ++j) win[j][i] = win[j + 1][i];
         win[K - 2][i] = in[i];
       }
-      *reinterpret_cast<word*>(y + size_t(t + k) * a.D) = W::pack(o);
+      if (t + k < end) *reinterpret_cast<word*>(y) = C::pack(o);
+      y += a.D;
     }
   }
+  for (t = max(t0, end); t < t1; ++t)
+    *reinterpret_cast<word*>(static_cast<T*>(a.y) + (size_t(b) * a.T + t) * a.D + d) = C::zero();
+}
+
+template <typename T, int K, int V>
+void launch_act(const ConvArgs& a, unsigned blocks, cudaStream_t s) {
+  if (a.act == SDM_ACT_SILU)
+    conv_kernel<T, K, V, true><<<blocks, kConvThreads, 0, s>>>(a);
+  else
+    conv_kernel<T, K, V, false><<<blocks, kConvThreads, 0, s>>>(a);
 }
 
 template <typename T, int K>
 int launch_k(const ConvArgs& a, bool vec, cudaStream_t s) {
   const long long blocks =
       ((long long)a.B * a.strips * a.pieces + kConvThreads - 1) / kConvThreads;
-  if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
+  if (blocks * kConvThreads > 0xFFFFFFFFLL) return SDM_EUNSUPPORTED;
   if (vec)
-    conv_kernel<T, K, Piece<T>::n><<<unsigned(blocks), kConvThreads, 0, s>>>(a);
+    launch_act<T, K, Piece<T>::n>(a, unsigned(blocks), s);
   else
-    conv_kernel<T, K, 1><<<unsigned(blocks), kConvThreads, 0, s>>>(a);
+    launch_act<T, K, 1>(a, unsigned(blocks), s);
   return last_launch_status();
 }
 

@@ -76,10 +76,6 @@ __device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_
 __device__ __forceinline__ float gelu_cdf(float g) {
   return 0.5f * erfcf(-0.70710678118654752f * g);
 }
-// Sigmoid; 0 where the exponential is inf.
-__device__ __forceinline__ float sigmoid(float g) {
-  return __fdividef(1.0f, 1.0f + exp2_fast(-kLog2e * g));
-}
 template <int ACT>
 __device__ __forceinline__ float gate(float g) {
   return ACT == SDM_ACT_SILU ? silu(g) : g * gelu_cdf(g);
@@ -404,13 +400,13 @@ __global__ void __launch_bounds__(256) join_kernel(const float* partial, __nv_bf
 // A decode step's product reads all of w for a handful of tokens: HBM bounds it, and what counts is
 // that every SM reads its even share with enough loads under way.  A block takes 8 columns f: the 8
 // rows of Wg and the 8 of Wu are the 16 rows of one mma.m16n8k16, tokens its 8 columns, so that a lane
-// ends with g and u of the same elements.  The eight warps take K steps of 32 in turn, straight from
+// ends with g and u of the same elements.  The four warps take K steps of 32 in turn, straight from
 // global memory in 16-byte words (a lane's 8 consecutive k stand for the two groups of four that it
 // holds of two MMAs; x is read the same way, so the order of k is the same on both sides), and their
 // sums meet in shared memory.
-constexpr int kFewThreads = 256;
+constexpr int kFewThreads = 128;
 constexpr int kFewF = 8;
-constexpr int kFewTokens = 64;
+constexpr int kFewTokens = 16;
 
 __device__ __forceinline__ uint4 load_stream(const void* p) {  // read once: past L1
   uint4 v;
@@ -432,7 +428,7 @@ template <int ACT, int NT>
 __global__ void __launch_bounds__(kFewThreads) few_kernel(const __nv_bfloat16* __restrict__ x,
                                                           const __nv_bfloat16* __restrict__ w, int M,
                                                           int D, int F, __nv_bfloat16* h) {
-  constexpr int kWarps = kFewThreads / 32, kAhead = NT <= 2 ? 4 : 2;
+  constexpr int kWarps = kFewThreads / 32, kAhead = 8 / NT;
   __shared__ float4 part[kWarps][NT][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -491,12 +487,8 @@ int launch_few(const void* x, const void* w, int M, int D, int F, void* h, cudaS
   const unsigned blocks = unsigned(F / kFewF);
   if (M <= 8)
     few_kernel<ACT, 1><<<blocks, kFewThreads, 0, s>>>(xp, wp, M, D, F, hp);
-  else if (M <= 16)
-    few_kernel<ACT, 2><<<blocks, kFewThreads, 0, s>>>(xp, wp, M, D, F, hp);
-  else if (M <= 32)
-    few_kernel<ACT, 4><<<blocks, kFewThreads, 0, s>>>(xp, wp, M, D, F, hp);
   else
-    few_kernel<ACT, 8><<<blocks, kFewThreads, 0, s>>>(xp, wp, M, D, F, hp);
+    few_kernel<ACT, 2><<<blocks, kFewThreads, 0, s>>>(xp, wp, M, D, F, hp);
   return last_launch_status();
 }
 

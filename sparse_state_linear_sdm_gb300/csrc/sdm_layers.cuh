@@ -58,10 +58,17 @@ __device__ __forceinline__ float exp2_fast(float x) {  // at most 2 units in the
   return y;
 }
 
-// x / (1 + e^-x).  For x below about -88 the exponential is inf and the quotient -0, its limit.
-__device__ __forceinline__ float silu(float x) {
-  return __fdividef(x, 1.0f + exp2_fast(-kLog2e * x));
+__device__ __forceinline__ float rcp_fast(float x) {  // one unit in the last place; 0 for inf
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+
+// 1 / (1 + e^-x).  For x below about -88 the exponential is inf and the result 0.
+__device__ __forceinline__ float sigmoid(float x) {
+  return rcp_fast(1.0f + exp2_fast(-kLog2e * x));
+}
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
 // Two fp32 operations an instruction.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {

@@ -26,7 +26,7 @@ constexpr int kSteps = 4;     // tokens taken together by a lane
 
 struct ScanArgs {
   sdm_ssm_args io;
-  int tiles_g, Dg;             // channel tiles of a group, channels of a group
+  int tiles_g, Dg;             // channel tiles of a group (one token: of a row), channels of a group
   int chunks, chunk;           // chunks of a sequence, tokens of a chunk (a multiple of kTT)
   float* ws_h;                 // [chunks][B][Dm][N]: state before chunk 0, then each chunk's own end
   float* ws_d;                 // [chunks][B][Dm]: sum of delta over each chunk
@@ -429,36 +429,41 @@ __device__ __forceinline__ void load4(const T* p, int n, bool vec, float (&v)[4]
 // One token: a lane has four states of a channel (16 bytes in, 16 bytes out) in each of R sequences,
 // L lanes a channel.  HBM bounds it, the states read and written once, so R states are under way in
 // every lane, and what a channel computes once (step size, gate) is done for each sequence by one of
-// its lanes: lane r < R for sequence r.
-template <typename T, int L>
+// its lanes: lane r < R for sequence r.  VEC: four states, and four entries of B and C, are a word.
+template <typename T, int L, bool VEC>
 __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_constant__ ScanArgs a) {
   constexpr int R = L < 4 ? L : 4;
   const sdm_ssm_args& io = a.io;
-  const long long id = (long long)blockIdx.x * kTokenThreads + threadIdx.x;
-  const int sub = int(id % L), own = sub % R;
-  const int d = int((id / L) % io.Dm);
-  const long long b0 = id / L / io.Dm * R;
-  const int n0 = sub * 4, left = io.N - n0, g = d / a.Dg;
+  const int sub = threadIdx.x % L, own = sub % R;
+  const int group = int(blockIdx.x) / a.tiles_g;  // of R sequences; tiles_g blocks hold its channels
+  const int channel = (int(blockIdx.x) - group * a.tiles_g) * (kTokenThreads / L) + int(threadIdx.x) / L;
+  const bool present = channel < io.Dm;  // lanes past the last channel only take part in the shuffles
+  const int d = present ? channel : 0;
+  const int b0 = group * R, rows = present ? min(R, io.B - b0) : 0;
+  const int n0 = sub * 4, left = io.N - n0;
+  const bool states = left > 0;
+  const size_t at = size_t(d) * io.N + n0, row = size_t(io.Dm) * io.N;
 
-  int slot[R], len[R];
+  int slot[R];
+  bool live[R];  // the sequence has a state and a token
   float h[R][4];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    slot[r] = -1;
-    len[r] = 0;
-    if (b0 + r < io.B) {
-      slot[r] = row_slot(io.slots, int(b0) + r, io.n_slots, d == 0 && sub == 0 ? a.dev_err : nullptr);
-      len[r] = slot[r] < 0 ? 0 : row_length(io.lengths, int(b0) + r, 1);
-    }
+    slot[r] = r < rows ? row_slot(io.slots, b0 + r, io.n_slots, d == 0 && sub == 0 ? a.dev_err : nullptr) : -1;
+    live[r] = slot[r] >= 0 && row_length(io.lengths, b0 + r, 1) > 0;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[r][j] = 0.f;
-    if (slot[r] >= 0 && io.state && left > 0)
-      load4(io.state + (size_t(slot[r]) * io.Dm + d) * io.N + n0, left, a.vec, h[r]);
+    if (slot[r] >= 0 && io.state && states) load4(io.state + at + size_t(unsigned(slot[r])) * row, left, VEC, h[r]);
   }
-  float x = 0.f, dl = 0.f, z = 0.f;
+  float A[4] = {0.f, 0.f, 0.f, 0.f};
+  if (states) load4(io.A + at, left, VEC, A);
   bool mine = false;
 #pragma unroll
-  for (int r = 0; r < R; ++r) mine = mine || (own == r && len[r] > 0);
+  for (int r = 0; r < R; ++r) mine = mine || (own == r && live[r]);
+  float x = 0.f, dl = 0.f, z = 0.f;
   if (mine) {
     const long long b = b0 + own;
     x = to_f32(static_cast<const T*>(io.x)[b * io.x_bs + d]);
@@ -467,30 +472,34 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
     if (io.dt_bias) dl += io.dt_bias[d];
     if (io.softplus) dl = softplus(dl);
   }
-  float A[4] = {0.f, 0.f, 0.f, 0.f};
-  if (left > 0) load4(io.A + size_t(d) * io.N + n0, left, a.vec, A);
+  const float dlx = dl * x;
 #pragma unroll
   for (int j = 0; j < 4; ++j) A[j] = decay_rate(A[j]);
 
+  const int bc = (io.G > 1 ? d / a.Dg * io.N : 0) + n0;
+  const T* pB = static_cast<const T*>(io.Bm) + b0 * io.B_bs + bc;
+  const T* pC = static_cast<const T*>(io.Cm) + b0 * io.C_bs + bc;
+  float* po = io.state_out + at;
   float y[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const float dr = __shfl_sync(0xFFFFFFFFu, dl, r, L), dx = __shfl_sync(0xFFFFFFFFu, dl * x, r, L);
+    const float dr = __shfl_sync(0xFFFFFFFFu, dl, r, L), dx = __shfl_sync(0xFFFFFFFFu, dlx, r, L);
     y[r] = 0.f;
-    if (len[r] > 0 && left > 0) {
-      const long long b = b0 + r;
+    if (live[r] && states) {
       float B[4], C[4];
-      load4(static_cast<const T*>(io.Bm) + b * io.B_bs + g * io.N + n0, left, a.vec_bc, B);
-      load4(static_cast<const T*>(io.Cm) + b * io.C_bs + g * io.N + n0, left, a.vec_bc, C);
+      load4(pB, left, VEC, B);
+      load4(pC, left, VEC, C);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         h[r][j] = fmaf(exp2_fast(dr * A[j]), h[r][j], dx * B[j]);
         y[r] = fmaf(h[r][j], C[j], y[r]);
       }
     }
-    if (slot[r] >= 0 && io.state_out && left > 0) {
-      float* p = io.state_out + (size_t(slot[r]) * io.Dm + d) * io.N + n0;
-      if (a.vec) {
+    pB += io.B_bs;
+    pC += io.C_bs;
+    if (slot[r] >= 0 && io.state_out && states) {
+      float* p = po + size_t(unsigned(slot[r])) * row;
+      if (VEC) {
         *reinterpret_cast<float4*>(p) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
       } else {
 #pragma unroll
@@ -515,13 +524,13 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
 #pragma unroll
     for (int o = 4; o < L; o *= 2) y[0] += __shfl_xor_sync(0xFFFFFFFFu, y[0], o);
   }
-  if (sub < R && b0 + own < io.B) {
+  if (sub < R && own < rows) {
     float v = 0.f;
     if (mine) {
       v = io.D ? fmaf(io.D[d], x, y[0]) : y[0];
       if (io.z) v *= silu(z);
     }
-    from_f32(v, static_cast<T*>(io.y) + (b0 + own) * io.Dm + d);
+    from_f32(v, static_cast<T*>(io.y) + size_t(b0 + own) * io.Dm + d);
   }
 }
 
@@ -568,17 +577,20 @@ int launch_scan(ScanArgs& a, cudaStream_t s) {
 }
 
 template <typename T, int L>
-int launch_token_l(const ScanArgs& a, cudaStream_t s) {
-  constexpr int R = L < 4 ? L : 4;
-  const long long blocks =
-      ((long long)((a.io.B + R - 1) / R) * a.io.Dm * L + kTokenThreads - 1) / kTokenThreads;
+int launch_token_l(ScanArgs& a, cudaStream_t s) {
+  constexpr int R = L < 4 ? L : 4, channels = kTokenThreads / L;
+  a.tiles_g = (a.io.Dm + channels - 1) / channels;
+  const long long blocks = (long long)((a.io.B + R - 1) / R) * a.tiles_g;
   if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
-  token_kernel<T, L><<<unsigned(blocks), kTokenThreads, 0, s>>>(a);
+  if (a.vec && a.vec_bc)
+    token_kernel<T, L, true><<<unsigned(blocks), kTokenThreads, 0, s>>>(a);
+  else
+    token_kernel<T, L, false><<<unsigned(blocks), kTokenThreads, 0, s>>>(a);
   return last_launch_status();
 }
 
 template <typename T>
-int launch_token(const ScanArgs& a, cudaStream_t s) {
+int launch_token(ScanArgs& a, cudaStream_t s) {
   switch (lanes_for(a.io.N, 4)) {
     case 1: return launch_token_l<T, 1>(a, s);
     case 2: return launch_token_l<T, 2>(a, s);

@@ -92,11 +92,13 @@ def _rows(t, name, dtype, shape, index, lead):
         ok = False
     if not ok:
         _refuse(t, name, dtype, shape, index)
-    st, n = t.stride(), 1
-    for k in range(len(shape) - 1, lead - 1, -1):
-        if st[k] != n and shape[k] > 1:
-            raise ValueError(f"{name} must be dense in its last {len(shape) - lead} dimension(s)")
-        n *= shape[k]
+    st = t.stride()
+    if len(shape) > lead + 1 or st[lead] != 1:
+        n = 1
+        for k in range(len(shape) - 1, lead - 1, -1):
+            if st[k] != n and shape[k] > 1:
+                raise ValueError(f"{name} must be dense in its last {len(shape) - lead} dimension(s)")
+            n *= shape[k]
     return (t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if lead == 2 and shape[1] > 1 else 0)
 
 
@@ -144,7 +146,7 @@ def _conv(x, w, bias, state, state_out, activation, lengths, slots, out, dev_err
     act = _activation(activation, ("silu", "none"))
     ps, po, rows, written = _state_rows(state, state_out, slots, nb, (K - 1, D), ty, index)
     if out is None:
-        out = x.new_empty(shape)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
         py = out.data_ptr()
     else:
         py = _dense(out, "out", ty, shape, index)
@@ -212,7 +214,7 @@ def _scan(x, dt, A, B, C, D, z, dt_bias, state, state_out, dt_softplus, lengths,
     pz, z_bs, z_ts = (0, 0, 0) if z is None else _rows(z, "z", ty, shape, index, lead)
     ps, po, rows, written = _state_rows(state, state_out, slots, nb, (Dm, N), _FP32, index)
     if out is None:
-        out = x.new_empty(shape)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
         py = out.data_ptr()
     else:
         py = _dense(out, "out", ty, shape, index)
@@ -283,7 +285,7 @@ def project_gated(x, w, activation="silu", out=None, dev_err=None):
     M, D, F, px, pw = _gated_operands(x, w, index)
     shape = (*x.shape[:-1], F)
     if out is None:
-        out = x.new_empty(shape)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
         ph = out.data_ptr()
     else:
         ph = _dense(out, "out", _BF16, shape, index)
@@ -310,9 +312,9 @@ def project_gated_backward(x, w, dh, activation="silu", dx=None, dw=None, worksp
     M, D, F, px, pw = _gated_operands(x, w, index)
     ph = _dense(dh, "dh", _BF16, (*x.shape[:-1], F), index)
     if dx is None:
-        dx = x.new_empty(x.shape)
+        dx = torch.empty(x.shape, dtype=_BF16, device=x.device)
     if dw is None:
-        dw = w.new_empty(w.shape)
+        dw = torch.empty(w.shape, dtype=_BF16, device=w.device)
     if workspace is None:
         workspace = torch.empty(max(16, project_gated_backward_workspace_size(M, D, F)), dtype=torch.uint8,
                                 device=x.device)
