@@ -15,7 +15,7 @@ namespace sdm {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kAhead = 4;  // tokens loaded while the ones before are computed
+constexpr int kAhead = 8;  // tokens under way: a register word each, reloaded as soon as it is taken
 constexpr int kMinStrip = 8;  // shortest strip: longer than the window
 
 struct ConvArgs {
@@ -185,18 +185,12 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const __grid_constan
   const T* ahead = x + (t0 + kAhead) * a.x_ts;
   int t = t0;
   for (; t < end; t += kAhead) {
-    word now[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) now[k] = next[k];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (t + kAhead + k < end) next[k] = *reinterpret_cast<const word*>(ahead);
-      ahead += a.x_ts;
-    }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       num in[C::n], o[C::n];
-      C::load(now[k], in);
+      C::load(next[k], in);
+      if (t + kAhead + k < end) next[k] = *reinterpret_cast<const word*>(ahead);
+      ahead += a.x_ts;
 #pragma unroll
       for (int i = 0; i < C::n; ++i) {
         num s = bias[i];

@@ -35,11 +35,10 @@ struct ScanArgs {
   int* dev_err;
 };
 
-// A in units of exp2.  A finite A stays finite, so that a step of size 0 has the decay 1 (0 times
-// an infinite rate would have none).
+// A in units of exp2, finite, so that a step of size 0 has the decay 1 (0 times an infinite rate
+// would have none).
 __device__ __forceinline__ float decay_rate(float A) {
-  const float r = A * kLog2e;
-  return isinf(r) && !isinf(A) ? copysignf(3.402823466e38f, A) : r;
+  return fminf(fmaxf(A * kLog2e, -3.402823466e38f), 3.402823466e38f);
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -407,29 +406,39 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
   }
 }
 
-// Four elements from p on; one word of them where `vec` says that p is aligned to it, the first n
-// where a row ends.
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, int n, bool vec, float (&v)[4]) {
-  if (vec) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 w = *reinterpret_cast<const float4*>(p);
-      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+// Four elements of a row: as they lie in memory (one word where VEC says that they are aligned to
+// it, else the first n one by one), and as numbers.
+template <typename T, bool VEC>
+struct Four {
+  uint32_t w[sizeof(T)];  // 4 sizeof(T) bytes
+  __device__ void load(const T* p, int n) {
+    if constexpr (VEC && sizeof(T) == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (VEC) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
     } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(p);
-      v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
-      v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xFFFF0000u);
-    }
-  } else {
+      T* e = reinterpret_cast<T*>(w);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = j < n ? to_f32(p[j]) : 0.f;
+      for (int j = 0; j < 4; ++j) e[j] = j < n ? p[j] : T(0.f);
+    }
   }
-}
+  __device__ void clear() {
+#pragma unroll
+    for (int j = 0; j < int(sizeof(T)); ++j) w[j] = 0;
+  }
+  __device__ float operator[](int j) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+    return __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+  }
+};
 
 // One token: a lane has four states of a channel (16 bytes in, 16 bytes out) in each of R sequences,
-// L lanes a channel.  HBM bounds it, the states read and written once, so R states are under way in
-// every lane, and what a channel computes once (step size, gate) is done for each sequence by one of
-// its lanes: lane r < R for sequence r.  VEC: four states, and four entries of B and C, are a word.
+// L lanes a channel.  HBM bounds it, the states read and written once: R states are under way in
+// every lane, everything that does not wait for a slot is asked for first, and what a channel
+// computes once (step size, gate) is done for each sequence by one of its lanes, lane r < R for
+// sequence r.  VEC: four states, and four entries of B and C, are a word.
 template <typename T, int L, bool VEC>
 __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_constant__ ScanArgs a) {
   constexpr int R = L < 4 ? L : 4;
@@ -445,66 +454,74 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
   const size_t at = size_t(d) * io.N + n0, row = size_t(io.Dm) * io.N;
 
   int slot[R];
-  bool live[R];  // the sequence has a state and a token
-  float h[R][4];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
+  for (int r = 0; r < R; ++r)
     slot[r] = r < rows ? row_slot(io.slots, b0 + r, io.n_slots, d == 0 && sub == 0 ? a.dev_err : nullptr) : -1;
-    live[r] = slot[r] >= 0 && row_length(io.lengths, b0 + r, 1) > 0;
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[r][j] = 0.f;
-    if (slot[r] >= 0 && io.state && states) load4(io.state + at + size_t(unsigned(slot[r])) * row, left, VEC, h[r]);
-  }
-  float A[4] = {0.f, 0.f, 0.f, 0.f};
-  if (states) load4(io.A + at, left, VEC, A);
-  bool mine = false;
-#pragma unroll
-  for (int r = 0; r < R; ++r) mine = mine || (own == r && live[r]);
   float x = 0.f, dl = 0.f, z = 0.f;
-  if (mine) {
+  if (own < rows) {
     const long long b = b0 + own;
     x = to_f32(static_cast<const T*>(io.x)[b * io.x_bs + d]);
     dl = to_f32(static_cast<const T*>(io.dt)[b * io.dt_bs + d]);
     if (io.z) z = to_f32(static_cast<const T*>(io.z)[b * io.z_bs + d]);
-    if (io.dt_bias) dl += io.dt_bias[d];
-    if (io.softplus) dl = softplus(dl);
   }
-  const float dlx = dl * x;
+  Four<float, VEC> A, h4[R];
+  Four<T, VEC> B[R], C[R];
+  A.clear();
+  if (states) A.load(io.A + at, left);
+  {
+    const int bc = (io.G > 1 ? d / a.Dg * io.N : 0) + n0;
+    const T* pB = static_cast<const T*>(io.Bm) + b0 * io.B_bs + bc;
+    const T* pC = static_cast<const T*>(io.Cm) + b0 * io.C_bs + bc;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) A[j] = decay_rate(A[j]);
+    for (int r = 0; r < R; ++r) {
+      B[r].clear();
+      C[r].clear();
+      if (r < rows && states) {
+        B[r].load(pB, left);
+        C[r].load(pC, left);
+      }
+      pB += io.B_bs;
+      pC += io.C_bs;
+    }
+  }
+  const float bias = io.dt_bias ? io.dt_bias[d] : 0.f, skip = io.D ? io.D[d] : 0.f;
+  bool live[R], mine = false;  // the sequence has a state and a token
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    h4[r].clear();
+    if (slot[r] >= 0 && io.state && states)
+      h4[r].load(io.state + at + size_t(unsigned(slot[r])) * row, left);
+    live[r] = slot[r] >= 0 && row_length(io.lengths, b0 + r, 1) > 0;
+    mine = mine || (own == r && live[r]);
+  }
 
-  const int bc = (io.G > 1 ? d / a.Dg * io.N : 0) + n0;
-  const T* pB = static_cast<const T*>(io.Bm) + b0 * io.B_bs + bc;
-  const T* pC = static_cast<const T*>(io.Cm) + b0 * io.C_bs + bc;
-  float* po = io.state_out + at;
-  float y[R];
+  dl += bias;
+  if (io.softplus) dl = softplus(dl);
+  const float dlx = dl * x;
+  float rate[4], y[R];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) rate[j] = decay_rate(A[j]);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const float dr = __shfl_sync(0xFFFFFFFFu, dl, r, L), dx = __shfl_sync(0xFFFFFFFFu, dlx, r, L);
+    float h[4];
     y[r] = 0.f;
-    if (live[r] && states) {
-      float B[4], C[4];
-      load4(pB, left, VEC, B);
-      load4(pC, left, VEC, C);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[r][j] = fmaf(exp2_fast(dr * A[j]), h[r][j], dx * B[j]);
-        y[r] = fmaf(h[r][j], C[j], y[r]);
+    for (int j = 0; j < 4; ++j) {
+      h[j] = h4[r][j];
+      if (live[r]) {
+        h[j] = fmaf(exp2_fast(dr * rate[j]), h[j], dx * B[r][j]);
+        y[r] = fmaf(h[j], C[r][j], y[r]);
       }
     }
-    pB += io.B_bs;
-    pC += io.C_bs;
     if (slot[r] >= 0 && io.state_out && states) {
-      float* p = po + size_t(unsigned(slot[r])) * row;
-      if (VEC) {
-        *reinterpret_cast<float4*>(p) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
+      float* p = io.state_out + at + size_t(unsigned(slot[r])) * row;
+      if constexpr (VEC) {
+        *reinterpret_cast<float4*>(p) = make_float4(h[0], h[1], h[2], h[3]);
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (j < left) p[j] = h[r][j];
+          if (j < left) p[j] = h[j];
       }
     }
   }
@@ -525,12 +542,9 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
     for (int o = 4; o < L; o *= 2) y[0] += __shfl_xor_sync(0xFFFFFFFFu, y[0], o);
   }
   if (sub < R && own < rows) {
-    float v = 0.f;
-    if (mine) {
-      v = io.D ? fmaf(io.D[d], x, y[0]) : y[0];
-      if (io.z) v *= silu(z);
-    }
-    from_f32(v, static_cast<T*>(io.y) + size_t(b0 + own) * io.Dm + d);
+    float v = fmaf(skip, x, y[0]);
+    if (io.z) v *= silu(z);
+    from_f32(mine ? v : 0.f, static_cast<T*>(io.y) + size_t(b0 + own) * io.Dm + d);
   }
 }
 
