@@ -30,11 +30,20 @@ enum Mode { kForward = 0, kSlope = 1, kInput = 2, kWeight = 3 };
 constexpr int kHalf = 128;                       // rows (and columns) of a tile each CTA stages
 constexpr int kOperand = kHalf * kTileK * 2;     // 16 KB
 constexpr int kStage = 2 * kOperand;
-constexpr int kStages = 6;
 constexpr int kEpilogueWarps = 8;                // two for each quarter of the tile's rows
 constexpr int kRoles = 64 + 32 * kEpilogueWarps; // copy warp, MMA warp, epilogue warps
-constexpr int kBars = 2 * kStages + 5;           // full[], empty[], acc_full[2], acc_empty[2], drain
-constexpr int kSmem = kStages * kStage + 1024 + 256;
+constexpr int kPatch = 32 * 64 * 2;               // 32 rows x 64 columns of bf16: a warp's output
+// Shared memory: a ring of stages, then patches through which the epilogue warps load and store.
+template <int MODE>
+struct Layout {
+  static constexpr int patches = MODE == kSlope ? 2 : MODE == kForward ? 1 : 0;  // of each warp
+  static constexpr int stages = MODE == kSlope ? 5 : 6;
+  static constexpr int bars = 2 * stages + 5 + kEpilogueWarps;  // full[], empty[], acc_full[2],
+                                                                // acc_empty[2], drain, patch[]
+  static constexpr int off_patch = stages * kStage;
+  static constexpr int off_bars = off_patch + patches * kEpilogueWarps * kPatch;
+  static constexpr int bytes = off_bars + 512 + 1024 /* alignment slack */;
+};
 constexpr uint32_t kColumns = 512;
 constexpr int kRowGroup = 32;                    // row tiles of a group of the tile order
 
@@ -43,8 +52,7 @@ struct GatedArgs {
   int row_tiles, col_tiles, splits;
   int kblocks, per_split;  // K steps in all, and of each split
   int F, act;
-  __nv_bfloat16* out;      // h, dx or dw; [dg | du] for kSlope
-  const __nv_bfloat16* dh;
+  __nv_bfloat16* out;      // dx or dw
   float* partial;          // [splits][rows][cols] where splits > 1
   int* dev_err;
 };
@@ -111,105 +119,114 @@ __device__ __forceinline__ Unit unit_at(int u, const GatedArgs& a) {
   return r;
 }
 
-// The epilogue of one warp: 32 rows, and half of the tile's columns.
+// 16-byte piece j of row r of a patch in the 128-byte swizzle that its copies use.
+__device__ __forceinline__ uint32_t patch_at(int r, int j) { return uint32_t(r * 128 + ((j ^ (r & 7)) << 4)); }
+__device__ __forceinline__ uint4 patch_load(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(p));
+  return v;
+}
+__device__ __forceinline__ void patch_store(uint32_t p, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void patch_copy_out(const CUtensorMap* map, int x, int y, uint32_t p) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(p)
+               : "memory");
+}
+__device__ __forceinline__ void copies_out_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_out_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void copies_out_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// h, or dg and du, of a warp's 32 rows x 64 columns: from TMEM (gate and up columns) through
+// registers into the warp's patches.  kSlope's first patch holds dh on entry and dg on exit.
 template <int MODE, int ACT>
-struct Epilogue {
-  const GatedArgs& a;
-  int m, half;
-  uint4 dh[MODE == kSlope ? kHalf / 16 : 1];
-
-  __device__ Epilogue(const GatedArgs& args, const Unit& un, int rank, int row, int half_)
-      : a(args), m((un.row * 2 + rank) * kHalf + row), half(half_) {}
-
-  // What the epilogue reads of memory: asked for before the products are awaited.
-  __device__ void fetch(const Unit& un) {
-    if constexpr (MODE == kSlope) {
-      const int f0 = un.col * kHalf + half * (kHalf / 2);
-#pragma unroll
-      for (int j = 0; j < kHalf / 16; ++j)
-        if (m < a.rows && f0 + 8 * j < a.F)
-          dh[j] = __ldcs(reinterpret_cast<const uint4*>(a.dh + size_t(m) * a.F + f0 + 8 * j));
-    }
-  }
-
-  __device__ void run(const Unit& un, uint32_t taddr) {
-    if constexpr (MODE == kForward || MODE == kSlope) {
-      const int c0 = half * (kHalf / 2), f0 = un.col * kHalf + c0;
-#pragma unroll
-      for (int c = 0; c < kHalf / 2; c += 32) {
-        uint32_t g[32], u[32];
-        tmem_load32(taddr + uint32_t(c0 + c), g);
-        tmem_load32(taddr + uint32_t(kHalf + c0 + c), u);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // F % 8 == 0: a 16-byte piece is in or out
-          const int f = f0 + c + 8 * j;
-          if (m >= a.rows || f >= a.F) break;
-          float o[8];
-          if constexpr (MODE == kForward) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              o[i] = gate<ACT>(__uint_as_float(g[8 * j + i])) * __uint_as_float(u[8 * j + i]);
-            *reinterpret_cast<uint4*>(a.out + size_t(m) * a.F + f) = Piece<__nv_bfloat16>::pack(o);
-          } else {
-            float d[8], o2[8];
-            Piece<__nv_bfloat16>::load(dh[c / 8 + j], d);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float v, s;
-              gate_slope<ACT>(__uint_as_float(g[8 * j + i]), v, s);
-              o[i] = d[i] * __uint_as_float(u[8 * j + i]) * s;
-              o2[i] = d[i] * v;
-            }
-            __nv_bfloat16* p = a.out + size_t(m) * (2 * size_t(a.F)) + f;
-            *reinterpret_cast<uint4*>(p) = Piece<__nv_bfloat16>::pack(o);
-            *reinterpret_cast<uint4*>(p + a.F) = Piece<__nv_bfloat16>::pack(o2);
-          }
-        }
-        __syncwarp();  // tcgen05.ld takes the whole warp
-      }
-    } else {
-      const int c0 = half * kHalf, n0 = un.col * 2 * kHalf + c0;
+__device__ __forceinline__ void gate_patch(uint32_t tgate, uint32_t tup, uint32_t patch, int lane) {
 #pragma unroll 1
-      for (int c = 0; c < kHalf; c += 32) {
-        uint32_t r[32];
-        tmem_load32(taddr + uint32_t(c0 + c), r);
+  for (int c = 0; c < 64; c += 16) {
+    uint32_t g[16], u[16];
+    tmem_load16(tgate + uint32_t(c), g);
+    tmem_load16(tup + uint32_t(c), u);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = n0 + c + 8 * j;
-          if (m >= a.rows || n >= a.cols) break;
-          float o[8];
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t at = patch + patch_at(lane, c / 8 + j);
+      float o[8];
+      if constexpr (MODE == kForward) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(r[8 * j + i]);
-          if (a.splits > 1) {
-            float* p = a.partial + (size_t(un.split) * a.rows + m) * a.cols + n;
-            *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<float4*>(p + 4) = make_float4(o[4], o[5], o[6], o[7]);
-          } else {
-            *reinterpret_cast<uint4*>(a.out + size_t(m) * a.cols + n) = Piece<__nv_bfloat16>::pack(o);
-          }
+        for (int i = 0; i < 8; ++i)
+          o[i] = gate<ACT>(__uint_as_float(g[8 * j + i])) * __uint_as_float(u[8 * j + i]);
+        patch_store(at, Piece<__nv_bfloat16>::pack(o));
+      } else {
+        float d[8], o2[8];
+        Piece<__nv_bfloat16>::load(patch_load(at), d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float v, s;
+          gate_slope<ACT>(__uint_as_float(g[8 * j + i]), v, s);
+          o[i] = d[i] * __uint_as_float(u[8 * j + i]) * s;
+          o2[i] = d[i] * v;
         }
-        __syncwarp();
+        patch_store(at, Piece<__nv_bfloat16>::pack(o));
+        patch_store(at + kPatch, Piece<__nv_bfloat16>::pack(o2));
       }
     }
   }
+}
+
+// dx or dw of a warp's 32 rows x 128 columns, straight to memory.
+__device__ __forceinline__ void store_sums(const GatedArgs& a, const Unit& un, int m, int n0, uint32_t taddr) {
+#pragma unroll 1
+  for (int c = 0; c < kHalf; c += 32) {
+    uint32_t r[32];
+    tmem_load32(taddr + uint32_t(c), r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + c + 8 * j;
+      if (m >= a.rows || n >= a.cols) break;
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(r[8 * j + i]);
+      if (a.splits > 1) {
+        float* p = a.partial + (size_t(un.split) * a.rows + m) * a.cols + n;
+        *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(o[4], o[5], o[6], o[7]);
+      } else {
+        *reinterpret_cast<uint4*>(a.out + size_t(m) * a.cols + n) = Piece<__nv_bfloat16>::pack(o);
+      }
+    }
+    __syncwarp();  // tcgen05.ld takes the whole warp
+  }
+}
+
+// Tensor maps of a launch: the operands (B2: the rank-1 CTA's, Wu), and what the epilogue moves in
+// patches: dh in; h, or dg and du, out.
+struct Maps {
+  CUtensorMap A, B, B2, dh, out, out2;
 };
 
 // Every wait is bounded; a wait that runs out stops both CTAs, which drain the copies and MMAs in
 // flight, free TMEM and report SDM_DEV_TIMEOUT.
 template <int MODE, int ACT>
 __global__ void __launch_bounds__(kRoles, 1)
-    gated_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ GatedArgs a) {
+    gated_kernel(const __grid_constant__ Maps tm, const __grid_constant__ GatedArgs a) {
+  using Lay = Layout<MODE>;
+  constexpr int kStages = Lay::stages;
+  constexpr bool kGate = MODE == kForward || MODE == kSlope;
   constexpr bool kAMN = MODE == kWeight, kBMN = MODE == kInput || MODE == kWeight;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (ring - raw) + kStages * kStage);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (ring - raw) + Lay::off_bars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Lay::bars);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile uint32_t* issued = tmem_slot + 2;  // copies issued per stage, read by the leader after a stop
   const int FULL = 0, EMPTY = kStages, ACC_FULL = 2 * kStages, ACC_EMPTY = 2 * kStages + 2,
-            DRAIN = 2 * kStages + 4;
+            DRAIN = 2 * kStages + 4, PATCH = 2 * kStages + 5;
   auto bar = [&](int i) { return smem_u32(bars + i); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -229,11 +246,12 @@ __global__ void __launch_bounds__(kRoles, 1)
       mbar_init(bar(ACC_EMPTY + i), 2 * kEpilogueWarps);  // both CTAs' epilogue warps
     }
     mbar_init(bar(DRAIN), 1);
+    for (int i = 0; i < kEpilogueWarps; ++i) mbar_init(bar(PATCH + i), 1);
     *stop = 0;
     for (int s = 0; s < kStages; ++s) issued[s] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm.A)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm.B)) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -251,7 +269,7 @@ __global__ void __launch_bounds__(kRoles, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ---- copies (both CTAs) ----
-      const CUtensorMap* mapB = (MODE == kForward || MODE == kSlope) && rank ? &tmB2 : &tmB;
+      const CUtensorMap* mapB = kGate && rank ? &tm.B2 : &tm.B;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -269,10 +287,10 @@ __global__ void __launch_bounds__(kRoles, 1)
           const uint32_t full = cluster_addr(bar(FULL + stage), 0);
           if (leader) mbar_expect_tx(bar(FULL + stage), 2 * kStage);
           if (kAMN) {
-            tma_load_2d_pair(sa, &tmA, m0, kb * kTileK, full);
-            tma_load_2d_pair(sa + kOperand / 2, &tmA, m0 + kHalf / 2, kb * kTileK, full);
+            tma_load_2d_pair(sa, &tm.A, m0, kb * kTileK, full);
+            tma_load_2d_pair(sa + kOperand / 2, &tm.A, m0 + kHalf / 2, kb * kTileK, full);
           } else {
-            tma_load_2d_pair(sa, &tmA, kb * kTileK, m0, full);
+            tma_load_2d_pair(sa, &tm.A, kb * kTileK, m0, full);
           }
           if (kBMN) {
             tma_load_2d_pair(sb, mapB, n0, kb * kTileK, full);
@@ -327,23 +345,62 @@ __global__ void __launch_bounds__(kRoles, 1)
       mbar_wait_teardown(bar(DRAIN), 0);
     }
   } else {
-    // ---- epilogue (both CTAs): warp w reads TMEM lanes 32 * (w % 4) .. + 31 ----
-    const int quad = warp & 3;
+    // ---- epilogue (both CTAs): warp w reads TMEM lanes 32 * (w % 4) .. + 31, half of the columns ----
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t patch = ring + Lay::off_patch + uint32_t((warp - 2) * Lay::patches * kPatch);
+    const uint32_t patch_bar = bar(PATCH + warp - 2);
+    uint32_t patch_loads = 0;  // copies of dh asked for, and how many of them were awaited
+    uint32_t patch_waits = 0;
     int it = 0;
     for (int u = cid; u < units; u += ncl, ++it) {
       const int acc = it & 1;
       const uint32_t acc_par = uint32_t(it >> 1) & 1u;
       const Unit un = unit_at(u, a);
-      Epilogue<MODE, ACT> e(a, un, int(rank), quad * 32 + lane, (warp - 2) >> 2);
-      e.fetch(un);
+      const int m0 = (un.row * 2 + int(rank)) * kHalf + quad * 32;
+      const int f0 = un.col * kHalf + half * 64;
+      // A patch outside the matrix is neither loaded nor stored; one across its edge is cut there.
+      const bool inside = kGate && m0 < a.rows && f0 < a.F;
+      if (kGate && lane == 0) copies_out_read();  // the patches' last copies have read them
+      if (MODE == kSlope && inside) {
+        if (lane == 0) {
+          mbar_expect_tx(patch_bar, kPatch);
+          tma_load_2d(patch, &tm.dh, f0, m0, patch_bar);
+        }
+        ++patch_loads;
+      }
+      __syncwarp();
       if (!__all_sync(0xFFFFFFFFu,
                       mbar_wait_cluster(bar(ACC_FULL + acc), acc_par, stop, peer_stop, kWaitNs)))
         break;
       tc_fence_after();
-      e.run(un, tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * 256));
+      const uint32_t taddr = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * 256);
+      if constexpr (kGate) {
+        if (inside) {
+          if (MODE == kSlope) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(patch_bar, patch_waits & 1u, stop, peer_stop, kWaitNs)))
+              break;
+            ++patch_waits;
+          }
+          gate_patch<MODE, ACT>(taddr + uint32_t(half * 64), taddr + uint32_t(kHalf + half * 64), patch, lane);
+          fence_async_proxy();
+        }
+      } else {
+        store_sums(a, un, m0 + lane, un.col * 2 * kHalf + half * kHalf, taddr + uint32_t(half * kHalf));
+      }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(bar(ACC_EMPTY + acc), 0));
+      if (lane == 0) {
+        mbar_arrive_cluster(cluster_addr(bar(ACC_EMPTY + acc), 0));
+        if (inside) {
+          patch_copy_out(&tm.out, f0, m0, patch);
+          if (MODE == kSlope) patch_copy_out(&tm.out2, f0, m0, patch + kPatch);
+        }
+        if (kGate) copies_out_commit();
+      }
+    }
+    if (kGate && lane == 0) {
+      copies_out_done();
+      if (patch_waits != patch_loads) mbar_wait_teardown(patch_bar, patch_waits & 1u);
     }
   }
 
@@ -528,14 +585,8 @@ Plan plan(int mode, int M, int D, int F) {
   return p;
 }
 
-// Row-major bf16 [rows, cols] in boxes of box_rows x 64.
-bool tile_map(CUtensorMap* map, const void* base, int rows, int cols, int box_rows) {
-  return bf16_tile_map(map, base, rows, cols, box_rows);
-}
-
 template <int MODE, int ACT>
-int launch_mode(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& B2, GatedArgs a,
-                const Plan& p, cudaStream_t s) {
+int launch_mode(const Maps& tm, GatedArgs a, const Plan& p, cudaStream_t s) {
   a.row_tiles = p.row_tiles;
   a.col_tiles = p.col_tiles;
   a.splits = p.splits;
@@ -551,14 +602,15 @@ int launch_mode(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& B
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kRoles);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = Layout<MODE>::bytes;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // Pairs that can be resident at once: a larger persistent grid would run in two waves.
   static PerDevice resident;
   long long pairs = resident.get([&] {
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return -1;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<MODE>::bytes) != cudaSuccess)
+      return -1;
     const int most = sm_count() / 2;
     cfg.gridDim = dim3(unsigned(most > 0 ? most * 2 : 2));
     int active = 0;
@@ -568,7 +620,7 @@ int launch_mode(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& B
   if (pairs <= 0) return SDM_ECUDA;
   if (units < pairs) pairs = units;
   cfg.gridDim = dim3(unsigned(pairs * 2));
-  if (cudaLaunchKernelEx(&cfg, fn, A, B, B2, a) != cudaSuccess) return SDM_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, fn, tm, a) != cudaSuccess) return SDM_ECUDA;
   if (a.splits > 1) {
     const size_t n = size_t(a.rows) * a.cols;
     join_kernel<<<unsigned((n / 8 + 255) / 256), 256, 0, s>>>(a.partial, a.out, n, a.splits);
@@ -577,10 +629,9 @@ int launch_mode(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& B
 }
 
 template <int MODE>
-int launch_act(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& B2, const GatedArgs& a,
-               const Plan& p, cudaStream_t s) {
-  return a.act == SDM_ACT_SILU ? launch_mode<MODE, SDM_ACT_SILU>(A, B, B2, a, p, s)
-                               : launch_mode<MODE, SDM_ACT_GELU>(A, B, B2, a, p, s);
+int launch_act(const Maps& tm, const GatedArgs& a, const Plan& p, cudaStream_t s) {
+  return a.act == SDM_ACT_SILU ? launch_mode<MODE, SDM_ACT_SILU>(tm, a, p, s)
+                               : launch_mode<MODE, SDM_ACT_GELU>(tm, a, p, s);
 }
 
 int check_gated(const void* x, const void* w, long long M, int D, int F, int act) {
@@ -606,17 +657,17 @@ extern "C" int sdm_project_gated(const void* x, const void* w, long long M, int 
   if (M <= kFewTokens)
     return act == SDM_ACT_SILU ? launch_few<SDM_ACT_SILU>(x, w, int(M), D, F, h, as_stream(stream))
                                : launch_few<SDM_ACT_GELU>(x, w, int(M), D, F, h, as_stream(stream));
-  CUtensorMap tx, tg, tu;
-  if (!tile_map(&tx, x, int(M), D, kHalf) || !tile_map(&tg, w, F, D, kHalf) ||
-      !tile_map(&tu, static_cast<const __nv_bfloat16*>(w) + size_t(F) * D, F, D, kHalf))
+  Maps tm = {};
+  if (!bf16_tile_map(&tm.A, x, int(M), D, kHalf) || !bf16_tile_map(&tm.B, w, F, D, kHalf) ||
+      !bf16_tile_map(&tm.B2, static_cast<const __nv_bfloat16*>(w) + size_t(F) * D, F, D, kHalf) ||
+      !bf16_tile_map(&tm.out, h, int(M), F, 32))
     return SDM_ECUDA;
   GatedArgs a = {};
   a.rows = int(M);
   a.cols = a.F = F;
   a.act = act;
-  a.out = static_cast<__nv_bfloat16*>(h);
   a.dev_err = dev_err;
-  return launch_act<kForward>(tx, tg, tu, a, plan(kForward, int(M), D, F), as_stream(stream));
+  return launch_act<kForward>(tm, a, plan(kForward, int(M), D, F), as_stream(stream));
 }
 
 extern "C" size_t sdm_project_gated_backward_workspace_size(long long M, int D, int F) {
@@ -642,28 +693,28 @@ extern "C" int sdm_project_gated_backward(const void* x, const void* w, const vo
     return cudaMemsetAsync(dw, 0, size_t(2) * F * D * 2, s) == cudaSuccess ? SDM_OK : SDM_ECUDA;
   if (!aligned16(workspace)) return SDM_EALIGN;
   if (workspace_bytes < sdm_project_gated_backward_workspace_size(M, D, F)) return SDM_ENOSPACE;
-  __nv_bfloat16* slope = static_cast<__nv_bfloat16*>(workspace);
-  CUtensorMap tx, tg, tu, ts, tw, tst, txt;
-  if (!tile_map(&tx, x, int(M), D, kHalf) || !tile_map(&tg, w, F, D, kHalf) ||
-      !tile_map(&tu, static_cast<const __nv_bfloat16*>(w) + size_t(F) * D, F, D, kHalf) ||
-      !tile_map(&ts, slope, int(M), 2 * F, kHalf) || !tile_map(&tw, w, 2 * F, D, kTileK) ||
-      !tile_map(&tst, slope, int(M), 2 * F, kTileK) || !tile_map(&txt, x, int(M), D, kTileK))
+  __nv_bfloat16* slope = static_cast<__nv_bfloat16*>(workspace);  // [dg | du], [M, 2F]
+  Maps ts = {}, ti = {}, tw = {};
+  if (!bf16_tile_map(&ts.A, x, int(M), D, kHalf) || !bf16_tile_map(&ts.B, w, F, D, kHalf) ||
+      !bf16_tile_map(&ts.B2, static_cast<const __nv_bfloat16*>(w) + size_t(F) * D, F, D, kHalf) ||
+      !bf16_tile_map(&ts.dh, dh, int(M), F, 32) || !bf16_tile_map(&ts.out, slope, int(M), F, 32, 2LL * F) ||
+      !bf16_tile_map(&ts.out2, slope + F, int(M), F, 32, 2LL * F) ||
+      !bf16_tile_map(&ti.A, slope, int(M), 2 * F, kHalf) || !bf16_tile_map(&ti.B, w, 2 * F, D, kTileK) ||
+      !bf16_tile_map(&tw.A, slope, int(M), 2 * F, kTileK) || !bf16_tile_map(&tw.B, x, int(M), D, kTileK))
     return SDM_ECUDA;
   GatedArgs a = {};
   a.rows = int(M);
   a.cols = a.F = F;
   a.act = act;
-  a.out = slope;
-  a.dh = static_cast<const __nv_bfloat16*>(dh);
   a.dev_err = dev_err;
-  st = launch_act<kSlope>(tx, tg, tu, a, plan(kSlope, int(M), D, F), s);
+  st = launch_act<kSlope>(ts, a, plan(kSlope, int(M), D, F), s);
   if (st != SDM_OK) return st;
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + round256(size_t(M) * 2 * F * 2));
   a.cols = D;
   a.out = static_cast<__nv_bfloat16*>(dx);
-  st = launch_mode<kInput, 0>(ts, tw, tw, a, plan(kInput, int(M), D, F), s);
+  st = launch_mode<kInput, 0>(ti, a, plan(kInput, int(M), D, F), s);
   if (st != SDM_OK) return st;
   a.rows = 2 * F;
   a.out = static_cast<__nv_bfloat16*>(dw);
-  return launch_mode<kWeight, 0>(tst, txt, txt, a, plan(kWeight, int(M), D, F), s);
+  return launch_mode<kWeight, 0>(tw, a, plan(kWeight, int(M), D, F), s);
 }
