@@ -4,18 +4,19 @@
 //   dg = dh * u * act'(g),  du = dh * act(g)
 //   dx = dg Wg + du Wu = [dg | du] w,   dw = [dg | du]^T x
 //
-// Four products of one shape run on one kernel, a persistent pair of CTAs (cta_group::2) that
-// forms 256 x 256 tiles with fp32 accumulators in TMEM, double-buffered, TMA feeding a ring of
-// stages (the roles of the projection kernel in sdm_project.cu, with eight epilogue warps: with four,
-// kSlope's elementwise work was longer than its products):
+// The products run on one kernel, a persistent pair of CTAs (cta_group::2) that forms 256 x 256
+// tiles with fp32 accumulators in TMEM, double-buffered, TMA feeding a ring of stages (the roles of
+// the projection kernel in sdm_project.cu, with eight epilogue warps: with four, kSlope's
+// elementwise work was longer than its products):
 //   kForward   the pair's two halves of the column tile are 128 columns of Wg and the same 128 of
 //              Wu, so one thread of the epilogue holds g and u of an element and h leaves the chip
 //              once: neither g nor u is ever written.
 //   kSlope     the same product again in the backward pass (g and u were not kept: 4F bytes a token
 //              less to hold between the passes, for a third of the backward's flops); its epilogue
-//              reads dh and writes dg and du, rounded to bf16 for the two products that follow.
-//   kInput     dx = [dg | du] w: w's rows are the reduction here, so its tile is read MN-major.
-//   kWeight    dw = [dg | du]^T x: the tokens are the reduction, both operands MN-major.
+//              takes dh and leaves dg and du, rounded to bf16 for the two products that follow.
+//   kGrads     those two in one launch, so that their tiles share the card's last round:
+//              dx = [dg | du] w, where w's rows are the reduction and its tile is read MN-major, and
+//              dw = [dg | du]^T x, where the tokens are and both operands are MN-major.
 // No operand is transposed in memory: TMA boxes of 64 x 64 in the 128-byte swizzle serve as either
 // major, and only the descriptors differ.  Sums are fp32; dg and du are the only rounding between
 // inputs and outputs.
@@ -25,7 +26,8 @@
 namespace sdm {
 namespace {
 
-enum Mode { kForward = 0, kSlope = 1, kInput = 2, kWeight = 3 };
+enum Mode { kForward = 0, kSlope = 1, kGrads = 2 };
+enum Grads { kBoth = 0, kInput = 1, kWeight = 2 };  // what a kGrads launch computes
 
 constexpr int kHalf = 128;                       // rows (and columns) of a tile each CTA stages
 constexpr int kOperand = kHalf * kTileK * 2;     // 16 KB
@@ -47,13 +49,19 @@ struct Layout {
 constexpr uint32_t kColumns = 512;
 constexpr int kRowGroup = 32;                    // row tiles of a group of the tile order
 
-struct GatedArgs {
-  int rows, cols;       // of the output, in elements (kForward, kSlope: tokens and F)
+// One product: its output [rows, cols], its tiles, and the cut of its reduction (K steps of 64).
+struct Product {
+  int rows, cols;
   int row_tiles, col_tiles, splits;
-  int kblocks, per_split;  // K steps in all, and of each split
-  int F, act;
-  __nv_bfloat16* out;      // dx or dw
+  int kblocks, per_split;
+  bool a_mn;               // kGrads: A read MN-major (dw)
+  __nv_bfloat16* out;      // kGrads: dx or dw
   float* partial;          // [splits][rows][cols] where splits > 1
+  __host__ __device__ int units() const { return row_tiles * col_tiles * splits; }
+};
+struct GatedArgs {
+  Product p[2];            // kForward, kSlope: the first; kGrads: both, the one of longer units first
+  int act;
   int* dev_err;
 };
 
@@ -102,20 +110,29 @@ __device__ __forceinline__ void gate_slope(float g, float& a, float& s) {
   }
 }
 
-// Work unit -> row tile, column tile, split: groups of kRowGroup row tiles, row tiles fastest, so
-// that units running at once share a few rows of A and a few column tiles of B in L2.
+// Work unit -> product, row tile, column tile, split: groups of kRowGroup row tiles, row tiles
+// fastest, so that units running at once share a few rows of A and a few column tiles of B in L2.
 struct Unit {
-  int row, col, split;
+  int which, row, col, k_lo, k_hi, split;
 };
+template <int MODE, int KIND>
 __device__ __forceinline__ Unit unit_at(int u, const GatedArgs& a) {
-  const int tiles = a.row_tiles * a.col_tiles;
   Unit r;
+  r.which = 0;
+  if (MODE == kGrads && KIND == kBoth && u >= a.p[0].units()) {
+    u -= a.p[0].units();
+    r.which = 1;
+  }
+  const Product& p = a.p[r.which];
+  const int tiles = p.row_tiles * p.col_tiles;
   r.split = u / tiles;
   u -= r.split * tiles;
-  const int g = u / (kRowGroup * a.col_tiles), w = u - g * kRowGroup * a.col_tiles;
-  const int gm = min(kRowGroup, a.row_tiles - g * kRowGroup);
+  const int g = u / (kRowGroup * p.col_tiles), w = u - g * kRowGroup * p.col_tiles;
+  const int gm = min(kRowGroup, p.row_tiles - g * kRowGroup);
   r.col = w / gm;
   r.row = g * kRowGroup + (w - r.col * gm);
+  r.k_lo = r.split * p.per_split;
+  r.k_hi = min(p.kblocks, r.k_lo + p.per_split);
   return r;
 }
 
@@ -179,7 +196,7 @@ __device__ __forceinline__ void gate_patch(uint32_t tgate, uint32_t tup, uint32_
 }
 
 // dx or dw of a warp's 32 rows x 128 columns, straight to memory.
-__device__ __forceinline__ void store_sums(const GatedArgs& a, const Unit& un, int m, int n0, uint32_t taddr) {
+__device__ __forceinline__ void store_sums(const Product& a, const Unit& un, int m, int n0, uint32_t taddr) {
 #pragma unroll 1
   for (int c = 0; c < kHalf; c += 32) {
     uint32_t r[32];
@@ -203,21 +220,23 @@ __device__ __forceinline__ void store_sums(const GatedArgs& a, const Unit& un, i
   }
 }
 
-// Tensor maps of a launch: the operands (B2: the rank-1 CTA's, Wu), and what the epilogue moves in
-// patches: dh in; h, or dg and du, out.
+// Tensor maps of a launch: the operands of each product (kForward, kSlope: B[1] is the rank-1 CTA's,
+// Wu), and what the epilogue moves in patches: dh in; h, or dg and du, out.
 struct Maps {
-  CUtensorMap A, B, B2, dh, out, out2;
+  CUtensorMap A[2], B[2], dh, out, out2;
 };
 
+// KIND: the activation, or of kGrads the products (known where there is one, so that the one thread
+// that issues MMAs has nothing to choose: 2 % of the whole gradient).
 // Every wait is bounded; a wait that runs out stops both CTAs, which drain the copies and MMAs in
 // flight, free TMEM and report SDM_DEV_TIMEOUT.
-template <int MODE, int ACT>
+template <int MODE, int KIND>
 __global__ void __launch_bounds__(kRoles, 1)
     gated_kernel(const __grid_constant__ Maps tm, const __grid_constant__ GatedArgs a) {
   using Lay = Layout<MODE>;
   constexpr int kStages = Lay::stages;
   constexpr bool kGate = MODE == kForward || MODE == kSlope;
-  constexpr bool kAMN = MODE == kWeight, kBMN = MODE == kInput || MODE == kWeight;
+  constexpr bool kBMN = MODE == kGrads;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
@@ -234,7 +253,7 @@ __global__ void __launch_bounds__(kRoles, 1)
   const bool leader = rank == 0;
   const uint32_t peer_stop = cluster_addr(smem_u32(const_cast<int*>(stop)), rank ^ 1u);
   const int cid = blockIdx.x / 2, ncl = gridDim.x / 2;
-  const int units = a.row_tiles * a.col_tiles * a.splits;
+  const int units = a.p[0].units() + (MODE == kGrads && KIND == kBoth ? a.p[1].units() : 0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -250,8 +269,8 @@ __global__ void __launch_bounds__(kRoles, 1)
     *stop = 0;
     for (int s = 0; s < kStages; ++s) issued[s] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm.A)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm.B)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm.A[0])) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm.B[0])) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -265,20 +284,23 @@ __global__ void __launch_bounds__(kRoles, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  allow_next();
+  if (MODE == kGrads) wait_previous();  // kSlope's dg and du
 
   if (warp == 0) {
     if (lane == 0) {
       // ---- copies (both CTAs) ----
-      const CUtensorMap* mapB = kGate && rank ? &tm.B2 : &tm.B;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int u = cid; ok && u < units; u += ncl) {
-        const Unit un = unit_at(u, a);
+        const Unit un = unit_at<MODE, KIND>(u, a);
+        const CUtensorMap* mapA = &tm.A[un.which];
+        const CUtensorMap* mapB = &tm.B[kGate ? int(rank) : un.which];
+        const bool a_mn = MODE == kGrads && (KIND == kBoth ? a.p[un.which].a_mn : KIND == kWeight);
         const int m0 = (un.row * 2 + int(rank)) * kHalf;
         const int n0 = kBMN ? un.col * 2 * kHalf + int(rank) * kHalf : un.col * kHalf;
-        const int k_lo = un.split * a.per_split, k_hi = min(a.kblocks, k_lo + a.per_split);
-        for (int kb = k_lo; kb < k_hi; ++kb) {
+        for (int kb = un.k_lo; kb < un.k_hi; ++kb) {
           if (!mbar_wait_cluster(bar(EMPTY + stage), phase ^ 1u, stop, peer_stop, kWaitNs)) {
             ok = false;
             break;
@@ -286,11 +308,11 @@ __global__ void __launch_bounds__(kRoles, 1)
           const uint32_t sa = ring + uint32_t(stage) * kStage, sb = sa + kOperand;
           const uint32_t full = cluster_addr(bar(FULL + stage), 0);
           if (leader) mbar_expect_tx(bar(FULL + stage), 2 * kStage);
-          if (kAMN) {
-            tma_load_2d_pair(sa, &tm.A, m0, kb * kTileK, full);
-            tma_load_2d_pair(sa + kOperand / 2, &tm.A, m0 + kHalf / 2, kb * kTileK, full);
+          if (a_mn) {
+            tma_load_2d_pair(sa, mapA, m0, kb * kTileK, full);
+            tma_load_2d_pair(sa + kOperand / 2, mapA, m0 + kHalf / 2, kb * kTileK, full);
           } else {
-            tma_load_2d_pair(sa, &tm.A, kb * kTileK, m0, full);
+            tma_load_2d_pair(sa, mapA, kb * kTileK, m0, full);
           }
           if (kBMN) {
             tma_load_2d_pair(sb, mapB, n0, kb * kTileK, full);
@@ -309,20 +331,20 @@ __global__ void __launch_bounds__(kRoles, 1)
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ---- MMAs (leader only) ----
-      constexpr uint32_t id = idesc(kAMN, kBMN);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       int it = 0;
       for (int u = cid; ok && u < units; u += ncl, ++it) {
-        const Unit un = unit_at(u, a);
-        const int k_lo = un.split * a.per_split, k_hi = min(a.kblocks, k_lo + a.per_split);
+        const Unit un = unit_at<MODE, KIND>(u, a);
+        const bool a_mn = MODE == kGrads && (KIND == kBoth ? a.p[un.which].a_mn : KIND == kWeight);
+        const uint32_t id = a_mn ? idesc(true, kBMN) : idesc(false, kBMN);
         const int acc = it & 1;
         const uint32_t acc_par = uint32_t(it >> 1) & 1u;
         if (!mbar_wait_cluster(bar(ACC_EMPTY + acc), acc_par ^ 1u, stop, peer_stop, kWaitNs)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + uint32_t(acc * 256);
-        for (int kb = k_lo; kb < k_hi; ++kb) {
+        for (int kb = un.k_lo; kb < un.k_hi; ++kb) {
           if (!mbar_wait_cluster(bar(FULL + stage), phase, stop, peer_stop, kWaitNs)) {
             ok = false;
             break;
@@ -331,8 +353,8 @@ __global__ void __launch_bounds__(kRoles, 1)
           const uint32_t sa = ring + uint32_t(stage) * kStage, sb = sa + kOperand;
 #pragma unroll
           for (int kk = 0; kk < kTileK / 16; ++kk)
-            mma2(d, kAMN ? mn_desc(sa + kk * 2048) : sw128_desc(sa + kk * 32),
-                 kBMN ? mn_desc(sb + kk * 2048) : sw128_desc(sb + kk * 32), kb > k_lo || kk > 0, id);
+            mma2(d, a_mn ? mn_desc(sa + kk * 2048) : sw128_desc(sa + kk * 32),
+                 kBMN ? mn_desc(sb + kk * 2048) : sw128_desc(sb + kk * 32), kb > un.k_lo || kk > 0, id);
           mma2_commit_both(bar(EMPTY + stage));
           if (++stage == kStages) {
             stage = 0;
@@ -355,11 +377,11 @@ __global__ void __launch_bounds__(kRoles, 1)
     for (int u = cid; u < units; u += ncl, ++it) {
       const int acc = it & 1;
       const uint32_t acc_par = uint32_t(it >> 1) & 1u;
-      const Unit un = unit_at(u, a);
+      const Unit un = unit_at<MODE, KIND>(u, a);
       const int m0 = (un.row * 2 + int(rank)) * kHalf + quad * 32;
       const int f0 = un.col * kHalf + half * 64;
       // A patch outside the matrix is neither loaded nor stored; one across its edge is cut there.
-      const bool inside = kGate && m0 < a.rows && f0 < a.F;
+      const bool inside = kGate && m0 < a.p[0].rows && f0 < a.p[0].cols;
       if (kGate && lane == 0) copies_out_read();  // the patches' last copies have read them
       if (MODE == kSlope && inside) {
         if (lane == 0) {
@@ -381,11 +403,11 @@ __global__ void __launch_bounds__(kRoles, 1)
               break;
             ++patch_waits;
           }
-          gate_patch<MODE, ACT>(taddr + uint32_t(half * 64), taddr + uint32_t(kHalf + half * 64), patch, lane);
+          gate_patch<MODE, KIND>(taddr + uint32_t(half * 64), taddr + uint32_t(kHalf + half * 64), patch, lane);
           fence_async_proxy();
         }
       } else {
-        store_sums(a, un, m0 + lane, un.col * 2 * kHalf + half * kHalf, taddr + uint32_t(half * kHalf));
+        store_sums(a.p[un.which], un, m0 + lane, un.col * 2 * kHalf + half * kHalf, taddr + uint32_t(half * kHalf));
       }
       tc_fence_before();
       __syncwarp();
@@ -435,21 +457,24 @@ __global__ void __launch_bounds__(kRoles, 1)
   cluster_sync_all();  // the peer's shared memory outlives the leader's drain
 }
 
-// Sums the splits' partial results in their order and rounds once.
-__global__ void __launch_bounds__(256) join_kernel(const float* partial, __nv_bfloat16* out,
-                                                   size_t n, int splits) {
-  const size_t i = (size_t(blockIdx.x) * 256 + threadIdx.x) * 8;
+// Sums the splits' partial results of the products that have any, in their order, and rounds once.
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ GatedArgs a, unsigned first_blocks) {
+  wait_previous();
+  const Product& p = a.p[blockIdx.x >= first_blocks];
+  const unsigned block = blockIdx.x >= first_blocks ? blockIdx.x - first_blocks : blockIdx.x;
+  const size_t n = size_t(p.rows) * p.cols, i = (size_t(block) * 256 + threadIdx.x) * 8;
   if (i >= n) return;
   float o[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) o[j] = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    const float4* p = reinterpret_cast<const float4*>(partial + size_t(s) * n + i);
-    const float4 v = __ldcs(p), w = __ldcs(p + 1);
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const float4* q = reinterpret_cast<const float4*>(p.partial + size_t(s) * n + i);
+    const float4 v = __ldcs(q), w = __ldcs(q + 1);
     o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
     o[4] += w.x, o[5] += w.y, o[6] += w.z, o[7] += w.w;
   }
-  *reinterpret_cast<uint4*>(out + i) = Piece<__nv_bfloat16>::pack(o);
+  *reinterpret_cast<uint4*>(p.out + i) = Piece<__nv_bfloat16>::pack(o);
 }
 
 // ---- few tokens ----
@@ -551,55 +576,81 @@ int launch_few(const void* x, const void* w, int M, int D, int F, void* h, cudaS
 
 int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
 
-// Splits of the reduction (K steps of 64) so that the 76 pairs of SMs are busy: the number s of
-// least time where a unit takes its K steps and about 8 more for its start and its epilogue, and
-// joining moves the partials twice (a K step is 512 clocks of a pair; HBM moves about 2 MB in it).
-int splits_for(long long tiles, int kblocks, double out_elems) {
-  int best = 1;
-  double least = 0;
-  for (int s = 1; s <= 16 && s <= kblocks; ++s) {
-    const int per = ceil_div(kblocks, s);
-    if (ceil_div(kblocks, per) != s) continue;
-    const double t = double(ceil_div(tiles * s, 76)) * (per + 8) +
-                     (s > 1 ? out_elems * (8.0 * s + 2.0) / 1.8e6 + 10 : 0);
-    if (s == 1 || t < least) {
-      best = s;
-      least = t;
-    }
-  }
-  return best;
-}
+constexpr int kPairs = 76;  // pairs of SMs
 
-struct Plan {
-  int row_tiles, col_tiles, splits, kblocks;
-};
-Plan plan(int mode, int M, int D, int F) {
-  Plan p;
-  const int rows = mode == kWeight ? 2 * F : M;
+Product product(int rows, int cols, int tile_cols, long long reduction) {
+  Product p = {};
+  p.rows = rows;
+  p.cols = cols;
   p.row_tiles = ceil_div(rows, 2 * kHalf);
-  p.col_tiles = mode == kForward || mode == kSlope ? ceil_div(F, kHalf) : ceil_div(D, 2 * kHalf);
-  p.kblocks = ceil_div(mode == kInput ? 2LL * F : mode == kWeight ? M : D, kTileK);
-  p.splits = mode == kForward || mode == kSlope
-                 ? 1
-                 : splits_for((long long)p.row_tiles * p.col_tiles, p.kblocks, double(rows) * D);
+  p.col_tiles = ceil_div(cols, tile_cols);
+  p.kblocks = p.per_split = ceil_div(reduction, kTileK);
+  p.splits = 1;
   return p;
 }
 
-template <int MODE, int ACT>
-int launch_mode(const Maps& tm, GatedArgs a, const Plan& p, cudaStream_t s) {
-  a.row_tiles = p.row_tiles;
-  a.col_tiles = p.col_tiles;
-  a.splits = p.splits;
-  a.kblocks = p.kblocks;
-  a.per_split = ceil_div(p.kblocks, p.splits);
-  const long long units = (long long)p.row_tiles * p.col_tiles * p.splits;
+void cut(Product& p, int splits) {
+  p.per_split = ceil_div(p.kblocks, splits);
+  p.splits = ceil_div(p.kblocks, p.per_split);  // none of them empty
+}
+
+// K steps of the busiest pair, the first, where units are dealt out in turn, those of product a (the
+// longer) before those of b.  A unit costs about 8 steps more for its start and its epilogue.
+double busiest(const Product& a, const Product& b) {
+  const long long na = a.units(), nb = b.units();
+  const double ra = double((na + kPairs - 1) / kPairs);
+  const long long left = na + nb - (long long)ra * kPairs;
+  return ra * (a.per_split + 8) + (left > 0 ? double((left + kPairs - 1) / kPairs) * (b.per_split + 8) : 0.0);
+}
+// Moving a product's partials twice, and a launch, in K steps (512 clocks of a pair; HBM moves about
+// 1.8 MB in one).
+double joining(const Product& p) {
+  return p.splits > 1 ? double(p.rows) * p.cols * (8.0 * p.splits + 2.0) / 1.8e6 + 5 : 0.0;
+}
+
+// With eight rounds of tiles or more the last one's loss is small: neither are reductions split then,
+// nor are the products put in one launch.
+bool one_launch(const Product (&p)[2]) {
+  return (long long)p[0].row_tiles * p[0].col_tiles + (long long)p[1].row_tiles * p[1].col_tiles < 8 * kPairs;
+}
+
+// The two products of the gradient, dx and dw, the one of longer units first.  With few tiles
+// their reductions are split so that every pair of SMs has its share: the cut of least time among
+// up to 8 splits of each.
+void plan_grads(int M, int D, int F, Product (&p)[2]) {
+  Product x = product(M, D, 2 * kHalf, 2LL * F), w = product(2 * F, D, 2 * kHalf, M);
+  w.a_mn = true;
+  Product best[2] = {x, w};
+  double least = -1;
+  const int most = one_launch(best) ? 8 : 1;
+  for (int i = 1; i <= most; ++i)
+    for (int j = 1; j <= most; ++j) {
+      cut(x, i);
+      cut(w, j);
+      const bool swap = w.per_split > x.per_split;
+      const double t = (swap ? busiest(w, x) : busiest(x, w)) + joining(x) + joining(w);
+      if (least < 0 || t < least) {
+        least = t;
+        best[0] = swap ? w : x;
+        best[1] = swap ? x : w;
+      }
+    }
+  p[0] = best[0];
+  p[1] = best[1];
+}
+
+template <int MODE, int KIND>
+int launch_mode(const Maps& tm, const GatedArgs& a, cudaStream_t s) {
+  const long long units = (long long)a.p[0].row_tiles * a.p[0].col_tiles * a.p[0].splits +
+                          (MODE == kGrads && KIND == kBoth ? (long long)a.p[1].row_tiles * a.p[1].col_tiles * a.p[1].splits : 0);
   if (units > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
-  auto fn = gated_kernel<MODE, ACT>;
-  cudaLaunchAttribute attr[1];
+  auto fn = gated_kernel<MODE, KIND>;
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1] = after_previous();
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kRoles);
   cfg.dynamicSmemBytes = Layout<MODE>::bytes;
@@ -620,18 +671,31 @@ int launch_mode(const Maps& tm, GatedArgs a, const Plan& p, cudaStream_t s) {
   if (pairs <= 0) return SDM_ECUDA;
   if (units < pairs) pairs = units;
   cfg.gridDim = dim3(unsigned(pairs * 2));
+  if (MODE == kGrads) cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, fn, tm, a) != cudaSuccess) return SDM_ECUDA;
-  if (a.splits > 1) {
-    const size_t n = size_t(a.rows) * a.cols;
-    join_kernel<<<unsigned((n / 8 + 255) / 256), 256, 0, s>>>(a.partial, a.out, n, a.splits);
-  }
+  return last_launch_status();
+}
+
+int launch_join(const GatedArgs& a, cudaStream_t s) {
+  unsigned blocks[2];
+  for (int i = 0; i < 2; ++i)
+    blocks[i] = a.p[i].splits > 1 ? unsigned((size_t(a.p[i].rows) * a.p[i].cols / 8 + 255) / 256) : 0;
+  if (blocks[0] + blocks[1] == 0) return SDM_OK;
+  cudaLaunchAttribute attr[1] = {after_previous()};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks[0] + blocks[1]);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, join_kernel, a, blocks[0]) != cudaSuccess) return SDM_ECUDA;
   return last_launch_status();
 }
 
 template <int MODE>
-int launch_act(const Maps& tm, const GatedArgs& a, const Plan& p, cudaStream_t s) {
-  return a.act == SDM_ACT_SILU ? launch_mode<MODE, SDM_ACT_SILU>(tm, a, p, s)
-                               : launch_mode<MODE, SDM_ACT_GELU>(tm, a, p, s);
+int launch_act(const Maps& tm, const GatedArgs& a, cudaStream_t s) {
+  return a.act == SDM_ACT_SILU ? launch_mode<MODE, SDM_ACT_SILU>(tm, a, s)
+                               : launch_mode<MODE, SDM_ACT_GELU>(tm, a, s);
 }
 
 int check_gated(const void* x, const void* w, long long M, int D, int F, int act) {
@@ -642,6 +706,9 @@ int check_gated(const void* x, const void* w, long long M, int D, int F, int act
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+size_t partial_bytes(const Product& p) {
+  return p.splits > 1 ? round256(size_t(p.splits) * p.rows * p.cols * 4) : 0;
+}
 
 }  // namespace
 }  // namespace sdm
@@ -658,28 +725,22 @@ extern "C" int sdm_project_gated(const void* x, const void* w, long long M, int 
     return act == SDM_ACT_SILU ? launch_few<SDM_ACT_SILU>(x, w, int(M), D, F, h, as_stream(stream))
                                : launch_few<SDM_ACT_GELU>(x, w, int(M), D, F, h, as_stream(stream));
   Maps tm = {};
-  if (!bf16_tile_map(&tm.A, x, int(M), D, kHalf) || !bf16_tile_map(&tm.B, w, F, D, kHalf) ||
-      !bf16_tile_map(&tm.B2, static_cast<const __nv_bfloat16*>(w) + size_t(F) * D, F, D, kHalf) ||
+  if (!bf16_tile_map(&tm.A[0], x, int(M), D, kHalf) || !bf16_tile_map(&tm.B[0], w, F, D, kHalf) ||
+      !bf16_tile_map(&tm.B[1], static_cast<const __nv_bfloat16*>(w) + size_t(F) * D, F, D, kHalf) ||
       !bf16_tile_map(&tm.out, h, int(M), F, 32))
     return SDM_ECUDA;
   GatedArgs a = {};
-  a.rows = int(M);
-  a.cols = a.F = F;
+  a.p[0] = product(int(M), F, kHalf, D);
   a.act = act;
   a.dev_err = dev_err;
-  return launch_act<kForward>(tm, a, plan(kForward, int(M), D, F), as_stream(stream));
+  return launch_act<kForward>(tm, a, as_stream(stream));
 }
 
 extern "C" size_t sdm_project_gated_backward_workspace_size(long long M, int D, int F) {
   if (M < 1 || D < 1 || F < 1 || M > 0x7FFFFFFFLL - 256) return 0;
-  const Plan pi = plan(kInput, int(M), D, F), pw = plan(kWeight, int(M), D, F);
-  size_t part = 0;
-  if (pi.splits > 1) part = size_t(pi.splits) * M * D * 4;
-  if (pw.splits > 1) {
-    const size_t n = size_t(pw.splits) * 2 * F * D * 4;
-    part = n > part ? n : part;
-  }
-  return round256(size_t(M) * 2 * F * 2) + part;
+  Product p[2];
+  plan_grads(int(M), D, F, p);
+  return round256(size_t(M) * 2 * F * 2) + partial_bytes(p[0]) + partial_bytes(p[1]);
 }
 
 extern "C" int sdm_project_gated_backward(const void* x, const void* w, const void* dh, long long M,
@@ -694,27 +755,44 @@ extern "C" int sdm_project_gated_backward(const void* x, const void* w, const vo
   if (!aligned16(workspace)) return SDM_EALIGN;
   if (workspace_bytes < sdm_project_gated_backward_workspace_size(M, D, F)) return SDM_ENOSPACE;
   __nv_bfloat16* slope = static_cast<__nv_bfloat16*>(workspace);  // [dg | du], [M, 2F]
-  Maps ts = {}, ti = {}, tw = {};
-  if (!bf16_tile_map(&ts.A, x, int(M), D, kHalf) || !bf16_tile_map(&ts.B, w, F, D, kHalf) ||
-      !bf16_tile_map(&ts.B2, static_cast<const __nv_bfloat16*>(w) + size_t(F) * D, F, D, kHalf) ||
+  Maps ts = {}, tg = {};
+  GatedArgs a = {};
+  plan_grads(int(M), D, F, a.p);
+  const int ix = a.p[0].a_mn ? 1 : 0, iw = 1 - ix;  // dx's place, dw's
+  if (!bf16_tile_map(&ts.A[0], x, int(M), D, kHalf) || !bf16_tile_map(&ts.B[0], w, F, D, kHalf) ||
+      !bf16_tile_map(&ts.B[1], static_cast<const __nv_bfloat16*>(w) + size_t(F) * D, F, D, kHalf) ||
       !bf16_tile_map(&ts.dh, dh, int(M), F, 32) || !bf16_tile_map(&ts.out, slope, int(M), F, 32, 2LL * F) ||
       !bf16_tile_map(&ts.out2, slope + F, int(M), F, 32, 2LL * F) ||
-      !bf16_tile_map(&ti.A, slope, int(M), 2 * F, kHalf) || !bf16_tile_map(&ti.B, w, 2 * F, D, kTileK) ||
-      !bf16_tile_map(&tw.A, slope, int(M), 2 * F, kTileK) || !bf16_tile_map(&tw.B, x, int(M), D, kTileK))
+      !bf16_tile_map(&tg.A[ix], slope, int(M), 2 * F, kHalf) || !bf16_tile_map(&tg.B[ix], w, 2 * F, D, kTileK) ||
+      !bf16_tile_map(&tg.A[iw], slope, int(M), 2 * F, kTileK) || !bf16_tile_map(&tg.B[iw], x, int(M), D, kTileK))
     return SDM_ECUDA;
-  GatedArgs a = {};
-  a.rows = int(M);
-  a.cols = a.F = F;
-  a.act = act;
-  a.dev_err = dev_err;
-  st = launch_act<kSlope>(ts, a, plan(kSlope, int(M), D, F), s);
+  GatedArgs as = {};
+  as.p[0] = product(int(M), F, kHalf, D);
+  as.act = act;
+  as.dev_err = a.dev_err = dev_err;
+  st = launch_act<kSlope>(ts, as, s);
   if (st != SDM_OK) return st;
-  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + round256(size_t(M) * 2 * F * 2));
-  a.cols = D;
-  a.out = static_cast<__nv_bfloat16*>(dx);
-  st = launch_mode<kInput, 0>(ti, a, plan(kInput, int(M), D, F), s);
-  if (st != SDM_OK) return st;
-  a.rows = 2 * F;
-  a.out = static_cast<__nv_bfloat16*>(dw);
-  return launch_mode<kWeight, 0>(tw, a, plan(kWeight, int(M), D, F), s);
+  uint8_t* partial = static_cast<uint8_t*>(workspace) + round256(size_t(M) * 2 * F * 2);
+  a.p[0].partial = reinterpret_cast<float*>(partial);
+  a.p[1].partial = reinterpret_cast<float*>(partial + partial_bytes(a.p[0]));
+  a.p[ix].out = static_cast<__nv_bfloat16*>(dx);
+  a.p[iw].out = static_cast<__nv_bfloat16*>(dw);
+  if (!one_launch(a.p)) {
+    auto alone = [&](int i, GatedArgs& one, Maps& maps) {
+      one = a;
+      one.p[0] = a.p[i];
+      maps = tg;
+      maps.A[0] = tg.A[i];
+      maps.B[0] = tg.B[i];
+    };
+    GatedArgs one;
+    Maps maps;
+    alone(ix, one, maps);
+    st = launch_mode<kGrads, kInput>(maps, one, s);
+    if (st != SDM_OK) return st;
+    alone(iw, one, maps);
+    return launch_mode<kGrads, kWeight>(maps, one, s);
+  }
+  st = launch_mode<kGrads, kBoth>(tg, a, s);
+  return st != SDM_OK ? st : launch_join(a, s);
 }

@@ -41,6 +41,21 @@ struct PerDevice {
   }
 };
 
+// A kernel that follows another of the same call may be launched with after_previous(): its blocks
+// then start while the last ones of the kernel before it finish, and wait_previous() in the kernel
+// (before it touches what that one wrote or reads) waits until it has.  allow_next() in the earlier
+// kernel lets that happen as soon as all of its blocks have begun.
+inline cudaLaunchAttribute after_previous() {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 inline bool bad_dtype(int dt) { return dt != SDM_F32 && dt != SDM_BF16; }

@@ -22,6 +22,7 @@ constexpr int kThreads = 128;
 constexpr int kLaneStates = 8;  // states a lane holds of each of its channels, at most
 constexpr int kTokenThreads = 128;
 constexpr int kTT = 16;       // tokens of a shared-memory tile
+constexpr int kMinChunk = 48; // tokens of a chunk, at least
 constexpr int kSteps = 4;     // tokens taken together by a lane
 
 struct ScanArgs {
@@ -82,6 +83,8 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
   using S = Tile<T, L, kS>;
   constexpr int V = S::V;
   extern __shared__ __align__(16) uint8_t smem[];
+  if (PASS == kReduce) allow_next();
+  if (PASS == kJoin) wait_previous();
   const sdm_ssm_args& io = a.io;
   const int tid = threadIdx.x;
 
@@ -259,17 +262,27 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
   }
   if (PASS == kJoin && slot >= 0) {
     const size_t per = size_t(io.B) * io.Dm;
-    for (int q = 0; q < chunk; ++q) {
+    // Two chunks at a time: what they bring does not depend on the state, so it is asked for together.
+    for (int q0 = 0; q0 < chunk; q0 += 2) {
+      float sum[2][2], end[2][2][kS];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int c = ch + k;
-        if (c >= nch) continue;
-        const float s = a.ws_d[q * per + bd + c];
-        const float* e = a.ws_h + ((q + 1) * per + bd + c) * io.N + sub * kS;
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < kS; ++j)
-          h[k][j] = fmaf(exp2_fast(s * A[k][j]), h[k][j], sub * kS + j < io.N ? e[j] : 0.f);
-      }
+        for (int k = 0; k < 2; ++k) {
+          const int c = ch + k, q = q0 + i;
+          const bool in = c < nch && q < chunk;
+          sum[i][k] = in ? a.ws_d[q * per + bd + c] : 0.f;  // a chunk of none: decay 1, nothing added
+          const float* e = a.ws_h + ((q + 1) * per + bd + c) * io.N + sub * kS;
+#pragma unroll
+          for (int j = 0; j < kS; ++j) end[i][k][j] = in && sub * kS + j < io.N ? e[j] : 0.f;
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int j = 0; j < kS; ++j)
+            h[k][j] = fmaf(exp2_fast(sum[i][k] * A[k][j]), h[k][j], end[i][k][j]);
     }
   }
 
@@ -565,7 +578,15 @@ int launch_pass(const ScanArgs& a, int chunks, cudaStream_t s) {
     return SDM_ECUDA;
   const long long blocks = (long long)a.tiles_g * a.io.G * a.io.B * chunks;
   if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
-  fn<<<unsigned(blocks), kThreads, bytes, s>>>(a);
+  cudaLaunchAttribute attr[1] = {after_previous()};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = PASS == kJoin ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, fn, a) != cudaSuccess) return SDM_ECUDA;
   return last_launch_status();
 }
 
@@ -617,12 +638,14 @@ int launch_token(ScanArgs& a, cudaStream_t s) {
 }
 
 // Chunks of a sequence and tokens of a chunk: one chunk where the channels alone give the card
-// enough blocks, else as many as bring it there, of 128 tokens at least.
+// enough blocks, else as many as bring it there, of kMinChunk tokens at least (shorter ones cost
+// more in joining them than they save: 512 tokens of 2048 channels take 35 us in chunks of 64, 40 in
+// chunks of 32, 50 in chunks of 128).
 void cut(int B, int T, int Dm, int N, int G, int* chunks, int* chunk) {
   const int L = lanes_for(N, kLaneStates), CH = 2 * kThreads / L;
   const long long blocks = (long long)B * G * ((Dm / G + CH - 1) / CH);
   long long n = blocks >= 304 ? 1 : (608 + blocks - 1) / blocks;
-  n = n < T / 128 ? n : T / 128;
+  n = n < T / kMinChunk ? n : T / kMinChunk;
   if (n < 1) n = 1;
   const int per = int(((T + n - 1) / n + kTT - 1) / kTT) * kTT;
   *chunk = per;
