@@ -88,13 +88,29 @@ __device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_
       : "memory");
 }
 
-// g Phi(g), the exact gelu.
-__device__ __forceinline__ float gelu_cdf(float g) {
-  return 0.5f * erfcf(-0.70710678118654752f * g);
+// Phi(g) of the exact gelu, g Phi(g), and e = exp(-g^2 / 2), which its slope needs too:
+// Phi(-|g|) = erfc(x) / 2 with x = |g| / sqrt(2) = e t p(t) / 2, t = 1 / (1 + 0.4 x), where p is the
+// polynomial of degree 8 nearest to erfc(x) exp(x^2) / t on 0 < t <= 1 in relative error (1.3e-7;
+// 5e-7 with its roundings), by weighted least squares on Chebyshev points, the weights moved until the
+// error was level.  The tail keeps its relative precision, and erfc and exp share an exponential.
+__device__ __forceinline__ float gelu_cdf(float g, float& e) {
+  e = exp2_fast(-0.5f * kLog2e * g * g);
+  const float t = rcp_fast(fmaf(fabsf(g), 0.4f * 0.70710678118654752f, 1.0f));
+  float p = fmaf(t, 0.05026422068476677f, -0.18291062116622925f);
+  p = fmaf(t, p, 0.16910173f);
+  p = fmaf(t, p, -0.005622821860015392f);
+  p = fmaf(t, p, 0.1414395123720169f);
+  p = fmaf(t, p, 0.16853958368301392f);
+  p = fmaf(t, p, 0.20784306526184082f);
+  p = fmaf(t, p, 0.22566957771778107f);
+  p = fmaf(t, p, 0.22567586600780487f);
+  const float q = 0.5f * e * (t * p);
+  return g > 0.0f ? 1.0f - q : q;
 }
 template <int ACT>
 __device__ __forceinline__ float gate(float g) {
-  return ACT == SDM_ACT_SILU ? silu(g) : g * gelu_cdf(g);
+  float e;
+  return ACT == SDM_ACT_SILU ? silu(g) : g * gelu_cdf(g, e);
 }
 // act(g) and act'(g).
 template <int ACT>
@@ -104,9 +120,10 @@ __device__ __forceinline__ void gate_slope(float g, float& a, float& s) {
     a = g * p;
     s = fmaf(a, 1.0f - p, p);
   } else {
-    const float p = gelu_cdf(g);
+    float e;
+    const float p = gelu_cdf(g, e);
     a = g * p;
-    s = fmaf(g * 0.39894228040143268f, exp2_fast(-0.5f * kLog2e * g * g), p);
+    s = fmaf(g * 0.39894228040143268f, e, p);
   }
 }
 
