@@ -1,0 +1,120 @@
+"""Host checks of the convolution, scan and gated entry points: bad arguments are refused before anything is
+launched, and calls with nothing to do return at once.  No GPU needed."""
+import ctypes
+import struct
+
+import pytest
+import torch
+
+import sparse_state_linear_sdm_gb300 as sdm
+from sparse_state_linear_sdm_gb300 import layers
+
+OK, EINVAL, EALIGN, EUNSUPPORTED, ENOSPACE = 0, -1, -2, -6, -7
+FAKE, ODD = 0x10000, 0x10001  # never dereferenced on these paths
+F32, BF16 = 0, 1
+
+
+def conv(x=FAKE, bs=64, ts=16, dt=BF16, w=FAKE, bias=FAKE, wdt=BF16, B=2, T=4, D=16, K=4, act=1, state=FAKE,
+         out=FAKE, rows=2, lengths=None, slots=None, y=FAKE, err=None):
+    return layers._fn("sdm_causal_conv")(x, bs, ts, dt, w, bias, wdt, B, T, D, K, act, state, out, rows, lengths,
+                                         slots, y, err, None)
+
+
+def test_conv_refusals():
+    assert conv(B=0) == EINVAL
+    assert conv(T=-1) == EINVAL
+    assert conv(D=0) == EINVAL
+    assert conv(K=1) == EINVAL
+    assert conv(dt=3) == EINVAL
+    assert conv(wdt=-1) == EINVAL
+    assert conv(act=2) == EINVAL
+    assert conv(K=9) == EUNSUPPORTED
+    assert conv(B=1 << 20, T=1 << 12, rows=1 << 20) == EUNSUPPORTED
+    assert conv(rows=1) == EINVAL                       # two sequences, one row, no slots
+    assert conv(slots=FAKE, rows=0) == EINVAL
+    assert conv(x=ODD) == EALIGN
+    assert conv(y=None) == EALIGN
+    assert conv(w=None) == EALIGN
+    assert conv(state=ODD) == EALIGN
+    assert conv(dt=F32, x=0x10002) == EALIGN
+    assert conv(lengths=0x10002) == EALIGN
+    assert conv(T=0) == OK                              # in place and no token: nothing to do
+    assert conv(T=0, out=None, x=None, y=None) == OK
+
+
+SCAN = dict(x=FAKE, dt=FAKE, Bm=FAKE, Cm=FAKE, z=FAKE, x_bs=64, x_ts=16, dt_bs=64, dt_ts=16, B_bs=32, B_ts=8, C_bs=32,
+            C_ts=8, z_bs=64, z_ts=16, A=FAKE, D=FAKE, dt_bias=FAKE, state=FAKE, state_out=FAKE, lengths=0, slots=0,
+            y=FAKE, dtype=BF16, B=2, T=4, Dm=16, N=8, G=1, softplus=1, n_slots=2)
+
+
+def scan(ws=0, ws_bytes=0, err=None, **kw):
+    args = layers._scan_args(*{**SCAN, **kw}.values())
+    return layers._fn("sdm_selective_scan")(args, ws, ws_bytes, err, None)
+
+
+def test_scan_arguments_are_laid_out_as_the_header_says():
+    assert struct.calcsize("@5P10q8P8i") == 5 * 8 + 10 * 8 + 8 * 8 + 8 * 4
+    assert layers._fn("sdm_selective_scan")(None, 0, 0, None, None) == EINVAL
+
+
+def test_scan_refusals():
+    assert scan(B=0) == EINVAL
+    assert scan(T=-1) == EINVAL
+    assert scan(N=0) == EINVAL
+    assert scan(G=3) == EINVAL                          # 16 channels in 3 groups
+    assert scan(dtype=2) == EINVAL
+    assert scan(N=129) == EUNSUPPORTED
+    assert scan(B=1 << 16, T=1 << 16, n_slots=1 << 16) == EUNSUPPORTED
+    assert scan(n_slots=1) == EINVAL
+    assert scan(slots=FAKE, n_slots=0) == EINVAL
+    assert scan(A=0) == EALIGN
+    assert scan(x=0) == EALIGN
+    assert scan(z=ODD) == EALIGN
+    assert scan(state=0x10002) == EALIGN
+    assert scan(dtype=F32, Bm=0x10002) == EALIGN
+    assert scan(y=0) == EALIGN
+    assert scan(T=0) == OK
+    need = sdm.selective_scan_workspace_size(1, 4096, 64, 16)
+    long = dict(B=1, T=4096, Dm=64, N=16, n_slots=1)
+    assert need > 0
+    assert scan(**long) == EALIGN                       # a workspace is needed
+    assert scan(ws=FAKE, ws_bytes=need - 1, **long) == ENOSPACE
+    assert scan(ws=0x10008, ws_bytes=need, **long) == EALIGN
+
+
+def test_scan_workspace_sizes():
+    size = sdm.selective_scan_workspace_size
+    assert size(1, 1, 64, 16) == 0 and size(1, 40, 64, 16) == 0          # too short to cut
+    assert size(16, 4096, 8192, 16) == 0                                 # channels enough
+    assert size(0, 4096, 64, 16) == 0 and size(1, 4096, 63, 16, 2) == 0  # no such sizes
+    assert size(1, 1 << 20, 8192, 128) % 4 == 0
+
+
+def test_gated_refusals():
+    f = layers._fn("sdm_project_gated")
+    call = lambda x=FAKE, w=FAKE, M=8, D=64, F=64, act=1, h=FAKE: f(x, w, M, D, F, act, h, None, None)  # noqa: E731
+    assert call(M=-1) == EINVAL and call(D=0) == EINVAL and call(F=0) == EINVAL
+    assert call(act=0) == EINVAL and call(act=3) == EINVAL
+    assert call(D=60) == EUNSUPPORTED and call(F=68) == EUNSUPPORTED
+    assert call(M=1 << 31) == EUNSUPPORTED
+    assert call(x=0x10008) == EALIGN and call(w=None) == EALIGN and call(h=None) == EALIGN
+    assert call(M=0, x=None, h=None) == OK
+    b = layers._fn("sdm_project_gated_backward")
+    need = sdm.project_gated_backward_workspace_size(8, 64, 64)
+    grad = lambda dh=FAKE, dx=FAKE, dw=FAKE, ws=FAKE, n=need, D=64: b(  # noqa: E731
+        FAKE, FAKE, dh, 8, D, 64, 1, dx, dw, ws, n, None, None)
+    assert need >= 8 * 2 * 64 * 2
+    assert grad(dh=None) == EALIGN and grad(dx=0x10008) == EALIGN and grad(dw=None) == EALIGN and grad(ws=None) == EALIGN
+    assert grad(n=need - 1) == ENOSPACE and grad(D=68) == EUNSUPPORTED
+    assert sdm.project_gated_backward_workspace_size(0, 64, 64) == 0
+
+
+def test_python_calls_refuse_host_tensors():
+    x = torch.zeros(2, 3, 8)
+    for call in (lambda: sdm.causal_conv(x, torch.zeros(8, 4)),
+                 lambda: sdm.causal_conv_step(x[:, 0], torch.zeros(8, 4), state=torch.zeros(2, 3, 8)),
+                 lambda: sdm.selective_scan(x, x, torch.zeros(8, 4), x, x),
+                 lambda: sdm.project_gated(x, torch.zeros(16, 8)),
+                 lambda: sdm.project_gated_backward(x, torch.zeros(16, 8), x)):
+        with pytest.raises(TypeError):
+            call()
