@@ -86,6 +86,10 @@ def lib() -> ctypes.CDLL:
             L.sdm_project_select_workspace_size.argtypes = [i, i, i, i, i, i]
             L.sdm_project_select_workspace_size.restype = sz
             L.sdm_project_select.argtypes = [p, p, i, i, i, i, i, i, i, p, p, p, p, p, sz, p, p]
+            L.sdm_selective_scan_workspace_size.argtypes = [i, i, i, i, i]
+            L.sdm_selective_scan_workspace_size.restype = sz
+            L.sdm_project_gated_backward_workspace_size.argtypes = [ll, i, i]
+            L.sdm_project_gated_backward_workspace_size.restype = sz
             for name in ("sdm_init_state_from_M0", "sdm_select", "sdm_select_tuned", "sdm_scan_forward",
                          "sdm_scan_forward_tuned", "sdm_scan_launch_info", "sdm_gen_inputs", "sdm_gen_M0",
                          "sdm_forward_chunks", "sdm_forward_tuned", "sdm_forward", "sdm_scan_forward_train",

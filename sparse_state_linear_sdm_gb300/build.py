@@ -1,8 +1,11 @@
-"""Build libsdm.so (the C-ABI CUDA library) in-tree for sm_103a.
+"""Build libsdm.so (the C-ABI CUDA library) and _layers.so (the Python binding of its
+layer entry points) in-tree for sm_103a.
 
-Each translation unit under csrc/ is compiled by its own nvcc process (in
-parallel), then linked into ``sparse_state_linear_sdm_gb300/libsdm.so``.  The
-CUDA runtime is linked statically so the library loads on its own.
+Each translation unit under csrc/ is compiled by its own process (in parallel:
+nvcc for the library's, the host compiler for the binding's, against torch's
+headers), then linked into ``sparse_state_linear_sdm_gb300/libsdm.so`` and
+``_layers.so``.  The CUDA runtime is linked statically into the library, so it
+loads on its own; the binding needs it and torch.
 """
 from __future__ import annotations
 
@@ -17,6 +20,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsdm.so")
+BINDING = os.path.join(PKG, "_layers.so")
+BINDING_SRC = os.path.join(CSRC, "sdm_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr"]
@@ -35,14 +40,45 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        os.path.join(os.path.dirname(PKG), "include", "sdm.h")]
+        BINDING_SRC, os.path.join(os.path.dirname(PKG), "include", "sdm.h")]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r
+
+
+def _compile_binding(cc: str) -> str:
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")]
+    obj = os.path.join(BUILD, "sdm_binding.o")
+    _run([shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-Wall",
+          *[a for d in dirs for a in ("-isystem", d)], "-c", BINDING_SRC, "-o", obj], "compiling the binding")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    _run([shutil.which("g++") or "c++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libsdm.so", "-L", libs,
+          "-ltorch_python", "-ltorch", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], "linking the binding")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -62,14 +98,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     srcs = _sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        binding = ex.submit(_compile_binding, cc)
         objs = list(ex.map(compile_one, srcs))
+        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
 
 

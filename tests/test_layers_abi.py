@@ -1,23 +1,23 @@
 """Host checks of the convolution, scan and gated entry points: bad arguments are refused before anything is
 launched, and calls with nothing to do return at once.  No GPU needed."""
 import ctypes
-import struct
 
 import pytest
 import torch
 
 import sparse_state_linear_sdm_gb300 as sdm
-from sparse_state_linear_sdm_gb300 import layers
 
 OK, EINVAL, EALIGN, EUNSUPPORTED, ENOSPACE = 0, -1, -2, -6, -7
 FAKE, ODD = 0x10000, 0x10001  # never dereferenced on these paths
 F32, BF16 = 0, 1
+P, I, LL, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
 
 
 def conv(x=FAKE, bs=64, ts=16, dt=BF16, w=FAKE, bias=FAKE, wdt=BF16, B=2, T=4, D=16, K=4, act=1, state=FAKE,
          out=FAKE, rows=2, lengths=None, slots=None, y=FAKE, err=None):
-    return layers._fn("sdm_causal_conv")(x, bs, ts, dt, w, bias, wdt, B, T, D, K, act, state, out, rows, lengths,
-                                         slots, y, err, None)
+    f = sdm.lib().sdm_causal_conv
+    f.argtypes = [P, LL, LL, I, P, P, I, I, I, I, I, I, P, P, I, P, P, P, P, P]
+    return f(x, bs, ts, dt, w, bias, wdt, B, T, D, K, act, state, out, rows, lengths, slots, y, err, None)
 
 
 def test_conv_refusals():
@@ -47,14 +47,24 @@ SCAN = dict(x=FAKE, dt=FAKE, Bm=FAKE, Cm=FAKE, z=FAKE, x_bs=64, x_ts=16, dt_bs=6
             y=FAKE, dtype=BF16, B=2, T=4, Dm=16, N=8, G=1, softplus=1, n_slots=2)
 
 
+class ScanArgs(ctypes.Structure):
+    """sdm_ssm_args."""
+    _fields_ = ([(n, P) for n in ("x", "dt", "Bm", "Cm", "z")]
+                + [(n, LL) for n in ("x_bs", "x_ts", "dt_bs", "dt_ts", "B_bs", "B_ts", "C_bs", "C_ts", "z_bs", "z_ts")]
+                + [(n, P) for n in ("A", "D", "dt_bias", "state", "state_out", "lengths", "slots", "y")]
+                + [(n, I) for n in ("dtype", "B", "T", "Dm", "N", "G", "softplus", "n_slots")])
+
+
 def scan(ws=0, ws_bytes=0, err=None, **kw):
-    args = layers._scan_args(*{**SCAN, **kw}.values())
-    return layers._fn("sdm_selective_scan")(args, ws, ws_bytes, err, None)
+    f = sdm.lib().sdm_selective_scan
+    f.argtypes = [P, P, SZ, P, P]
+    return f(ctypes.byref(ScanArgs(**{**SCAN, **kw})), ws, ws_bytes, err, None)
 
 
-def test_scan_arguments_are_laid_out_as_the_header_says():
-    assert struct.calcsize("@5P10q8P8i") == 5 * 8 + 10 * 8 + 8 * 8 + 8 * 4
-    assert layers._fn("sdm_selective_scan")(None, 0, 0, None, None) == EINVAL
+def test_scan_needs_its_arguments():
+    f = sdm.lib().sdm_selective_scan
+    f.argtypes = [P, P, SZ, P, P]
+    assert f(None, None, 0, None, None) == EINVAL
 
 
 def test_scan_refusals():
@@ -91,7 +101,8 @@ def test_scan_workspace_sizes():
 
 
 def test_gated_refusals():
-    f = layers._fn("sdm_project_gated")
+    f = sdm.lib().sdm_project_gated
+    f.argtypes = [P, P, LL, I, I, I, P, P, P]
     call = lambda x=FAKE, w=FAKE, M=8, D=64, F=64, act=1, h=FAKE: f(x, w, M, D, F, act, h, None, None)  # noqa: E731
     assert call(M=-1) == EINVAL and call(D=0) == EINVAL and call(F=0) == EINVAL
     assert call(act=0) == EINVAL and call(act=3) == EINVAL
@@ -99,7 +110,8 @@ def test_gated_refusals():
     assert call(M=1 << 31) == EUNSUPPORTED
     assert call(x=0x10008) == EALIGN and call(w=None) == EALIGN and call(h=None) == EALIGN
     assert call(M=0, x=None, h=None) == OK
-    b = layers._fn("sdm_project_gated_backward")
+    b = sdm.lib().sdm_project_gated_backward
+    b.argtypes = [P, P, P, LL, I, I, I, P, P, P, SZ, P, P]
     need = sdm.project_gated_backward_workspace_size(8, 64, 64)
     grad = lambda dh=FAKE, dx=FAKE, dw=FAKE, ws=FAKE, n=need, D=64: b(  # noqa: E731
         FAKE, FAKE, dh, 8, D, 64, 1, dx, dw, ws, n, None, None)
