@@ -109,7 +109,7 @@ struct Channels<T, 1> {
 };
 
 template <typename T, int K, int V, bool ACT>
-__global__ void __launch_bounds__(kConvThreads) conv_kernel(const __grid_constant__ ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, 4) conv_kernel(const __grid_constant__ ConvArgs a) {
   using C = Channels<T, V>;
   using word = typename C::word;
   using num = typename C::num;

@@ -499,17 +499,18 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Gated
 // A decode step's product reads all of w for a handful of tokens: HBM bounds it, and what counts is
 // that every SM reads its even share with enough loads under way.  A block takes 8 columns f: the 8
 // rows of Wg and the 8 of Wu are the 16 rows of one mma.m16n8k16, tokens its 8 columns, so that a lane
-// ends with g and u of the same elements.  The four warps take K steps of 32 in turn, straight from
-// global memory in 16-byte words (a lane's 8 consecutive k stand for the two groups of four that it
-// holds of two MMAs; x is read the same way, so the order of k is the same on both sides), and their
-// sums meet in shared memory.
+// ends with g and u of the same elements.  Each of the four warps takes runs of 8 K steps of 32 (512
+// bytes of a row: 14.5 us at 4 tokens of 2048 x 8192 where the warps take single steps in turn, 12.8
+// so), straight from global memory in 16-byte words (a lane's 8 consecutive k stand for the two groups
+// of four that it holds of two MMAs; x is read the same way, so the order of k is the same on both
+// sides), and their sums meet in shared memory.
 constexpr int kFewThreads = 128;
 constexpr int kFewF = 8;
 constexpr int kFewTokens = 16;
 
 __device__ __forceinline__ uint4 load_stream(const void* p) {  // read once: past L1
   uint4 v;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
       : "l"(p));
   return v;
@@ -542,11 +543,11 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __nv_bfloat16* _
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int k0 = warp * 32; k0 < D; k0 += kWarps * 32 * kAhead) {
+  for (int k0 = warp * 32 * kAhead; k0 < D; k0 += kWarps * 32 * kAhead) {
     uint4 vg[kAhead], vu[kAhead], vx[kAhead][NT];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int k = k0 + j * kWarps * 32;
+      const int k = k0 + j * 32;
       const bool in = k + c * 8 < D;  // D % 8 == 0
       vg[j] = in ? load_stream(wg + k) : zero;
       vu[j] = in ? load_stream(wu + k) : zero;

@@ -54,6 +54,34 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
+// Four elements of a row: as they lie in memory (one word where VEC says that they are aligned to
+// it, else the first n one by one), and as numbers.
+template <typename T, bool VEC>
+struct Four {
+  uint32_t w[sizeof(T)];  // 4 sizeof(T) bytes
+  __device__ void load(const T* p, int n) {
+    if constexpr (VEC && sizeof(T) == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (VEC) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      T* e = reinterpret_cast<T*>(w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = j < n ? p[j] : T(0.f);
+    }
+  }
+  __device__ void clear() {
+#pragma unroll
+    for (int j = 0; j < int(sizeof(T)); ++j) w[j] = 0;
+  }
+  __device__ float operator[](int j) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+    return __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+  }
+};
+
 // Passes over a sequence: one block takes all tokens (kWhole); or the sequence is cut in chunks,
 // every chunk but the last is reduced to its end state from zero and its sum of delta (kReduce), and
 // each chunk then starts from the given state carried through those before it (kJoin).  Chunks
@@ -201,9 +229,14 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
             make_ulonglong2(dl, mul2(dl, pack2(x[2 * i], x[2 * i + 1])));
       }
     }
-    for (int e = tid; e < kTT * S::NP; e += kThreads) {
-      sB[e] = to_f32(raw_bc(st, 0)[e]);
-      if (PASS != kReduce) sC[e] = to_f32(raw_bc(st, 1)[e]);
+    for (int v = tid; v < kTT * S::NP / 4; v += kThreads) {
+      Four<T, true> f;
+      f.load(raw_bc(st, 0) + 4 * v, 4);
+      reinterpret_cast<float4*>(sB)[v] = make_float4(f[0], f[1], f[2], f[3]);
+      if (PASS != kReduce) {
+        f.load(raw_bc(st, 1) + 4 * v, 4);
+        reinterpret_cast<float4*>(sC)[v] = make_float4(f[0], f[1], f[2], f[3]);
+      }
     }
   };
 
@@ -219,7 +252,8 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
       for (int i = 0; i < V / 2; ++i) {
         uint64_t y = *reinterpret_cast<const uint64_t*>(&dx[t * (S::CH / 2) + i * S::RV + pr]);
         y = fma2(skip[i], pack2(x[2 * i], x[2 * i + 1]), y);
-        if (io.z) y = mul2(y, pack2(silu(z[2 * i]), silu(z[2 * i + 1])));
+        if (io.z)
+          y = mul2(mul2(y, pack2(z[2 * i], z[2 * i + 1])), pack2(sigmoid(z[2 * i]), sigmoid(z[2 * i + 1])));
         unpack2(y, o[2 * i], o[2 * i + 1]);
       }
       T* p = gy + size_t(t0 + t) * io.Dm + pc;
@@ -418,34 +452,6 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
     }
   }
 }
-
-// Four elements of a row: as they lie in memory (one word where VEC says that they are aligned to
-// it, else the first n one by one), and as numbers.
-template <typename T, bool VEC>
-struct Four {
-  uint32_t w[sizeof(T)];  // 4 sizeof(T) bytes
-  __device__ void load(const T* p, int n) {
-    if constexpr (VEC && sizeof(T) == 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (VEC) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      w[0] = v.x, w[1] = v.y;
-    } else {
-      T* e = reinterpret_cast<T*>(w);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) e[j] = j < n ? p[j] : T(0.f);
-    }
-  }
-  __device__ void clear() {
-#pragma unroll
-    for (int j = 0; j < int(sizeof(T)); ++j) w[j] = 0;
-  }
-  __device__ float operator[](int j) const {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
-    return __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
-  }
-};
 
 // One token: a lane has four states of a channel (16 bytes in, 16 bytes out) in each of R sequences,
 // L lanes a channel.  HBM bounds it, the states read and written once: R states are under way in
