@@ -51,6 +51,15 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n)
                : "memory");
 }
+// One element where rows are not aligned to 16 bytes: 4 bytes are copied like 16, 2 bytes are loaded.
+__device__ __forceinline__ void copy1(float* dst, const float* src, bool in) {
+  const int n = in ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void copy1(__nv_bfloat16* dst, const __nv_bfloat16* src, bool in) {
+  *dst = in ? *src : __nv_bfloat16(0.f);
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
@@ -162,13 +171,15 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
         if (PASS != kReduce && io.z) copy16(raw(st, 2) + v * V, gz + tt * io.z_ts + cc, in);
       }
     } else {
+#pragma unroll 4
       for (int e = tid; e < kTT * S::CH; e += kThreads) {
         const int t = e / S::CH, c = e % S::CH;
         const bool in = t < nt && c < nch;
-        const long long tt = t0 + t;
-        raw(st, 0)[e] = in ? gx[tt * io.x_ts + c] : T(0.f);
-        raw(st, 1)[e] = in ? gdt[tt * io.dt_ts + c] : T(0.f);
-        if (PASS != kReduce && io.z) raw(st, 2)[e] = in ? gz[tt * io.z_ts + c] : T(0.f);
+        const long long tt = in ? t0 + t : 0;
+        const int cc = in ? c : 0;
+        copy1(raw(st, 0) + e, gx + tt * io.x_ts + cc, in);
+        copy1(raw(st, 1) + e, gdt + tt * io.dt_ts + cc, in);
+        if (PASS != kReduce && io.z) copy1(raw(st, 2) + e, gz + tt * io.z_ts + cc, in);
       }
     }
     constexpr int NV = S::NP / V;
@@ -184,12 +195,14 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
         if (PASS != kReduce) copy16(raw_bc(st, 1) + v * V, gC + tt * io.C_ts + nn, in);
       }
     } else {
+#pragma unroll 4
       for (int e = tid; e < kTT * S::NP; e += kThreads) {
         const int t = e / S::NP, n = e % S::NP;
         const bool in = t < nt && n < io.N;
-        const long long tt = t0 + t;
-        raw_bc(st, 0)[e] = in ? gB[tt * io.B_ts + n] : T(0.f);
-        if (PASS != kReduce) raw_bc(st, 1)[e] = in ? gC[tt * io.C_ts + n] : T(0.f);
+        const long long tt = in ? t0 + t : 0;
+        const int nn = in ? n : 0;
+        copy1(raw_bc(st, 0) + e, gB + tt * io.B_ts + nn, in);
+        if (PASS != kReduce) copy1(raw_bc(st, 1) + e, gC + tt * io.C_ts + nn, in);
       }
     }
     copies_commit();
