@@ -280,6 +280,16 @@ def test_scan_decays_that_vanish_and_steps_of_zero():
     assert torch.isfinite(y[0, :3]).all() and (y[0, 5].abs() < 1e-30).all()
 
 
+@pytest.mark.parametrize("T", [1, 64, 400])
+def test_steps_of_size_zero_keep_the_state_bit_for_bit(T):
+    """softplus of a very negative number is 0: a decay of exactly 1, over one token, many, and many in chunks."""
+    rn = _gen(17)
+    k = dict(x=rn(2, T, 40), dt=torch.full((2, T, 40), -3.0e38, device="cuda"), A=-torch.exp(rn(40, 16)),
+             B=rn(2, T, 16), C=rn(2, T, 16), state=rn(2, 40, 16))
+    y, st = sdm.selective_scan(**k, state_out=torch.empty_like(k["state"]))
+    assert torch.equal(st, k["state"])
+
+
 def test_slots_outside_the_pool_are_reported_and_skipped():
     k = _scan_case(SCAN[9])
     good = k["slots"].clone()
