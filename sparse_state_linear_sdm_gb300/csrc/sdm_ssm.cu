@@ -20,7 +20,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kLaneStates = 8;  // states a lane holds of each of its channels, at most
-constexpr int kTokenThreads = 128;
+constexpr int kTokenThreads = 64;
+constexpr int token_rows(int lanes) { return lanes < 2 ? 1 : 2; }  // sequences a lane works on
 constexpr int kTT = 16;       // tokens of a shared-memory tile
 constexpr int kMinChunk = 48; // tokens of a chunk, at least
 constexpr int kSteps = 4;     // tokens taken together by a lane
@@ -475,14 +476,14 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
   }
 }
 
-// One token: a lane has four states of a channel (16 bytes in, 16 bytes out) in each of R sequences,
-// L lanes a channel.  HBM bounds it, the states read and written once: R states are under way in
-// every lane, everything that does not wait for a slot is asked for first, and what a channel
-// computes once (step size, gate) is done for each sequence by one of its lanes, lane r < R for
-// sequence r.  VEC: four states, and four entries of B and C, are a word.
-template <typename T, int L, bool VEC>
+// One token: a lane has 4 Q states of a channel in each of R sequences, L lanes a channel.  HBM bounds
+// it, the states read and written once: R states are under way in every lane, everything that does
+// not wait for a slot is asked for first, and what a channel computes once (step size, gate) is done
+// for each sequence by one of its lanes, lane r < R for sequence r.  VEC: four states, and four
+// entries of B and C, are a word.
+template <typename T, int L, int Q, bool VEC>
 __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_constant__ ScanArgs a) {
-  constexpr int R = L < 4 ? L : 4;
+  constexpr int R = token_rows(L);
   const sdm_ssm_args& io = a.io;
   const int sub = threadIdx.x % L, own = sub % R;
   const int group = int(blockIdx.x) / a.tiles_g;  // of R sequences; tiles_g blocks hold its channels
@@ -490,8 +491,10 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
   const bool present = channel < io.Dm;  // lanes past the last channel only take part in the shuffles
   const int d = present ? channel : 0;
   const int b0 = group * R, rows = present ? min(R, io.B - b0) : 0;
-  const int n0 = sub * 4, left = io.N - n0;
-  const bool states = left > 0;
+  const int n0 = sub * 4 * Q;
+  int left[Q];  // states of word q that exist
+#pragma unroll
+  for (int q = 0; q < Q; ++q) left[q] = io.N - n0 - 4 * q;
   const size_t at = size_t(d) * io.N + n0, row = size_t(io.Dm) * io.N;
 
   int slot[R];
@@ -505,21 +508,22 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
     dl = to_f32(static_cast<const T*>(io.dt)[b * io.dt_bs + d]);
     if (io.z) z = to_f32(static_cast<const T*>(io.z)[b * io.z_bs + d]);
   }
-  Four<float, VEC> A, h4[R];
-  Four<T, VEC> B[R], C[R];
-  A.clear();
-  if (states) A.load(io.A + at, left);
-  {
-    const int bc = (io.G > 1 ? d / a.Dg * io.N : 0) + n0;
-    const T* pB = static_cast<const T*>(io.Bm) + b0 * io.B_bs + bc;
-    const T* pC = static_cast<const T*>(io.Cm) + b0 * io.C_bs + bc;
+  Four<float, VEC> A[Q], h4[R][Q];
+  Four<T, VEC> B[R][Q], C[R][Q];
+  const int bc = (io.G > 1 ? d / a.Dg * io.N : 0) + n0;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    A[q].clear();
+    if (left[q] > 0) A[q].load(io.A + at + 4 * q, left[q]);
+    const T* pB = static_cast<const T*>(io.Bm) + b0 * io.B_bs + bc + 4 * q;
+    const T* pC = static_cast<const T*>(io.Cm) + b0 * io.C_bs + bc + 4 * q;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      B[r].clear();
-      C[r].clear();
-      if (r < rows && states) {
-        B[r].load(pB, left);
-        C[r].load(pC, left);
+      B[r][q].clear();
+      C[r][q].clear();
+      if (r < rows && left[q] > 0) {
+        B[r][q].load(pB, left[q]);
+        C[r][q].load(pC, left[q]);
       }
       pB += io.B_bs;
       pC += io.C_bs;
@@ -529,9 +533,12 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
   bool live[R], mine = false;  // the sequence has a state and a token
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    h4[r].clear();
-    if (slot[r] >= 0 && io.state && states)
-      h4[r].load(io.state + at + size_t(unsigned(slot[r])) * row, left);
+    const float* p = io.state + at + size_t(unsigned(max(slot[r], 0))) * row;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      h4[r][q].clear();
+      if (slot[r] >= 0 && io.state && left[q] > 0) h4[r][q].load(p + 4 * q, left[q]);
+    }
     live[r] = slot[r] >= 0 && row_length(io.lengths, b0 + r, 1) > 0;
     mine = mine || (own == r && live[r]);
   }
@@ -539,48 +546,46 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
   dl += bias;
   if (io.softplus) dl = softplus(dl);
   const float dlx = dl * x;
-  float rate[4], y[R];
+  float rate[Q][4], y[R];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) rate[j] = decay_rate(A[j]);
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rate[q][j] = decay_rate(A[q][j]);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const float dr = __shfl_sync(0xFFFFFFFFu, dl, r, L), dx = __shfl_sync(0xFFFFFFFFu, dlx, r, L);
-    float h[4];
+    float* p = io.state_out + at + size_t(unsigned(max(slot[r], 0))) * row;
+    const bool keep = slot[r] >= 0 && io.state_out;
     y[r] = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      h[j] = h4[r][j];
-      if (live[r]) {
-        h[j] = fmaf(decay(dr, rate[j]), h[j], dx * B[r][j]);
-        y[r] = fmaf(h[j], C[r][j], y[r]);
-      }
-    }
-    if (slot[r] >= 0 && io.state_out && states) {
-      float* p = io.state_out + at + size_t(unsigned(slot[r])) * row;
-      if constexpr (VEC) {
-        *reinterpret_cast<float4*>(p) = make_float4(h[0], h[1], h[2], h[3]);
-      } else {
+    for (int q = 0; q < Q; ++q) {
+      float h[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < left) p[j] = h[j];
+      for (int j = 0; j < 4; ++j) {
+        h[j] = h4[r][q][j];
+        if (live[r]) {
+          h[j] = fmaf(decay(dr, rate[q][j]), h[j], dx * B[r][q][j]);
+          y[r] = fmaf(h[j], C[r][q][j], y[r]);
+        }
+      }
+      if (keep && left[q] > 0) {
+        if constexpr (VEC) {
+          *reinterpret_cast<float4*>(p + 4 * q) = make_float4(h[0], h[1], h[2], h[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < left[q]) p[4 * q + j] = h[j];
+        }
       }
     }
   }
   // Sums over the channel's lanes; lane r keeps sequence r's.
-  if constexpr (R >= 2) {
+  if constexpr (R == 2) {
     const bool odd = sub & 1;
+    const float give = odd ? y[0] : y[1], keep = odd ? y[1] : y[0];
+    y[0] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
 #pragma unroll
-    for (int r = 0; r < R; r += 2) {
-      const float give = odd ? y[r] : y[r + 1], keep = odd ? y[r + 1] : y[r];
-      y[r / 2] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-    }
-  }
-  if constexpr (R == 4) {
-    const bool up = sub & 2;
-    const float give = up ? y[0] : y[1], keep = up ? y[1] : y[0];
-    y[0] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 2);
-#pragma unroll
-    for (int o = 4; o < L; o *= 2) y[0] += __shfl_xor_sync(0xFFFFFFFFu, y[0], o);
+    for (int o = 2; o < L; o *= 2) y[0] += __shfl_xor_sync(0xFFFFFFFFu, y[0], o);
   }
   if (sub < R && own < rows) {
     float v = fmaf(skip, x, y[0]);
@@ -639,28 +644,28 @@ int launch_scan(ScanArgs& a, cudaStream_t s) {
   }
 }
 
-template <typename T, int L>
+template <typename T, int L, int Q>
 int launch_token_l(ScanArgs& a, cudaStream_t s) {
-  constexpr int R = L < 4 ? L : 4, channels = kTokenThreads / L;
+  constexpr int R = token_rows(L), channels = kTokenThreads / L;
   a.tiles_g = (a.io.Dm + channels - 1) / channels;
   const long long blocks = (long long)((a.io.B + R - 1) / R) * a.tiles_g;
   if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
   if (a.vec && a.vec_bc)
-    token_kernel<T, L, true><<<unsigned(blocks), kTokenThreads, 0, s>>>(a);
+    token_kernel<T, L, Q, true><<<unsigned(blocks), kTokenThreads, 0, s>>>(a);
   else
-    token_kernel<T, L, false><<<unsigned(blocks), kTokenThreads, 0, s>>>(a);
+    token_kernel<T, L, Q, false><<<unsigned(blocks), kTokenThreads, 0, s>>>(a);
   return last_launch_status();
 }
 
 template <typename T>
 int launch_token(ScanArgs& a, cudaStream_t s) {
-  switch (lanes_for(a.io.N, 4)) {
-    case 1: return launch_token_l<T, 1>(a, s);
-    case 2: return launch_token_l<T, 2>(a, s);
-    case 4: return launch_token_l<T, 4>(a, s);
-    case 8: return launch_token_l<T, 8>(a, s);
-    case 16: return launch_token_l<T, 16>(a, s);
-    case 32: return launch_token_l<T, 32>(a, s);
+  if (a.io.N <= 4) return launch_token_l<T, 1, 1>(a, s);
+  switch (lanes_for(a.io.N, 8)) {
+    case 1: return launch_token_l<T, 1, 2>(a, s);
+    case 2: return launch_token_l<T, 2, 2>(a, s);
+    case 4: return launch_token_l<T, 4, 2>(a, s);
+    case 8: return launch_token_l<T, 8, 2>(a, s);
+    case 16: return launch_token_l<T, 16, 2>(a, s);
     default: return SDM_EUNSUPPORTED;
   }
 }
