@@ -23,15 +23,17 @@ constexpr int kLaneStates = 8;  // states a lane holds of each of its channels, 
 constexpr int kTokenThreads = 64;
 constexpr int token_rows(int lanes) { return lanes < 2 ? 1 : 2; }  // sequences a lane works on
 constexpr int kTT = 16;       // tokens of a shared-memory tile
-constexpr int kMinChunk = 48; // tokens of a chunk, at least
+constexpr int kMinChunk = 32; // tokens of a chunk, at least
 constexpr int kSteps = 4;     // tokens taken together by a lane
 
 struct ScanArgs {
   sdm_ssm_args io;
   int tiles_g, Dg;             // channel tiles of a group (one token: of a row), channels of a group
   int chunks, chunk;           // chunks of a sequence, tokens of a chunk (a multiple of kTT)
-  float* ws_h;                 // [chunks][B][Dm][N]: state before chunk 0, then each chunk's own end
+  float* ws_h;                 // [chunks][B][Dm][ws_n]: state before chunk 0, then each chunk's own end
   float* ws_d;                 // [chunks][B][Dm]: sum of delta over each chunk
+  int ws_n;                    // N up to a multiple of 4
+  bool vec_s;                  // rows of A and of the states start on 16 bytes
   bool vec;                    // rows of x, dt, z and y in 16-byte pieces; one token: four states a word
   bool vec_bc;                 // rows of B and C in 16-byte pieces; one token: four entries a word
   int* dev_err;
@@ -294,52 +296,88 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
   const int sub = tid % L, pair = tid / L;
   const int ch = (pair % S::RV) * V + 2 * (pair / S::RV);  // the pair's first channel in the tile
   float A[2][kS], h[2][kS], dsum[2] = {0.f, 0.f};
-  const size_t bd = size_t(b) * io.Dm + d0;
+  const size_t per = size_t(io.B) * io.Dm, bd = size_t(b) * io.Dm + d0;  // channels; of a chunk, of this tile
+  // This lane's states of a row that starts at p: words of four where `vec` says that rows start on
+  // 16 bytes (those of the workspace always do), zeros past the last state.
+  auto get = [&](const float* p, bool vec, float (&v)[kS]) {
+#pragma unroll
+    for (int j = 0; j < kS; j += 4) {
+      const int n = sub * kS + j;
+      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (vec) {
+        if (n < io.N) w = *reinterpret_cast<const float4*>(p + n);
+      } else {
+        if (n < io.N) w.x = p[n];
+        if (n + 1 < io.N) w.y = p[n + 1];
+        if (n + 2 < io.N) w.z = p[n + 2];
+        if (n + 3 < io.N) w.w = p[n + 3];
+      }
+      v[j] = w.x;
+      v[j + 1] = n + 1 < io.N ? w.y : 0.f;
+      v[j + 2] = n + 2 < io.N ? w.z : 0.f;
+      v[j + 3] = n + 3 < io.N ? w.w : 0.f;
+    }
+  };
+  auto put = [&](float* p, bool vec, const float (&v)[kS]) {
+#pragma unroll
+    for (int j = 0; j < kS; j += 4) {
+      const int n = sub * kS + j;
+      if (vec) {
+        if (n < io.N) *reinterpret_cast<float4*>(p + n) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < io.N) p[n + i] = v[j + i];
+      }
+    }
+  };
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int c = ch + k;
 #pragma unroll
-    for (int j = 0; j < kS; ++j) {
-      const int n = sub * kS + j;
-      const bool in = c < nch && n < io.N;
-      A[k][j] = in ? decay_rate(io.A[size_t(d0 + c) * io.N + n]) : 0.f;
-      h[k][j] = 0.f;
-      if (in && slot >= 0) {
-        if (PASS == kWhole || (PASS == kReduce && chunk == 0)) {
-          const float v = io.state ? io.state[(size_t(slot) * io.Dm + d0 + c) * io.N + n] : 0.f;
-          if (PASS == kReduce)
-            a.ws_h[(bd + c) * io.N + n] = v;
-          else
-            h[k][j] = v;
-        } else if (PASS == kJoin) {
-          h[k][j] = a.ws_h[(bd + c) * io.N + n];
+    for (int j = 0; j < kS; ++j) A[k][j] = h[k][j] = 0.f;
+    if (c < nch) {
+      get(io.A + size_t(d0 + c) * io.N, a.vec_s, A[k]);
+#pragma unroll
+      for (int j = 0; j < kS; ++j) A[k][j] = decay_rate(A[k][j]);
+      if (slot >= 0) {
+        const float* given = io.state + (size_t(slot) * io.Dm + d0 + c) * io.N;
+        if (PASS == kWhole && io.state) get(given, a.vec_s, h[k]);
+        if (PASS == kJoin) get(a.ws_h + (bd + c) * a.ws_n, true, h[k]);
+        if (PASS == kReduce && chunk == 0) {
+          float v[kS];
+#pragma unroll
+          for (int j = 0; j < kS; ++j) v[j] = 0.f;
+          if (io.state) get(given, a.vec_s, v);
+          put(a.ws_h + (bd + c) * a.ws_n, true, v);
         }
       }
     }
   }
   if (PASS == kJoin && slot >= 0) {
-    const size_t per = size_t(io.B) * io.Dm;
-    // Two chunks at a time: what they bring does not depend on the state, so it is asked for together.
-    for (int q0 = 0; q0 < chunk; q0 += 2) {
-      float sum[2][2], end[2][2][kS];
+    // Four chunks at a time: what they bring does not depend on the state, so it is asked for together.
+    constexpr int kBatch = 4;
+    for (int q0 = 0; q0 < chunk; q0 += kBatch) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int k = 0; k < 2; ++k) {
+        const int c = min(ch + k, nch - 1);  // lanes past the last channel follow it, to no effect
+        float sum[kBatch], end[kBatch][kS];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int c = ch + k, q = q0 + i;
-          const bool in = c < nch && q < chunk;
-          sum[i][k] = in ? a.ws_d[q * per + bd + c] : 0.f;  // a chunk of none: decay 1, nothing added
-          const float* e = a.ws_h + ((q + 1) * per + bd + c) * io.N + sub * kS;
+        for (int i = 0; i < kBatch; ++i) {
+          const int q = q0 + i;
+          sum[i] = 0.f;  // a chunk of none: decay 1, nothing added
 #pragma unroll
-          for (int j = 0; j < kS; ++j) end[i][k][j] = in && sub * kS + j < io.N ? e[j] : 0.f;
+          for (int j = 0; j < kS; ++j) end[i][j] = 0.f;
+          if (q < chunk) {
+            sum[i] = a.ws_d[q * per + bd + c];
+            get(a.ws_h + ((q + 1) * per + bd + c) * a.ws_n, true, end[i]);
+          }
         }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int j = 0; j < kS; ++j)
-            h[k][j] = fmaf(decay(sum[i][k], A[k][j]), h[k][j], end[i][k][j]);
+          for (int j = 0; j < kS; ++j) h[k][j] = fmaf(decay(sum[i], A[k][j]), h[k][j], end[i][j]);
+      }
     }
   }
 
@@ -461,17 +499,16 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
   }
   const bool last = PASS == kWhole || (PASS == kJoin && chunk == a.chunks - 1);
   if (slot >= 0 && (PASS == kReduce || (last && io.state_out))) {
-    const size_t per = size_t(io.B) * io.Dm;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int c = ch + k;
       if (c >= nch) continue;
-      float* dst = PASS == kReduce ? a.ws_h + ((chunk + 1) * per + bd + c) * io.N
-                                   : io.state_out + (size_t(slot) * io.Dm + d0 + c) * io.N;
-#pragma unroll
-      for (int j = 0; j < kS; ++j)
-        if (sub * kS + j < io.N) dst[sub * kS + j] = h[k][j];
-      if (PASS == kReduce && sub == 0) a.ws_d[chunk * per + bd + c] = dsum[k];
+      if (PASS == kReduce) {
+        put(a.ws_h + ((chunk + 1) * per + bd + c) * a.ws_n, true, h[k]);
+        if (sub == 0) a.ws_d[chunk * per + bd + c] = dsum[k];
+      } else {
+        put(io.state_out + (size_t(slot) * io.Dm + d0 + c) * io.N, a.vec_s, h[k]);
+      }
     }
   }
 }
@@ -670,10 +707,11 @@ int launch_token(ScanArgs& a, cudaStream_t s) {
   }
 }
 
-// Chunks of a sequence and tokens of a chunk: one chunk where the channels alone give the card
-// enough blocks, else as many as bring it there, of kMinChunk tokens at least (shorter ones cost
-// more in joining them than they save: 512 tokens of 2048 channels take 35 us in chunks of 64, 40 in
-// chunks of 32, 50 in chunks of 128).
+// Chunks of a sequence and tokens of a chunk: one chunk where the channels alone give the card two
+// blocks an SM, else as many as give it four, of kMinChunk tokens at least.  Two passes cost 1.5 times
+// the arithmetic of one: 4 x 2048 tokens of 4096 channels (128 blocks) take 304 us in five chunks and
+// 377 in one.  Four blocks an SM against three: 32768 tokens of 2048 channels 554 us against 627;
+// chunks of 32 tokens against 64: 512 tokens of 1024 channels 28.5 us against 31.3.
 void cut(int B, int T, int Dm, int N, int G, int* chunks, int* chunk) {
   const int L = lanes_for(N, kLaneStates), CH = 2 * kThreads / L;
   const long long blocks = (long long)B * G * ((Dm / G + CH - 1) / CH);
@@ -699,7 +737,7 @@ extern "C" size_t sdm_selective_scan_workspace_size(int B, int T, int Dm, int N,
   int chunks, chunk;
   cut(B, T, Dm, N, G, &chunks, &chunk);
   if (chunks <= 1) return 0;
-  return size_t(chunks) * B * Dm * (N + 1) * 4;
+  return size_t(chunks) * B * Dm * ((N + 3) / 4 * 4 + 1) * 4;
 }
 
 extern "C" int sdm_selective_scan(const sdm_ssm_args* args, void* workspace, size_t workspace_bytes,
@@ -737,8 +775,9 @@ extern "C" int sdm_selective_scan(const sdm_ssm_args* args, void* workspace, siz
   if (need) {
     if (!aligned16(workspace)) return SDM_EALIGN;
     if (workspace_bytes < need) return SDM_ENOSPACE;
+    a.ws_n = (io.N + 3) / 4 * 4;
     a.ws_h = static_cast<float*>(workspace);
-    a.ws_d = a.ws_h + size_t(a.chunks) * io.B * io.Dm * io.N;
+    a.ws_d = a.ws_h + size_t(a.chunks) * io.B * io.Dm * a.ws_n;
   }
   const int V = io.dtype == SDM_F32 ? 4 : 8;
   auto rows16 = [&](const void* p, long long bs, long long ts) {
@@ -746,6 +785,7 @@ extern "C" int sdm_selective_scan(const sdm_ssm_args* args, void* workspace, siz
   };
   a.vec = a.Dg % V == 0 && rows16(io.x, io.x_bs, io.x_ts) && rows16(io.dt, io.dt_bs, io.dt_ts) &&
           rows16(io.z, io.z_bs, io.z_ts) && !off(io.y, 15);
+  a.vec_s = io.N % 4 == 0 && !off(io.A, 15) && !off(io.state, 15) && !off(io.state_out, 15);
   a.vec_bc = io.N % V == 0 && rows16(io.Bm, io.B_bs, io.B_ts) && rows16(io.Cm, io.C_bs, io.C_ts);
   return io.dtype == SDM_F32 ? launch_scan<float>(a, s) : launch_scan<__nv_bfloat16>(a, s);
 }
