@@ -14,7 +14,7 @@
 namespace sdm {
 namespace {
 
-constexpr int kConvThreads = 128;
+constexpr int kConvThreads = 64;
 constexpr int kAhead = 8;  // tokens under way: a register word each, reloaded as soon as it is taken
 constexpr int kMinStrip = 8;  // shortest strip: longer than the window
 
@@ -109,7 +109,7 @@ struct Channels<T, 1> {
 };
 
 template <typename T, int K, int V, bool ACT>
-__global__ void __launch_bounds__(kConvThreads, 4) conv_kernel(const __grid_constant__ ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, 8) conv_kernel(const __grid_constant__ ConvArgs a) {
   using C = Channels<T, V>;
   using word = typename C::word;
   using num = typename C::num;
@@ -119,18 +119,17 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_kernel(const __grid_cons
   const int b = int(row / unsigned(a.strips)), strip = int(row - unsigned(b) * unsigned(a.strips));
   if (b >= a.B) return;
   const int d = piece * V;
-  const int slot = row_slot(a.slots, b, a.n_slots, a.dev_err);
-  const int len = slot < 0 ? 0 : row_length(a.lengths, b, a.T);
+  const int asked = asked_slot(a.slots, b);
+  const int given = row_length(a.lengths, b, a.T);
   const int t0 = strip * a.strip, t1 = min(t0 + a.strip, a.T);
-  const int end = min(t1, len);  // tokens of this strip that exist: [t0, end)
   const T* x = static_cast<const T*>(a.x) + b * a.x_bs + d;
   auto token = [&](int t) {  // zero past the sequence
-    return t < len ? *reinterpret_cast<const word*>(x + t * a.x_ts) : C::zero();
+    return t < given ? *reinterpret_cast<const word*>(x + t * a.x_ts) : C::zero();
   };
 
   word next[kAhead];
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k) next[k] = t0 + k < end ? token(t0 + k) : C::zero();
+  for (int k = 0; k < kAhead; ++k) next[k] = t0 + k < t1 ? token(t0 + k) : C::zero();
 
   num w[K][C::n], bias[C::n];
   {
@@ -148,6 +147,9 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_kernel(const __grid_cons
     C::join(tap, bias);
   }
 
+  const int slot = checked_slot(a.slots, asked, a.n_slots, a.dev_err);
+  const int len = slot < 0 ? 0 : given;
+  const int end = min(t1, len);  // tokens of this strip that exist: [t0, end)
   const size_t srow = size_t(max(slot, 0)) * (K - 1) * a.D + d;
   num win[K - 1][C::n];
   {

@@ -127,13 +127,16 @@ __device__ __forceinline__ int row_length(const int32_t* lengths, int b, int T) 
 }
 
 // The state row of batch row b: its slot, or -1 for a padding row.  A slot past the pool is
-// reported and treated as padding, so no access leaves the pool.
-__device__ __forceinline__ int row_slot(const int32_t* slots, int b, int n_slots, int* dev_err) {
-  if (!slots) return b;
-  const int s = slots[b];
-  if (s < n_slots) return s < 0 ? -1 : s;
+// reported and treated as padding, so no access leaves the pool.  Asked for first and looked at
+// later (checked_slot), it is on its way while everything that does not need it is asked for too.
+__device__ __forceinline__ int asked_slot(const int32_t* slots, int b) { return slots ? slots[b] : b; }
+__device__ __forceinline__ int checked_slot(const int32_t* slots, int slot, int n_slots, int* dev_err) {
+  if (!slots || slot < n_slots) return slot < 0 ? -1 : slot;
   if (dev_err) atomicOr(dev_err, SDM_DEV_INDEX_RANGE);
   return -1;
+}
+__device__ __forceinline__ int row_slot(const int32_t* slots, int b, int n_slots, int* dev_err) {
+  return checked_slot(slots, asked_slot(slots, b), n_slots, dev_err);
 }
 
 }  // namespace sdm
