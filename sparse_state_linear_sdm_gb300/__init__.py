@@ -1,8 +1,9 @@
 """GB300 (sm_103a) Sparse Delta Memory forward hot path.
 
 The compute lives in ``libsdm.so`` (CUDA C++, C ABI declared in include/sdm.h);
-``api`` is a thin ctypes binding for torch tensors and ``workloads`` defines the
-seeded synthetic configurations.  Importing the package does not load the
+``api`` is a thin ctypes binding for torch tensors, ``layers`` has the layers beside
+the memory (convolution, selective scan, gated projections), and ``workloads`` defines
+the seeded synthetic configurations.  Importing the package does not load the
 library; the first API call does (and fails loudly if it cannot).
 """
 from .api import (BWD_DM0_ONLY, BWD_FINAL_ZERO, SELECT_AUTO, SELECT_COUNTING, SELECT_GENERAL, SDM_BF16, SDM_DEV_DUP_WRITE, SDM_DEV_INDEX_RANGE, SDM_DEV_TIMEOUT, SDM_F32, DecodeStep, SDMError,

