@@ -46,7 +46,8 @@ struct ScanArgs {
 // A in units of exp2, finite, so that a step of size 0 has the decay 1 (0 times an infinite rate
 // would have none).
 __device__ __forceinline__ float decay_rate(float A) {
-  return fminf(fmaxf(A * kLog2e, -3.402823466e38f), 3.402823466e38f);
+  const float r = A * kLog2e;
+  return r == r ? fminf(fmaxf(r, -3.402823466e38f), 3.402823466e38f) : r;  // NaN stays
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
