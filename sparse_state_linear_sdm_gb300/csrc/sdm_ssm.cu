@@ -98,6 +98,15 @@ struct Four {
       for (int j = 0; j < 4; ++j) e[j] = j < n ? p[j] : T(0.f);
     }
   }
+  // The same for what is read once: L2 keeps other lines before it.
+  __device__ void load_once(const T* p, int n) {
+    if constexpr (VEC && sizeof(T) == 4) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+      load(p, n);
+    }
+  }
   __device__ void clear() {
 #pragma unroll
     for (int j = 0; j < int(sizeof(T)); ++j) w[j] = 0;
@@ -521,9 +530,9 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
 // One token: a lane has 4 Q states of a channel in each of R sequences, L lanes a channel.  HBM bounds
 // it, the states read and written once: R states are under way in every lane, everything that does
 // not wait for a slot is asked for first, and what a channel computes once (step size, gate) is done
-// for each sequence by one of its lanes, lane r < R for sequence r.  256 x 4096 x 16 bf16 with slots
-// takes 27 us of device time, 0.78 of the rate that HBM would give; blocks that stay and walk over the
-// sequences took 46.  VEC: four states, and four entries of B and C, are a word.
+// for each sequence by one of its lanes, lane r < R for sequence r.  States pass once through L2,
+// marked so (26.6 us a call at 256 x 4096 x 16 bf16 with slots, 0.79 of HBM's rate; 30.6 unmarked;
+// blocks that stay and walk over the sequences took 46).  VEC: four states, and four entries of B and C, are a word.
 template <typename T, int L, int Q, bool VEC>
 __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_constant__ ScanArgs a) {
   constexpr int R = token_rows(L);
@@ -580,7 +589,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       h4[r][q].clear();
-      if (slot[r] >= 0 && io.state && left[q] > 0) h4[r][q].load(p + 4 * q, left[q]);
+      if (slot[r] >= 0 && io.state && left[q] > 0) h4[r][q].load_once(p + 4 * q, left[q]);
     }
     live[r] = slot[r] >= 0 && row_length(io.lengths, b0 + r, 1) > 0;
     mine = mine || (own == r && live[r]);
@@ -613,7 +622,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
       }
       if (keep && left[q] > 0) {
         if constexpr (VEC) {
-          *reinterpret_cast<float4*>(p + 4 * q) = make_float4(h[0], h[1], h[2], h[3]);
+          __stcs(reinterpret_cast<float4*>(p + 4 * q), make_float4(h[0], h[1], h[2], h[3]));
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
