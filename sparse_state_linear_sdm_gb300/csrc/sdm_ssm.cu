@@ -722,15 +722,18 @@ int launch_token(ScanArgs& a, cudaStream_t s) {
   }
 }
 
-// Chunks of a sequence and tokens of a chunk: one chunk where the channels alone give the card two
-// blocks an SM, else as many as give it four, of kMinChunk tokens at least.  Two passes cost 1.5 times
-// the arithmetic of one: 4 x 2048 tokens of 4096 channels (128 blocks) take 304 us in five chunks and
-// 377 in one.  Four blocks an SM against three: 32768 tokens of 2048 channels 554 us against 627;
-// chunks of 32 tokens against 64: 512 tokens of 1024 channels 28.5 us against 31.3.
+// Chunks of a sequence and tokens of a chunk: one chunk where the channels alone give the card 208
+// blocks, else as many as keep within four blocks an SM, of kMinChunk tokens at least.  A block's
+// tokens wait on one another, so an SM with two blocks takes little longer than with one (2048
+// tokens, 4096 channels a sequence: 343, 436, 560 and 707 us with one to four), and two passes cost
+// 1.5 times the arithmetic of one: 128 blocks take 287 us in four chunks and 343 in one, 192 blocks
+// 380 and 436, 256 blocks 515 and 436.  Four blocks an SM against three: 32768 tokens of 2048
+// channels 554 us against 627; chunks of 32 tokens against 64: 512 tokens of 1024 channels 28.5 us
+// against 31.3.
 void cut(int B, int T, int Dm, int N, int G, int* chunks, int* chunk) {
   const int L = lanes_for(N, kLaneStates), CH = 2 * kThreads / L;
   const long long blocks = (long long)B * G * ((Dm / G + CH - 1) / CH);
-  long long n = blocks >= 304 ? 1 : (608 + blocks - 1) / blocks;
+  long long n = blocks >= 208 ? 1 : 608 / blocks;
   n = n < T / kMinChunk ? n : T / kMinChunk;
   if (n < 1) n = 1;
   const int per = int(((T + n - 1) / n + kTT - 1) / kTT) * kTT;
