@@ -491,17 +491,21 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
     if (t_lo + kTT < t_end) load_tile(1, t_lo + kTT);
     __syncthreads();
     int st = 0;
-    for (int t0 = t_lo; t0 < t_end; t0 += kTT, st ^= 1) {
+    for (int t0 = t_lo; t0 < t_end; st ^= 1) {
       const int nt = min(kTT, t_end - t0);
+      // Either steps from tile to tile; so written, the compiler gives the whole pass 124 registers
+      // instead of 96, and two blocks an SM take 404 us instead of 437, four 697 instead of 707.
+      const int next = PASS == kWhole ? t0 + nt : t0 + kTT;
       int t = 0;
       for (; t + kSteps <= nt; t += kSteps) steps(t, std::integral_constant<int, kSteps>());
       for (; t < nt; ++t) steps(t, std::integral_constant<int, 1>());
       copies_wait();
       __syncthreads();
       if (PASS != kReduce) store_tile(st, t0);
-      if (t0 + kTT < t_end) prepare_tile(st ^ 1);
+      if (next < t_end) prepare_tile(st ^ 1);
       __syncthreads();
-      if (t0 + 2 * kTT < t_end) load_tile(st, t0 + 2 * kTT);
+      if (next + kTT < t_end) load_tile(st, next + kTT);
+      t0 = next;
     }
   }
 
@@ -725,9 +729,9 @@ int launch_token(ScanArgs& a, cudaStream_t s) {
 // Chunks of a sequence and tokens of a chunk: one chunk where the channels alone give the card 208
 // blocks, else as many as keep within four blocks an SM, of kMinChunk tokens at least.  A block's
 // tokens wait on one another, so an SM with two blocks takes little longer than with one (2048
-// tokens, 4096 channels a sequence: 343, 436, 560 and 707 us with one to four), and two passes cost
+// tokens, 4096 channels a sequence: 343, 404, 550 and 697 us with one to four), and two passes cost
 // 1.5 times the arithmetic of one: 128 blocks take 287 us in four chunks and 343 in one, 192 blocks
-// 380 and 436, 256 blocks 515 and 436.  Four blocks an SM against three: 32768 tokens of 2048
+// 380 and 404, 256 blocks 515 and 404.  Four blocks an SM against three: 32768 tokens of 2048
 // channels 554 us against 627; chunks of 32 tokens against 64: 512 tokens of 1024 channels 28.5 us
 // against 31.3.
 void cut(int B, int T, int Dm, int N, int G, int* chunks, int* chunk) {
