@@ -10,7 +10,7 @@
 // Each (t, d, n) costs one exp2 and four fp32 operations (two products, two fused multiply-adds).
 // A GB300 SM does 32 exp2 and 31 such foursomes a clock (measured), so with N = 16 and bf16 the
 // arithmetic takes 1.5 times as long as HBM does for the 8 bytes of an element: the arithmetic is
-// what has to be kept fed.  16 x 2048 x 4096 x 16 bf16 takes 0.71 ms, a third of the exp2 rate: 121
+// what has to be kept fed.  16 x 2048 x 4096 x 16 bf16 takes 0.69 ms, a third of the exp2 rate: 121
 // instructions for 512 (t, d, n), 81 of them in the recurrence, at 65 % issue.  Two of an
 // instruction's operations are packed in the input product and the read-out; packing the exponent's
 // product costs more in moves than it saves (a loop of its own: 98 clocks a warp and 512 (t, d, n)
@@ -141,8 +141,11 @@ struct Tile {
   static constexpr int bytes = off_c + kTT * NP * 4;
 };
 
+// Four blocks an SM is what a full card gives each, so 128 registers a thread: left to itself the
+// compiler stops at 96 (five blocks), and 16 x 2048 x 4096 x 16 takes 707 us instead of 685; with 168
+// (three blocks) 750.
 template <typename T, int L, int kS, int PASS>
-__global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) scan_kernel(const __grid_constant__ ScanArgs a) {
   using S = Tile<T, L, kS>;
   constexpr int V = S::V;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -491,21 +494,17 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const __grid_constant__ 
     if (t_lo + kTT < t_end) load_tile(1, t_lo + kTT);
     __syncthreads();
     int st = 0;
-    for (int t0 = t_lo; t0 < t_end; st ^= 1) {
+    for (int t0 = t_lo; t0 < t_end; t0 += kTT, st ^= 1) {
       const int nt = min(kTT, t_end - t0);
-      // Either steps from tile to tile; so written, the compiler gives the whole pass 124 registers
-      // instead of 96, and two blocks an SM take 404 us instead of 437, four 697 instead of 707.
-      const int next = PASS == kWhole ? t0 + nt : t0 + kTT;
       int t = 0;
       for (; t + kSteps <= nt; t += kSteps) steps(t, std::integral_constant<int, kSteps>());
       for (; t < nt; ++t) steps(t, std::integral_constant<int, 1>());
       copies_wait();
       __syncthreads();
       if (PASS != kReduce) store_tile(st, t0);
-      if (next < t_end) prepare_tile(st ^ 1);
+      if (t0 + kTT < t_end) prepare_tile(st ^ 1);
       __syncthreads();
-      if (next + kTT < t_end) load_tile(st, next + kTT);
-      t0 = next;
+      if (t0 + 2 * kTT < t_end) load_tile(st, t0 + 2 * kTT);
     }
   }
 
@@ -729,11 +728,11 @@ int launch_token(ScanArgs& a, cudaStream_t s) {
 // Chunks of a sequence and tokens of a chunk: one chunk where the channels alone give the card 208
 // blocks, else as many as keep within four blocks an SM, of kMinChunk tokens at least.  A block's
 // tokens wait on one another, so an SM with two blocks takes little longer than with one (2048
-// tokens, 4096 channels a sequence: 343, 404, 550 and 697 us with one to four), and two passes cost
-// 1.5 times the arithmetic of one: 128 blocks take 287 us in four chunks and 343 in one, 192 blocks
-// 380 and 404, 256 blocks 515 and 404.  Four blocks an SM against three: 32768 tokens of 2048
-// channels 554 us against 627; chunks of 32 tokens against 64: 512 tokens of 1024 channels 28.5 us
-// against 31.3.
+// tokens, 4096 channels a sequence: 343, 397, 560 and 685 us with one to four), and two passes cost
+// 1.5 times the arithmetic of one: 128 blocks take 275 us in four chunks and 343 in one, 192 blocks
+// 380 and 397, 256 blocks 515 and 397.  Four blocks an SM against three: 32768 tokens of 2048
+// channels 554 us against 627 (512 now); chunks of 32 tokens against 64: 512 tokens of 1024 channels
+// 28.5 us against 31.3.
 void cut(int B, int T, int Dm, int N, int G, int* chunks, int* chunk) {
   const int L = lanes_for(N, kLaneStates), CH = 2 * kThreads / L;
   const long long blocks = (long long)B * G * ((Dm / G + CH - 1) / CH);
