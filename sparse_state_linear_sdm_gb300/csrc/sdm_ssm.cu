@@ -11,7 +11,7 @@
 // A GB300 SM does 32 exp2 and 31 such foursomes a clock (measured), so with N = 16 and bf16 the
 // arithmetic takes 1.5 times as long as HBM does for the 8 bytes of an element: the arithmetic is
 // what has to be kept fed.  16 x 2048 x 4096 x 16 bf16 takes 0.69 ms, a third of the exp2 rate: 121
-// instructions for 512 (t, d, n), 81 of them in the recurrence, at 65 % issue.  Two of an
+// instructions for 512 (t, d, n), 81 of them in the recurrence, at 67 % issue.  Two of an
 // instruction's operations are packed in the input product and the read-out; packing the exponent's
 // product costs more in moves than it saves (a loop of its own: 98 clocks a warp and 512 (t, d, n)
 // so, 115 with all of it packed, 102 with none).
