@@ -48,7 +48,8 @@ typedef enum {
   SDM_EBOUNDS = -5,      /* reserved: device-detected bounds error */
   SDM_EUNSUPPORTED = -6, /* sizes valid for the method but beyond the library's limits */
   SDM_ENOSPACE = -7,     /* the workspace passed is smaller than required */
-  SDM_ESCRATCH = -8      /* too large for sdm_scan_forward_noalloc's fixed scratch */
+  SDM_ESCRATCH = -8,     /* too large for sdm_scan_forward_noalloc's fixed scratch */
+  SDM_EOVERLAP = -9      /* an output overlaps another tensor of the call */
 } sdm_status;
 
 typedef enum { SDM_F32 = 0, SDM_BF16 = 1 } sdm_dtype;
@@ -489,12 +490,16 @@ typedef enum { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1, SDM_ACT_GELU = 2 } sdm_activa
 #define SDM_MAX_CONV 8    /* taps of the short convolution */
 #define SDM_MAX_SSM_N 128 /* states a channel of the selective scan */
 
+#define SDM_CONV_IN_PLACE 8 /* tokens of a convolution whose y may be x */
+
 /* sdm_causal_conv - short causal depthwise convolution over T tokens (T = 1: one decode token):
  *   y[b,t,d] = act(bias[d] + sum_{j<K} w[d,j] u[b, t-K+1+j, d])
  * with u the K-1 inputs before token 0 (the state) followed by x.
  *   x [B, T, D] dt;  w [D, K], bias [D] (or NULL) w_dt;  y [B, T, D] dt, dense.
  *   state, state_out [n_slots, K-1, D] dt: the last K-1 inputs, oldest first.
- *   act: SDM_ACT_NONE or SDM_ACT_SILU.  Requires 2 <= K <= SDM_MAX_CONV. */
+ *   act: SDM_ACT_NONE or SDM_ACT_SILU.  Requires 2 <= K <= SDM_MAX_CONV.
+ * y overlaps nothing else (SDM_EOVERLAP), except that up to SDM_CONV_IN_PLACE tokens, which one
+ * thread walks, it may be x itself: a token of a longer prompt is read for the K-1 after it too. */
 int sdm_causal_conv(const void* x, long long x_bstride, long long x_tstride, int dt, const void* w,
                     const void* bias, int w_dt, int B, int T, int D, int K, int act,
                     const void* state, void* state_out, int n_slots, const int32_t* lengths,

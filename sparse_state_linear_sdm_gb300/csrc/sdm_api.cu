@@ -17,6 +17,7 @@ const char* sdm_status_str(int status) {
     case SDM_EBOUNDS: return "device-detected bounds error";
     case SDM_EUNSUPPORTED: return "sizes beyond the library's limits";
     case SDM_ENOSPACE: return "workspace smaller than required";
+    case SDM_EOVERLAP: return "an output overlaps another tensor of the call";
     case SDM_ESCRATCH: return "problem too large for the fixed no-allocation scratch";
     default: return "unknown status";
   }

@@ -35,6 +35,7 @@ struct Raised {};
   throw Raised();
 }
 [[noreturn]] void raise_status(const char* fn, int status) {
+  if (status == SDM_EOVERLAP) raise(PyExc_ValueError, "%s: an output overlaps another tensor of the call", fn);
   PyObject* e = PyObject_CallFunction(sdm_error, "si", fn, status);
   if (e) {
     PyErr_SetObject(sdm_error, e);

@@ -19,6 +19,7 @@ namespace {
 constexpr int kConvThreads = 64;
 constexpr int kAhead = 8;  // tokens under way: a register word each, reloaded as soon as it is taken
 constexpr int kMinStrip = 8;  // shortest strip: longer than the window
+static_assert(kMinStrip == SDM_CONV_IN_PLACE, "so many tokens are one strip");
 
 struct ConvArgs {
   const void* x;
@@ -270,6 +271,17 @@ extern "C" int sdm_causal_conv(const void* x, long long x_bstride, long long x_t
     return SDM_EALIGN;
   if (T > 0 && (!x || !y || off(x, odd) || off(y, odd))) return SDM_EALIGN;
   if (T == 0 && (state == state_out || !state_out)) return SDM_OK;
+  const long long row = (long long)D * es, wes = w_dt == SDM_F32 ? 4 : 2, taps = K - 1;
+  const Extent ex{x, B, x_bstride * es, T, x_tstride * es, row};
+  const long long yn = (long long)B * T * row;
+  // y as x: every strip but the first reads the end of the one before it, which another thread may
+  // have overwritten; so may the first, which keeps the sequence's end as the state.
+  const bool in_place = x == y && T <= kMinStrip && (B == 1 || x_bstride == (long long)T * D) &&
+                        (T == 1 || x_tstride == D);
+  for (const Extent& e : {in_place ? Extent{} : ex, dense(w, wes * D * K), dense(bias, wes * D),
+                          dense(state, n_slots * taps * row), dense(state_out, n_slots * taps * row),
+                          dense(lengths, 4LL * B), dense(slots, 4LL * B)})
+    if (meets(e, y, yn)) return SDM_EOVERLAP;
 
   const int V = 16 / es;
   // 16-byte pieces where every row of every operand starts on 16 bytes, else single elements.

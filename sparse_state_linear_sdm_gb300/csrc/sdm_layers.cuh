@@ -121,6 +121,37 @@ __device__ __forceinline__ float softplus(float x) {
   return a;
 }
 
+// The memory of a tensor of a call: n1 x n2 rows of `bytes`, s1 and s2 bytes apart.
+struct Extent {
+  const void* p;
+  long long n1, s1, n2, s2, bytes;
+};
+inline Extent dense(const void* p, long long bytes) { return {p, 1, 0, 1, 0, bytes}; }
+
+// Whether any byte of `e` lies in the `bytes` from p on.
+inline bool meets(const Extent& e, const void* p, long long bytes) {
+  if (!e.p || !p || e.n1 < 1 || e.n2 < 1 || e.bytes < 1 || bytes < 1) return false;
+  // a: the start of e's lowest row, as a distance from p
+  long long a = (long long)(reinterpret_cast<uintptr_t>(e.p) - reinterpret_cast<uintptr_t>(p));
+  long long n1 = e.n1, n2 = e.n2, s1 = e.s1, s2 = e.s2;
+  if (s1 < 0) a += (n1 - 1) * s1, s1 = -s1;
+  if (s2 < 0) a += (n2 - 1) * s2, s2 = -s2;
+  if (a >= bytes || a + (n1 - 1) * s1 + (n2 - 1) * s2 + e.bytes <= 0) return false;
+  if (n1 > n2) {
+    long long t = n1;
+    n1 = n2, n2 = t;
+    t = s1, s1 = s2, s2 = t;
+  }
+  // Row by row of the shorter direction: the first row of the other that ends past p starts before
+  // the end, or none does.
+  for (long long i = 0; i < n1; ++i, a += s1) {
+    const long long short_by = -(a + e.bytes);  // 0 or more: row 0 ends before p
+    const long long j = short_by < 0 ? 0 : s2 ? short_by / s2 + 1 : n2;
+    if (j < n2 && a + j * s2 < bytes) return true;
+  }
+  return false;
+}
+
 // The sequence length of batch row b, clamped to [0, T] (T without lengths).
 __device__ __forceinline__ int row_length(const int32_t* lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;

@@ -357,3 +357,42 @@ def test_layer_calls_refuse_what_they_cannot_run():
     chunked = _scan_case(SCAN[10])
     with pytest.raises(sdm.SDMError):
         sdm.selective_scan(**chunked, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+# ---- outputs that share memory with inputs ----
+
+
+def _expects_overlap(call):
+    with pytest.raises(ValueError, match="overlaps"):
+        call()
+
+
+def test_conv_output_over_its_input():
+    """Up to eight tokens y may be x; a longer prompt's may not, nor may it touch another tensor of the call."""
+    for T, dtype in ((1, "bf16"), (4, "f32"), (8, "bf16"), (8, "f32")):
+        rn, ty = _gen(21), TYPES[dtype]
+        x, w, st = rn(3, T, 512).to(ty), rn(512, 4).to(ty), rn(3, 3, 512).to(ty)
+        want, end = sdm.causal_conv(x, w, state=st, state_out=torch.empty_like(st))
+        got, kept = sdm.causal_conv(x, w, state=st, state_out=torch.empty_like(st), out=x)
+        assert got is x and torch.equal(got, want) and torch.equal(kept, end)
+    rn = _gen(22)
+    w = rn(512, 4)
+    for T in (9, 1000):
+        x = rn(1, T, 512)
+        kept = x.clone()
+        _expects_overlap(lambda: sdm.causal_conv(x, w, out=x))
+        assert torch.equal(x, kept)
+    both = rn(1, 16, 512)
+    _expects_overlap(lambda: sdm.causal_conv(both[:, 5:15], w, out=both[:, :10]))
+    _expects_overlap(lambda: sdm.causal_conv(rn(1, 4, 512), w, out=w.view(1, 4, 512)))
+
+
+def test_conv_output_between_the_rows_of_its_input():
+    """Memory that lies between the sequences of a strided x is not x's: y may be there."""
+    rn = _gen(23)
+    wide = rn(2, 3, 40, 64)
+    x, room = wide[:, 0], wide[0, 1:]
+    w = rn(64, 4)
+    want, _ = sdm.causal_conv(x, w)
+    got, _ = sdm.causal_conv(x, w, out=room)
+    assert got is room and torch.equal(got, want)

@@ -130,3 +130,24 @@ def test_python_calls_refuse_host_tensors():
                  lambda: sdm.project_gated_backward(x, torch.zeros(16, 8), x)):
         with pytest.raises(TypeError):
             call()
+
+
+EOVERLAP = -9
+FAR = 0x4000000  # past every tensor at FAKE
+
+
+def test_conv_refuses_an_output_over_another_tensor():
+    """A prompt's strips read tokens that other threads' outputs would replace.  Nothing here is launched."""
+    apart = dict(w=FAR, bias=FAR + 0x1000, state=FAR + 0x2000, out=FAR + 0x4000)
+    long = dict(apart, B=1, T=4096, ts=16, bs=4096 * 16, rows=1)
+    nbytes = 4096 * 16 * 2
+    assert conv(**long) == EOVERLAP                                          # y is x
+    assert conv(**dict(long, y=FAKE + nbytes - 16)) == EOVERLAP              # x's last bytes
+    assert conv(**dict(long, y=FAKE - nbytes + 16)) == EOVERLAP              # and its first
+    assert conv(**dict(long, T=9, bs=9 * 16)) == EOVERLAP
+    assert conv(**dict(apart, y=FAKE, ts=32, bs=128)) == EOVERLAP            # a slice's rows, not where y's are
+    assert conv(**dict(apart, T=1, y=FAKE, bs=32)) == EOVERLAP
+    for name in ("w", "bias", "state", "out"):
+        assert conv(**dict(long, y=apart[name])) == EOVERLAP, name
+    assert conv(**dict(long, y=FAR + 0x8000, lengths=FAR + 0x8000)) == EOVERLAP
+    assert conv(**dict(long, y=FAR + 0x8000, slots=FAR + 0x8004)) == EOVERLAP
