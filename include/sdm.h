@@ -484,7 +484,8 @@ int sdm_gen_M0(unsigned long long seed, int H, long long N, int d_v, float scale
  *            and no state is touched.  A slot >= n_slots is treated as padding and reported as
  *            SDM_DEV_INDEX_RANGE.  Live slots of one call are distinct.
  *   state    read (NULL: zeros); state_out written (NULL: not kept); the same buffer updates it
- *            in place.  n_slots: rows of either. */
+ *            in place.  n_slots: rows of either.  Otherwise state_out overlaps nothing that the
+ *            call reads (SDM_EOVERLAP). */
 typedef enum { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1, SDM_ACT_GELU = 2 } sdm_activation;
 
 #define SDM_MAX_CONV 8    /* taps of the short convolution */

@@ -282,6 +282,11 @@ extern "C" int sdm_causal_conv(const void* x, long long x_bstride, long long x_t
                           dense(state, n_slots * taps * row), dense(state_out, n_slots * taps * row),
                           dense(lengths, 4LL * B), dense(slots, 4LL * B)})
     if (meets(e, y, yn)) return SDM_EOVERLAP;
+  const long long sn = n_slots * taps * row;
+  for (const Extent& e : {ex, dense(w, wes * D * K), dense(bias, wes * D),
+                          state == state_out ? Extent{} : dense(state, sn), dense(lengths, 4LL * B),
+                          dense(slots, 4LL * B)})
+    if (meets(e, state_out, sn)) return SDM_EOVERLAP;
 
   const int V = 16 / es;
   // 16-byte pieces where every row of every operand starts on 16 bytes, else single elements.

@@ -396,3 +396,19 @@ def test_conv_output_between_the_rows_of_its_input():
     want, _ = sdm.causal_conv(x, w)
     got, _ = sdm.causal_conv(x, w, out=room)
     assert got is room and torch.equal(got, want)
+
+
+def test_new_states_over_old_ones():
+    """The same rows or others, not some of both."""
+    rn = _gen(24)
+    x, w, pool = rn(2, 6, 32), rn(32, 4), rn(3, 3, 32)
+    _expects_overlap(lambda: sdm.causal_conv(x, w, state=pool[:2], state_out=pool[1:]))
+    _expects_overlap(lambda: sdm.causal_conv_step(x[:, 0], w, state=pool[1:], state_out=pool[:2]))
+    k = _scan_case(SCAN[5])
+    pool = rn(3, *k["state"].shape[1:])
+    _expects_overlap(lambda: sdm.selective_scan(**{**k, "state": pool[:2]}, state_out=pool[1:]))
+    both = rn(4, *k["state"].shape[1:])
+    both[:2] = k["state"]
+    want, end = sdm.selective_scan(**k, state_out=torch.empty_like(k["state"]))
+    got, _ = sdm.selective_scan(**{**k, "state": both[:2]}, state_out=both[2:])     # side by side
+    assert torch.equal(got, want) and torch.equal(both[2:], end) and torch.equal(both[:2], k["state"])

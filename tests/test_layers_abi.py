@@ -151,3 +151,23 @@ def test_conv_refuses_an_output_over_another_tensor():
         assert conv(**dict(long, y=apart[name])) == EOVERLAP, name
     assert conv(**dict(long, y=FAR + 0x8000, lengths=FAR + 0x8000)) == EOVERLAP
     assert conv(**dict(long, y=FAR + 0x8000, slots=FAR + 0x8004)) == EOVERLAP
+
+
+def test_new_states_over_what_the_call_reads_are_refused():
+    """One sequence's new state would replace what another still reads.  Nothing here is launched."""
+    apart = dict(w=FAR, bias=FAR + 0x1000, y=FAR + 0x8000)
+    row = 3 * 16 * 2                                     # a sequence's state of the convolution, in bytes
+    assert conv(**apart, state=FAR + 0x2000, out=FAR + 0x2000 + row) == EOVERLAP
+    assert conv(**apart, state=FAR + 0x2000 + row, out=FAR + 0x2000) == EOVERLAP
+    for over in (FAKE, FAR, FAR + 0x1000):
+        assert conv(**apart, state=FAR + 0x2000, out=over) == EOVERLAP, hex(over)
+    assert conv(**apart, state=FAR + 0x2000, out=FAR + 0x4000, lengths=FAR + 0x4000) == EOVERLAP
+    assert conv(T=0, **apart, state=FAR + 0x2000, out=FAR + 0x2000 + row) == EOVERLAP
+    apart = dict(A=FAR, D=FAR + 0x1000, dt_bias=FAR + 0x1800, y=FAR + 0x8000)
+    row = 16 * 8 * 4
+    for T in (1, 4):
+        assert scan(**apart, T=T, state=FAR + 0x2000, state_out=FAR + 0x2000 + row) == EOVERLAP
+        assert scan(**apart, T=T, state=FAR + 0x2000 + row, state_out=FAR + 0x2000) == EOVERLAP
+        for over in (FAKE, FAR, FAR + 0x1000, FAR + 0x1800):
+            assert scan(**apart, T=T, state=FAR + 0x4000, state_out=over) == EOVERLAP, hex(over)
+        assert scan(**apart, T=T, state=0, state_out=FAR + 0x2000, slots=FAR + 0x2000) == EOVERLAP
