@@ -510,7 +510,9 @@ int sdm_causal_conv(const void* x, long long x_bstride, long long x_tstride, int
  *   delta = softplus(dt + dt_bias) (softplus 0: without it)
  *   h_t[d,n] = exp(delta_t[d] A[d,n]) h_{t-1}[d,n] + delta_t[d] x_t[d] B_t[g,n]
  *   y_t[d] = (sum_n C_t[g,n] h_t[d,n] + D[d] x_t[d]) silu(z_t[d]),  g = d / (Dm / G)
- * Requires Dm % G == 0 and 1 <= N <= SDM_MAX_SSM_N.  States and sums are fp32. */
+ * Requires Dm % G == 0 and 1 <= N <= SDM_MAX_SSM_N.  States and sums are fp32.
+ * y may be x, dt or z itself (dense ones: a block reads of these only what it writes); otherwise
+ * it and the workspace overlap nothing else (SDM_EOVERLAP). */
 typedef struct {
   const void *x, *dt, *Bm, *Cm, *z; /* [B,T,Dm], [B,T,Dm], [B,T,G,N] (2x), [B,T,Dm] or NULL */
   long long x_bs, x_ts, dt_bs, dt_ts, B_bs, B_ts, C_bs, C_ts, z_bs, z_ts;

@@ -748,21 +748,30 @@ bool sizes_ok(int B, int T, int Dm, int N, int G) {
   return B >= 1 && T >= 0 && Dm >= 1 && N >= 1 && G >= 1 && Dm % G == 0;
 }
 
-// Whether the new states overlap what the call reads; the state itself may be updated in place.
-bool overlap(const sdm_ssm_args& io) {
+// Whether y, the new states or the workspace overlap anything else of the call.  The state may be
+// updated in place, and y may be x, dt or z: a block reads of these only the tokens and channels whose
+// y it writes, a tile into shared memory before that tile's y; the pass that reduces chunks is over
+// when the first y is written.
+bool overlap(const sdm_ssm_args& io, const void* workspace, size_t workspace_bytes) {
   const long long es = io.dtype == SDM_F32 ? 4 : 2, row = io.Dm * es, bc = (long long)io.G * io.N * es;
-  const long long sn = 4LL * io.n_slots * io.Dm * io.N;
+  const long long sn = 4LL * io.n_slots * io.Dm * io.N, yn = (long long)io.B * io.T * row, wn = (long long)workspace_bytes;
   auto rows = [&](const void* p, long long bs, long long ts, long long bytes) {
     return Extent{p, io.B, bs * es, io.T, ts * es, bytes};
   };
-  for (const Extent& e :
-       {rows(io.x, io.x_bs, io.x_ts, row), rows(io.dt, io.dt_bs, io.dt_ts, row), rows(io.z, io.z_bs, io.z_ts, row),
-        rows(io.Bm, io.B_bs, io.B_ts, bc), rows(io.Cm, io.C_bs, io.C_ts, bc), dense(io.A, 4LL * io.Dm * io.N),
-        dense(io.D, 4LL * io.Dm), dense(io.dt_bias, 4LL * io.Dm),
-        io.state == io.state_out ? Extent{} : dense(io.state, sn), dense(io.lengths, 4LL * io.B),
-        dense(io.slots, 4LL * io.B)})
-    if (meets(e, io.state_out, sn)) return true;
-  return false;
+  auto like_y = [&](const Extent& e) {
+    return e.p == io.y && (io.B == 1 || e.s1 == io.T * row) && (io.T == 1 || e.s2 == row);
+  };
+  const Extent state = dense(io.state, sn), y = dense(io.y, yn);
+  for (const Extent& e : {rows(io.x, io.x_bs, io.x_ts, row), rows(io.dt, io.dt_bs, io.dt_ts, row),
+                          rows(io.z, io.z_bs, io.z_ts, row)})
+    if ((!like_y(e) && meets(e, io.y, yn)) || meets(e, io.state_out, sn) || meets(e, workspace, wn)) return true;
+  for (const Extent& e : {rows(io.Bm, io.B_bs, io.B_ts, bc), rows(io.Cm, io.C_bs, io.C_ts, bc),
+                          dense(io.A, 4LL * io.Dm * io.N), dense(io.D, 4LL * io.Dm), dense(io.dt_bias, 4LL * io.Dm),
+                          dense(io.lengths, 4LL * io.B), dense(io.slots, 4LL * io.B)})
+    if (meets(e, io.y, yn) || meets(e, io.state_out, sn) || meets(e, workspace, wn)) return true;
+  return (io.state != io.state_out && meets(state, io.state_out, sn)) || meets(state, io.y, yn) ||
+         meets(state, workspace, wn) || meets(y, io.state_out, sn) || meets(y, workspace, wn) ||
+         meets(dense(io.state_out, sn), workspace, wn);
 }
 
 }  // namespace
@@ -802,7 +811,7 @@ extern "C" int sdm_selective_scan(const sdm_ssm_args* args, void* workspace, siz
   a.dev_err = dev_err;
   cudaStream_t s = as_stream(stream);
   if (io.T == 1) {
-    if (overlap(io)) return SDM_EOVERLAP;
+    if (overlap(io, nullptr, 0)) return SDM_EOVERLAP;
     // Four states a word, and four entries of B and C (8 bytes of bf16, 16 of fp32).
     const uintptr_t word = io.dtype == SDM_F32 ? 15 : 7;
     a.vec = io.N % 4 == 0 && !off(io.A, 15) && !off(io.state, 15) && !off(io.state_out, 15);
@@ -818,7 +827,7 @@ extern "C" int sdm_selective_scan(const sdm_ssm_args* args, void* workspace, siz
     a.ws_h = static_cast<float*>(workspace);
     a.ws_d = a.ws_h + size_t(a.chunks) * io.B * io.Dm * a.ws_n;
   }
-  if (overlap(io)) return SDM_EOVERLAP;
+  if (overlap(io, need ? workspace : nullptr, need)) return SDM_EOVERLAP;
   const int V = io.dtype == SDM_F32 ? 4 : 8;
   auto rows16 = [&](const void* p, long long bs, long long ts) {
     return !p || (!off(p, 15) && bs % V == 0 && ts % V == 0);

@@ -412,3 +412,29 @@ def test_new_states_over_old_ones():
     want, end = sdm.selective_scan(**k, state_out=torch.empty_like(k["state"]))
     got, _ = sdm.selective_scan(**{**k, "state": both[:2]}, state_out=both[2:])     # side by side
     assert torch.equal(got, want) and torch.equal(both[2:], end) and torch.equal(both[:2], k["state"])
+
+
+def _dense_scan(T, dtype, seed=25):
+    rn, ty = _gen(seed), TYPES[dtype]
+    return dict(x=rn(2, T, 48).to(ty), dt=rn(2, T, 48).to(ty), z=rn(2, T, 48).to(ty), A=-torch.exp(rn(48, 16)),
+                B=rn(2, T, 16).to(ty), C=rn(2, T, 16).to(ty), state=rn(2, 48, 16))
+
+
+@pytest.mark.parametrize("T", [1, 70, 700])
+@pytest.mark.parametrize("name", ["x", "dt", "z"])
+def test_scan_output_over_x_dt_or_z(name, T):
+    for dtype in ("bf16", "f32"):
+        k = _dense_scan(T, dtype)
+        want, end = sdm.selective_scan(**k, state_out=torch.empty_like(k["state"]))
+        got, st = sdm.selective_scan(**k, state_out=torch.empty_like(k["state"]), out=k[name])
+        assert got is k[name] and torch.equal(got, want) and torch.equal(st, end)
+
+
+def test_scan_output_over_anything_else():
+    k = _dense_scan(33, "f32")
+    wide = torch.zeros(2, 34, 48, device="cuda")
+    _expects_overlap(lambda: sdm.selective_scan(**{**k, "x": wide[:, 1:]}, out=wide.view(-1)[:2 * 33 * 48].view(2, 33, 48)))
+    flat = torch.zeros(2 * 33 * 48, device="cuda")
+    _expects_overlap(lambda: sdm.selective_scan(**{**k, "B": flat[:2 * 33 * 16].view(2, 33, 16)}, out=flat.view(2, 33, 48)))
+    _expects_overlap(lambda: sdm.selective_scan(**{**k, "state": flat[:2 * 48 * 16].view(2, 48, 16)},
+                                                out=flat.view(2, 33, 48)))

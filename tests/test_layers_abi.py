@@ -171,3 +171,23 @@ def test_new_states_over_what_the_call_reads_are_refused():
         for over in (FAKE, FAR, FAR + 0x1000, FAR + 0x1800):
             assert scan(**apart, T=T, state=FAR + 0x4000, state_out=over) == EOVERLAP, hex(over)
         assert scan(**apart, T=T, state=0, state_out=FAR + 0x2000, slots=FAR + 0x2000) == EOVERLAP
+
+
+def test_scan_refuses_outputs_over_another_tensor():
+    """y may be x, dt or z, but not begin elsewhere in them, nor lie over what every block reads.  Nothing here is
+    launched."""
+    apart = dict(x=FAR, dt=FAR + 0x10000, z=FAR + 0x20000, Bm=FAR + 0x30000, Cm=FAR + 0x40000, A=FAR + 0x50000,
+                 D=FAR + 0x60000, dt_bias=FAR + 0x70000, state=FAR + 0x80000, state_out=FAR + 0x90000,
+                 lengths=FAR + 0xA0000, slots=FAR + 0xB0000)
+    for T in (1, 4):
+        for name in ("Bm", "Cm", "A", "D", "dt_bias", "state", "state_out", "lengths", "slots"):
+            assert scan(**apart, T=T, y=apart[name]) == EOVERLAP, name
+        for name in ("x", "dt", "z"):
+            assert scan(**apart, T=T, y=apart[name] + 16) == EOVERLAP, name
+            assert scan(**{**apart, name + "_bs": 16 * T + 16}, T=T, y=apart[name]) == EOVERLAP, name
+    assert scan(**apart, z_ts=32, z_bs=128, y=apart["z"]) == EOVERLAP        # half of a wider projection
+    need = sdm.selective_scan_workspace_size(1, 4096, 64, 16)
+    big = {n: FAR + (i << 24) for i, n in enumerate(apart)}
+    long = dict(big, B=1, T=4096, Dm=64, N=16, n_slots=1, y=FAR + (20 << 24), ws_bytes=need, x_ts=64, dt_ts=64, z_ts=64)
+    for name in (*big, "y"):
+        assert scan(ws=long[name], **long) == EOVERLAP, name
