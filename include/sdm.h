@@ -533,7 +533,8 @@ int sdm_selective_scan(const sdm_ssm_args* args, void* workspace, size_t workspa
  * one kernel:  h = act(x Wg^T) * (x Wu^T).
  *   x [M, D] bf16;  w [2F, D] bf16, one row per output column: Wg's F rows, then Wu's;
  *   h [M, F] bf16;  act: SDM_ACT_SILU or SDM_ACT_GELU (the exact one, g Phi(g)).
- * fp32 accumulation, one rounding.  Requires D % 8 == 0 and F % 8 == 0 (SDM_EUNSUPPORTED). */
+ * fp32 accumulation, one rounding.  Requires D % 8 == 0 and F % 8 == 0 (SDM_EUNSUPPORTED).
+ * h overlaps neither x nor w (SDM_EOVERLAP). */
 int sdm_project_gated(const void* x, const void* w, long long M, int D, int F, int act, void* h,
                       int* dev_err, void* stream);
 
@@ -542,7 +543,8 @@ int sdm_project_gated(const void* x, const void* w, long long M, int D, int F, i
  * g and u are recomputed from x and w.  dx [M, D], dw [2F, D] bf16, summed in fp32; dg and du are
  * rounded to bf16 between the products.  M = 0 writes dw = 0.  The workspace holds [dg | du] and
  * the partial sums of products that are split over their reduction; results do not depend on
- * timing. */
+ * timing.  dx, dw and the workspace overlap neither one another nor x and w, nor the workspace dh
+ * (SDM_EOVERLAP); dh has been read when dx and dw are written. */
 size_t sdm_project_gated_backward_workspace_size(long long M, int D, int F);
 int sdm_project_gated_backward(const void* x, const void* w, const void* dh, long long M, int D,
                                int F, int act, void* dx, void* dw, void* workspace,

@@ -743,6 +743,8 @@ extern "C" int sdm_project_gated(const void* x, const void* w, long long M, int 
   if (st != SDM_OK) return st;
   if (M == 0) return SDM_OK;
   if (!aligned16(h)) return SDM_EALIGN;
+  const long long hn = M * F * 2;
+  if (meets(dense(x, M * D * 2), h, hn) || meets(dense(w, 4LL * F * D), h, hn)) return SDM_EOVERLAP;
   if (M <= kFewTokens)
     return act == SDM_ACT_SILU ? launch_few<SDM_ACT_SILU>(x, w, int(M), D, F, h, as_stream(stream))
                                : launch_few<SDM_ACT_GELU>(x, w, int(M), D, F, h, as_stream(stream));
@@ -772,10 +774,18 @@ extern "C" int sdm_project_gated_backward(const void* x, const void* w, const vo
   if (st != SDM_OK) return st;
   if (!aligned16(dw) || (M > 0 && (!aligned16(dh) || !aligned16(dx)))) return SDM_EALIGN;
   cudaStream_t s = as_stream(stream);
+  const long long xn = M * D * 2, wn = 4LL * F * D;
+  if (M == 0 && meets(dense(w, wn), dw, wn)) return SDM_EOVERLAP;
   if (M == 0)
     return cudaMemsetAsync(dw, 0, size_t(2) * F * D * 2, s) == cudaSuccess ? SDM_OK : SDM_ECUDA;
   if (!aligned16(workspace)) return SDM_EALIGN;
-  if (workspace_bytes < sdm_project_gated_backward_workspace_size(M, D, F)) return SDM_ENOSPACE;
+  const size_t need = sdm_project_gated_backward_workspace_size(M, D, F);
+  if (workspace_bytes < need) return SDM_ENOSPACE;
+  for (const Extent& e : {dense(x, xn), dense(w, wn), dense(workspace, (long long)need)})
+    if (meets(e, dx, xn) || meets(e, dw, wn)) return SDM_EOVERLAP;
+  if (meets(dense(dx, xn), dw, wn)) return SDM_EOVERLAP;
+  for (const Extent& e : {dense(x, xn), dense(w, wn), dense(dh, M * F * 2)})
+    if (meets(e, workspace, (long long)need)) return SDM_EOVERLAP;
   __nv_bfloat16* slope = static_cast<__nv_bfloat16*>(workspace);  // [dg | du], [M, 2F]
   Maps ts = {}, tg = {};
   GatedArgs a = {};

@@ -136,3 +136,21 @@ def test_gated_refuses_what_it_cannot_run():
         sdm.project_gated(x, w[:120].contiguous())                         # F % 8
     with pytest.raises(sdm.SDMError):
         sdm.project_gated_backward(x, w, dh, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_gated_outputs_over_other_tensors():
+    """Refused over x, w or one another; dh's memory may take dx, which is written when dh has been read."""
+    for M in (5, 300):
+        x, w, dh = _inputs(M, 128, 128, seed=9)
+        kept = x.clone()
+        with pytest.raises(ValueError, match="overlaps"):
+            sdm.project_gated(x, w, out=x)
+        both = torch.empty(M * 128 + 256 * 128, dtype=torch.bfloat16, device="cuda")
+        for outs in (dict(dx=x), dict(dw=w),
+                     dict(dx=both[:M * 128].view(M, 128), dw=both[M * 128 - 8:][:256 * 128].view(256, 128))):
+            with pytest.raises(ValueError, match="overlaps"):
+                sdm.project_gated_backward(x, w, dh, **outs)
+        assert torch.equal(x, kept)
+        want = sdm.project_gated_backward(x, w, dh)
+        dx, dw = sdm.project_gated_backward(x, w, dh, dx=dh)
+        assert dx is dh and torch.equal(dx, want[0]) and torch.equal(dw, want[1])

@@ -191,3 +191,27 @@ def test_scan_refuses_outputs_over_another_tensor():
     long = dict(big, B=1, T=4096, Dm=64, N=16, n_slots=1, y=FAR + (20 << 24), ws_bytes=need, x_ts=64, dt_ts=64, z_ts=64)
     for name in (*big, "y"):
         assert scan(ws=long[name], **long) == EOVERLAP, name
+
+
+def test_gated_refuses_outputs_over_another_tensor():
+    """Tiles of x and w are read while others' outputs are written.  Nothing here is launched."""
+    f = sdm.lib().sdm_project_gated
+    f.argtypes = [P, P, LL, I, I, I, P, P, P]
+    for M in (4, 40):                                    # few tokens, and tiles
+        n = M * 64 * 2
+        for h in (FAKE, FAKE + n - 16, FAKE - n + 16, FAR, FAR + 128 * 64 * 2 - 16):
+            assert f(FAKE, FAR, M, 64, 64, 1, h, None, None) == EOVERLAP, (M, hex(h))
+    b = sdm.lib().sdm_project_gated_backward
+    b.argtypes = [P, P, P, LL, I, I, I, P, P, P, SZ, P, P]
+    need = sdm.project_gated_backward_workspace_size(40, 64, 64)
+    at = dict(x=FAR, w=FAR + (1 << 20), dh=FAR + (2 << 20), dx=FAR + (3 << 20), dw=FAR + (4 << 20), ws=FAR + (5 << 20))
+
+    def grad(**kw):
+        a = {**at, **kw}
+        return b(a["x"], a["w"], a["dh"], 40, 64, 64, 1, a["dx"], a["dw"], a["ws"], need, None, None)
+
+    for out, over in (("dx", ("x", "w", "dw", "ws")), ("dw", ("x", "w", "dx", "ws")), ("ws", ("x", "w", "dh", "dx", "dw"))):
+        for name in over:
+            assert grad(**{out: at[name]}) == EOVERLAP, (out, name)
+            assert grad(**{out: at[name] + 16}) == EOVERLAP, (out, name)
+    assert b(None, FAR, None, 0, 64, 64, 1, None, FAR, None, 0, None, None) == EOVERLAP
