@@ -488,6 +488,8 @@ int sdm_gen_M0(unsigned long long seed, int H, long long N, int d_v, float scale
  *            call reads (SDM_EOVERLAP). */
 typedef enum { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1, SDM_ACT_GELU = 2 } sdm_activation;
 
+/* B * T <= 2^31 - 1, and T short of 2^31 by the last strip's or chunk's rounding
+ * (SDM_EUNSUPPORTED). */
 #define SDM_MAX_CONV 8    /* taps of the short convolution */
 #define SDM_MAX_SSM_N 128 /* states a channel of the selective scan */
 

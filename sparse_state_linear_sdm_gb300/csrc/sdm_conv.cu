@@ -261,7 +261,10 @@ extern "C" int sdm_causal_conv(const void* x, long long x_bstride, long long x_t
                                int* dev_err, void* stream) {
   if (B < 1 || T < 0 || D < 1 || K < 2 || bad_dtype(dt) || bad_dtype(w_dt)) return SDM_EINVAL;
   if (act != SDM_ACT_NONE && act != SDM_ACT_SILU) return SDM_EINVAL;
-  if (K > SDM_MAX_CONV || (long long)B * T > 0x7FFFFFFFLL || D > 0x7FFFFFF) return SDM_EUNSUPPORTED;
+  // A token's index may run past T by a strip and the tokens under way, and stays an int.
+  constexpr int kPast = 256;
+  if (K > SDM_MAX_CONV || (long long)B * T > 0x7FFFFFFFLL || T > 0x7FFFFFFF - kPast || D > 0x7FFFFFF)
+    return SDM_EUNSUPPORTED;
   if ((state || state_out || slots) && n_slots < (slots ? 1 : B)) return SDM_EINVAL;
   const int es = dt == SDM_F32 ? 4 : 2;
   const uintptr_t odd = uintptr_t(es - 1), wodd = uintptr_t(w_dt == SDM_F32 ? 3 : 1);

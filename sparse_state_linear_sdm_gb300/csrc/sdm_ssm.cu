@@ -733,15 +733,15 @@ int launch_token(ScanArgs& a, cudaStream_t s) {
 // 380 and 397, 256 blocks 515 and 397.  Four blocks an SM against three: 32768 tokens of 2048
 // channels 554 us against 627 (512 now); chunks of 32 tokens against 64: 512 tokens of 1024 channels
 // 28.5 us against 31.3.
-void cut(int B, int T, int Dm, int N, int G, int* chunks, int* chunk) {
+void cut(int B, int T, int Dm, int N, int G, int* chunks, long long* chunk) {
   const int L = lanes_for(N, kLaneStates), CH = 2 * kThreads / L;
-  const long long blocks = (long long)B * G * ((Dm / G + CH - 1) / CH);
+  const long long blocks = (long long)B * G * (((long long)Dm / G + CH - 1) / CH);
   long long n = blocks >= 208 ? 1 : 608 / blocks;
   n = n < T / kMinChunk ? n : T / kMinChunk;
   if (n < 1) n = 1;
-  const int per = int(((T + n - 1) / n + kTT - 1) / kTT) * kTT;
+  const long long per = ((T + n - 1) / n + kTT - 1) / kTT * kTT;
   *chunk = per;
-  *chunks = T > 0 ? (T + per - 1) / per : 1;
+  *chunks = T > 0 ? int((T + per - 1) / per) : 1;
 }
 
 bool sizes_ok(int B, int T, int Dm, int N, int G) {
@@ -781,7 +781,8 @@ using namespace sdm;
 
 extern "C" size_t sdm_selective_scan_workspace_size(int B, int T, int Dm, int N, int G) {
   if (!sizes_ok(B, T, Dm, N, G) || N > SDM_MAX_SSM_N) return 0;
-  int chunks, chunk;
+  int chunks;
+  long long chunk;
   cut(B, T, Dm, N, G, &chunks, &chunk);
   if (chunks <= 1) return 0;
   return size_t(chunks) * B * Dm * ((N + 3) / 4 * 4 + 1) * 4;
@@ -794,6 +795,11 @@ extern "C" int sdm_selective_scan(const sdm_ssm_args* args, void* workspace, siz
   if (!sizes_ok(io.B, io.T, io.Dm, io.N, io.G) || bad_dtype(io.dtype)) return SDM_EINVAL;
   if (io.N > SDM_MAX_SSM_N || (long long)io.B * io.T > 0x7FFFFFFFLL || io.Dm > 0x3FFFFFF)
     return SDM_EUNSUPPORTED;
+  int chunks;
+  long long chunk;
+  cut(io.B, io.T, io.Dm, io.N, io.G, &chunks, &chunk);
+  // A token's index may run past the last chunk's end by two tiles, and stays an int.
+  if (chunks * chunk > 0x7FFFFFFFLL - 2 * kTT) return SDM_EUNSUPPORTED;
   if ((io.state || io.state_out || io.slots) && io.n_slots < (io.slots ? 1 : io.B)) return SDM_EINVAL;
   const uintptr_t odd = io.dtype == SDM_F32 ? 3 : 1;
   auto off = [](const void* p, uintptr_t m) { return (reinterpret_cast<uintptr_t>(p) & m) != 0; };
@@ -819,7 +825,8 @@ extern "C" int sdm_selective_scan(const sdm_ssm_args* args, void* workspace, siz
     return io.dtype == SDM_F32 ? launch_token<float>(a, s) : launch_token<__nv_bfloat16>(a, s);
   }
   const size_t need = sdm_selective_scan_workspace_size(io.B, io.T, io.Dm, io.N, io.G);
-  cut(io.B, io.T, io.Dm, io.N, io.G, &a.chunks, &a.chunk);
+  a.chunks = chunks;
+  a.chunk = int(chunk);
   if (need) {
     if (!aligned16(workspace)) return SDM_EALIGN;
     if (workspace_bytes < need) return SDM_ENOSPACE;

@@ -215,3 +215,13 @@ def test_gated_refuses_outputs_over_another_tensor():
             assert grad(**{out: at[name]}) == EOVERLAP, (out, name)
             assert grad(**{out: at[name] + 16}) == EOVERLAP, (out, name)
     assert b(None, FAR, None, 0, 64, 64, 1, None, FAR, None, 0, None, None) == EOVERLAP
+
+
+def test_prompts_whose_token_indexes_would_wrap_are_refused():
+    """The last strip, chunk or tile of a prompt just under 2^31 tokens ends past 2^31.  Nothing here is launched."""
+    for T in (0x7FFFFFFF, 0x7FFFFFFF - 64):
+        assert conv(B=1, T=T, D=1, rows=1) == EUNSUPPORTED
+    for T in (0x7FFFFFFF, 0x7FFFFFFF - 20):
+        for Dm in (1, 1 << 20):                          # cut into many chunks, and whole
+            assert scan(B=1, T=T, Dm=Dm, n_slots=1) == EUNSUPPORTED
+    assert sdm.selective_scan_workspace_size(1, 0x7FFFFFFF, 1, 16) > 0
