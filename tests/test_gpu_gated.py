@@ -154,3 +154,52 @@ def test_gated_outputs_over_other_tensors():
         want = sdm.project_gated_backward(x, w, dh)
         dx, dw = sdm.project_gated_backward(x, w, dh, dx=dh)
         assert dx is dh and torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
+def _check_rows(got, want, label):
+    """Row by row in norm: a sum of terms of random sign whose factors dg and du were rounded by up to 2^-8 of themselves,
+    evenly, is off by 2^-8 / sqrt(3) of its own size in the mean, and its own rounding adds as much again in squares:
+    0.0032 in all, over a row's hundreds of entries.  2^-7 is 2.4 times that; eight wrong entries of a row of 2056 are
+    eight times 2^-7."""
+    off = np.linalg.norm(_host(got) - want, axis=1) / np.linalg.norm(want, axis=1)
+    assert (off < 2.0 ** -7).all(), f"{label}: row {int(off.argmax())} is {float(off.max()):.4f} of its norm off"
+
+
+def _check_slices(x, w, dh, act, dx, dw, tokens, columns):
+    """dx of some tokens and dw of some columns' rows of Wg and Wu (over all tokens) against the 64-bit definition, each
+    entry within its bound and each row in norm."""
+    F = w.shape[0] // 2
+    t = torch.as_tensor(tokens, device="cuda")
+    want, _, bound, _ = ref.gated_grad(_host(x[t]), _host(w), _host(dh[t]), act)
+    _check(dx[t], want, bound, "dx")
+    _check_rows(dx[t], want, "dx")
+    f = torch.as_tensor(columns, device="cuda")
+    rows = torch.cat([f, f + F])
+    _, want, _, bound = ref.gated_grad(_host(x), _host(w[rows]), _host(dh[:, f]), act)
+    _check(dw[rows], want, bound, "dw")
+    _check_rows(dw[rows], want, "dw")
+
+
+# The tiles of dx and dw together are more than the card's 76 pairs of SMs, so that a pair goes on from one unit to
+# another: both accumulators, ring phases carried over, and a unit of dw after one of dx.
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M,D,F", [(1000, 1024, 2736), (9000, 264, 4000), (5000, 776, 1304)])
+def test_gated_gradient_of_more_tiles_than_pairs(M, D, F, act):
+    x, w, dh = _inputs(M, D, F, seed=13)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dx, dw = sdm.project_gated_backward(x, w, dh, activation=act, dev_err=err)
+    assert err.item() == 0
+    _check_slices(x, w, dh, act, dx, dw, [*range(0, M, 61), *range(M - 20, M)], [*range(0, F, 53), *range(F - 20, F)])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M,D,F", [(21003, 1032, 5000), (2000, 2056, 9000), (45000, 520, 4104)])
+def test_gated_gradient_of_large_batches(M, D, F, act):
+    """608 tiles of dx and dw and more, a launch for each product, with ragged M, D and F."""
+    tiles = lambda n: -(-n // 256)  # noqa: E731
+    assert tiles(M) * tiles(D) + tiles(2 * F) * tiles(D) >= 608
+    x, w, dh = _inputs(M, D, F, seed=15)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dx, dw = sdm.project_gated_backward(x, w, dh, activation=act, dev_err=err)
+    assert err.item() == 0
+    _check_slices(x, w, dh, act, dx, dw, [*range(0, M, M // 40), *range(M - 10, M)], [*range(0, F, F // 40), *range(F - 10, F)])
