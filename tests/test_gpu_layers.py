@@ -438,3 +438,48 @@ def test_scan_output_over_anything_else():
     _expects_overlap(lambda: sdm.selective_scan(**{**k, "B": flat[:2 * 33 * 16].view(2, 33, 16)}, out=flat.view(2, 33, 48)))
     _expects_overlap(lambda: sdm.selective_scan(**{**k, "state": flat[:2 * 48 * 16].view(2, 48, 16)},
                                                 out=flat.view(2, 33, 48)))
+
+
+# ---- prompts cut in chunks ----
+
+CUT = [
+    # dtype, B, T, Dm, N, G, gate, skip, bias, softplus, lengths, pool, columns before x
+    ("bf16", 1, 1000, 256, 16, 1, True, True, True, True, None, 0, 0),           # one long prompt, 16-byte rows
+    ("bf16", 1, 300, 40, 32, 1, True, True, True, True, None, 0, 0),
+    ("f32", 1, 300, 40, 32, 2, True, False, True, True, None, 0, 0),
+    ("bf16", 2, 330, 48, 64, 1, False, True, True, True, (330, 101), 4, 0),
+    ("f32", 2, 300, 33, 64, 1, True, True, False, True, None, 0, 1),
+    ("bf16", 1, 290, 24, 100, 1, True, True, True, True, None, 0, 0),
+    ("f32", 3, 310, 24, 100, 2, True, True, True, True, (310, 64, 0), 5, 0),
+    ("bf16", 1, 350, 32, 128, 2, True, True, True, True, None, 0, 0),
+    ("f32", 1, 300, 18, 128, 1, False, False, False, True, None, 0, 0),
+    ("bf16", 2, 400, 300, 16, 2, True, True, True, True, None, 0, 0),            # groups of 150: a part of a tile
+    ("f32", 2, 300, 402, 12, 3, True, True, True, True, (299, 300), 3, 0),       # of 134
+    ("f32", 1, 500, 270, 16, 1, True, True, True, True, None, 0, 2),
+    ("bf16", 4, 200, 96, 8, 3, True, True, True, True, (200, 199, 31, 33), 0, 0),
+    ("bf16", 1, 450, 64, 16, 1, True, True, True, False, None, 0, 0),            # without softplus
+]
+
+
+@pytest.mark.parametrize("c", CUT, ids=[f"{c[0]}-{c[1]}x{c[2]}x{c[3]}-N{c[4]}-G{c[5]}" for c in CUT])
+def test_scan_in_chunks_against_its_definition(c):
+    """States that remember hundreds of tokens (rates of about 0.01 in the first half of the channels, steps of about
+    0.3), so that a wrong join of the chunks would show, and states that forget within a chunk.  The bound per token
+    covers the join's own roundings: a chunk's sum of c <= 64 step sizes is off by at most c U of itself, which moves its
+    decay by c U |A| sum, under the 6 U a token for the slow channels and scaled by the decay itself for the others."""
+    k = _scan_case(c, seed=31)
+    k["A"][:c[3] // 2] *= 0.01
+    assert sdm.selective_scan_workspace_size(c[1], c[2], c[3], c[4], c[5]) > 0
+    want, wstate, ey, es = _scan_ref(k)
+    y, out_state = sdm.selective_scan(**k, state_out=torch.zeros_like(k["state"]))
+    _check(y, want, ey, c[0], "y")
+    slots = k["slots"]
+    live = np.arange(k["state"].shape[0]) if slots is None else np.array([s for s in _host(slots).astype(int) if s >= 0])
+    at = torch.from_numpy(live).cuda()
+    _check(out_state[at], wstate[live], es[live], "f32", "state")
+    inplace = k["state"].clone()
+    y2, _ = sdm.selective_scan(**{**k, "state": inplace})
+    assert torch.equal(y2, y) and torch.equal(inplace[at], out_state[at])
+    rest = np.setdiff1d(np.arange(k["state"].shape[0]), live)
+    rest = torch.from_numpy(rest).cuda()
+    assert torch.equal(inplace[rest], k["state"][rest]) and not out_state[rest].any()
