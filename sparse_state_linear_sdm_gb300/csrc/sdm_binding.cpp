@@ -12,11 +12,11 @@
 #include <ATen/core/LegacyTypeDispatch.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
 #include <cstdio>
-#include <exception>
 #include <string>
 
 #include "../../include/sdm.h"
@@ -347,6 +347,19 @@ PyObject* gated_grad(PyObject* const* a) {
   return pair(dx.release(), dw.o);
 }
 
+// torch's own exceptions become the Python errors that its own calls raise (out of memory:
+// torch.OutOfMemoryError).
+template <PyObject* (*F)(PyObject* const*)>
+PyObject* translated(PyObject* const* args) {
+  HANDLE_TH_ERRORS
+  try {
+    return F(args);
+  } catch (const Raised&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
 // No C++ exception leaves an entry point.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -355,10 +368,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   try {
-    return F(args);
-  } catch (const Raised&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return translated<F>(args);
   } catch (...) {
     PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
   }

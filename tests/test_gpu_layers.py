@@ -483,3 +483,13 @@ def test_scan_in_chunks_against_its_definition(c):
     rest = np.setdiff1d(np.arange(k["state"].shape[0]), live)
     rest = torch.from_numpy(rest).cuda()
     assert torch.equal(inplace[rest], k["state"][rest]) and not out_state[rest].any()
+
+
+# ---- errors and empty batches ----
+
+
+def test_an_output_that_does_not_fit_is_an_out_of_memory_error():
+    x = torch.zeros(1 << 20, 8, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(1 << 21, 8, dtype=torch.bfloat16, device="cuda")       # h: 2 TB
+    with pytest.raises(torch.OutOfMemoryError):
+        sdm.project_gated(x, w)
