@@ -226,6 +226,7 @@ PyObject* conv(PyObject* const* a) {
   void* pe = c.dense(optional(a[9], "dev_err"), "dev_err", at::kInt, {1});
   Held y;
   void* py = output(c, a[8], "out", x.sizes(), ty, &y.o);
+  if (nb == 0) return pair(y.release(), st.written);
   const int r = sdm_causal_conv(px, bs, ts, dt, pw, pb, wdt, as_int(nb, "B"), as_int(T, "T"), as_int(D, "D"),
                                 as_int(K, "K"), act, st.in, st.out, st.rows, static_cast<const int32_t*>(pl),
                                 static_cast<const int32_t*>(ps), py, static_cast<int*>(pe), c.stream());
@@ -282,6 +283,7 @@ PyObject* scan(PyObject* const* a) {
   s.softplus = PyObject_IsTrue(a[10]);
   Held y;
   s.y = output(c, a[13], "out", x.sizes(), ty, &y.o);
+  if (nb == 0) return pair(y.release(), st.written);
   at::Tensor own;
   size_t bytes = 0;
   void* ws = c.workspace(optional(a[14], "workspace"),

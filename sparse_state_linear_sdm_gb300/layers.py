@@ -44,7 +44,8 @@ def causal_conv(x, w, bias=None, state=None, state_out=None, activation="silu", 
     fp32 or bf16, K from 2 to 8; state, state_out [rows, K-1, D] of x's type, the last K-1 inputs (state None:
     zeros; state_out None: `state` is updated in place, or not kept where there is none).  activation: "silu" or
     "none".  lengths: int32 [B], the tokens of each sequence that exist (y is 0 past them).  slots: int32 [B],
-    the row of the state each sequence uses, negative for a padding row.  Returns (y, state written)."""
+    the row of the state each sequence uses, negative for a padding row.  A batch of no sequences has an empty y.
+    Returns (y, state written)."""
     return (_module or _binding()).conv(x, w, bias, state, state_out, _activation(activation, ("silu", "none")),
                                         lengths, slots, out, dev_err, 2)
 

@@ -493,3 +493,26 @@ def test_an_output_that_does_not_fit_is_an_out_of_memory_error():
     w = torch.zeros(1 << 21, 8, dtype=torch.bfloat16, device="cuda")       # h: 2 TB
     with pytest.raises(torch.OutOfMemoryError):
         sdm.project_gated(x, w)
+
+
+def test_a_batch_of_no_sequences():
+    """An empty batch has an empty output and leaves the states alone, as the projections' does."""
+    rn = _gen(26)
+    x, w = rn(0, 7, 16), rn(16, 4)
+    y, st = sdm.causal_conv(x, w)
+    assert y.shape == (0, 7, 16) and y.dtype == x.dtype and st is None
+    pool, none = rn(3, 3, 16), torch.empty(0, dtype=torch.int32, device="cuda")
+    kept = pool.clone()
+    y, st = sdm.causal_conv_step(rn(0, 16), w, state=pool, slots=none)
+    assert y.shape == (0, 16) and st is pool and torch.equal(pool, kept)
+    y, st = sdm.causal_conv(x, w, state=rn(0, 3, 16), lengths=none)
+    assert y.shape == (0, 7, 16) and st.shape == (0, 3, 16)
+    A, pool = -torch.exp(rn(16, 4)), rn(2, 16, 4)
+    y, st = sdm.selective_scan(x, x, A, rn(0, 7, 4), rn(0, 7, 4), state=pool, slots=none)
+    assert y.shape == (0, 7, 16) and st is pool
+    y, st = sdm.selective_step(rn(0, 16), rn(0, 16), A, rn(0, 1, 4), rn(0, 1, 4), state=rn(0, 16, 4))
+    assert y.shape == (0, 16) and st.shape == (0, 16, 4)
+    with pytest.raises(ValueError):
+        sdm.causal_conv(x, rn(15, 4))
+    with pytest.raises(TypeError):
+        sdm.selective_scan(x, x, A.double(), rn(0, 7, 4), rn(0, 7, 4))
