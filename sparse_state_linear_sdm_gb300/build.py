@@ -5,7 +5,7 @@ Each translation unit under csrc/ is compiled by its own process (in parallel:
 nvcc for the library's, the host compiler for the binding's, against torch's
 headers), then linked into ``sparse_state_linear_sdm_gb300/libsdm.so`` and
 ``_layers.so``.  The CUDA runtime is linked statically into the library, so it
-loads on its own; the binding needs it and torch.
+builds and loads on its own; the binding needs it and torch.
 """
 from __future__ import annotations
 
@@ -22,6 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsdm.so")
 BINDING = os.path.join(PKG, "_layers.so")
 BINDING_SRC = os.path.join(CSRC, "sdm_binding.cpp")
+HEADER = os.path.join(os.path.dirname(PKG), "include", "sdm.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr"]
@@ -38,16 +39,18 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        BINDING_SRC, os.path.join(os.path.dirname(PKG), "include", "sdm.h")]
+def _newer_than(path, deps) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    """Whether the library is newer than its sources."""
+    return _newer_than(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [HEADER])
+
+
+def binding_up_to_date() -> bool:
+    """Whether the binding is newer than its sources."""
+    return _newer_than(BINDING, [BINDING_SRC, HEADER])
 
 
 def _run(cmd, what):
@@ -82,6 +85,7 @@ def _link_binding(obj: str) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Builds the library where it is absent or stale; returns its path."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -98,21 +102,32 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     srcs = _sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        binding = ex.submit(_compile_binding, cc)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
         objs = list(ex.map(compile_one, srcs))
-        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
     return LIB
 
 
+def build_binding(force: bool = False, **library) -> str:
+    """Builds the library (with the arguments of build()) and, beside it, the binding where they are absent or
+    stale; returns the binding's path."""
+    if not force and binding_up_to_date():
+        build(**library)
+        return BINDING
+    os.makedirs(BUILD, exist_ok=True)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        obj = ex.submit(_compile_binding, nvcc())
+        build(force=force, **library)
+        _link_binding(obj.result())
+    return BINDING
+
+
 if __name__ == "__main__":
-    build(force="--force" in sys.argv, verbose=True,
-          extra_flags=["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else [])
+    build_binding(force="--force" in sys.argv, verbose=True,
+                  extra_flags=["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else [])
     print(LIB)

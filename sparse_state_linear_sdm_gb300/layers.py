@@ -21,7 +21,7 @@ def _binding():
     global _module
     if _module is None:
         _api.lib()
-        spec = importlib.util.spec_from_file_location("_layers", _build.BINDING)
+        spec = importlib.util.spec_from_file_location("_layers", _build.build_binding())
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         m.set_error(_api.SDMError)

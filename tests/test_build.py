@@ -1,0 +1,38 @@
+"""What is rebuilt when: the library alone, and the binding beside it.  No GPU needed."""
+import os
+
+import pytest
+
+from sparse_state_linear_sdm_gb300 import build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build.build_binding()
+
+
+def test_what_was_just_built_is_current():
+    assert build.up_to_date() and build.binding_up_to_date()
+
+
+def test_the_library_is_built_without_the_binding(monkeypatch, tmp_path):
+    """No torch headers and no host compiler are needed for it."""
+    src = tmp_path / "one.cu"
+    src.write_text('extern "C" int one() { return 1; }\n')
+
+    def none(*_):
+        raise AssertionError("the binding is not the library's")
+
+    monkeypatch.setattr(build, "_sources", lambda: [str(src)])
+    monkeypatch.setattr(build, "BUILD", str(tmp_path / "obj"))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "absent.so"))
+    for name in ("_compile_binding", "_link_binding"):
+        monkeypatch.setattr(build, name, none)
+    assert build.build() == str(tmp_path / "lib.so") and os.path.exists(tmp_path / "lib.so")
+    assert not os.path.exists(build.BINDING)
+
+
+def test_the_library_does_not_age_with_the_binding(monkeypatch, tmp_path):
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "absent.so"))
+    assert build.up_to_date() and not build.binding_up_to_date()
