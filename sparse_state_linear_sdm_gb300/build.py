@@ -5,13 +5,15 @@ Each translation unit under csrc/ is compiled by its own process (in parallel:
 nvcc for the library's, the host compiler for the binding's, against torch's
 headers), then linked into ``sparse_state_linear_sdm_gb300/libsdm.so`` and
 ``_layers.so``.  The CUDA runtime is linked statically into the library, so it
-builds and loads on its own; the binding needs it and torch.
+builds and loads on its own; the binding needs it and torch, and is rebuilt when
+torch or Python is another than the one it was compiled for.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -22,6 +24,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsdm.so")
 BINDING = os.path.join(PKG, "_layers.so")
 BINDING_SRC = os.path.join(CSRC, "sdm_binding.cpp")
+BINDING_TAG = BINDING + ".tag"  # what the binding was compiled for
 HEADER = os.path.join(os.path.dirname(PKG), "include", "sdm.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -48,9 +51,18 @@ def up_to_date() -> bool:
     return _newer_than(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [HEADER])
 
 
+def _binding_tag() -> str:
+    import torch
+
+    return f"torch {torch.__version__}, python {sys.version}, {platform.machine()}"
+
+
 def binding_up_to_date() -> bool:
-    """Whether the binding is newer than its sources."""
-    return _newer_than(BINDING, [BINDING_SRC, HEADER])
+    """Whether the binding is newer than its sources and was compiled for this torch and Python."""
+    if not _newer_than(BINDING, [BINDING_SRC, HEADER]) or not os.path.exists(BINDING_TAG):
+        return False
+    with open(BINDING_TAG) as f:
+        return f.read() == _binding_tag()
 
 
 def _run(cmd, what):
@@ -81,7 +93,11 @@ def _link_binding(obj: str) -> None:
     tmp = BINDING + f".tmp{os.getpid()}"
     _run([shutil.which("g++") or "c++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libsdm.so", "-L", libs,
           "-ltorch_python", "-ltorch", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], "linking the binding")
+    if os.path.exists(BINDING_TAG):
+        os.remove(BINDING_TAG)  # until the new one is in place
     os.replace(tmp, BINDING)
+    with open(BINDING_TAG, "w") as f:
+        f.write(_binding_tag())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:

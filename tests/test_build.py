@@ -1,4 +1,4 @@
-"""What is rebuilt when: the library alone, and the binding beside it.  No GPU needed."""
+"""What is rebuilt when: the library alone, and the binding for the torch and Python that load it.  No GPU needed."""
 import os
 
 import pytest
@@ -13,6 +13,25 @@ def built():
 
 def test_what_was_just_built_is_current():
     assert build.up_to_date() and build.binding_up_to_date()
+
+
+def test_a_binding_of_another_torch_or_python_is_stale(monkeypatch, tmp_path):
+    monkeypatch.setattr(build, "_binding_tag", lambda: "another torch")
+    assert not build.binding_up_to_date()
+    monkeypatch.undo()
+    monkeypatch.setattr(build, "BINDING_TAG", str(tmp_path / "none"))
+    assert not build.binding_up_to_date()
+
+
+def test_the_tag_names_torch_and_python(monkeypatch):
+    import sys
+
+    import torch
+
+    assert torch.__version__ in build._binding_tag() and sys.version in build._binding_tag()
+    before = build._binding_tag()
+    monkeypatch.setattr(torch, "__version__", "0.0")
+    assert build._binding_tag() != before
 
 
 def test_the_library_is_built_without_the_binding(monkeypatch, tmp_path):
