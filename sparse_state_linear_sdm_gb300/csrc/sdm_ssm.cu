@@ -68,6 +68,16 @@ __device__ __forceinline__ float decay(float delta, float rate) {
   return exp2_fast(fmaf(delta, rate, 2.0e-8f));
 }
 
+// A state carried over a chunk that adds `end` to it: exp(sum A) h + end.  Where the state grows, the
+// factor may pass the largest float although its product with h, and each token's own factor, do
+// not: it is then applied in two halves, and a state of 0 stays 0.
+__device__ __forceinline__ float carried_up(float h, float sum, float rate, float end) {
+  const float e = fmaf(sum, rate, 2.0e-8f);
+  if (!(e > 64.0f)) return fmaf(exp2_fast(e), h, end);
+  const float half = exp2_fast(0.5f * e);
+  return h == 0.0f ? end : fmaf(half, half * h, end);
+}
+
 // One element where rows are not aligned to 16 bytes: 4 bytes are copied like 16, 2 bytes are loaded.
 __device__ __forceinline__ void copy1(float* dst, const float* src, bool in) {
   const int n = in ? 4 : 0;
@@ -374,6 +384,11 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const __grid_constant
   if (PASS == kJoin && slot >= 0) {
     // Four chunks at a time: what they bring does not depend on the state, so it is asked for together.
     constexpr int kBatch = 4;
+    bool grows = !io.softplus;  // steps may be negative
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < kS; ++j) grows = grows || A[k][j] > 0.0f;
     for (int q0 = 0; q0 < chunk; q0 += kBatch) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -389,6 +404,13 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const __grid_constant
             sum[i] = a.ws_d[q * per + bd + c];
             get(a.ws_h + ((q + 1) * per + bd + c) * a.ws_n, true, end[i]);
           }
+        }
+        if (grows) {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int j = 0; j < kS; ++j) h[k][j] = carried_up(h[k][j], sum[i], A[k][j], end[i][j]);
+          continue;
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)

@@ -516,3 +516,37 @@ def test_a_batch_of_no_sequences():
         sdm.causal_conv(x, rn(15, 4))
     with pytest.raises(TypeError):
         sdm.selective_scan(x, x, A.double(), rn(0, 7, 4), rn(0, 7, 4))
+
+
+# ---- growing states ----
+
+
+@pytest.mark.parametrize("softplus", [True, False])
+def test_scan_of_growing_states_in_chunks(softplus):
+    """A chunk's whole factor, e^96 and e^1900 here, passes the largest float; the states do not: nothing grows from 0,
+    and 1e-30 to 5e11.  The bound is the definition's, which takes the factors token by token."""
+    T, Dm, N = 700, 24, 16
+    assert sdm.selective_scan_workspace_size(1, T, Dm, N, 1) > 0
+    rn = _gen(33)
+    dt = torch.full((1, T, Dm), 20.0 if softplus else -20.0, device="cuda")
+    A = torch.full((Dm, N), 2.0 if softplus else -2.0, device="cuda")
+    B, C = rn(1, T, N), rn(1, T, N)
+    y, st = sdm.selective_scan(torch.zeros(1, T, Dm, device="cuda"), dt, A, B, C, dt_softplus=softplus,
+                               state=torch.zeros(1, Dm, N, device="cuda"))
+    assert not y.any() and not st.any()
+
+    T = 80                                      # two chunks of 48 and 32 tokens
+    dt = torch.zeros(1, T, Dm, device="cuda")
+    dt[:, :48] = 1.0 if softplus else -1.0
+    if softplus:                                # log(e - 1): a step of 1; and one of 0
+        dt = torch.where(dt > 0, 0.5413248546129181, -3.0e38)
+    state = torch.full((1, Dm, N), 1e-30, device="cuda")
+    k = dict(x=torch.zeros(1, T, Dm, device="cuda"), dt=dt, A=A, B=B[:, :T].contiguous().unsqueeze(2),
+             C=C[:, :T].contiguous().unsqueeze(2), D=None, z=None, dt_bias=None, state=state, dt_softplus=softplus,
+             lengths=None, slots=None)
+    assert sdm.selective_scan_workspace_size(1, T, Dm, N, 1) > 0
+    want, wstate, ey, es = _scan_ref(k)
+    y, st = sdm.selective_scan(**k, state_out=torch.empty_like(state))
+    assert wstate.max() > 1e11
+    _check(y, want, ey, "f32", "y")
+    _check(st, wstate, es, "f32", "state")
