@@ -6,11 +6,19 @@
 // where u is the K-1 inputs carried from before token 0 (the state) followed by x, and the new
 // state is the last K-1 inputs of each sequence.  2K flop for each element read and written
 // once: HBM bounds it, so each thread keeps its 16-byte piece of channels (8 bf16 or 4 fp32)
-// and walks a strip of tokens with the last K-1 inputs in registers: every input is read once,
+// and walks a strip of tokens with the last K-1 inputs beside it: every input is read once,
 // except the K-1 tokens before a strip.  The next kAhead tokens are always under way, as raw words,
-// and two multiply-adds go in one instruction: 8 x 4096 x 4096 bf16 with silu takes 100 us, 5.4 TB/s
-// (0.79 of a copy's rate); with four tokens under way 110 us, with weights loaded one by one and
-// inputs held as fp32 266 us.
+// and two multiply-adds go in one instruction: 8 x 4096 x 4096 bf16 with silu and four taps takes
+// 99 us, 5.4 TB/s (0.80 of a copy's rate); with four tokens under way 110 us, with weights loaded one
+// by one and inputs held as fp32 266 us.  fp32 takes 169 us (0.94), 185 with eight taps.
+//
+// The window and the weights are in registers for up to four taps in bf16 and for any number in fp32.
+// The bound of 128 registers was chosen at four taps (105 us without it); more taps of 8 channels do
+// not fit in it and spill (1.4 KB a thread at eight): 156, 210, 251 and 361 us with 5 to 8 taps,
+// where HBM would let them take 79.
+//
+// A token is a strip of one, whose thread still goes through the arithmetic of kAhead tokens: 10 us for
+// 256 x 4096 with four taps, 19 for rows off 16 bytes (an element a thread), 37 with eight taps.
 #include "sdm_layers.cuh"
 
 namespace sdm {

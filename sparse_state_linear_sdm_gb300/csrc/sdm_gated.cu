@@ -19,11 +19,14 @@
 //              dw = [dg | du]^T x, where the tokens are and both operands are MN-major.
 // No operand is transposed in memory: TMA boxes of 64 x 64 in the 128-byte swizzle serve as either
 // major, and only the descriptors differ.  Sums are fp32; dg and du are the only rounding between
-// inputs and outputs.
+// inputs and outputs: the tensor cores take them at full rate as bf16, like x and w beside them, and
+// at half of it or less, with twice the bytes to hold and read, in anything wider.  Each is half a unit of
+// bf16 off, so dx and dw are 0.0023 of their norm off where their own rounding alone makes 0.0017.
 //
 // The tensor pipe bounds the large cases, and the card's power: 16,384 tokens of 2048 x 8192 take
-// 0.63 ms back to back (1,750 TFLOP/s), the gradient of 32,768 tokens 4.2 ms (1,560; 1,750 in ten
-// calls from idle).
+// 0.62 to 0.64 ms back to back (1,720 to 1,780 TFLOP/s), the gradient of 32,768 tokens 4.17 to 4.27 ms
+// (1,545 to 1,580; 1,750 in ten calls from idle).  Neither the forward nor the slope pass splits its
+// reduction, so few tiles leave pairs idle: 256 tokens of 2048 x 1024 are 8 units and take 16.8 us.
 #include "sdm_layers.cuh"
 #include "sdm_tcgen05.cuh"
 

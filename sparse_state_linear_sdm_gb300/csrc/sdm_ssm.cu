@@ -151,9 +151,11 @@ struct Tile {
   static constexpr int bytes = off_c + kTT * NP * 4;
 };
 
-// Four blocks an SM is what a full card gives each, so 128 registers a thread: left to itself the
-// compiler stops at 96 (five blocks), and 16 x 2048 x 4096 x 16 takes 707 us instead of 685; with 168
-// (three blocks) 750.
+// Four blocks an SM, so 128 registers a thread: left to itself the compiler stops at 96 (five blocks),
+// and 16 x 2048 x 4096 x 16 takes 707 us instead of 685; with 168 (three blocks) 750.  Four is what a
+// full card gives each SM with more than 8 states in bf16 and more than 16 in fp32; the other
+// instances' tiles leave shared memory for fewer: fp32 with 9 to 16 states 3 blocks (71,680 bytes
+// each), bf16 with up to 8 states 2 (83,968), fp32 with up to 8 states 1 (134,144).
 template <typename T, int L, int kS, int PASS>
 __global__ void __launch_bounds__(kThreads, 4) scan_kernel(const __grid_constant__ ScanArgs a) {
   using S = Tile<T, L, kS>;
@@ -755,6 +757,12 @@ int launch_token(ScanArgs& a, cudaStream_t s) {
 // 380 and 397, 256 blocks 515 and 397.  Four blocks an SM against three: 32768 tokens of 2048
 // channels 554 us against 627 (512 now); chunks of 32 tokens against 64: 512 tokens of 1024 channels
 // 28.5 us against 31.3.
+//
+// All of that is bf16 with 16 states, and the two numbers stand for every type and state count although
+// instances with fewer blocks an SM would cut later: fp32 with 8 states, a block an SM, takes 587 us for 9 sequences
+// of 2048 x 4096 (cut) and 792 for 13 (not cut, two rounds of 396).  Nor is the join in the rule, whose
+// blocks walk all chunks before theirs: 32,768 tokens of 64 channels, 512 chunks, take 304 us, of 256
+// channels 245.
 void cut(int B, int T, int Dm, int N, int G, int* chunks, long long* chunk) {
   const int L = lanes_for(N, kLaneStates), CH = 2 * kThreads / L;
   const long long blocks = (long long)B * G * (((long long)Dm / G + CH - 1) / CH);

@@ -45,7 +45,8 @@ def causal_conv(x, w, bias=None, state=None, state_out=None, activation="silu", 
     zeros; state_out None: `state` is updated in place, or not kept where there is none).  activation: "silu" or
     "none".  lengths: int32 [B], the tokens of each sequence that exist (y is 0 past them).  slots: int32 [B],
     the row of the state each sequence uses, negative for a padding row.  A batch of no sequences has an empty y.
-    Returns (y, state written)."""
+    out: y's memory; it may be x itself up to 8 tokens, and overlaps no other tensor of the call (nor does state_out,
+    but for `state` itself): ValueError.  Returns (y, state written)."""
     return (_module or _binding()).conv(x, w, bias, state, state_out, _activation(activation, ("silu", "none")),
                                         lengths, slots, out, dev_err, 2)
 
@@ -74,7 +75,9 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, state=None, sta
     x, dt, z: [B, T, Dm]; B, C: [B, T, N], or [B, T, G, N] where groups of Dm / G channels share them; all of x's
     type (fp32 or bf16), rows of any stride.  A [Dm, N], D [Dm], dt_bias [Dm]: fp32.  N up to 128.  state,
     state_out: fp32 [rows, Dm, N] (state None: zeros; state_out None: `state` is updated in place, or not kept where
-    there is none).  lengths, slots: as for causal_conv.  Returns (y of x's type, state written)."""
+    there is none).  lengths, slots, an empty batch: as for causal_conv.  out: y's memory; it may be x, dt or z itself,
+    and overlaps no other tensor of the call (nor does state_out, but for `state` itself): ValueError.  Returns (y of
+    x's type, state written)."""
     return (_module or _binding()).scan(x, dt, A, B, C, D, z, dt_bias, state, state_out, dt_softplus, lengths, slots,
                                         out, workspace, dev_err, 2)
 
@@ -92,7 +95,8 @@ def project_gated(x, w, activation="silu", out=None, dev_err=None):
     """Gated feed-forward projections in one kernel: h = act(x Wg^T) * (x Wu^T) (sdm_project_gated).
 
     x: [..., D] bf16; w: [2*F, D] bf16, one row per output column, Wg's F rows and then Wu's; D and F multiples of
-    8.  activation: "silu" or "gelu" (the exact one).  Returns h [..., F] bf16."""
+    8.  activation: "silu" or "gelu" (the exact one).  Returns h [..., F] bf16, in `out` where it is given (not over
+    x or w: ValueError)."""
     return (_module or _binding()).gated(x, w, _activation(activation, ("silu", "gelu")), out, dev_err)
 
 
@@ -103,6 +107,8 @@ def project_gated_backward_workspace_size(M: int, D: int, F: int) -> int:
 
 def project_gated_backward(x, w, dh, activation="silu", dx=None, dw=None, workspace=None, dev_err=None):
     """Gradient of project_gated: (dx [..., D], dw [2*F, D]) for dh [..., F], all bf16
-    (sdm_project_gated_backward).  The forward pass keeps nothing but its inputs: the projections are recomputed."""
+    (sdm_project_gated_backward).  The forward pass keeps nothing but its inputs: the projections are recomputed.
+    dx, dw, workspace: memory for them, which overlaps neither x and w nor one another (ValueError); dx and dw may
+    take dh's."""
     return (_module or _binding()).gated_grad(x, w, dh, _activation(activation, ("silu", "gelu")), dx, dw, workspace,
                                               dev_err)

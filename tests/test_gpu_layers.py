@@ -539,7 +539,7 @@ def test_scan_of_growing_states_in_chunks(softplus):
     dt = torch.zeros(1, T, Dm, device="cuda")
     dt[:, :48] = 1.0 if softplus else -1.0
     if softplus:                                # log(e - 1): a step of 1; and one of 0
-        dt = torch.where(dt > 0, 0.5413248546129181, -3.0e38)
+        dt = torch.where(dt > 0, 0.5413248546129181, -200.0)
     state = torch.full((1, Dm, N), 1e-30, device="cuda")
     k = dict(x=torch.zeros(1, T, Dm, device="cuda"), dt=dt, A=A, B=B[:, :T].contiguous().unsqueeze(2),
              C=C[:, :T].contiguous().unsqueeze(2), D=None, z=None, dt_bias=None, state=state, dt_softplus=softplus,
