@@ -281,6 +281,7 @@ PyObject* scan(PyObject* const* a) {
   s.N = as_int(N, "N");
   s.G = as_int(G, "G");
   s.softplus = PyObject_IsTrue(a[10]);
+  if (s.softplus < 0) throw Raised();  // its truth is an error
   Held y;
   s.y = output(c, a[13], "out", x.sizes(), ty, &y.o);
   if (nb == 0) return pair(y.release(), st.written);

@@ -495,6 +495,12 @@ def test_an_output_that_does_not_fit_is_an_out_of_memory_error():
         sdm.project_gated(x, w)
 
 
+def test_a_flag_without_a_truth_value_is_its_own_error():
+    k = _scan_case(SCAN[5])
+    with pytest.raises(ValueError, match="ambiguous"):
+        sdm.selective_scan(**{**k, "dt_softplus": np.array([True, False])})
+
+
 def test_a_batch_of_no_sequences():
     """An empty batch has an empty output and leaves the states alone, as the projections' does."""
     rn = _gen(26)
