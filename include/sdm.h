@@ -552,6 +552,94 @@ int sdm_project_gated_backward(const void* x, const void* w, const void* dh, lon
                                int F, int act, void* dx, void* dw, void* workspace,
                                size_t workspace_bytes, int* dev_err, void* stream);
 
+/* sdm_linear_attention - linear attention with a decay for each head, over T tokens (T = 1: one decode token):
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale q_t S_t      (S_t [dk, dv] of every sequence and head)
+ * Head h of H takes the queries and keys of head h / (H / Hk) of Hk.
+ *   q, k [B, T, Hk, dk], v [B, T, H, dv] dt: rows of Hk * dk or H * dv dense elements, strides as above;
+ *   g  fp32 logarithms of the decays, at most 0 where nothing grows: [B, T, H] with strides between
+ *      sequences and tokens (both 0: one row [H] for all of them), or NULL (no decay);
+ *   o  [B, T, H, dv] dt, dense;  state, state_out fp32 [n_slots, H, dk, dv].
+ * Sums and states are fp32.  bf16 operands of up to SDM_LINEAR_TILE_D columns whose rows start on 16 bytes go
+ * to the tensor cores in chunks of 128 tokens: there the masked products of a chunk and the state
+ * in front of it are rounded to bf16 as they are read (the state itself is not).
+ * Requires H % Hk == 0, dk <= SDM_MAX_LINEAR_D, dv <= SDM_MAX_LINEAR_D.  o and the workspace overlap nothing else
+ * (SDM_EOVERLAP), nor does state_out but for the state itself. */
+#define SDM_MAX_LINEAR_D 256
+#define SDM_LINEAR_TILE_D 128
+typedef struct {
+  const void *q, *k, *v;
+  const float* g;
+  long long q_bs, q_ts, k_bs, k_ts, v_bs, v_ts, g_bs, g_ts;
+  const float* state;               /* [n_slots, H, dk, dv] or NULL */
+  float* state_out;                 /* [n_slots, H, dk, dv] or NULL */
+  const int32_t *lengths, *slots;
+  void* o;
+  int dtype;                        /* of q, k, v and o */
+  int B, T, H, Hk, dk, dv, n_slots;
+  float scale;
+} sdm_linear_args;
+/* Bytes of device workspace for these sizes; 0 where none is needed. */
+size_t sdm_linear_attention_workspace_size(int dtype, int B, int T, int H, int dk, int dv);
+int sdm_linear_attention(const sdm_linear_args* args, void* workspace, size_t workspace_bytes,
+                         int* dev_err, void* stream);
+
+/* sdm_residual_norm - the norms after and before a block with its gate, residual scale and residual, in one pass:
+ *   a = x / rms(x) * after * act(gate)        rms over each of `groups` groups of D / groups channels
+ *   r = residual + scale * a
+ *   y = r / rms(r) * weight                   rms(v) = sqrt(mean(v^2) + eps)
+ * after, gate, scale, residual, weight: each may be NULL (that factor, term or norm is left out).  x, residual and gate are
+ * M rows of D dense channels, row strides in elements (_rs); y and r are dense.
+ *   x, gate, y    x_dtype;  residual, r  r_dtype (x_dtype, or fp32);  after, scale, weight [D]  w_dtype;
+ *   act           of the gate: SDM_ACT_SILU or SDM_ACT_NONE.
+ *   y             written; NULL where weight is.  r: written unless NULL (not both NULL).
+ * Computed in fp32, each output rounded once; y is the norm of r as it was before its rounding.  Requires
+ * groups == 1 where there is a weight, and D / groups <= 16384.  y and r may lie exactly over an input of the same row
+ * size (the stream updated in place); otherwise they overlap nothing (SDM_EOVERLAP). */
+typedef struct {
+  const void *x, *residual, *gate;
+  long long x_rs, residual_rs, gate_rs;
+  const void *after, *scale, *weight;
+  int x_dtype, r_dtype, w_dtype, act;
+  long long M;
+  int D, groups;
+  float eps;
+} sdm_norm_args;
+int sdm_residual_norm(const sdm_norm_args* args, void* y, void* r, void* stream);
+
+/* sdm_residual_norm_backward - its gradient.  args as in the forward call (args->residual is not read); r: what it left
+ * (x itself where nothing came between; only read with a weight); dy, dr: the gradients of y (with a weight) and of
+ * r (or NULL: none).  Written, each unless NULL: dx, dgate [M, D] x_dtype, dresidual [M, D] r_dtype, all dense;
+ * dafter, dscale, dweight [D] w_dtype, summed in fp32 in an order that sizes alone decide.  M = 0 writes sums of 0.
+ * The workspace holds partial sums.  dx, dgate and dresidual may lie exactly over an input of the same row size; otherwise the
+ * outputs and the workspace overlap nothing (SDM_EOVERLAP). */
+typedef struct {
+  const void *r, *dy, *dr;
+  long long r_rs, dy_rs, dr_rs;
+  void *dx, *dresidual, *dgate, *dafter, *dscale, *dweight;
+} sdm_norm_grads;
+size_t sdm_residual_norm_backward_workspace_size(long long M, int D, int groups);
+int sdm_residual_norm_backward(const sdm_norm_args* args, const sdm_norm_grads* grads, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* sdm_project - a projection with bias, activation and residual in one kernel:  y = residual + act(x w^T + bias).
+ *   x [M, D], w [N, D], bias [N] or NULL, residual [M, N] or NULL, y [M, N]: bf16;  act: any sdm_activation.
+ * fp32 accumulation, one rounding.  Requires D % 8 == 0 and N % 8 == 0 (SDM_EUNSUPPORTED).  y may be the residual itself;
+ * otherwise it and the workspace overlap nothing (SDM_EOVERLAP).  The workspace holds partial sums where few tiles are
+ * split over their reduction (sdm_project_workspace_size: 0 where none is needed); results do not depend on timing. */
+size_t sdm_project_workspace_size(long long M, int D, int N);
+int sdm_project(const void* x, const void* w, const void* bias, const void* residual, long long M, int D, int N, int act,
+                void* y, void* workspace, size_t workspace_bytes, int* dev_err, void* stream);
+
+/* sdm_project_backward - its gradient for dy [M, N] bf16 (that of the residual is dy itself):
+ *   dz = dy act'(x w^T + bias);  dx = dz w;  dw = dz^T x;  dbias = sum of dz over the M tokens.
+ * dx [M, D], dw [N, D], dbias [N] (or NULL): bf16, summed in fp32.  With an activation the product is formed again and
+ * dz rounded to bf16 before it is used.  M = 0 writes dw = 0 and dbias = 0.  dx, dw, dbias and the workspace overlap nothing
+ * (SDM_EOVERLAP); results do not depend on timing. */
+size_t sdm_project_backward_workspace_size(long long M, int D, int N, int act);
+int sdm_project_backward(const void* x, const void* w, const void* bias, const void* dy, long long M, int D, int N, int act,
+                         void* dx, void* dw, void* dbias, void* workspace, size_t workspace_bytes, int* dev_err,
+                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif

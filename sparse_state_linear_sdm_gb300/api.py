@@ -90,6 +90,13 @@ def lib() -> ctypes.CDLL:
             L.sdm_selective_scan_workspace_size.restype = sz
             L.sdm_project_gated_backward_workspace_size.argtypes = [ll, i, i]
             L.sdm_project_gated_backward_workspace_size.restype = sz
+            L.sdm_linear_attention_workspace_size.argtypes = [i] * 6
+            L.sdm_residual_norm_backward_workspace_size.argtypes = [ll, i, i]
+            L.sdm_project_workspace_size.argtypes = [ll, i, i]
+            L.sdm_project_backward_workspace_size.argtypes = [ll, i, i, i]
+            for name in ("sdm_linear_attention_workspace_size", "sdm_residual_norm_backward_workspace_size",
+                         "sdm_project_workspace_size", "sdm_project_backward_workspace_size"):
+                getattr(L, name).restype = sz
             for name in ("sdm_init_state_from_M0", "sdm_select", "sdm_select_tuned", "sdm_scan_forward",
                          "sdm_scan_forward_tuned", "sdm_scan_launch_info", "sdm_gen_inputs", "sdm_gen_M0",
                          "sdm_forward_chunks", "sdm_forward_tuned", "sdm_forward", "sdm_scan_forward_train",

@@ -1,5 +1,6 @@
-// Python binding of the convolution, the scan and the gated projections: checks of the tensors,
-// allocation of outputs and workspaces, and the call of the C entry points (include/sdm.h).
+// Python binding of the layers beside the memory (the convolution, the scan, the gated projections, linear attention,
+// the norms, the projections with an epilogue): checks of the tensors, allocation of outputs and workspaces, and the
+// call of the C entry points (include/sdm.h).
 //
 // These calls are on a decode step's path, where a kernel of two microseconds should not wait for
 // twenty of argument handling in Python, so what api.py does in Python is done here on the tensors
@@ -15,6 +16,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <string>
@@ -146,7 +148,7 @@ struct State {
   PyObject* written = Py_None;
 };
 // state and state_out: in place where only `state` is given.
-State state_rows(const Call& c, PyObject* o_in, PyObject* o_out, bool slots, int64_t nb, int64_t d1, int64_t d2,
+State state_rows(const Call& c, PyObject* o_in, PyObject* o_out, bool slots, int64_t nb, at::IntArrayRef row,
                  at::ScalarType type) {
   State s;
   s.written = o_out == Py_None ? o_in : o_out;
@@ -160,8 +162,10 @@ State state_rows(const Call& c, PyObject* o_in, PyObject* o_out, bool slots, int
   if (!slots && n != nb)
     raise(PyExc_ValueError, "state must have one row a sequence (%lld) without slots, got %lld", (long long)nb,
           (long long)n);
-  s.in = c.dense(in, "state", type, {n, d1, d2});
-  s.out = c.dense(out, "state_out", type, {n, d1, d2});
+  c10::SmallVector<int64_t, 4> shape{n};
+  shape.append(row.begin(), row.end());
+  s.in = c.dense(in, "state", type, shape);
+  s.out = c.dense(out, "state_out", type, shape);
   s.rows = as_int(n, "state");
   return s;
 }
@@ -220,7 +224,7 @@ PyObject* conv(PyObject* const* a) {
   const void* px = c.rows(x, "x", ty, x.sizes(), lead, &bs, &ts);
   const void* pw = c.dense(w, "w", wt, {D, K});
   const void* pb = c.dense(bias, "bias", wt, {D});
-  const State st = state_rows(c, a[3], a[4], slots.defined(), nb, K - 1, D, ty);
+  const State st = state_rows(c, a[3], a[4], slots.defined(), nb, {K - 1, D}, ty);
   const void* pl = c.dense(lengths, "lengths", at::kInt, {nb});
   const void* ps = c.dense(slots, "slots", at::kInt, {nb});
   void* pe = c.dense(optional(a[9], "dev_err"), "dev_err", at::kInt, {1});
@@ -268,7 +272,7 @@ PyObject* scan(PyObject* const* a) {
   s.A = static_cast<const float*>(c.dense(A, "A", at::kFloat, {Dm, N}));
   s.D = static_cast<const float*>(c.dense(D, "D", at::kFloat, {Dm}));
   s.dt_bias = static_cast<const float*>(c.dense(bias, "dt_bias", at::kFloat, {Dm}));
-  const State st = state_rows(c, a[8], a[9], slots.defined(), nb, Dm, N, at::kFloat);
+  const State st = state_rows(c, a[8], a[9], slots.defined(), nb, {Dm, N}, at::kFloat);
   s.state = static_cast<const float*>(st.in);
   s.state_out = static_cast<float*>(st.out);
   s.n_slots = st.rows;
@@ -350,6 +354,280 @@ PyObject* gated_grad(PyObject* const* a) {
   return pair(dx.release(), dw.o);
 }
 
+// linear(q, k, v, decay, scale, state, state_out, lengths, slots, out, workspace, dev_err, lead) -> (o, state written)
+PyObject* linear(PyObject* const* a) {
+  const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"),
+                   &decay = optional(a[3], "decay"), &lengths = optional(a[7], "lengths"), &slots = optional(a[8], "slots");
+  const int lead = int(PyLong_AsLong(a[12]));
+  const Call c(q);
+  if (q.dim() != lead + 2) raise(PyExc_ValueError, lead == 2 ? "q must be [B, T, Hk, dk]" : "q must be [B, Hk, dk]");
+  if (v.dim() != lead + 2) raise(PyExc_ValueError, lead == 2 ? "v must be [B, T, H, dv]" : "v must be [B, H, dv]");
+  const at::ScalarType ty = q.scalar_type();
+  const int64_t nb = q.size(0), T = lead == 2 ? q.size(1) : 1, Hk = q.size(lead), dk = q.size(lead + 1);
+  const int64_t H = v.size(lead), dv = v.size(lead + 1);
+  int64_t vs[4];
+  int n = 0;
+  for (int i = 0; i < lead; ++i) vs[n++] = q.size(i);
+  vs[n++] = H;
+  const at::IntArrayRef gs(vs, size_t(n));  // the decays' shape, and without dv v's
+  vs[n++] = dv;
+  const at::IntArrayRef vshape(vs, size_t(n));
+
+  sdm_linear_args s = {};
+  s.dtype = code(ty, "q");
+  s.q = c.rows(q, "q", ty, q.sizes(), lead, &s.q_bs, &s.q_ts);
+  s.k = c.rows(k, "k", ty, q.sizes(), lead, &s.k_bs, &s.k_ts);
+  s.v = c.rows(v, "v", ty, vshape, lead, &s.v_bs, &s.v_ts);
+  s.g = static_cast<const float*>(decay.defined() && decay.dim() == 1
+                                      ? c.dense(decay, "decay", at::kFloat, {H})
+                                      : c.rows(decay, "decay", at::kFloat, gs, lead, &s.g_bs, &s.g_ts));
+  s.scale = a[4] == Py_None ? float(1.0 / std::sqrt(double(dk > 0 ? dk : 1))) : float(PyFloat_AsDouble(a[4]));
+  if (PyErr_Occurred()) throw Raised();
+  const State st = state_rows(c, a[5], a[6], slots.defined(), nb, {H, dk, dv}, at::kFloat);
+  s.state = static_cast<const float*>(st.in);
+  s.state_out = static_cast<float*>(st.out);
+  s.n_slots = st.rows;
+  s.lengths = static_cast<const int32_t*>(c.dense(lengths, "lengths", at::kInt, {nb}));
+  s.slots = static_cast<const int32_t*>(c.dense(slots, "slots", at::kInt, {nb}));
+  void* pe = c.dense(optional(a[11], "dev_err"), "dev_err", at::kInt, {1});
+  s.B = as_int(nb, "B");
+  s.T = as_int(T, "T");
+  s.H = as_int(H, "H");
+  s.Hk = as_int(Hk, "Hk");
+  s.dk = as_int(dk, "dk");
+  s.dv = as_int(dv, "dv");
+  Held o;
+  s.o = output(c, a[9], "out", vshape, ty, &o.o);
+  if (nb == 0) return pair(o.release(), st.written);
+  at::Tensor own;
+  size_t bytes = 0;
+  void* ws = c.workspace(optional(a[10], "workspace"),
+                         T > 1 ? sdm_linear_attention_workspace_size(s.dtype, s.B, s.T, s.H, s.dk, s.dv) : 0, &own, &bytes);
+  const int r = sdm_linear_attention(&s, ws, bytes, static_cast<int*>(pe), c.stream());
+  if (r != SDM_OK) raise_status("sdm_linear_attention", r);
+  return pair(o.release(), st.written);
+}
+
+// Address of a tensor [..., D] whose rows are dense and one stride apart; the stride of a single row does not matter: 0.
+const void* strided_rows(const Call& c, const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape,
+                         long long* rs) {
+  *rs = 0;
+  if (!t.defined()) return nullptr;
+  c.fits(t, name, type, shape);
+  const int n = int(shape.size());
+  if (shape[n - 1] > 1 && t.numel() && t.stride(n - 1) != 1)
+    raise(PyExc_ValueError, "%s must be dense in its last dimension", name);
+  int64_t next = -1;  // stride that the dimension before must have
+  for (int i = n - 2; i >= 0 && t.numel(); --i) {
+    if (shape[i] == 1) continue;
+    if (next < 0)
+      *rs = t.stride(i);
+    else if (t.stride(i) != next)
+      raise(PyExc_ValueError, "%s must have one stride between its rows", name);
+    next = t.stride(i) * shape[i];
+  }
+  return t.data_ptr();
+}
+
+// What the norm's calls have in common.  Weights are [D], all of one type.
+struct Norm {
+  sdm_norm_args s = {};
+  at::ScalarType x_type, r_type, w_type = at::kFloat;
+  int64_t D;
+};
+Norm norm_operands(const Call& c, PyObject* const* a, const at::Tensor& x, const at::Tensor& weight, const at::Tensor& after,
+                   const at::Tensor& gate, const at::Tensor& scale, const at::Tensor& like_r) {
+  Norm m;
+  if (x.dim() < 1) raise(PyExc_ValueError, "x must be [..., D]");
+  m.D = x.size(-1);
+  m.x_type = x.scalar_type();
+  m.r_type = like_r.defined() ? like_r.scalar_type() : m.x_type;
+  m.s.x_dtype = code(m.x_type, "x");
+  m.s.r_dtype = code(m.r_type, "the residual");
+  if (m.r_type != m.x_type && m.r_type != at::kFloat)
+    raise(PyExc_TypeError, "the residual must be x's type or float32, got %s", c10::toString(m.r_type));
+  for (const at::Tensor* w : {&after, &scale, &weight})
+    if (w->defined()) m.w_type = w->scalar_type();
+  m.s.w_dtype = code(m.w_type, "weight");
+  m.s.x = strided_rows(c, x, "x", m.x_type, x.sizes(), &m.s.x_rs);
+  m.s.gate = strided_rows(c, gate, "gate", m.x_type, x.sizes(), &m.s.gate_rs);
+  m.s.after = c.dense(after, "after", m.w_type, {m.D});
+  m.s.scale = c.dense(scale, "scale", m.w_type, {m.D});
+  m.s.weight = c.dense(weight, "weight", m.w_type, {m.D});
+  m.s.M = m.D ? x.numel() / m.D : 0;
+  m.s.D = as_int(m.D, "D");
+  m.s.groups = int(PyLong_AsLong(a[0]));
+  m.s.eps = float(PyFloat_AsDouble(a[1]));
+  m.s.act = int(PyLong_AsLong(a[2]));
+  if (PyErr_Occurred()) throw Raised();
+  if (m.s.groups < 1 || m.D % m.s.groups) raise(PyExc_ValueError, "groups must divide the channels");
+  if (weight.defined() && m.s.groups > 1) raise(PyExc_ValueError, "groups are those of `after`: weight's norm is over whole rows");
+  return m;
+}
+
+// norm(x, residual, weight, after, gate, scale, out, residual_out, groups, eps, act) -> (y or None, r)
+PyObject* norm(PyObject* const* a) {
+  const at::Tensor &x = tensor(a[0], "x"), &residual = optional(a[1], "residual"), &weight = optional(a[2], "weight"),
+                   &after = optional(a[3], "after"), &gate = optional(a[4], "gate"), &scale = optional(a[5], "scale");
+  const Call c(x);
+  Norm m = norm_operands(c, a + 8, x, weight, after, gate, scale, residual);
+  m.s.residual = strided_rows(c, residual, "residual", m.r_type, x.sizes(), &m.s.residual_rs);
+  const bool moves = residual.defined() || after.defined() || gate.defined() || scale.defined();
+  if (!moves && !weight.defined()) raise(PyExc_ValueError, "nothing to compute: no weight, after, gate, scale or residual");
+  Held y, r;
+  void *py = nullptr, *pr = nullptr;
+  if (weight.defined()) py = output(c, a[6], "out", x.sizes(), m.x_type, &y.o);
+  if (moves) {
+    pr = output(c, a[7], "residual_out", x.sizes(), m.r_type, &r.o);
+  } else {
+    Py_INCREF(a[0]);
+    r.o = a[0];
+  }
+  if (m.s.M) {
+    const int st = sdm_residual_norm(&m.s, py, pr, c.stream());
+    if (st != SDM_OK) raise_status("sdm_residual_norm", st);
+  }
+  if (!y.o) {
+    Py_INCREF(Py_None);
+    y.o = Py_None;
+  }
+  return pair(y.release(), r.o);
+}
+
+// norm_grad(x, r, dy, dr, weight, after, gate, scale, residual, workspace, groups, eps, act)
+//   -> (dx, dresidual, dweight, dafter, dgate, dscale), None for what there is not
+PyObject* norm_grad(PyObject* const* a) {
+  const at::Tensor &x = tensor(a[0], "x"), &r = optional(a[1], "r"), &dy = optional(a[2], "dy"), &dr = optional(a[3], "dr"),
+                   &weight = optional(a[4], "weight"), &after = optional(a[5], "after"), &gate = optional(a[6], "gate"),
+                   &scale = optional(a[7], "scale");
+  const Call c(x);
+  Norm m = norm_operands(c, a + 10, x, weight, after, gate, scale, r.defined() ? r : dr);
+  const int residual = PyObject_IsTrue(a[8]);
+  if (residual < 0) throw Raised();
+  const bool inner = after.defined() || gate.defined() || scale.defined();
+  if (weight.defined() != dy.defined()) raise(PyExc_ValueError, "dy is the gradient of weight's norm: both or neither");
+  if (!dy.defined() && !dr.defined()) raise(PyExc_ValueError, "a gradient is needed: dy or dr");
+  if (weight.defined() && !r.defined() && (inner || residual))
+    raise(PyExc_ValueError, "weight's norm needs r, what the forward call left");
+  sdm_norm_grads g = {};
+  g.dy = strided_rows(c, dy, "dy", m.x_type, x.sizes(), &g.dy_rs);
+  g.dr = strided_rows(c, dr, "dr", m.r_type, x.sizes(), &g.dr_rs);
+  if (r.defined()) {
+    g.r = strided_rows(c, r, "r", m.r_type, x.sizes(), &g.r_rs);
+  } else if (m.r_type == m.x_type) {
+    g.r = m.s.x, g.r_rs = m.s.x_rs;
+  } else if (weight.defined()) {
+    raise(PyExc_TypeError, "dr must be x's type where r is x");
+  }
+  Held out[6];  // in the order of the result
+  const bool one = residual && !inner && m.r_type == m.x_type;  // dx and dresidual are the same values
+  if (residual) g.dresidual = output(c, Py_None, "dresidual", x.sizes(), m.r_type, &out[1].o);
+  if (one) {
+    Py_INCREF(out[1].o);
+    out[0].o = out[1].o;
+  } else {
+    g.dx = output(c, Py_None, "dx", x.sizes(), m.x_type, &out[0].o);
+  }
+  if (weight.defined()) g.dweight = output(c, Py_None, "dweight", {m.D}, m.w_type, &out[2].o);
+  if (after.defined()) g.dafter = output(c, Py_None, "dafter", {m.D}, m.w_type, &out[3].o);
+  if (gate.defined()) g.dgate = output(c, Py_None, "dgate", x.sizes(), m.x_type, &out[4].o);
+  if (scale.defined()) g.dscale = output(c, Py_None, "dscale", {m.D}, m.w_type, &out[5].o);
+  at::Tensor own;
+  size_t bytes = 0;
+  const bool sums = g.dweight || g.dafter || g.dscale;
+  void* ws = c.workspace(optional(a[9], "workspace"),
+                         sums ? sdm_residual_norm_backward_workspace_size(m.s.M, m.s.D, m.s.groups) : 0, &own, &bytes);
+  if (m.D) {
+    const int st = sdm_residual_norm_backward(&m.s, &g, ws, bytes, c.stream());
+    if (st != SDM_OK) raise_status("sdm_residual_norm_backward", st);
+  }
+  PyObject* t = PyTuple_New(6);
+  if (!t) throw Raised();
+  for (int i = 0; i < 6; ++i) {
+    PyObject* o = out[i].release();
+    if (!o) {
+      Py_INCREF(Py_None);
+      o = Py_None;
+    }
+    PyTuple_SET_ITEM(t, i, o);
+  }
+  return t;
+}
+
+struct Dense {
+  int64_t M, D, N;
+  const void *x, *w, *bias;
+  c10::SmallVector<int64_t, 6> shape;  // of y
+};
+Dense dense_operands(const Call& c, const at::Tensor& x, const at::Tensor& w, const at::Tensor& bias) {
+  if (x.dim() < 1 || w.dim() != 2) raise(PyExc_ValueError, "x must be [..., D] and w [N, D]");
+  Dense d;
+  d.D = x.size(-1);
+  d.N = w.size(0);
+  d.M = d.D ? x.numel() / d.D : 0;
+  d.x = c.dense(x, "x", at::kBFloat16, x.sizes());
+  d.w = c.dense(w, "w", at::kBFloat16, {d.N, d.D});
+  d.bias = c.dense(bias, "bias", at::kBFloat16, {d.N});
+  d.shape.assign(x.sizes().begin(), x.sizes().end());
+  d.shape.back() = d.N;
+  as_int(d.D, "D");
+  as_int(d.N, "N");
+  return d;
+}
+
+// dense(x, w, bias, residual, act, out, workspace, dev_err) -> y
+PyObject* dense(PyObject* const* a) {
+  const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w"), &bias = optional(a[2], "bias"),
+                   &residual = optional(a[3], "residual");
+  const Call c(x);
+  const Dense d = dense_operands(c, x, w, bias);
+  const void* pr = c.dense(residual, "residual", at::kBFloat16, d.shape);
+  void* pe = c.dense(optional(a[7], "dev_err"), "dev_err", at::kInt, {1});
+  Held y;
+  void* py = output(c, a[5], "out", d.shape, at::kBFloat16, &y.o);
+  at::Tensor own;
+  size_t bytes = 0;
+  void* ws = c.workspace(optional(a[6], "workspace"), sdm_project_workspace_size(d.M, int(d.D), int(d.N)), &own, &bytes);
+  const int r = sdm_project(d.x, d.w, d.bias, pr, d.M, int(d.D), int(d.N), int(PyLong_AsLong(a[4])), py, ws, bytes,
+                            static_cast<int*>(pe), c.stream());
+  if (r != SDM_OK) raise_status("sdm_project", r);
+  return y.release();
+}
+
+// dense_grad(x, w, dy, bias, act, dx, dw, dbias, workspace, dev_err) -> (dx, dw, dbias or None)
+PyObject* dense_grad(PyObject* const* a) {
+  const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w"), &dy = tensor(a[2], "dy"), &bias = optional(a[3], "bias");
+  const Call c(x);
+  const Dense d = dense_operands(c, x, w, bias);
+  const int act = int(PyLong_AsLong(a[4]));
+  const void* py = c.dense(dy, "dy", at::kBFloat16, d.shape);
+  void* pe = c.dense(optional(a[9], "dev_err"), "dev_err", at::kInt, {1});
+  Held dx, dw, db;
+  void* px = output(c, a[5], "dx", x.sizes(), at::kBFloat16, &dx.o);
+  void* pw = output(c, a[6], "dw", w.sizes(), at::kBFloat16, &dw.o);
+  void* pb = nullptr;
+  if (bias.defined()) {
+    pb = output(c, a[7], "dbias", {d.N}, at::kBFloat16, &db.o);
+  } else {
+    if (a[7] != Py_None) raise(PyExc_ValueError, "dbias needs the bias");
+    Py_INCREF(Py_None);
+    db.o = Py_None;
+  }
+  at::Tensor own;
+  size_t bytes = 0;
+  void* ws = c.workspace(optional(a[8], "workspace"), sdm_project_backward_workspace_size(d.M, int(d.D), int(d.N), act),
+                         &own, &bytes);
+  const int r = sdm_project_backward(d.x, d.w, d.bias, py, d.M, int(d.D), int(d.N), act, px, pw, pb, ws, bytes,
+                                     static_cast<int*>(pe), c.stream());
+  if (r != SDM_OK) raise_status("sdm_project_backward", r);
+  PyObject* t = PyTuple_New(3);
+  if (!t) throw Raised();
+  PyTuple_SET_ITEM(t, 0, dx.release());
+  PyTuple_SET_ITEM(t, 1, dw.release());
+  PyTuple_SET_ITEM(t, 2, db.release());
+  return t;
+}
+
 // torch's own exceptions become the Python errors that its own calls raise (out of memory:
 // torch.OutOfMemoryError).
 template <PyObject* (*F)(PyObject* const*)>
@@ -393,6 +671,11 @@ PyMethodDef methods[] = {method<conv, 11>("conv"),
                          method<scan, 17>("scan"),
                          method<gated, 5>("gated"),
                          method<gated_grad, 8>("gated_grad"),
+                         method<linear, 13>("linear"),
+                         method<norm, 11>("norm"),
+                         method<norm_grad, 13>("norm_grad"),
+                         method<dense, 8>("dense"),
+                         method<dense_grad, 10>("dense_grad"),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layers", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

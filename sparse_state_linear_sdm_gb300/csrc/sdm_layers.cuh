@@ -121,6 +121,37 @@ __device__ __forceinline__ float softplus(float x) {
   return a;
 }
 
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes to shared memory, zeros where !in.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
+  const int n = in ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n)
+               : "memory");
+}
+// One element where rows are not aligned to 16 bytes: 4 bytes are copied like 16, 2 bytes are loaded.
+__device__ __forceinline__ void copy1(float* dst, const float* src, bool in) {
+  const int n = in ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void copy1(__nv_bfloat16* dst, const __nv_bfloat16* src, bool in) {
+  *dst = in ? *src : __nv_bfloat16(0.f);
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// A state carried over a chunk that adds `end` to it: exp(sum A) h + end.  Where the state grows, the
+// factor may pass the largest float although its product with h, and each token's own factor, do
+// not: it is then applied in two halves, and a state of 0 stays 0.
+__device__ __forceinline__ float carried_up(float h, float sum, float rate, float end) {
+  const float e = fmaf(sum, rate, 2.0e-8f);
+  if (!(e > 64.0f)) return fmaf(exp2_fast(e), h, end);
+  const float half = exp2_fast(0.5f * e);
+  return h == 0.0f ? end : fmaf(half, half * h, end);
+}
+
 // The memory of a tensor of a call: n1 x n2 rows of `bytes`, s1 and s2 bytes apart.
 struct Extent {
   const void* p;

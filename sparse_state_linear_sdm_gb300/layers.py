@@ -1,5 +1,6 @@
 """The layers that stand beside the memory layer in a recurrent stack: the short causal convolution, the selective
-state space scan and the gated feed-forward projections (include/sdm.h, second half).
+state space scan, linear attention, the gated feed-forward projections, and what joins them, norms with gates and
+residuals and projections with an epilogue (include/sdm.h, second half).
 
 As in ``api``, every step runs in libsdm.so's CUDA kernels on the current stream, and a tensor that is not on a CUDA
 device is refused.  The tensors are checked and the outputs allocated in ``csrc/sdm_binding.cpp``: these calls are on a
@@ -8,6 +9,8 @@ decode step's path.
 from __future__ import annotations
 
 import importlib.util
+
+import torch
 
 from . import api as _api
 from . import build as _build
@@ -112,3 +115,116 @@ def project_gated_backward(x, w, dh, activation="silu", dx=None, dw=None, worksp
     take dh's."""
     return (_module or _binding()).gated_grad(x, w, dh, _activation(activation, ("silu", "gelu")), dx, dw, workspace,
                                               dev_err)
+
+
+def linear_attention_workspace_size(dtype, B: int, T: int, H: int, dk: int, dv: int) -> int:
+    """Bytes of workspace linear_attention needs for q, k, v of torch type `dtype`; 0 where it needs none."""
+    code = _api.SDM_BF16 if dtype == torch.bfloat16 else _api.SDM_F32
+    return int(_api.lib().sdm_linear_attention_workspace_size(code, B, T, H, dk, dv))
+
+
+def linear_attention(q, k, v, decay=None, scale=None, state=None, state_out=None, lengths=None, slots=None, out=None,
+                     workspace=None, dev_err=None):
+    """Linear attention with a decay for each head over a batch of prompts (sdm_linear_attention):
+    S_t = exp(decay_t) S_{t-1} + k_t v_t^T,  o_t = scale q_t S_t.
+
+    q, k: [B, T, Hk, dk]; v: [B, T, H, dv], Hk dividing H (heads h with the same h // (H / Hk) share their queries and
+    keys); fp32 or bf16, a token's heads dense, tokens and sequences of any stride.  decay: fp32 logarithms, [B, T, H] of
+    any strides between tokens and sequences, [H] (the same for every token) or None; at most 0 where nothing is to
+    grow, -inf forgets everything before.  scale: dk ** -0.5 if None.  dk and dv up to 256.  state, state_out: fp32
+    [rows, H, dk, dv] (state None: zeros; state_out None: `state` is updated in place, or not kept where there is none).
+    lengths, slots, an empty batch: as for causal_conv.  out: o's memory; it overlaps no other tensor of the call (nor does
+    state_out, but for `state` itself): ValueError.  Returns (o [B, T, H, dv], state written).
+
+    bf16 with dk and dv up to 128 and rows on 16 bytes runs in chunks on the tensor cores, everything else token by
+    token; states are fp32 in both."""
+    return (_module or _binding()).linear(q, k, v, decay, scale, state, state_out, lengths, slots, out, workspace, dev_err,
+                                          2)
+
+
+def linear_attention_step(q, k, v, decay=None, scale=None, *, state, state_out=None, slots=None, out=None, dev_err=None):
+    """linear_attention for one decode token of every sequence: q, k [B, Hk, dk]; v, o [B, H, dv]; decay [B, H], [H] or
+    None."""
+    if state is None:
+        raise ValueError("a step needs the state")
+    return (_module or _binding()).linear(q, k, v, decay, scale, state, state_out, None, slots, out, None, dev_err, 1)
+
+
+def residual_norm(x, residual=None, weight=None, *, after=None, gate=None, scale=None, groups=1, eps=1e-6,
+                  activation="silu", out=None, residual_out=None):
+    """The norms after and before a block with its gate, residual scale and residual in one pass (sdm_residual_norm):
+    a = x / rms(x) * after * act(gate),  r = residual + scale * a,  y = r / rms(r) * weight.
+
+    Every operand but x may be None: its factor, term or norm is left out.  x, gate: [..., D] fp32 or bf16, and residual
+    of x's type or fp32: dense rows one stride apart.  after, scale, weight: [D], of one type, fp32 or bf16.  groups: the
+    norm of x is over each of `groups` groups of channels (its heads); it needs `weight` None.  activation of the gate:
+    "silu" or "none".  A group (a row) has up to 16384 channels.  out, residual_out: memory for y and r, each of
+    which may be an input of the same row size (the stream updated in place); otherwise they overlap nothing: ValueError.
+    Returns (y of x's type, or None without a weight; r of residual's type, x itself where nothing changes it)."""
+    return (_module or _binding()).norm(x, residual, weight, after, gate, scale, out, residual_out, groups, eps,
+                                        _activation(activation, ("silu", "none")))
+
+
+def residual_norm_backward_workspace_size(M: int, D: int, groups: int = 1) -> int:
+    """Bytes of workspace residual_norm_backward (and gated_norm_backward) needs for M rows."""
+    return int(_api.lib().sdm_residual_norm_backward_workspace_size(M, D, groups))
+
+
+def residual_norm_backward(x, r, dy, dr=None, weight=None, *, after=None, gate=None, scale=None, residual=True, groups=1,
+                           eps=1e-6, activation="silu", workspace=None):
+    """Gradient of residual_norm (sdm_residual_norm_backward): (dx, dresidual, dweight, dafter, dgate, dscale), None for
+    what the call does not have.
+
+    r: what the forward call returned (None where it was x itself, or without a weight); dy: y's gradient, with a
+    weight; dr: the gradient that reaches r from elsewhere, or None.  residual: whether there was one.  Without after, gate and
+    scale, dx and dresidual are the same values, and one tensor where their types are the same.  The weights' gradients are
+    summed in fp32 in an order that sizes alone decide."""
+    return (_module or _binding()).norm_grad(x, r, dy, dr, weight, after, gate, scale, residual, workspace, groups, eps,
+                                             _activation(activation, ("silu", "none")))
+
+
+def gated_norm(x, weight, gate=None, groups=1, eps=1e-6, activation="silu", out=None):
+    """x / rms(x) * weight * act(gate), the norm over each of `groups` groups of channels (an attention's heads before its
+    last projection): residual_norm's first half.  Returns y of x's type and shape."""
+    if weight is None:
+        raise ValueError("a norm needs its weight")
+    return (_module or _binding()).norm(x, None, None, weight, gate, None, None, out, groups, eps,
+                                        _activation(activation, ("silu", "none")))[1]
+
+
+def gated_norm_backward(x, weight, dy, gate=None, groups=1, eps=1e-6, activation="silu", workspace=None):
+    """Gradient of gated_norm: (dx, dweight, dgate), dgate None without a gate."""
+    if weight is None:
+        raise ValueError("a norm needs its weight")
+    g = (_module or _binding()).norm_grad(x, None, None, dy, None, weight, gate, None, False, workspace, groups, eps,
+                                          _activation(activation, ("silu", "none")))
+    return g[0], g[3], g[4]
+
+
+def project_workspace_size(M: int, D: int, N: int) -> int:
+    """Bytes of workspace project needs for M tokens; 0 where it needs none."""
+    return int(_api.lib().sdm_project_workspace_size(M, D, N))
+
+
+def project(x, w, bias=None, residual=None, activation="none", out=None, workspace=None, dev_err=None):
+    """A projection with bias, activation and residual in one kernel: y = residual + act(x w^T + bias) (sdm_project).
+
+    x: [..., D]; w: [N, D]; bias: [N]; residual: [..., N]; all bf16 and dense; D and N multiples of 8.  activation:
+    "none", "silu" or "gelu" (the exact one).  out: y's memory; it may be the residual itself, and overlaps nothing else:
+    ValueError.  Returns y [..., N] bf16."""
+    return (_module or _binding()).dense(x, w, bias, residual, _activation(activation, ("none", "silu", "gelu")), out,
+                                         workspace, dev_err)
+
+
+def project_backward_workspace_size(M: int, D: int, N: int, activation="none") -> int:
+    """Bytes of workspace project_backward needs for M tokens."""
+    act = _activation(activation, ("none", "silu", "gelu"))
+    return int(_api.lib().sdm_project_backward_workspace_size(M, D, N, act))
+
+
+def project_backward(x, w, dy, bias=None, activation="none", dx=None, dw=None, dbias=None, workspace=None, dev_err=None):
+    """Gradient of project for dy [..., N] (sdm_project_backward): (dx [..., D], dw [N, D], dbias [N] or None without a
+    bias), all bf16.  The residual's gradient is dy itself.  The forward pass keeps nothing but its inputs: with an activation the
+    projection is formed again.  dx, dw, dbias, workspace: memory for them, which overlaps nothing (ValueError)."""
+    return (_module or _binding()).dense_grad(x, w, dy, bias, _activation(activation, ("none", "silu", "gelu")), dx, dw,
+                                              dbias, workspace, dev_err)
