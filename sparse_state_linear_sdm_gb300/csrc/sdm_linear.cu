@@ -523,6 +523,8 @@ void cut_steps(int B, int T, int H, int dk, int dv, int* segments, int* segment)
   *segments = n > 1 ? int((T + per - 1) / per) : 1;
 }
 
+constexpr int kTileTokens = 32;  // tokens of a prompt from which on chunks pay
+
 // What of the output, the new states and the workspace overlaps anything else of the call.
 bool overlap(const sdm_linear_args& io, const void* workspace, size_t workspace_bytes) {
   const long long es = io.dtype == SDM_F32 ? 4 : 2, qk = (long long)io.Hk * io.dk * es, vr = (long long)io.H * io.dv * es;
@@ -564,6 +566,11 @@ extern "C" size_t sdm_linear_attention_workspace_size(int dtype, int B, int T, i
   if (!sizes_ok(dtype, B, T, H, dk, dv) || dk > SDM_MAX_LINEAR_D || dv > SDM_MAX_LINEAR_D) return 0;
   int segments, segment;
   cut_steps(B, T, H, dk, dv, &segments, &segment);
+  if (dtype == SDM_BF16 && dk <= SDM_LINEAR_TILE_D && dv <= SDM_LINEAR_TILE_D) {  // which form it is, strides decide
+    int n;
+    cut_tiles(B, T, H, &n, &segment);
+    segments = n > segments ? n : segments;
+  }
   if (segments <= 1) return 0;
   return size_t(segments) * B * H * (size_t(dk) * dv + 4) * 4;
 }
@@ -595,8 +602,20 @@ extern "C" int sdm_linear_attention(const sdm_linear_args* args, void* workspace
     if (overlap(io, nullptr, 0)) return SDM_EOVERLAP;
     return io.dtype == SDM_F32 ? launch_token<float>(a, s) : launch_token<__nv_bfloat16>(a, s);
   }
+  const int V = io.dtype == SDM_F32 ? 4 : 8;
+  auto rows16 = [&](const void* p, long long bs, long long ts) { return !off(p, 15) && bs % V == 0 && ts % V == 0; };
+  a.vec_qk = io.dk % V == 0 && rows16(io.q, io.q_bs, io.q_ts) && rows16(io.k, io.k_bs, io.k_ts);
+  a.vec_v = io.dv % V == 0 && rows16(io.v, io.v_bs, io.v_ts);
+  a.vec_o = io.dv % V == 0 && !off(io.o, 15);
+  auto steps_on = [&](long long bs, long long ts) { return ts > 0 && (io.B == 1 || bs > 0); };
+  const bool tiles = io.dtype == SDM_BF16 && io.T >= kTileTokens && io.dk <= SDM_LINEAR_TILE_D && io.dv <= SDM_LINEAR_TILE_D &&
+                     a.vec_qk && a.vec_v && a.vec_o && steps_on(io.q_bs, io.q_ts) && steps_on(io.k_bs, io.k_ts) &&
+                     steps_on(io.v_bs, io.v_ts);
   const size_t need = sdm_linear_attention_workspace_size(io.dtype, io.B, io.T, io.H, io.dk, io.dv);
-  cut_steps(io.B, io.T, io.H, io.dk, io.dv, &a.segments, &a.segment);
+  if (tiles)
+    cut_tiles(io.B, io.T, io.H, &a.segments, &a.segment);
+  else
+    cut_steps(io.B, io.T, io.H, io.dk, io.dv, &a.segments, &a.segment);
   if (need) {
     if (!aligned16(workspace)) return SDM_EALIGN;
     if (workspace_bytes < need) return SDM_ENOSPACE;
@@ -604,10 +623,6 @@ extern "C" int sdm_linear_attention(const sdm_linear_args* args, void* workspace
     a.ws_g = a.ws_s + size_t(a.segments) * io.B * io.H * io.dk * io.dv;
   }
   if (overlap(io, need ? workspace : nullptr, need)) return SDM_EOVERLAP;
-  const int V = io.dtype == SDM_F32 ? 4 : 8;
-  auto rows16 = [&](const void* p, long long bs, long long ts) { return !off(p, 15) && bs % V == 0 && ts % V == 0; };
-  a.vec_qk = io.dk % V == 0 && rows16(io.q, io.q_bs, io.q_ts) && rows16(io.k, io.k_bs, io.k_ts);
-  a.vec_v = io.dv % V == 0 && rows16(io.v, io.v_bs, io.v_ts);
-  a.vec_o = io.dv % V == 0 && !off(io.o, 15);
+  if (tiles) return launch_tiles(a, s);
   return io.dtype == SDM_F32 ? launch_type<float>(a, s) : launch_type<__nv_bfloat16>(a, s);
 }

@@ -52,4 +52,9 @@ __device__ __forceinline__ Place place_of(const LinearArgs& a) {
 // The kernel that turns segments' ends into the states in front of them.
 int launch_front(const LinearArgs& a, cudaStream_t s);
 
+// The tensor cores' form: bf16, dk and dv up to SDM_LINEAR_TILE_D and multiples of 8, rows on 16 bytes, positive strides.
+// Segments of its own.
+void cut_tiles(int B, int T, int H, int* segments, int* segment);
+int launch_tiles(LinearArgs a, cudaStream_t s);
+
 }  // namespace sdm
