@@ -5,17 +5,18 @@
 //   o_i = scale (sum_{j<=i} A_ij (q_i k_j) v_j  +  G_i q_i S)
 //   S'  = G_last S + sum_j k_j (A_last,j v_j)^T
 //
-// Four products a chunk: q k^T, q S, (A q k^T) v and k^T (A v).  A CTA takes a sequence's head, its state in
-// registers (fp32, 64 a thread), and walks its chunks; every product has its accumulator in TMEM (128 columns each,
-// all 512 together).  Warps by role: TMA and decays; MMAs; eight that turn q k^T into the masked bf16 products and
-// write o; eight that weight v and update the state.  q, k and v come through a ring of four 32 KB slots, in
-// the order of their use, so that the slot of q takes the next k, and so on.
+// Four products a chunk: q k^T, q S, (A q k^T) v and (A v)^T k, the last one the state transposed.  A CTA takes a
+// sequence's head, its state in registers (fp32, 64 a thread), and walks its chunks.  Warps by role: TMA and
+// decays; MMAs; eight that turn q k^T into the masked bf16 products, scale q S by G and write o; eight that weight
+// v and update the state.  q, k and v come through a ring of five 32 KB slots in the order of their use.
+// An MMA of 128 x 128 x 16 whose operands both lie in shared memory waits for them (64 bytes a clock: 128 clocks instead
+// of 64), so the masked products and the weighted v are first operands out of TMEM.
 //
 // What is rounded to bf16: the masked products and the state as q reads it, as an MMA takes them (each half a unit, as o
 // itself).  The state is not: A v is cut into three bf16 parts whose products are summed in fp32 (two parts
 // leave 3e-6 of the state, three 1e-8), which costs two more MMAs of six a chunk and no byte.
 // The A_ij of a row are formed by one product after the other from the diagonal on, so a decay of 0 leaves 0 before it
-// and no difference of sums is taken; G and A_last,j come from sums of g in 64 bits.
+// and no difference of sums is taken; G and A_last,j come from sums of g in two floats.
 #include "sdm_linear.cuh"
 #include "sdm_tcgen05.cuh"
 
@@ -25,20 +26,22 @@ namespace {
 constexpr int kChunk = 128;
 constexpr int kSlot = 32768;             // 128 tokens of 128 columns: two boxes of 64 columns
 constexpr int kBox = kChunk * 128;       // bytes of a box
-constexpr int kSlots = 4;
-constexpr int kSlice = 16;               // tokens of a weighted slice of v: one K step
+constexpr int kSlots = 5;
+constexpr int kSlice = 32;               // tokens of a weighted slice of v: two K steps
 constexpr int kTileThreads = 32 * 18;
 constexpr int kMaskWarp = 2, kStateWarp = 10;  // first warps of the two groups of eight
 
 enum Bar {
-  kFull = 0, kEmpty = 4,          // slots
-  kScoreFull = 8, kScoreEmpty,    // q k^T
-  kMaskFull, kMaskEmpty,          // the masked products in shared memory
-  kOutFull, kOutEmpty,            // both accumulators of o
+  kFull = 0, kEmpty = kSlots,     // slots
+  kScoreFull = 2 * kSlots,        // q k^T
+  kReadFull,                      // q S
+  kMaskFull,                      // the masked products, in the place of q k^T
+  kOutFull, kOutEmpty,            // o
   kStateFull, kStateEmpty,        // the state as q reads it
   kPartFull, kPartEmpty = kPartFull + 2,  // weighted slices
   kSumFull = kPartEmpty + 2, kSumEmpty,   // k^T (A v)
-  kDecayFull, kDecayEmpty = kDecayFull + 2,
+  kStaged,                        // o has left the slot of v, of even and of odd chunks: the copies may be late by two
+  kDecayFull = kStaged + 2, kDecayEmpty = kDecayFull + 2,
   kCut = kDecayEmpty + 2,         // tokens past the end cleared
   kDrain, kBars
 };
@@ -47,24 +50,23 @@ struct Decays {  // of a chunk
   float each[kChunk];  // e^g
   float from[kChunk];  // products from the chunk's start up to each token
   float to[kChunk];    // products after each token up to the chunk's end; 0 past the sequence's
+  float block[kChunk]; // products from the start of each token's block of 32
   float all, pad[3];
 };
 
 template <int DK, int DV>
 struct Tiles {
-  static constexpr int part = DV / 64 * kSlice * 128;  // one of three parts of a slice
   static constexpr int off_state = kSlots * kSlot;
-  static constexpr int off_mask = off_state + DK * DV * 2;
-  static constexpr int off_parts = off_mask + 2 * kBox;
-  static constexpr int off_decays = off_parts + 2 * 3 * part;
+  static constexpr int off_decays = off_state + DK * DV * 2;
   static constexpr int off_bars = off_decays + 2 * int(sizeof(Decays));
   static constexpr int bytes = off_bars + 512 + 1024 /* alignment slack */;
 };
 
-constexpr uint32_t kScore = 0, kOutState = 128, kOutChunk = 256, kSum = 384;  // TMEM columns
+// TMEM columns.  Of each 32 of q k^T the masked products take 16; a slice's three parts are 16 columns each.
+constexpr uint32_t kScore = 0, kOut = 128, kSum = 256, kParts = 384, kPartCols = kSlice / 2;
 
 struct TileMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
 };
 
 // D fp32, A and B bf16, M 128; bits 15 and 16: A, B MN-major.
@@ -77,13 +79,42 @@ __device__ __forceinline__ uint64_t mn_box_desc(uint32_t saddr, uint32_t box) {
   return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(box >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
          (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
+// The whole warp calls these; one lane of it, always the same, issues the MMA or the commit.
 __device__ __forceinline__ void mma1(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate, uint32_t id) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xFFFFFFFF;\n setp.ne.b32 p, %3, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(accumulate), "r"(id)
       : "memory");
 }
+// A from TMEM: 16 bf16 of a row in eight columns.
+__device__ __forceinline__ void mma1_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate, uint32_t id) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xFFFFFFFF;\n setp.ne.b32 p, %3, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(accumulate), "r"(id)
+      : "memory");
+}
+__device__ __forceinline__ void commit1(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xFFFFFFFF;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+// 16 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store4(uint32_t taddr, const uint4& a) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -92,13 +123,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 __device__ __forceinline__ uint32_t swizzled(int row, int piece) { return uint32_t(row * 128 + ((piece ^ (row & 7)) << 4)); }
-__device__ __forceinline__ uint4 shared_load(uint32_t p) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
-  return v;
-}
 __device__ __forceinline__ void shared_store(uint32_t p, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int x, int y, int z, int w, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(w), "r"(src)
+               : "memory");
 }
 __device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -107,6 +139,19 @@ __device__ __forceinline__ float finite_exp2(float x) {
   const float y = exp2f(x);
   return y > 3.402823466e38f ? 3.402823466e38f : y;
 }
+
+// A sum in two floats: as good as one in 64 bits here, and the card adds few of those.
+struct Sum {
+  float hi, lo;
+  __device__ __forceinline__ Sum operator+(const Sum& o) const {
+    const float s = hi + o.hi, z = s - hi;
+    return {s, (lo + o.lo) + ((hi - (s - z)) + (o.hi - z))};
+  }
+  __device__ __forceinline__ Sum from_lane(int lane) const {
+    return {__shfl_sync(0xFFFFFFFFu, hi, lane & 31), __shfl_sync(0xFFFFFFFFu, lo, lane & 31)};
+  }
+  __device__ __forceinline__ float exp() const { return finite_exp2(fmaf(hi, kLog2e, lo * kLog2e)); }
+};
 
 // Every wait is bounded; one that runs out stops the CTA, which waits for the copies and MMAs in flight, frees TMEM and
 // reports SDM_DEV_TIMEOUT.
@@ -132,7 +177,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
       int n = 1;
-      if (i == kScoreEmpty || i == kMaskFull || i == kOutEmpty || i == kStateFull || i == kPartFull || i == kPartFull + 1 ||
+      if (i == kMaskFull || i == kStaged || i == kStaged + 1 || i == kOutEmpty || i == kStateFull || i == kPartFull || i == kPartFull + 1 ||
           i == kSumEmpty || i == kCut)
         n = 8;  // the warps of a group
       if (i == kDecayEmpty || i == kDecayEmpty + 1) n = PASS == kReduce ? 8 : 16;
@@ -146,12 +191,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  // The masked products' blocks above the diagonal stay 0.
-  if (PASS != kReduce) {
-    for (uint32_t i = threadIdx.x * 16; i < 2 * kBox; i += kTileThreads * 16)
-      *reinterpret_cast<uint4*>(smem + L::off_mask + i) = make_uint4(0, 0, 0, 0);
-    async_proxy_fence();
   }
   tc_fence_before();
   __syncthreads();
@@ -178,53 +217,71 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = c * kChunk + lane * 4 + i;
-        next[i] = g && t < tokens ? g[(p.t_lo + t) * io.g_ts] : 0.f;
+        const float x = g && t < tokens ? g[(p.t_lo + t) * io.g_ts] : 0.f;
+        next[i] = x < -1e30f ? -1e30f : x > 1e30f ? 1e30f : x;  // sums stay finite
       }
     };
-    ask(0);
-    double total = 0.0;
-    int load = 0;
-    for (int c = 0; c < chunks; ++c) {
-      if (!wait_all(kDecayEmpty + (c & 1), uint32_t(c >> 1) + 1)) break;
-      float e[4];
+    Sum total = {0.f, 0.f};
+    // The decays of chunk c, four tokens a lane.
+    auto decay = [&](int c) {
+      if (!wait_all(kDecayEmpty + (c & 1), uint32_t(c >> 1) + 1)) return false;
+      Sum up[4], down[4];  // sums up to and after each token of the lane's
+      up[0] = {next[0], 0.f};
+      down[3] = {0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = next[i];
-      if (c + 1 < chunks) ask(c + 1);
+      for (int i = 1; i < 4; ++i) {
+        up[i] = up[i - 1] + Sum{next[i], 0.f};
+        down[3 - i] = down[4 - i] + Sum{next[4 - i], 0.f};
+      }
       Decays& d = decays[c & 1];
-      double up[4], down[4];  // sums up to and after each token of the lane's
-      up[0] = e[0];
 #pragma unroll
-      for (int i = 1; i < 4; ++i) up[i] = up[i - 1] + double(e[i]);
-      down[3] = 0.0;
-#pragma unroll
-      for (int i = 2; i >= 0; --i) down[i] = down[i + 1] + double(e[i + 1]);
-      double before = up[3], after = up[3];  // scans of the lanes' sums
+      for (int i = 0; i < 4; ++i) d.each[lane * 4 + i] = exp2f(kLog2e * next[i]);
+      if (c + 1 < chunks) ask(c + 1);
+      Sum before = up[3], after = up[3], within = up[3];  // scans over the lanes; within: over eight, a block of 32 tokens
 #pragma unroll
       for (int m = 1; m < 32; m *= 2) {
-        const double x = __shfl_up_sync(0xFFFFFFFFu, before, m), y = __shfl_down_sync(0xFFFFFFFFu, after, m);
-        if (lane >= m) before += x;
-        if (lane + m < 32) after += y;
+        const Sum x = before.from_lane(lane - m), y = after.from_lane(lane + m);
+        if (lane >= m) before = before + x;
+        if (lane + m < 32) after = after + y;
+        if (m < 8) {
+          const Sum z = within.from_lane(lane - m);
+          if (lane % 8 >= m) within = within + z;
+        }
       }
-      const double all = __shfl_sync(0xFFFFFFFFu, before, 31);
-      double left = __shfl_up_sync(0xFFFFFFFFu, before, 1), right = __shfl_down_sync(0xFFFFFFFFu, after, 1);
-      if (lane == 0) left = 0.0;
-      if (lane == 31) right = 0.0;
-      const double log2e = 1.4426950408889634;
+      const Sum all = before.from_lane(31), zero = {0.f, 0.f};
+      Sum left = before.from_lane(lane - 1), right = after.from_lane(lane + 1), block = within.from_lane(lane - 1);
+      if (lane == 0) left = zero;
+      if (lane == 31) right = zero;
+      if (lane % 8 == 0) block = zero;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = lane * 4 + i;
-        d.each[t] = exp2f(float(double(e[i]) * log2e));
-        d.from[t] = finite_exp2(float((left + up[i]) * log2e));
-        d.to[t] = c * kChunk + t < tokens ? finite_exp2(float((right + down[i]) * log2e)) : 0.f;
+        d.block[t] = (block + up[i]).exp();
+        d.from[t] = (left + up[i]).exp();
+        d.to[t] = c * kChunk + t < tokens ? (right + down[i]).exp() : 0.f;
       }
-      if (lane == 0) d.all = finite_exp2(float(all * log2e));
-      total += all;
+      if (lane == 0) d.all = all.exp();
+      total = total + all;
       arrive(kDecayFull + (c & 1));
-      bool ok = true;
+      return true;
+    };
+    ask(0);
+    int load = 0;
+    uint32_t taken = 0;  // by slot, the parity of the next wait for its commits
+    bool ok = chunks == 0 || decay(0);
+    for (int c = 0; c < chunks && ok; ++c) {
       if (lane == 0) {
         for (int i = 3 - kLoads; i < 3 && ok; ++i, ++load) {
           const int slot = load % kSlots;
-          ok = wait(kEmpty + slot, uint32_t(load / kSlots) + 1);
+          // The slot's last load: v's is free when o has left its place, the others' when their MMAs are done.
+          const int old = load - kSlots;
+          if (old >= 0 && PASS != kReduce && old % kLoads == kLoads - 1) {
+            const int chunk = old / kLoads;
+            ok = wait(kStaged + (chunk & 1), uint32_t(chunk >> 1));
+          } else if (old >= 0) {
+            ok = wait(kEmpty + slot, taken >> slot);
+            taken ^= 1u << slot;
+          }
           if (!ok) break;
           const uint32_t dst = base + uint32_t(slot) * kSlot;
           const int boxes = i == 2 ? kBoxesV : kBoxesK, t = p.t_lo + c * kChunk;
@@ -235,187 +292,206 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           issued[slot] = issued[slot] + 1u;
         }
       }
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      ok = __all_sync(0xFFFFFFFFu, ok) && (c + 1 == chunks || decay(c + 1));
     }
-    if (PASS == kReduce && lane == 0) a.ws_g[p.seg * nbh + bh] = float(total);
+    if (PASS == kReduce && lane == 0) a.ws_g[p.seg * nbh + bh] = total.hi + total.lo;
   } else if (warp == 1) {
     // ---- MMAs ----
-    if (lane == 0) {
-      int slices = 0;  // so far
-      bool ok = true;
-      for (int c = 0; c < chunks && ok; ++c) {
-        const int n = min(kChunk, tokens - c * kChunk), first = c * kLoads;
-        const int iq = first, ik = first + kLoads - 2, iv = first + kLoads - 1;  // loads
-        const uint32_t sq = base + uint32_t(iq % kSlots) * kSlot, sk = base + uint32_t(ik % kSlots) * kSlot,
-                       sv = base + uint32_t(iv % kSlots) * kSlot;
-        if (n < kChunk && !(ok = wait(kCut, 0))) break;
-        if (!(ok = wait(kFull + ik % kSlots, uint32_t(ik / kSlots)))) break;
-        if (PASS != kReduce) {
-          if (!(ok = wait(kFull + iq % kSlots, uint32_t(iq / kSlots)))) break;
-          if (!(ok = wait(kScoreEmpty, uint32_t(c) + 1))) break;
-          tc_fence_after();
+    int slices = 0;  // so far
+    bool ok = true;
+    auto slot_of = [&](int load) { return base + uint32_t(load % kSlots) * kSlot; };
+    auto step = [](int kk) { return uint64_t(kk / 4 * kBox + kk % 4 * 32) >> 4; };  // K steps along a row of boxes
+    for (int c = 0; c < chunks && ok; ++c) {
+      const int n = min(kChunk, tokens - c * kChunk), first = c * kLoads;
+      const int iq = first, ik = first + kLoads - 2, iv = first + kLoads - 1;  // loads
+      const uint64_t k_rows = mn_box_desc(slot_of(ik), kBox), v_rows = mn_box_desc(slot_of(iv), kBox);
+      if (n < kChunk && !(ok = wait_all(kCut, 0))) break;
+      if (!(ok = wait_all(kFull + ik % kSlots, uint32_t(ik / kSlots)))) break;
+      if (PASS != kReduce) {
+        const uint64_t q = sw128_desc(slot_of(iq)), k = sw128_desc(slot_of(ik));
+        if (!(ok = wait_all(kFull + iq % kSlots, uint32_t(iq / kSlots)))) break;
+        if (c > 0 && !(ok = wait_all(kOutFull, uint32_t(c) - 1))) break;  // the masked products before have been read
+        tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < DK / 16; ++kk) {
-            const uint32_t off = uint32_t(kk / 4 * kBox + kk % 4 * 32);
-            mma1(tmem + kScore, sw128_desc(sq + off), sw128_desc(sk + off), kk > 0, tile_idesc(128, false, false));
-          }
-          mma_commit(bar(kScoreFull));
-          if (!(ok = wait(kStateFull, uint32_t(c)))) break;
-          if (!(ok = wait(kOutEmpty, uint32_t(c) + 1))) break;
-          tc_fence_after();
-          const uint32_t ss = base + L::off_state;
+        for (int kk = 0; kk < DK / 16; ++kk)
+          mma1(tmem + kScore, q + step(kk), k + step(kk), kk > 0, tile_idesc(128, false, false));
+        commit1(bar(kScoreFull));
+        if (!(ok = wait_all(kStateFull, uint32_t(c)))) break;
+        if (!(ok = wait_all(kOutEmpty, uint32_t(c) + 1))) break;
+        tc_fence_after();
+        const uint64_t state = sw128_desc(base + L::off_state);
 #pragma unroll
-          for (int kk = 0; kk < DK / 16; ++kk)
-            mma1(tmem + kOutState, sw128_desc(sq + uint32_t(kk / 4 * kBox + kk % 4 * 32)),
-                 mn_box_desc(ss + uint32_t(kk * 2048), DK * 128), kk > 0, tile_idesc(DV, false, true));
-          mma_commit(bar(kStateEmpty));
-          mma_commit(bar(kEmpty + iq % kSlots));
-        }
-        if (!(ok = wait(kSumEmpty, uint32_t(c) + 1))) break;
-        const int ns = (n + kSlice - 1) / kSlice;
-        for (int s = 0; s < ns; ++s, ++slices) {
-          const int b = slices & 1;
-          if (!(ok = wait(kPartFull + b, uint32_t(slices >> 1)))) break;
-          tc_fence_after();
-          const uint32_t sp = base + L::off_parts + uint32_t(b * 3 * L::part);
+        for (int kk = 0; kk < DK / 16; ++kk)
+          mma1(tmem + kOut, q + step(kk), state + uint64_t((kk / 4 * DV * 128 + kk % 4 * 32) >> 4), kk > 0,
+               tile_idesc(DV, false, false));
+        commit1(bar(kReadFull));
+        commit1(bar(kStateEmpty));
+        commit1(bar(kEmpty + iq % kSlots));
+      }
+      if (!(ok = wait_all(kSumEmpty, uint32_t(c) + 1))) break;
+      const int ns = (n + kSlice - 1) / kSlice;
+      for (int s = 0; s < ns; ++s, ++slices) {
+        const int b = slices & 1;
+        if (!(ok = wait_all(kPartFull + b, uint32_t(slices >> 1)))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kSlice / 16; ++kk)
 #pragma unroll
           for (int i = 0; i < 3; ++i)
-            mma1(tmem + kSum, mn_box_desc(sk + uint32_t(s * 2048), kBox), mn_box_desc(sp + uint32_t(i * L::part), kSlice * 128),
-                 s > 0 || i > 0, tile_idesc(DV, true, true));
-          mma_commit(bar(kPartEmpty + b));
-        }
-        if (!ok) break;
-        mma_commit(bar(kSumFull));
-        mma_commit(bar(kEmpty + ik % kSlots));
-        if (PASS != kReduce) {
-          if (!(ok = wait(kMaskFull, uint32_t(c)))) break;
-          if (!(ok = wait(kFull + iv % kSlots, uint32_t(iv / kSlots)))) break;
-          tc_fence_after();
-          const uint32_t sm = base + L::off_mask;
-#pragma unroll
-          for (int kk = 0; kk < kChunk / 16; ++kk)
-            mma1(tmem + kOutChunk, sw128_desc(sm + uint32_t(kk / 4 * kBox + kk % 4 * 32)),
-                 mn_box_desc(sv + uint32_t(kk * 2048), kBox), kk > 0, tile_idesc(DV, false, true));
-          mma_commit(bar(kMaskEmpty));
-          mma_commit(bar(kOutFull));
-        }
-        mma_commit(bar(kEmpty + iv % kSlots));
+            mma1_tmem(tmem + kSum, tmem + kParts + uint32_t(b * 3 + i) * kPartCols + uint32_t(kk * 8),
+                      k_rows + uint64_t((s * (kSlice / 16) + kk) * 2048 >> 4), s > 0 || kk > 0 || i > 0,
+                      tile_idesc(DK, false, true));
+        commit1(bar(kPartEmpty + b));
       }
-      mma_commit(bar(kDrain));
-      mbar_wait_teardown(bar(kDrain), 0);
+      if (!ok) break;
+      commit1(bar(kSumFull));
+      commit1(bar(kEmpty + ik % kSlots));
+      if (PASS != kReduce) {
+        if (!(ok = wait_all(kMaskFull, uint32_t(c)))) break;
+        if (!(ok = wait_all(kFull + iv % kSlots, uint32_t(iv / kSlots)))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kChunk / 16; ++kk)
+          mma1_tmem(tmem + kOut, tmem + kScore + uint32_t(kk / 2 * 32 + kk % 2 * 8), v_rows + uint64_t(kk * 2048 >> 4), 1,
+                    tile_idesc(DV, false, true));
+        commit1(bar(kOutFull));
+      }
+      if (PASS == kReduce) commit1(bar(kEmpty + iv % kSlots));
     }
+    commit1(bar(kDrain));
+    mbar_wait_teardown(bar(kDrain), 0);
   } else if (warp < kStateWarp) {
     // ---- masked products, then o ----
     if (PASS != kReduce) {
       const int quad = warp & 3, half = (warp - kMaskWarp) >> 2;
       const int row = quad * 32 + lane;
-      const uint32_t lanes = uint32_t(quad * 32) << 16;
+      const uint32_t lanes = uint32_t(quad * 32) << 16, out_at = tmem + lanes + kOut + uint32_t(half * (DV / 2));
       // Blocks of 32 columns up to the diagonal's: the first half of the warps takes the later ones.
       const int cut = (quad + 1) / 2, b_hi = half ? cut - 1 : quad, b_lo = half ? 0 : cut;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(io.o) +
-                           (((long long)p.b * io.T + p.t_lo + row) * io.H + p.h) * io.dv + half * (DV / 2);
+      // This warp's part of o lies where v was: 32 rows of DV / 2 columns, 128 or 64 bytes, in their swizzle.
+      constexpr int kRowBytes = DV;
+      auto staged = [&](int piece) {
+        return DV == 128 ? swizzled(lane, piece) : uint32_t(lane * 64 + ((piece ^ (lane >> 1 & 3)) << 4));
+      };
       for (int c = 0; c < chunks; ++c) {
         const int n = min(kChunk, tokens - c * kChunk);
         if (!wait_all(kDecayFull + (c & 1), uint32_t(c >> 1))) break;
         const Decays& d = decays[c & 1];
         if (!wait_all(kScoreFull, uint32_t(c))) break;
         tc_fence_after();
-        if (!wait_all(kMaskEmpty, uint32_t(c) + 1)) break;
-        float f = io.scale;  // A_ij scale of the column last passed
-        if (half) {          // from the diagonal to this warp's columns
-          f = io.scale;
-          for (int j = quad * 32 + 31; j > b_hi * 32 + 31; --j) f = j <= row ? f * d.each[j] : f;
+        float f = io.scale;  // A_ij scale of the column that is next
+        if (half) {          // past the blocks of the other half
+          f *= d.block[row];
+          for (int b = quad - 1; b > b_hi; --b) f *= d.block[b * 32 + 31];
         }
         for (int b = b_hi; b >= b_lo; --b) {
           uint32_t r[32];
           tmem_load32(tmem + lanes + kScore + uint32_t(b * 32), r);
-          const bool diagonal = b == quad;
-          const uint32_t dst = base + L::off_mask + uint32_t(b / 2 * kBox);
+          uint32_t pairs[16];
+          const float* each = d.each + b * 32;
+          if (b == quad) {  // the diagonal's
 #pragma unroll
-          for (int w = 3; w >= 0; --w) {
-            float v[8];
-#pragma unroll
-            for (int i = 7; i >= 0; --i) {
-              const int j = w * 8 + i;  // column in the block
-              // f: A of column j.  Past the columns of the block before, only the entry's own decay is left to apply.
-              v[i] = diagonal && j > lane ? 0.f : f * __uint_as_float(r[j]);
-              if (!diagonal || j <= lane) f *= d.each[b * 32 + j];
+            for (int j = 30; j >= 0; j -= 2) {  // columns j, j + 1 of the block
+              const float2 e = *reinterpret_cast<const float2*>(each + j);
+              const float hi = j + 1 > lane ? 0.f : f * __uint_as_float(r[j + 1]);
+              f = j + 1 > lane ? f : f * e.y;
+              const float lo = j > lane ? 0.f : f * __uint_as_float(r[j]);
+              f = j > lane ? f : f * e.x;
+              pairs[j / 2] = pack_bf16(__float_as_uint(lo), __float_as_uint(hi));
             }
-            shared_store(dst + swizzled(row, (b & 1) * 4 + w), Piece<__nv_bfloat16>::pack(v));
+          } else {
+#pragma unroll
+            for (int j = 28; j >= 0; j -= 4) {
+              const float4 e = *reinterpret_cast<const float4*>(each + j);
+              const float f2 = f * e.w, f1 = f2 * e.z, f0 = f1 * e.y;
+              pairs[j / 2 + 1] = pack_bf16(__float_as_uint(f2 * __uint_as_float(r[j + 2])),
+                                           __float_as_uint(f * __uint_as_float(r[j + 3])));
+              pairs[j / 2] = pack_bf16(__float_as_uint(f0 * __uint_as_float(r[j])),
+                                       __float_as_uint(f1 * __uint_as_float(r[j + 1])));
+              f = f0 * e.x;
+            }
           }
+          tmem_store16(tmem + lanes + kScore + uint32_t(b * 32), pairs);
         }
-        async_proxy_fence();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kScoreEmpty));
-          mbar_arrive(bar(kMaskFull));
+        if (!half) {  // nothing above the diagonal
+          const uint32_t zeros[16] = {};
+          for (int b = quad + 1; b < 4; ++b) tmem_store16(tmem + lanes + kScore + uint32_t(b * 32), zeros);
         }
+        // q S, on which the chunk's own products are added, takes the decays from the chunk's start.
         const float from = d.from[row] * io.scale;
-        if (!wait_all(kOutFull, uint32_t(c))) break;
+        if (!wait_all(kReadFull, uint32_t(c))) break;
         tc_fence_after();
-        const bool here = p.t_lo + c * kChunk + row < p.t_hi, live = row < n;
 #pragma unroll
         for (int x = 0; x < DV / 2; x += 16) {
-          uint32_t r1[16], r2[16];
-          tmem_load16(tmem + lanes + kOutState + uint32_t(half * (DV / 2) + x), r1);
-          tmem_load16(tmem + lanes + kOutChunk + uint32_t(half * (DV / 2) + x), r2);
+          uint32_t r[16];
+          tmem_load16(out_at + uint32_t(x), r);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(from * __uint_as_float(r[i]));
+          tmem_store16(out_at + uint32_t(x), r);
+        }
+        tmem_stored();
+        tc_fence_before();
+        arrive(kMaskFull);
+        if (!wait_all(kOutFull, uint32_t(c))) break;
+        tc_fence_after();
+        const bool live = row < n;
+        const int iv = c * kLoads + kLoads - 1;
+        const uint32_t patch = base + uint32_t(iv % kSlots) * kSlot + uint32_t((half * 4 + quad) * 32 * kRowBytes);
+#pragma unroll
+        for (int x = 0; x < DV / 2; x += 16) {
+          uint32_t r[16];
+          tmem_load16(out_at + uint32_t(x), r);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              v[i] = live ? fmaf(from, __uint_as_float(r1[8 * k + i]), __uint_as_float(r2[8 * k + i])) : 0.f;
-            if (here && half * (DV / 2) + x + 8 * k < io.dv)
-              *reinterpret_cast<uint4*>(out + x + 8 * k) = Piece<__nv_bfloat16>::pack(v);
+            for (int i = 0; i < 8; ++i) v[i] = live ? __uint_as_float(r[8 * k + i]) : 0.f;
+            shared_store(patch + staged(x / 8 + k), Piece<__nv_bfloat16>::pack(v));
           }
         }
-        out += (long long)kChunk * io.H * io.dv;
         tc_fence_before();
+        async_proxy_fence();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(kOutEmpty));
           mbar_arrive(bar(kDecayEmpty + (c & 1)));
+          tma_store_4d(&tm.o, half * (DV / 2), p.h, p.t_lo + c * kChunk + quad * 32, p.b, patch);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          mbar_arrive(bar(kStaged + (c & 1)));
         }
+        __syncwarp();
       }
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   } else {
     // ---- weighted v, then the state ----
-    constexpr int kCols = DV / 2;
+    // The state lies transposed: a thread has a column of v and half of the rows, s[i] that of row c0 + i.
+    constexpr int kCols = DK / 2;
     const int quad = warp & 3, half = (warp - kStateWarp) >> 2, tid = threadIdx.x - kStateWarp * 32;
-    const int row = quad * 32 + lane, c0 = half * kCols;
+    const int col = quad * 32 + lane, c0 = half * kCols;
     const uint32_t lanes = uint32_t(quad * 32) << 16;
-    const bool rows = row < DK;  // this warp has rows of the state
+    const bool cols = quad * 32 < DV;  // this warp has columns of v
     float s[kCols];
 #pragma unroll
     for (int i = 0; i < kCols; ++i) s[i] = 0.f;
     const float* src = PASS == kJoin ? a.ws_s + (p.seg * nbh + bh) * sn
                        : PASS == kWhole && io.state && p.slot >= 0 ? io.state + ((long long)p.slot * io.H + p.h) * sn
                                                                    : nullptr;
-    if (src && row < io.dk) {
-      src += (long long)row * io.dv + c0;
-      if (a.vec_s) {
+    if (src && col < io.dv) {
 #pragma unroll
-        for (int i = 0; i < kCols; i += 4)
-          if (c0 + i < io.dv) {
-            const float4 w = *reinterpret_cast<const float4*>(src + i);
-            s[i] = w.x, s[i + 1] = w.y, s[i + 2] = w.z, s[i + 3] = w.w;
-          }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kCols; ++i)
-          if (c0 + i < io.dv) s[i] = src[i];
-      }
+      for (int i = 0; i < kCols; ++i)
+        if (c0 + i < io.dk) s[i] = src[(c0 + i) * io.dv + col];
     }
     auto show_state = [&] {  // as q reads it
-      if (rows) {
+      if (cols) {
 #pragma unroll
         for (int i = 0; i < kCols; i += 8) {
           float v[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = s[i + k];
-          const int col = c0 + i;
-          shared_store(base + L::off_state + uint32_t(col / 64 * DK * 128) + swizzled(row, col / 8 % 8),
+          const int r = c0 + i;
+          shared_store(base + L::off_state + uint32_t(r / 64 * DV * 128) + swizzled(col, r / 8 % 8),
                        Piece<__nv_bfloat16>::pack(v));
         }
       }
@@ -447,27 +523,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int t0 = 0; t0 < n; t0 += kSlice, ++slices) {
         const int b = slices & 1;
         if (!(ok = wait_all(kPartEmpty + b, uint32_t(slices >> 1) + 1))) break;
-        constexpr int PR = DV / 8;  // pieces of a token
-        if (tid < kSlice * PR) {
-          const int t = tid / PR, piece = tid % PR;
-          const float w = d.to[t0 + t];
-          float x[8];
-          Piece<__nv_bfloat16>::load(shared_load(sv + uint32_t(piece / 8 * kBox) + swizzled(t0 + t, piece % 8)), x);
+        tc_fence_after();
+        if (cols) {  // half of the slice's tokens, eight at a time
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] *= w;
-          const uint32_t dst = base + L::off_parts + uint32_t(b * 3 * L::part + piece / 8 * kSlice * 128) + swizzled(t, piece % 8);
+          for (int j = 0; j < kSlice / 2; j += 8) {
+            const int t1 = t0 + half * (kSlice / 2) + j;
+            const uint32_t at = sv + uint32_t(col / 64 * kBox + t1 * 128 + col % 8 * 2);
+            const float4 w0 = *reinterpret_cast<const float4*>(&d.to[t1]), w1 = *reinterpret_cast<const float4*>(&d.to[t1 + 4]);
+            const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            float x[8], y[8];
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const uint4 h = Piece<__nv_bfloat16>::pack(x);
-            shared_store(dst + uint32_t(k * L::part), h);
-            if (k == 2) break;
-            float y[8];
-            Piece<__nv_bfloat16>::load(h, y);
+            for (int i = 0; i < 8; ++i) {
+              uint16_t h;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at + swizzled(i, col / 8 % 8)) : "memory");
+              x[i] = __uint_as_float(uint32_t(h) << 16);
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] -= y[i];
+            for (int i = 0; i < 8; ++i) x[i] *= w[i];
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              const uint4 h = Piece<__nv_bfloat16>::pack(x);
+              tmem_store4(tmem + lanes + kParts + uint32_t(b * 3 + k) * kPartCols + uint32_t(half * 8 + j / 2), h);
+              Piece<__nv_bfloat16>::load(h, y);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] -= y[i];
+            }
           }
+          tmem_stored();
         }
-        async_proxy_fence();
+        tc_fence_before();
         arrive(kPartFull + b);
       }
       if (!ok) break;
@@ -475,7 +559,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       arrive(kDecayEmpty + (c & 1));
       if (!wait_all(kSumFull, uint32_t(c))) break;
       tc_fence_after();
-      if (rows) {
+      if (cols) {
 #pragma unroll
         for (int i = 0; i < kCols; i += 16) {
           uint32_t r[16];
@@ -494,17 +578,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float* dst = PASS == kReduce                              ? a.ws_s + (p.seg * nbh + bh) * sn
                  : p.last && io.state_out && p.slot >= 0 ? io.state_out + ((long long)p.slot * io.H + p.h) * sn
                                                               : nullptr;
-    if (dst && row < io.dk) {
-      dst += (long long)row * io.dv + c0;
-      if (a.vec_s) {
+    if (dst && col < io.dv) {
 #pragma unroll
-        for (int i = 0; i < kCols; i += 4)
-          if (c0 + i < io.dv) *reinterpret_cast<float4*>(dst + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kCols; ++i)
-          if (c0 + i < io.dv) dst[i] = s[i];
-      }
+      for (int i = 0; i < kCols; ++i)
+        if (c0 + i < io.dk) dst[(c0 + i) * io.dv + col] = s[i];
     }
   }
 
@@ -529,15 +606,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
 }
 
-// [B, T, heads, d] with these strides in boxes of 128 tokens x 64 columns of a head; reads are zero outside.
-bool head_map(CUtensorMap* map, const void* p, int B, int T, int heads, int d, long long bs, long long ts) {
+// [B, T, heads, d] with these strides in boxes of some tokens and 64 or 32 columns of a head; reads are zero outside,
+// and nothing is written there.
+bool head_map(CUtensorMap* map, const void* p, int B, int T, int heads, int d, long long bs, long long ts, int rows = kChunk,
+              int cols = 64) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(T), cuuint64_t(B)};
   const cuuint64_t strides[3] = {cuuint64_t(d) * 2, cuuint64_t(ts) * 2, cuuint64_t(B > 1 ? bs : ts) * 2};
-  const cuuint32_t box[4] = {64, 1, kChunk, 1}, estr[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {cuuint32_t(cols), 1, cuuint32_t(rows), 1}, estr[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -592,7 +672,9 @@ int launch_tiles(LinearArgs a, cudaStream_t s) {
   TileMaps tm = {};
   if (!head_map(&tm.q, io.q, io.B, io.T, io.Hk, io.dk, io.q_bs, io.q_ts) ||
       !head_map(&tm.k, io.k, io.B, io.T, io.Hk, io.dk, io.k_bs, io.k_ts) ||
-      !head_map(&tm.v, io.v, io.B, io.T, io.H, io.dv, io.v_bs, io.v_ts))
+      !head_map(&tm.v, io.v, io.B, io.T, io.H, io.dv, io.v_bs, io.v_ts) ||
+      !head_map(&tm.o, io.o, io.B, io.T, io.H, io.dv, (long long)io.T * io.H * io.dv, (long long)io.H * io.dv, 32,
+                io.dv <= 64 ? 32 : 64))
     return SDM_ECUDA;
   if (io.dk <= 64) return io.dv <= 64 ? launch_sizes<64, 64>(tm, a, s) : launch_sizes<64, 128>(tm, a, s);
   return io.dv <= 64 ? launch_sizes<128, 64>(tm, a, s) : launch_sizes<128, 128>(tm, a, s);
