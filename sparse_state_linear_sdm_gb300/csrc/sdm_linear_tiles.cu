@@ -8,7 +8,7 @@
 // Four products a chunk: q k^T, q S, (A q k^T) v and (A v)^T k, the last one the state transposed.  A CTA takes a
 // sequence's head, its state in registers (fp32, 64 a thread), and walks its chunks.  Warps by role: TMA and
 // decays; MMAs; eight that turn q k^T into the masked bf16 products, scale q S by G and write o; eight that weight
-// v and update the state.  q, k and v come through a ring of five 32 KB slots in the order of their use.
+// v and update the state.  k, q and v of two chunks have a slot of 32 KB each.
 // An MMA of 128 x 128 x 16 whose operands both lie in shared memory waits for them (64 bytes a clock: 128 clocks instead
 // of 64), so the masked products and the weighted v are first operands out of TMEM.
 //
@@ -26,10 +26,12 @@ namespace {
 constexpr int kChunk = 128;
 constexpr int kSlot = 32768;             // 128 tokens of 128 columns: two boxes of 64 columns
 constexpr int kBox = kChunk * 128;       // bytes of a box
-constexpr int kSlots = 5;
+constexpr int kSlots = 6;                // two chunks
 constexpr int kSlice = 32;               // tokens of a weighted slice of v: two K steps
-constexpr int kTileThreads = 32 * 18;
-constexpr int kMaskWarp = 2, kStateWarp = 10;  // first warps of the two groups of eight
+// Warps: copies; the MMAs of o; those of the state; decays; and two groups of eight.
+constexpr int kTileThreads = 32 * 20;
+constexpr int kMaskWarp = 4, kStateWarp = 12;
+constexpr int kStateSlices = 2;          // slices of a chunk that the state's group weighs; the other group has the rest
 
 enum Bar {
   kFull = 0, kEmpty = kSlots,     // slots
@@ -40,17 +42,19 @@ enum Bar {
   kStateFull, kStateEmpty,        // the state as q reads it
   kPartFull, kPartEmpty = kPartFull + 2,  // weighted slices
   kSumFull = kPartEmpty + 2, kSumEmpty,   // k^T (A v)
-  kStaged,                        // o has left the slot of v, of even and of odd chunks: the copies may be late by two
-  kDecayFull = kStaged + 2, kDecayEmpty = kDecayFull + 2,
-  kCut = kDecayEmpty + 2,         // tokens past the end cleared
-  kDrain, kBars
+  kStaged,                        // o has left the slot of q, of even and of odd chunks: the copies may be late by two
+  kDone = kStaged + 2,            // the MMAs of o, of even and of odd chunks
+  kDecayFull = kDone + 2, kDecayEmpty,
+  kCut,                // tokens past the end cleared
+  kDrain, kBars = kDrain + 2
 };
 
 struct Decays {  // of a chunk
   float each[kChunk];  // e^g
   float from[kChunk];  // products from the chunk's start up to each token
   float to[kChunk];    // products after each token up to the chunk's end; 0 past the sequence's
-  float block[kChunk]; // products from the start of each token's block of 32
+  float block[kChunk]; // products from the start of each token's block of 32 up to it
+  float rest[kChunk];  // and those after it up to the block's end
   float all, pad[3];
 };
 
@@ -58,8 +62,8 @@ template <int DK, int DV>
 struct Tiles {
   static constexpr int off_state = kSlots * kSlot;
   static constexpr int off_decays = off_state + DK * DV * 2;
-  static constexpr int off_bars = off_decays + 2 * int(sizeof(Decays));
-  static constexpr int bytes = off_bars + 512 + 1024 /* alignment slack */;
+  static constexpr int off_bars = off_decays + int(sizeof(Decays));
+  static constexpr int bytes = off_bars + 448;
 };
 
 // TMEM columns.  Of each 32 of q k^T the masked products take 16; a slice's three parts are 16 columns each.
@@ -153,6 +157,9 @@ struct Sum {
   __device__ __forceinline__ float exp() const { return finite_exp2(fmaf(hi, kLog2e, lo * kLog2e)); }
 };
 
+// One copy of the loop: the roles' code competes for the instruction cache.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* stop) { return mbar_wait(bar, parity, stop); }
+
 // Every wait is bounded; one that runs out stops the CTA, which waits for the copies and MMAs in flight, frees TMEM and
 // reports SDM_DEV_TIMEOUT.
 template <int DK, int DV, int PASS>
@@ -161,14 +168,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   typedef Tiles<DK, DV> L;
   constexpr int kBoxesK = DK / 64, kBoxesV = DV / 64;
   constexpr int kLoads = PASS == kReduce ? 2 : 3;  // slots a chunk takes
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (base - raw);
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's atoms; there is no room to align it here
+  const uint32_t base = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::off_bars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile uint32_t* issued = tmem_slot + 2;
-  Decays* decays = reinterpret_cast<Decays*>(smem + L::off_decays);
+  Decays& d = *reinterpret_cast<Decays*>(smem + L::off_decays);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const sdm_linear_args& io = a.io;
@@ -180,10 +186,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (i == kMaskFull || i == kStaged || i == kStaged + 1 || i == kOutEmpty || i == kStateFull || i == kPartFull || i == kPartFull + 1 ||
           i == kSumEmpty || i == kCut)
         n = 8;  // the warps of a group
-      if (i == kDecayEmpty || i == kDecayEmpty + 1) n = PASS == kReduce ? 8 : 16;
+      if (i == kDecayEmpty) n = 16;
       mbar_init(bar(i), uint32_t(n));
     }
-    *stop = 0;
+    *stop = (base & 1023u) != 0;
     for (int i = 0; i < kSlots; ++i) issued[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -202,15 +208,95 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const long long bh = (long long)p.b * io.H + p.h, nbh = (long long)io.B * io.H, sn = (long long)io.dk * io.dv;
   if (PASS == kJoin) wait_previous();
 
-  auto wait = [&](int i, uint32_t parity) { return mbar_wait(bar(i), parity & 1u, stop); };
+  auto wait = [&](int i, uint32_t parity) {
+    return mbar_test(bar(i), parity & 1u) || wait_on(bar(i), parity & 1u, stop);
+  };
   auto wait_all = [&](int i, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(i, parity)); };
   auto arrive = [&](int i) {  // once for the warp
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(i));
   };
 
+  // Load i of chunk c: its slot, the turn of it, its address.
+  auto slot = [&](int c, int i) { return (c & 1) * 3 + i; };
+  auto turn = [&](int c) { return uint32_t(c >> 1); };
+  auto place = [&](int slot) { return base + uint32_t(slot) * kSlot; };
+
+  // Either group of eight: slice s of chunk c weighted and cut into its three parts, a column of v a thread.
+  const int quad = warp & 3, half = (warp - kMaskWarp) >> 2 & 1;
+  const int col = quad * 32 + lane;
+  const uint32_t lanes = uint32_t(quad * 32) << 16;
+  auto weigh = [&](int c, int s, uint32_t sv) {
+    const int slice = c * (kChunk / kSlice) + s, b = slice & 1;
+    if (!wait_all(kPartEmpty + b, uint32_t(slice >> 1) + 1)) return false;
+    tc_fence_after();
+    if (quad * 32 < DV) {  // half of the slice's tokens, eight at a time
+#pragma unroll 1
+      for (int j = 0; j < kSlice / 2; j += 8) {
+        const int t1 = s * kSlice + half * (kSlice / 2) + j;
+        const uint32_t at = sv + uint32_t(col / 64 * kBox + t1 * 128 + col % 8 * 2);
+        uint64_t x[4];  // tokens in pairs
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint16_t h[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h[k]) : "r"(at + swizzled(2 * i + k, col / 8 % 8)) : "memory");
+          const float2 w = *reinterpret_cast<const float2*>(&d.to[t1 + 2 * i]);
+          x[i] = mul2(pack2(__uint_as_float(uint32_t(h[0]) << 16), __uint_as_float(uint32_t(h[1]) << 16)), pack2(w.x, w.y));
+        }
+        // The first two parts are the upper halves of what is left, so what they leave is exact.
+        const uint64_t minus = pack2(-1.f, -1.f);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          uint32_t h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            unpack2(x[i], lo, hi);
+            const uint32_t l = __float_as_uint(lo), u = __float_as_uint(hi);
+            if (k == 2) {
+              h[i] = pack_bf16(l, u);
+            } else {
+              h[i] = __byte_perm(l, u, 0x7632);
+              x[i] = fma2(pack2(__uint_as_float(l & 0xFFFF0000u), __uint_as_float(u & 0xFFFF0000u)), minus, x[i]);
+            }
+          }
+          tmem_store4(tmem + lanes + kParts + uint32_t(b * 3 + k) * kPartCols + uint32_t(half * 8 + j / 2),
+                      make_uint4(h[0], h[1], h[2], h[3]));
+        }
+      }
+      tmem_stored();
+    }
+    tc_fence_before();
+    arrive(kPartFull + b);
+    return true;
+  };
+
   if (warp == 0) {
-    // ---- decays, then copies ----
+    // ---- copies: k, q, v of each chunk ----
+    if (lane == 0) {
+      bool ok = true;
+      for (int c = 0; c < chunks && ok; ++c) {
+        const int t = p.t_lo + c * kChunk;
+        for (int i = 0; i < kLoads; ++i) {
+          const int at = slot(c, i);
+          // The slot's last load: q's is free when o has left its place, the others' when their MMAs are done.
+          if (c > 1) ok = PASS != kReduce && i == 1 ? wait(kStaged + (c & 1), turn(c) + 1) : wait(kEmpty + at, turn(c) + 1);
+          if (!ok) break;
+          const uint32_t dst = place(at), full = bar(kFull + at);
+          const bool value = i == kLoads - 1;
+          const CUtensorMap* map = value ? &tm.v : i == 0 ? &tm.k : &tm.q;
+          const int boxes = value ? kBoxesV : kBoxesK, head = value ? p.h : p.hk;
+          mbar_expect_tx(full, uint32_t(boxes * kBox));
+          tma_load_4d(dst, map, 0, head, t, p.b, full);
+          if (boxes > 1) tma_load_4d(dst + kBox, map, 64, head, t, p.b, full);
+          issued[at] = issued[at] + 1u;
+        }
+      }
+    }
+  } else if (warp == 3) {
+    // ---- decays, four tokens a lane ----
     const float* g = io.g ? io.g + p.b * io.g_bs + p.h : nullptr;
     float next[4];
     auto ask = [&](int c) {
@@ -221,103 +307,80 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         next[i] = x < -1e30f ? -1e30f : x > 1e30f ? 1e30f : x;  // sums stay finite
       }
     };
-    Sum total = {0.f, 0.f};
-    // The decays of chunk c, four tokens a lane.
-    auto decay = [&](int c) {
-      if (!wait_all(kDecayEmpty + (c & 1), uint32_t(c >> 1) + 1)) return false;
+    ask(0);
+    const Sum zero = {0.f, 0.f};
+    Sum total = zero;
+    for (int c = 0; c < chunks; ++c) {
       Sum up[4], down[4];  // sums up to and after each token of the lane's
       up[0] = {next[0], 0.f};
-      down[3] = {0.f, 0.f};
+      down[3] = zero;
 #pragma unroll
       for (int i = 1; i < 4; ++i) {
         up[i] = up[i - 1] + Sum{next[i], 0.f};
         down[3 - i] = down[4 - i] + Sum{next[4 - i], 0.f};
       }
-      Decays& d = decays[c & 1];
+      float each[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d.each[lane * 4 + i] = exp2f(kLog2e * next[i]);
+      for (int i = 0; i < 4; ++i) each[i] = exp2_fast(kLog2e * next[i]);
       if (c + 1 < chunks) ask(c + 1);
-      Sum before = up[3], after = up[3], within = up[3];  // scans over the lanes; within: over eight, a block of 32 tokens
+      // Scans over eight lanes, a block of 32 tokens, then over the blocks.
+      Sum before = up[3], after = up[3];
 #pragma unroll
-      for (int m = 1; m < 32; m *= 2) {
+      for (int m = 1; m < 8; m *= 2) {
         const Sum x = before.from_lane(lane - m), y = after.from_lane(lane + m);
-        if (lane >= m) before = before + x;
-        if (lane + m < 32) after = after + y;
-        if (m < 8) {
-          const Sum z = within.from_lane(lane - m);
-          if (lane % 8 >= m) within = within + z;
-        }
+        if (lane % 8 >= m) before = before + x;
+        if (lane % 8 + m < 8) after = after + y;
       }
-      const Sum all = before.from_lane(31), zero = {0.f, 0.f};
-      Sum left = before.from_lane(lane - 1), right = after.from_lane(lane + 1), block = within.from_lane(lane - 1);
-      if (lane == 0) left = zero;
-      if (lane == 31) right = zero;
-      if (lane % 8 == 0) block = zero;
+      const Sum in_block = before.from_lane(lane | 7);
+      Sum earlier = zero, later = zero, all = zero;  // whole blocks
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const Sum x = in_block.from_lane(b * 8);
+        if (b < lane / 8) earlier = earlier + x;
+        if (b > lane / 8) later = later + x;
+        all = all + x;
+      }
+      Sum left = before.from_lane(lane - 1), right = after.from_lane(lane + 1);
+      if (lane % 8 == 0) left = zero;
+      if (lane % 8 == 7) right = zero;
+      float block[4], rest[4], from[4], to[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int t = lane * 4 + i;
-        d.block[t] = (block + up[i]).exp();
-        d.from[t] = (left + up[i]).exp();
-        d.to[t] = c * kChunk + t < tokens ? (right + down[i]).exp() : 0.f;
+        const Sum x = left + up[i], y = right + down[i];
+        block[i] = x.exp();
+        rest[i] = y.exp();
+        from[i] = (earlier + x).exp();
+        to[i] = c * kChunk + lane * 4 + i < tokens ? (later + y).exp() : 0.f;
       }
-      if (lane == 0) d.all = all.exp();
+      const float last = all.exp();
+      // All of it is computed here and not behind the wait, after which the other warps wait for it.
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        asm volatile("" ::"f"(each[i]), "f"(block[i]), "f"(rest[i]), "f"(from[i]), "f"(to[i]), "f"(last));
+      if (!wait_all(kDecayEmpty, uint32_t(c) + 1)) break;
+      auto put = [&](float* at, const float (&v)[4]) { reinterpret_cast<float4*>(at)[lane] = make_float4(v[0], v[1], v[2], v[3]); };
+      put(d.each, each), put(d.block, block), put(d.rest, rest), put(d.from, from), put(d.to, to);
+      if (lane == 0) d.all = last;
       total = total + all;
-      arrive(kDecayFull + (c & 1));
-      return true;
-    };
-    ask(0);
-    int load = 0;
-    uint32_t taken = 0;  // by slot, the parity of the next wait for its commits
-    bool ok = chunks == 0 || decay(0);
-    for (int c = 0; c < chunks && ok; ++c) {
-      if (lane == 0) {
-        for (int i = 3 - kLoads; i < 3 && ok; ++i, ++load) {
-          const int slot = load % kSlots;
-          // The slot's last load: v's is free when o has left its place, the others' when their MMAs are done.
-          const int old = load - kSlots;
-          if (old >= 0 && PASS != kReduce && old % kLoads == kLoads - 1) {
-            const int chunk = old / kLoads;
-            ok = wait(kStaged + (chunk & 1), uint32_t(chunk >> 1));
-          } else if (old >= 0) {
-            ok = wait(kEmpty + slot, taken >> slot);
-            taken ^= 1u << slot;
-          }
-          if (!ok) break;
-          const uint32_t dst = base + uint32_t(slot) * kSlot;
-          const int boxes = i == 2 ? kBoxesV : kBoxesK, t = p.t_lo + c * kChunk;
-          mbar_expect_tx(bar(kFull + slot), uint32_t(boxes * kBox));
-          for (int x = 0; x < boxes; ++x)
-            tma_load_4d(dst + uint32_t(x * kBox), i == 0 ? &tm.q : i == 1 ? &tm.k : &tm.v, x * 64, i == 2 ? p.h : p.hk, t,
-                        p.b, bar(kFull + slot));
-          issued[slot] = issued[slot] + 1u;
-        }
-      }
-      ok = __all_sync(0xFFFFFFFFu, ok) && (c + 1 == chunks || decay(c + 1));
+      arrive(kDecayFull);
     }
     if (PASS == kReduce && lane == 0) a.ws_g[p.seg * nbh + bh] = total.hi + total.lo;
   } else if (warp == 1) {
-    // ---- MMAs ----
-    int slices = 0;  // so far
-    bool ok = true;
-    auto slot_of = [&](int load) { return base + uint32_t(load % kSlots) * kSlot; };
-    auto step = [](int kk) { return uint64_t(kk / 4 * kBox + kk % 4 * 32) >> 4; };  // K steps along a row of boxes
-    for (int c = 0; c < chunks && ok; ++c) {
-      const int n = min(kChunk, tokens - c * kChunk), first = c * kLoads;
-      const int iq = first, ik = first + kLoads - 2, iv = first + kLoads - 1;  // loads
-      const uint64_t k_rows = mn_box_desc(slot_of(ik), kBox), v_rows = mn_box_desc(slot_of(iv), kBox);
-      if (n < kChunk && !(ok = wait_all(kCut, 0))) break;
-      if (!(ok = wait_all(kFull + ik % kSlots, uint32_t(ik / kSlots)))) break;
-      if (PASS != kReduce) {
-        const uint64_t q = sw128_desc(slot_of(iq)), k = sw128_desc(slot_of(ik));
-        if (!(ok = wait_all(kFull + iq % kSlots, uint32_t(iq / kSlots)))) break;
-        if (c > 0 && !(ok = wait_all(kOutFull, uint32_t(c) - 1))) break;  // the masked products before have been read
+    // ---- MMAs of o ----
+    if (PASS != kReduce) {
+      auto step = [](int kk) { return uint64_t(kk / 4 * kBox + kk % 4 * 32) >> 4; };  // K steps along a row of boxes
+      for (int c = 0; c < chunks; ++c) {
+        const int ik = slot(c, 0), iq = slot(c, 1), iv = slot(c, 2);
+        const uint64_t q = sw128_desc(place(iq)), k = sw128_desc(place(ik)), v_rows = mn_box_desc(place(iv), kBox);
+        if (tokens - c * kChunk < kChunk && !wait_all(kCut, 0)) break;
+        if (!wait_all(kFull + ik, turn(c)) || !wait_all(kFull + iq, turn(c))) break;
+        if (c > 0 && !wait_all(kOutFull, uint32_t(c) - 1)) break;  // the masked products before have been read
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < DK / 16; ++kk)
           mma1(tmem + kScore, q + step(kk), k + step(kk), kk > 0, tile_idesc(128, false, false));
         commit1(bar(kScoreFull));
-        if (!(ok = wait_all(kStateFull, uint32_t(c)))) break;
-        if (!(ok = wait_all(kOutEmpty, uint32_t(c) + 1))) break;
+        if (!wait_all(kStateFull, uint32_t(c)) || !wait_all(kOutEmpty, uint32_t(c) + 1)) break;
         tc_fence_after();
         const uint64_t state = sw128_desc(base + L::off_state);
 #pragma unroll
@@ -326,11 +389,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                tile_idesc(DV, false, false));
         commit1(bar(kReadFull));
         commit1(bar(kStateEmpty));
-        commit1(bar(kEmpty + iq % kSlots));
+        if (!wait_all(kMaskFull, uint32_t(c)) || !wait_all(kFull + iv, turn(c))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kChunk / 16; ++kk)
+          mma1_tmem(tmem + kOut, tmem + kScore + uint32_t(kk / 2 * 32 + kk % 2 * 8), v_rows + uint64_t(kk * 2048 >> 4), 1,
+                    tile_idesc(DV, false, true));
+        commit1(bar(kOutFull));
+        commit1(bar(kDone + (c & 1)));
       }
-      if (!(ok = wait_all(kSumEmpty, uint32_t(c) + 1))) break;
-      const int ns = (n + kSlice - 1) / kSlice;
-      for (int s = 0; s < ns; ++s, ++slices) {
+    }
+  } else if (warp == 2) {
+    // ---- MMAs of the state ----
+    int slices = 0;  // so far
+    bool ok = true;
+    for (int c = 0; c < chunks && ok; ++c) {
+      const int n = min(kChunk, tokens - c * kChunk), ik = slot(c, 0), iv = slot(c, kLoads - 1);
+      const uint64_t k_rows = mn_box_desc(place(ik), kBox);
+      if (n < kChunk && !wait_all(kCut, 0)) break;
+      if (!wait_all(kFull + ik, turn(c)) || !wait_all(kSumEmpty, uint32_t(c) + 1)) break;
+      for (int t0 = 0; t0 < n; t0 += kSlice, ++slices) {
         const int b = slices & 1;
         if (!(ok = wait_all(kPartFull + b, uint32_t(slices >> 1)))) break;
         tc_fence_after();
@@ -339,89 +417,95 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int i = 0; i < 3; ++i)
             mma1_tmem(tmem + kSum, tmem + kParts + uint32_t(b * 3 + i) * kPartCols + uint32_t(kk * 8),
-                      k_rows + uint64_t((s * (kSlice / 16) + kk) * 2048 >> 4), s > 0 || kk > 0 || i > 0,
-                      tile_idesc(DK, false, true));
+                      k_rows + uint64_t((t0 + kk * 16) * 128 >> 4), t0 > 0 || kk > 0 || i > 0, tile_idesc(DK, false, true));
         commit1(bar(kPartEmpty + b));
       }
       if (!ok) break;
       commit1(bar(kSumFull));
-      commit1(bar(kEmpty + ik % kSlots));
-      if (PASS != kReduce) {
-        if (!(ok = wait_all(kMaskFull, uint32_t(c)))) break;
-        if (!(ok = wait_all(kFull + iv % kSlots, uint32_t(iv / kSlots)))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kChunk / 16; ++kk)
-          mma1_tmem(tmem + kOut, tmem + kScore + uint32_t(kk / 2 * 32 + kk % 2 * 8), v_rows + uint64_t(kk * 2048 >> 4), 1,
-                    tile_idesc(DV, false, true));
-        commit1(bar(kOutFull));
-      }
-      if (PASS == kReduce) commit1(bar(kEmpty + iv % kSlots));
+      // Both groups of MMAs read k, and v is read for both.
+      if (PASS != kReduce && !wait_all(kDone + (c & 1), uint32_t(c >> 1))) break;
+      commit1(bar(kEmpty + ik));
+      commit1(bar(kEmpty + iv));
     }
-    commit1(bar(kDrain));
-    mbar_wait_teardown(bar(kDrain), 0);
   } else if (warp < kStateWarp) {
-    // ---- masked products, then o ----
-    if (PASS != kReduce) {
-      const int quad = warp & 3, half = (warp - kMaskWarp) >> 2;
-      const int row = quad * 32 + lane;
-      const uint32_t lanes = uint32_t(quad * 32) << 16, out_at = tmem + lanes + kOut + uint32_t(half * (DV / 2));
+    // ---- masked products, some of weighted v, then o ----
+    auto weigh_rest = [&](int c, int n) {
+      const int iv = slot(c, kLoads - 1);
+      if (n <= kStateSlices * kSlice) return true;
+      bool ok = wait_all(kFull + iv, turn(c)) && (n == kChunk || wait_all(kCut, 0));
+#pragma unroll 1
+      for (int i = kStateSlices; i * kSlice < n && ok; ++i) ok = weigh(c, i, place(iv));
+      return ok;
+    };
+    if (PASS == kReduce) {
+      for (int c = 0; c < chunks; ++c) {
+        if (!wait_all(kDecayFull, uint32_t(c)) || !weigh_rest(c, min(kChunk, tokens - c * kChunk))) break;
+        arrive(kDecayEmpty);
+      }
+    } else {
+      const int row = col;
+      const uint32_t out_at = tmem + lanes + kOut + uint32_t(half * (DV / 2));
       // Blocks of 32 columns up to the diagonal's: the first half of the warps takes the later ones.
       const int cut = (quad + 1) / 2, b_hi = half ? cut - 1 : quad, b_lo = half ? 0 : cut;
-      // This warp's part of o lies where v was: 32 rows of DV / 2 columns, 128 or 64 bytes, in their swizzle.
+      // This warp's part of o lies where q was: 32 rows of DV / 2 columns, 128 or 64 bytes, in their swizzle.
       constexpr int kRowBytes = DV;
       auto staged = [&](int piece) {
         return DV == 128 ? swizzled(lane, piece) : uint32_t(lane * 64 + ((piece ^ (lane >> 1 & 3)) << 4));
       };
       for (int c = 0; c < chunks; ++c) {
         const int n = min(kChunk, tokens - c * kChunk);
-        if (!wait_all(kDecayFull + (c & 1), uint32_t(c >> 1))) break;
-        const Decays& d = decays[c & 1];
+        if (!wait_all(kDecayFull, uint32_t(c))) break;
         if (!wait_all(kScoreFull, uint32_t(c))) break;
         tc_fence_after();
-        float f = io.scale;  // A_ij scale of the column that is next
-        if (half) {          // past the blocks of the other half
-          f *= d.block[row];
-          for (int b = quad - 1; b > b_hi; --b) f *= d.block[b * 32 + 31];
-        }
+        float f = io.scale * d.block[row];  // scale A of this row and the last column of the block that is next
+        for (int b = quad - 1; b > b_hi; --b) f *= d.block[b * 32 + 31];
+#pragma unroll 1
         for (int b = b_hi; b >= b_lo; --b) {
-          uint32_t r[32];
+          uint32_t r[32], pairs[16];
           tmem_load32(tmem + lanes + kScore + uint32_t(b * 32), r);
-          uint32_t pairs[16];
-          const float* each = d.each + b * 32;
-          if (b == quad) {  // the diagonal's
+          if (b == quad) {  // the diagonal's: from there on a product after the other
+            const float* each = d.each + b * 32;
+            float e = io.scale;
 #pragma unroll
             for (int j = 30; j >= 0; j -= 2) {  // columns j, j + 1 of the block
-              const float2 e = *reinterpret_cast<const float2*>(each + j);
-              const float hi = j + 1 > lane ? 0.f : f * __uint_as_float(r[j + 1]);
-              f = j + 1 > lane ? f : f * e.y;
-              const float lo = j > lane ? 0.f : f * __uint_as_float(r[j]);
-              f = j > lane ? f : f * e.x;
+              const float2 w = *reinterpret_cast<const float2*>(each + j);
+              const float hi = j + 1 > lane ? 0.f : e * __uint_as_float(r[j + 1]);
+              e = j + 1 > lane ? e : e * w.y;
+              const float lo = j > lane ? 0.f : e * __uint_as_float(r[j]);
+              e = j > lane ? e : e * w.x;
               pairs[j / 2] = pack_bf16(__float_as_uint(lo), __float_as_uint(hi));
             }
           } else {
+            const uint64_t both = pack2(f, f);
 #pragma unroll
-            for (int j = 28; j >= 0; j -= 4) {
-              const float4 e = *reinterpret_cast<const float4*>(each + j);
-              const float f2 = f * e.w, f1 = f2 * e.z, f0 = f1 * e.y;
-              pairs[j / 2 + 1] = pack_bf16(__float_as_uint(f2 * __uint_as_float(r[j + 2])),
-                                           __float_as_uint(f * __uint_as_float(r[j + 3])));
-              pairs[j / 2] = pack_bf16(__float_as_uint(f0 * __uint_as_float(r[j])),
-                                       __float_as_uint(f1 * __uint_as_float(r[j + 1])));
-              f = f0 * e.x;
+            for (int j = 0; j < 32; j += 4) {
+              const float4 w = *reinterpret_cast<const float4*>(d.rest + b * 32 + j);
+              float x0, x1;
+              unpack2(mul2(mul2(pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), pack2(w.x, w.y)), both), x0, x1);
+              pairs[j / 2] = pack_bf16(__float_as_uint(x0), __float_as_uint(x1));
+              unpack2(mul2(mul2(pack2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), pack2(w.z, w.w)), both), x0, x1);
+              pairs[j / 2 + 1] = pack_bf16(__float_as_uint(x0), __float_as_uint(x1));
             }
+            f *= d.block[b * 32 + 31];
           }
           tmem_store16(tmem + lanes + kScore + uint32_t(b * 32), pairs);
         }
+        if (!weigh_rest(c, n)) break;
         if (!half) {  // nothing above the diagonal
           const uint32_t zeros[16] = {};
           for (int b = quad + 1; b < 4; ++b) tmem_store16(tmem + lanes + kScore + uint32_t(b * 32), zeros);
         }
+        // o of the chunk before has long left for memory
+        if (c > 0 && lane == 0) {
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          mbar_arrive(bar(kStaged + ((c - 1) & 1)));
+        }
+        __syncwarp();
         // q S, on which the chunk's own products are added, takes the decays from the chunk's start.
         const float from = d.from[row] * io.scale;
         if (!wait_all(kReadFull, uint32_t(c))) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < DV / 2; x += 16) {
           uint32_t r[16];
           tmem_load16(out_at + uint32_t(x), r);
@@ -431,22 +515,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         tmem_stored();
         tc_fence_before();
-        arrive(kMaskFull);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kMaskFull));
+          mbar_arrive(bar(kDecayEmpty));
+        }
         if (!wait_all(kOutFull, uint32_t(c))) break;
         tc_fence_after();
-        const bool live = row < n;
-        const int iv = c * kLoads + kLoads - 1;
-        const uint32_t patch = base + uint32_t(iv % kSlots) * kSlot + uint32_t((half * 4 + quad) * 32 * kRowBytes);
-#pragma unroll
+        const uint32_t patch = place(slot(c, 1)) + uint32_t((half * 4 + quad) * 32 * kRowBytes);
+#pragma unroll 1
         for (int x = 0; x < DV / 2; x += 16) {
           uint32_t r[16];
           tmem_load16(out_at + uint32_t(x), r);
+          if (n < kChunk && row >= n) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = 0;
+          }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = live ? __uint_as_float(r[8 * k + i]) : 0.f;
-            shared_store(patch + staged(x / 8 + k), Piece<__nv_bfloat16>::pack(v));
+            const uint32_t* v = r + 8 * k;
+            shared_store(patch + staged(x / 8 + k), make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                               pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])));
           }
         }
         tc_fence_before();
@@ -454,11 +543,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(kOutEmpty));
-          mbar_arrive(bar(kDecayEmpty + (c & 1)));
           tma_store_4d(&tm.o, half * (DV / 2), p.h, p.t_lo + c * kChunk + quad * 32, p.b, patch);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          mbar_arrive(bar(kStaged + (c & 1)));
         }
         __syncwarp();
       }
@@ -468,11 +554,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ---- weighted v, then the state ----
     // The state lies transposed: a thread has a column of v and half of the rows, s[i] that of row c0 + i.
     constexpr int kCols = DK / 2;
-    const int quad = warp & 3, half = (warp - kStateWarp) >> 2, tid = threadIdx.x - kStateWarp * 32;
-    const int col = quad * 32 + lane, c0 = half * kCols;
-    const uint32_t lanes = uint32_t(quad * 32) << 16;
+    const int tid = threadIdx.x - kStateWarp * 32, c0 = half * kCols;
     const bool cols = quad * 32 < DV;  // this warp has columns of v
-    float s[kCols];
+    float s[kCols];  // the state
 #pragma unroll
     for (int i = 0; i < kCols; ++i) s[i] = 0.f;
     const float* src = PASS == kJoin ? a.ws_s + (p.seg * nbh + bh) * sn
@@ -499,13 +583,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       arrive(kStateFull);
     };
     if (PASS != kReduce && chunks > 0) show_state();
-    int slices = 0;
     for (int c = 0; c < chunks; ++c) {
-      const int n = min(kChunk, tokens - c * kChunk), first = c * kLoads, ik = first + kLoads - 2, iv = first + kLoads - 1;
-      const uint32_t sk = base + uint32_t(ik % kSlots) * kSlot, sv = base + uint32_t(iv % kSlots) * kSlot;
-      if (!wait_all(kFull + iv % kSlots, uint32_t(iv / kSlots))) break;
+      const int n = min(kChunk, tokens - c * kChunk), ik = slot(c, 0), iv = slot(c, kLoads - 1);
+      const uint32_t sk = place(ik), sv = place(iv);
+      if (!wait_all(kFull + iv, turn(c))) break;
       if (n < kChunk) {  // what lies behind the last token may be anything, and 0 times it is not 0
-        if (!wait_all(kFull + ik % kSlots, uint32_t(ik / kSlots))) break;
+        if (!wait_all(kFull + ik, turn(c))) break;
         for (int i = tid; i < (kChunk - n) * 8; i += 256) {
           const uint32_t at = uint32_t((n + i / 8) * 128 + i % 8 * 16);
 #pragma unroll
@@ -517,46 +600,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         arrive(kCut);
         if (!wait_all(kCut, 0)) break;  // the others of this group, whose rows are read below
       }
-      if (!wait_all(kDecayFull + (c & 1), uint32_t(c >> 1))) break;
-      const Decays& d = decays[c & 1];
+      if (!wait_all(kDecayFull, uint32_t(c))) break;
       bool ok = true;
-      for (int t0 = 0; t0 < n; t0 += kSlice, ++slices) {
-        const int b = slices & 1;
-        if (!(ok = wait_all(kPartEmpty + b, uint32_t(slices >> 1) + 1))) break;
-        tc_fence_after();
-        if (cols) {  // half of the slice's tokens, eight at a time
-#pragma unroll
-          for (int j = 0; j < kSlice / 2; j += 8) {
-            const int t1 = t0 + half * (kSlice / 2) + j;
-            const uint32_t at = sv + uint32_t(col / 64 * kBox + t1 * 128 + col % 8 * 2);
-            const float4 w0 = *reinterpret_cast<const float4*>(&d.to[t1]), w1 = *reinterpret_cast<const float4*>(&d.to[t1 + 4]);
-            const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-            float x[8], y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint16_t h;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at + swizzled(i, col / 8 % 8)) : "memory");
-              x[i] = __uint_as_float(uint32_t(h) << 16);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= w[i];
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              const uint4 h = Piece<__nv_bfloat16>::pack(x);
-              tmem_store4(tmem + lanes + kParts + uint32_t(b * 3 + k) * kPartCols + uint32_t(half * 8 + j / 2), h);
-              Piece<__nv_bfloat16>::load(h, y);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] -= y[i];
-            }
-          }
-          tmem_stored();
-        }
-        tc_fence_before();
-        arrive(kPartFull + b);
-      }
+#pragma unroll 1
+      for (int i = 0; i < kStateSlices && i * kSlice < n && ok; ++i) ok = weigh(c, i, sv);
       if (!ok) break;
       const float all = d.all;
-      arrive(kDecayEmpty + (c & 1));
+      arrive(kDecayEmpty);
       if (!wait_all(kSumFull, uint32_t(c))) break;
       tc_fence_after();
       if (cols) {
@@ -594,6 +644,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           make_uint4(0, 0, 0, 0);
   }
 
+  if (warp == 1 || warp == 2) {
+    __syncwarp();
+    commit1(bar(kDrain + warp - 1));
+    mbar_wait_teardown(bar(kDrain + warp - 1), 0);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
