@@ -5,8 +5,9 @@
 //   y = r / rms(r) * weight                rms(v) = sqrt(mean(v^2) + eps)
 //
 // any part of which may be absent.  HBM bounds it: a row is read once into registers, and both sums over it are taken there in
-// fp32 (a norm by itself, a gate and a residual addition would each read and write it again).  A row has 8 to 512 threads, at
-// most 32 channels each; a block of 128 threads has several short rows.  The weights come from L1.
+// fp32 (a norm by itself, a gate and a residual addition would each read and write it again).  A row has 8 to 1024 threads
+// of eight channels; a block of 128 threads has several short rows.  Blocks stay and take rows in turn, the next one on its way
+// while one is worked on.
 #include "sdm_norm.cuh"
 
 namespace sdm {
@@ -15,71 +16,113 @@ namespace {
 struct Forward {
   sdm_norm_args io;
   void *y, *r;
+  int slots;  // teams of a group
 };
 
+constexpr int kThreads = 1024;  // of an SM
+
 template <typename TX, typename TR, int TPR, int P, bool VEC>
-__global__ void __launch_bounds__(norm_block(TPR)) norm_kernel(const __grid_constant__ Forward a) {
+__global__ void __launch_bounds__(norm_block(TPR), kThreads / norm_block(TPR)) norm_kernel(const __grid_constant__ Forward a) {
   typedef Row<TPR, P, VEC> R;
   constexpr int E = R::E, RPB = norm_block(TPR) / TPR, W = norm_block(TPR) / 32;
-  __shared__ float part[2][W][1];
+  __shared__ float part[2][2][W][1];
+  __shared__ Kept<R, norm_block(TPR), 3> kept;
   const sdm_norm_args& io = a.io;
   const int t = threadIdx.x % TPR, n = io.D / io.groups;
-  const unsigned row = blockIdx.x * RPB + threadIdx.x / TPR, rows = unsigned(io.M) * unsigned(io.groups);
-  const bool live = row < rows;
-  const long long m = live ? row / unsigned(io.groups) : 0;
-  const long long off = live ? (long long)(row % unsigned(io.groups)) * n : 0;
-  const int cols = live ? n : 0;
+  const float rn = 1.0f / float(n);
+  const unsigned team = blockIdx.x * RPB + threadIdx.x / TPR;
+  const unsigned slot = team / unsigned(io.groups), group = team % unsigned(io.groups);
+  const bool used = slot < unsigned(a.slots);
+  const long long off = (long long)group * n, at = used ? off : 0;
+  const int mine = used ? n : 0;
 
-  float v[E], s[E], z[E], w[E];
-  R::load(static_cast<const TX*>(io.x) + m * io.x_rs + off, t, cols, v);
-  if (io.residual) R::load(static_cast<const TR*>(io.residual) + m * io.residual_rs + off, t, cols, s);
-  if (io.gate) R::load(static_cast<const TX*>(io.gate) + m * io.gate_rs + off, t, cols, z);
-  if (io.after) {
-    R::weights(io.after, io.w_dtype, off, t, cols, w);
-    float q[1] = {0.f};
+  // A row as it lies in memory; the next one is asked for while this one is worked on.
+  typename R::template Raw<TX> rx, rz;
+  typename R::template Raw<TR> rs;
+  const TX* px = static_cast<const TX*>(io.x) + slot * io.x_rs + off;
+  const TX* pz = static_cast<const TX*>(io.gate) + (io.gate ? slot * io.gate_rs + off : 0);
+  const TR* ps = static_cast<const TR*>(io.residual) + (io.residual ? slot * io.residual_rs + off : 0);
+  const long long out = slot * (long long)io.D + off, step = a.slots * (long long)io.D;
+  TX* y = static_cast<TX*>(a.y) + (a.y ? out : 0);
+  TR* r = static_cast<TR*>(a.r) + (a.r ? out : 0);
+  auto ask = [&](long long m0) {
+    const int cols = used && m0 + slot < io.M ? n : 0;
+    rx.ask(px, t, cols), px += a.slots * io.x_rs;
+    if (io.gate) rz.ask(pz, t, cols), pz += a.slots * io.gate_rs;
+    if (io.residual) rs.ask(ps, t, cols), ps += a.slots * io.residual_rs;
+  };
+  ask(0);
+  if (io.after) kept.put(0, io.after, io.w_dtype, at, t, mine);
+  if (io.scale) kept.put(1, io.scale, io.w_dtype, at, t, mine);
+  if (a.y) kept.put(2, io.weight, io.w_dtype, at, t, mine);
+
+  int turn = 0;
+  for (long long m0 = 0; m0 < io.M; m0 += a.slots, turn ^= 1) {
+    const int cols = used && m0 + slot < io.M ? n : 0;
+    float v[E], s[E], z[E], w[E];
+    rx.get(v);
+    if (io.gate) rz.get(z);
+    if (io.residual) rs.get(s);
+    if (m0 + a.slots < io.M) ask(m0 + a.slots);
+    if (io.after) {
+      float q[1] = {0.f};
 #pragma unroll
-    for (int e = 0; e < E; ++e) q[0] = fmaf(v[e], v[e], q[0]);
-    row_sums<TPR>(q, part[0]);
-    const float inv = rsqrtf(q[0] / float(n) + io.eps);
+      for (int e = 0; e < E; ++e) q[0] = fmaf(v[e], v[e], q[0]);
+      row_sums<TPR>(q, part[turn][0]);
+      const float inv = rsqrtf(fmaf(q[0], rn, io.eps));
+      kept.get(0, io.after, io.w_dtype, at, t, mine, w);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] *= inv * w[e];
-  }
-  if (io.gate) {
+      for (int e = 0; e < E; ++e) v[e] *= inv * w[e];
+    }
+    if (io.gate) {
+      if (io.act == SDM_ACT_SILU) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] *= io.act == SDM_ACT_SILU ? silu(z[e]) : z[e];
-  }
-  if (io.scale) {
-    R::weights(io.scale, io.w_dtype, off, t, cols, w);
+        for (int e = 0; e < E; ++e) v[e] *= silu(z[e]);
+      } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] *= w[e];
-  }
-  if (io.residual) {
+        for (int e = 0; e < E; ++e) v[e] *= z[e];
+      }
+    }
+    if (io.scale) {
+      kept.get(1, io.scale, io.w_dtype, at, t, mine, w);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] += s[e];
-  }
-  if (a.r) R::store(static_cast<TR*>(a.r) + m * io.D + off, t, cols, v);
-  if (a.y) {
-    R::weights(io.weight, io.w_dtype, 0, t, cols, w);
-    float q[1] = {0.f};
+      for (int e = 0; e < E; ++e) v[e] *= w[e];
+    }
+    if (io.residual) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) q[0] = fmaf(v[e], v[e], q[0]);
-    row_sums<TPR>(q, part[1]);
-    const float inv = rsqrtf(q[0] / float(n) + io.eps);
+      for (int e = 0; e < E; ++e) v[e] += s[e];
+    }
+    if (a.r) R::store(r, t, cols, v), r += step;
+    if (a.y) {
+      float q[1] = {0.f};
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] *= inv * w[e];
-    R::store(static_cast<TX*>(a.y) + m * io.D, t, cols, v);
+      for (int e = 0; e < E; ++e) q[0] = fmaf(v[e], v[e], q[0]);
+      row_sums<TPR>(q, part[turn][1]);
+      const float inv = rsqrtf(fmaf(q[0], rn, io.eps));
+      kept.get(2, io.weight, io.w_dtype, at, t, mine, w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] *= inv * w[e];
+      R::store(y, t, cols, v), y += step;
+    }
   }
 }
 
-template <typename TX, typename TR, int TPR, int P, bool VEC>
-struct Launch {
-  static int run(const Forward& a, cudaStream_t s) {
-    constexpr int block = norm_block(TPR), RPB = block / TPR;
-    const long long rows = a.io.M * a.io.groups;
-    norm_kernel<TX, TR, TPR, P, VEC><<<unsigned((rows + RPB - 1) / RPB), block, 0, s>>>(a);
+template <typename TX, typename TR, bool VEC>
+int launch(Forward a, cudaStream_t s) {
+  return norm_by_width<1024>(a.io.D / a.io.groups, [&](auto tpr, auto pieces) {
+    constexpr int block = norm_block(tpr), RPB = block / int(tpr);
+    // Teams of a group: as many as the card holds at once, and no more than there are rows.
+    const long long most = 152LL * (kThreads / block) * RPB / a.io.groups, slots = most < 1 ? 1 : most;
+    a.slots = int(slots < a.io.M ? slots : a.io.M);
+    const long long teams = (long long)a.slots * a.io.groups;
+    norm_kernel<TX, TR, tpr, pieces, VEC><<<unsigned((teams + RPB - 1) / RPB), block, 0, s>>>(a);
     return last_launch_status();
-  }
-};
+  });
+}
+template <typename TX, typename TR>
+int launch(const Forward& a, bool vec, cudaStream_t s) {
+  return vec ? launch<TX, TR, true>(a, s) : launch<TX, TR, false>(a, s);
+}
 
 }  // namespace
 }  // namespace sdm
@@ -114,5 +157,8 @@ extern "C" int sdm_residual_norm(const sdm_norm_args* args, void* y, void* r, vo
   const bool vec = (io.D / io.groups) % 8 == 0 && rows16(io.x, io.x_rs) && rows16(io.gate, io.gate_rs) &&
                    rows16(io.residual, io.residual_rs) && !misaligned(y, 15) && !misaligned(r, 15) &&
                    !misaligned(io.after, 15) && !misaligned(io.scale, 15) && !misaligned(io.weight, 15);
-  return norm_dispatch<Launch>(io.x_dtype, io.r_dtype, vec, io.D / io.groups, Forward{io, y, r}, as_stream(stream));
+  const Forward a{io, y, r, 0};
+  cudaStream_t s = as_stream(stream);
+  if (io.x_dtype == SDM_F32) return launch<float, float>(a, vec, s);
+  return io.r_dtype == SDM_F32 ? launch<__nv_bfloat16, float>(a, vec, s) : launch<__nv_bfloat16, __nv_bfloat16>(a, vec, s);
 }

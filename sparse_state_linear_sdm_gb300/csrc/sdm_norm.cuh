@@ -1,6 +1,8 @@
 // What the norms and their gradient share (sdm_norm.cu, sdm_norm_backward.cu): rows in registers, sums over a row.
 #pragma once
 
+#include <type_traits>
+
 #include "sdm_layers.cuh"
 
 namespace sdm {
@@ -60,6 +62,41 @@ struct Row {
         if (at(t, e) < n) from_f32(v[e], p + at(t, e));
     }
   }
+  // The same in two steps: asked for, and later taken as numbers.
+  template <typename T>
+  struct Raw {
+    static constexpr int N = VEC ? P * int(sizeof(T)) / 2 : 1;
+    uint4 w[N];
+    T v[VEC ? 1 : E];
+    __device__ void ask(const T* p, int t, int n) {
+      if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const int c = (i * TPR + t) * 8;
+#pragma unroll
+          for (int k = 0; k < int(sizeof(T)) / 2; ++k)
+            w[i * (int(sizeof(T)) / 2) + k] = c < n ? *(reinterpret_cast<const uint4*>(p + c) + k) : make_uint4(0, 0, 0, 0);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = at(t, e) < n ? p[at(t, e)] : T(0.f);
+      }
+    }
+    __device__ void get(float (&f)[E]) const {
+      if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          float x[Piece<T>::n];
+          Piece<T>::load(w[i], x);
+#pragma unroll
+          for (int j = 0; j < Piece<T>::n; ++j) f[i * Piece<T>::n + j] = x[j];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = to_f32(v[e]);
+      }
+    }
+  };
   // A weight vector of either type from channel `off` on.
   __device__ static void weights(const void* p, int dtype, long long off, int t, int n, float (&v)[E]) {
     if (dtype == SDM_F32)
@@ -95,27 +132,50 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float (*part)[K]) {
 
 constexpr int norm_block(int tpr) { return tpr < 128 ? 128 : tpr; }
 
-// The instances: threads of a row and pieces of a thread by the row's channels.
-template <template <typename, typename, int, int, bool> class Launch, typename TX, typename TR, bool VEC, typename... A>
-int norm_by_width(int n, A&&... a) {
-  if (n <= 64) return Launch<TX, TR, 8, 1, VEC>::run(a...);
-  if (n <= 128) return Launch<TX, TR, 16, 1, VEC>::run(a...);
-  if (n <= 256) return Launch<TX, TR, 32, 1, VEC>::run(a...);
-  if (n <= 1024) return Launch<TX, TR, 64, 2, VEC>::run(a...);
-  if (n <= 2048) return Launch<TX, TR, 128, 2, VEC>::run(a...);
-  if (n <= 4096) return Launch<TX, TR, 256, 2, VEC>::run(a...);
-  if (n <= 8192) return Launch<TX, TR, 512, 2, VEC>::run(a...);
-  return Launch<TX, TR, 512, 4, VEC>::run(a...);
+// Threads of a row and pieces of a thread by the row's channels, calling f(threads, pieces): eight channels a thread up to
+// 4096, then as many more as a block of at most `most` threads leaves.
+template <int MOST, bool TWO = false, typename F>
+auto norm_by_width(int n, F f) {
+  typedef std::integral_constant<int, 1> One;
+  if (n <= 64) return f(std::integral_constant<int, 8>(), One());
+  if (n <= 128) return f(std::integral_constant<int, 16>(), One());
+  if (n <= 256) return f(std::integral_constant<int, 32>(), One());
+  if (n <= 512) return f(std::integral_constant<int, 64>(), One());
+  if (n <= 1024) return f(std::integral_constant<int, 128>(), One());
+  if (n <= 2048) return f(std::integral_constant<int, 256>(), One());
+  if (TWO && n <= 4096) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
+  if (n <= 4096) return f(std::integral_constant<int, 512>(), One());
+  if (n <= 8192) return f(std::integral_constant<int, MOST>(), std::integral_constant<int, 1024 / MOST>());
+  return f(std::integral_constant<int, MOST>(), std::integral_constant<int, 2048 / MOST>());
 }
-template <template <typename, typename, int, int, bool> class Launch, typename... A>
-int norm_dispatch(int x_dtype, int r_dtype, bool vec, int n, A&&... a) {
-  typedef __nv_bfloat16 H;
-  if (x_dtype == SDM_F32)
-    return vec ? norm_by_width<Launch, float, float, true>(n, a...) : norm_by_width<Launch, float, float, false>(n, a...);
-  if (r_dtype == SDM_F32)
-    return vec ? norm_by_width<Launch, H, float, true>(n, a...) : norm_by_width<Launch, H, float, false>(n, a...);
-  return vec ? norm_by_width<Launch, H, H, true>(n, a...) : norm_by_width<Launch, H, H, false>(n, a...);
-}
+
+// A thread's own copies of the weights in shared memory: asked for row by row they waited for L2 behind the rows that
+// pass through L1.
+template <typename R, int BLOCK, int N>
+struct Kept {
+  static constexpr bool on = R::E == 8;
+  float4 v[on ? N * 2 * BLOCK : 1];
+  __device__ void put(int which, const void* p, int dtype, long long off, int t, int n) {
+    if constexpr (on) {
+      float w[R::E];
+      R::weights(p, dtype, off, t, n, w);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        v[(which * 2 + k) * BLOCK + threadIdx.x] = make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+  }
+  __device__ void get(int which, const void* p, int dtype, long long off, int t, int n, float (&w)[R::E]) const {
+    if constexpr (on) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 x = v[(which * 2 + k) * BLOCK + threadIdx.x];
+        w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
+      }
+    } else {
+      R::weights(p, dtype, off, t, n, w);
+    }
+  }
+};
 
 inline uintptr_t norm_odd(int dtype) { return dtype == SDM_F32 ? 3 : 1; }
 inline bool misaligned(const void* p, uintptr_t m) { return (reinterpret_cast<uintptr_t>(p) & m) != 0; }
