@@ -559,9 +559,10 @@ int sdm_project_gated_backward(const void* x, const void* w, const void* dh, lon
  *   g  fp32 logarithms of the decays, at most 0 where nothing grows: [B, T, H] with strides between
  *      sequences and tokens (both 0: one row [H] for all of them), or NULL (no decay);
  *   o  [B, T, H, dv] dt, dense;  state, state_out fp32 [n_slots, H, dk, dv].
- * Sums and states are fp32.  bf16 operands of up to SDM_LINEAR_TILE_D columns whose rows start on 16 bytes go
- * to the tensor cores in chunks of 128 tokens: there the masked products of a chunk and the state
- * in front of it are rounded to bf16 as they are read (the state itself is not).
+ * Sums and states are fp32.  bf16 prompts with dk up to SDM_LINEAR_TILE_D go to the tensor cores in chunks of 128
+ * tokens: there the masked products of a chunk and the state in front of it are rounded to bf16 as they are read (the
+ * state itself is not).  Rows that do not start on 16 bytes are copied for that where dk or dv is no multiple of 8; otherwise they
+ * are taken token by token.
  * Requires H % Hk == 0, dk <= SDM_MAX_LINEAR_D, dv <= SDM_MAX_LINEAR_D.  o and the workspace overlap nothing else
  * (SDM_EOVERLAP), nor does state_out but for the state itself. */
 #define SDM_MAX_LINEAR_D 256
@@ -579,7 +580,7 @@ typedef struct {
   float scale;
 } sdm_linear_args;
 /* Bytes of device workspace for these sizes; 0 where none is needed. */
-size_t sdm_linear_attention_workspace_size(int dtype, int B, int T, int H, int dk, int dv);
+size_t sdm_linear_attention_workspace_size(int dtype, int B, int T, int H, int Hk, int dk, int dv);
 int sdm_linear_attention(const sdm_linear_args* args, void* workspace, size_t workspace_bytes,
                          int* dev_err, void* stream);
 

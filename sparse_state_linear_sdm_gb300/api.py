@@ -90,7 +90,7 @@ def lib() -> ctypes.CDLL:
             L.sdm_selective_scan_workspace_size.restype = sz
             L.sdm_project_gated_backward_workspace_size.argtypes = [ll, i, i]
             L.sdm_project_gated_backward_workspace_size.restype = sz
-            L.sdm_linear_attention_workspace_size.argtypes = [i] * 6
+            L.sdm_linear_attention_workspace_size.argtypes = [i] * 7
             L.sdm_residual_norm_backward_workspace_size.argtypes = [ll, i, i]
             L.sdm_project_workspace_size.argtypes = [ll, i, i]
             L.sdm_project_backward_workspace_size.argtypes = [ll, i, i, i]

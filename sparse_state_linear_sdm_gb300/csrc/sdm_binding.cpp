@@ -402,7 +402,7 @@ PyObject* linear(PyObject* const* a) {
   at::Tensor own;
   size_t bytes = 0;
   void* ws = c.workspace(optional(a[10], "workspace"),
-                         T > 1 ? sdm_linear_attention_workspace_size(s.dtype, s.B, s.T, s.H, s.dk, s.dv) : 0, &own, &bytes);
+                         T > 1 ? sdm_linear_attention_workspace_size(s.dtype, s.B, s.T, s.H, s.Hk, s.dk, s.dv) : 0, &own, &bytes);
   const int r = sdm_linear_attention(&s, ws, bytes, static_cast<int*>(pe), c.stream());
   if (r != SDM_OK) raise_status("sdm_linear_attention", r);
   return pair(o.release(), st.written);

@@ -17,9 +17,11 @@ namespace {
 
 constexpr int kStepTokens = 16;  // tokens of a shared-memory tile
 constexpr int kRows = 16;        // state rows of a lane
-constexpr int kCols = 8;         // and columns
+constexpr int kCols = 4;         // and columns
+constexpr int kStepWarps = 8;    // of a block, at most
 
-// A warp holds a DK x cols piece of a state: R lanes share the rows, 32 / R groups of lanes have 8 columns each.
+// A warp holds a DK x cols piece of a state: R lanes share the rows, 32 / R groups of lanes have four columns each.  (With
+// eight, a head of 128 x 128 is four warps, one for each scheduler of an SM: 1.3 times the time.)
 template <int DK>
 struct Warp {
   static constexpr int R = DK / kRows;
@@ -41,12 +43,31 @@ struct StepTile {
   }
 };
 
-// The state is held as S = e^{hi + lo} s: a token then costs s += (e^{-(hi + lo)} v) k^T and o = e^{hi + lo} q s, two
-// multiply-adds a state instead of three, and a slow decay is not rounded at every token.  The sum of g since s was
-// last brought up to date is carried in two floats (in one, 4,000 tokens at 0.001 left 4e-6); past 4 in
-// size s takes the factor on, so nothing under- or overflows that does not in the definition.
+// Within a tile the state is held as S = e^{G_t} s, G_t the sum of g from the tile's start: a token then costs
+// s += (e^{-G_t} v) k^T and o = e^{G_t} q s, two multiply-adds a state instead of three, and a slow decay is not
+// rounded at every token.  Where |G_t| passes kLazy within a tile, its tokens decay s one by one instead.  The sums are
+// carried in two floats, and the exponential takes both (in one, 4,000 tokens at 0.001 left 4e-6).
+constexpr float kLazy = 30.f;
+
+struct TwoSum {
+  float hi, lo;
+  __device__ __forceinline__ TwoSum operator+(const TwoSum& o) const {
+    const float s = hi + o.hi, z = s - hi;
+    return {s, (lo + o.lo) + ((hi - (s - z)) + (o.hi - z))};
+  }
+  __device__ __forceinline__ TwoSum from_lane(int lane) const {
+    return {__shfl_sync(0xFFFFFFFFu, hi, lane & 31), __shfl_sync(0xFFFFFFFFu, lo, lane & 31)};
+  }
+  // e^(hi + lo): what the argument's rounding leaves is multiplied on.
+  __device__ __forceinline__ float exp(float sign) const {
+    const float x = hi * kLog2e, rest = fmaf(hi, kLog2e, -x) + fmaf(hi, 1.925963033500e-8f, lo * kLog2e);
+    const float e = exp2_fast(sign * x);
+    return fmaf(e, sign * 0.69314718f * rest, e);
+  }
+};
+
 template <typename T, int DK, int PASS>
-__global__ void __launch_bounds__(128, 2) step_kernel(const __grid_constant__ LinearArgs a) {
+__global__ void __launch_bounds__(32 * kStepWarps, 2) step_kernel(const __grid_constant__ LinearArgs a) {
   constexpr int R = Warp<DK>::R, CW = Warp<DK>::cols, V = Piece<T>::n;
   extern __shared__ __align__(16) uint8_t smem[];
   const sdm_linear_args& io = a.io;
@@ -185,13 +206,8 @@ __global__ void __launch_bounds__(128, 2) step_kernel(const __grid_constant__ Li
   else if (PASS == kWhole && io.state && p.slot >= 0)
     read_state(io.state + ((long long)p.slot * io.H + p.h) * sn);
 
-  float hi = 0.f, lo = 0.f;      // sum of g that s does not have yet
-  float all_hi = 0.f, all_lo = 0.f;  // and that of the segment
-  auto two_sum = [](float& h, float& l, float g) {
-    const float t = h + g, z = t - h;
-    l += (h - (t - z)) + (g - z);
-    h = t;
-  };
+  TwoSum pending = {0.f, 0.f};  // sum of g that s does not have yet
+  TwoSum all = {0.f, 0.f};      // and that of the segment
 
   if (p.t_lo < p.t_end) load_tile(0, p.t_lo);
   int st = 0;
@@ -215,49 +231,61 @@ __global__ void __launch_bounds__(128, 2) step_kernel(const __grid_constant__ Li
       __syncthreads();
       f = w;
     }
-    const float* g = raw_g(st);
-    for (int t = 0; t < nt; ++t, f += lay.row) {
-      const float gt = g[t];
-      if (PASS == kReduce) {
-        if (fabsf(gt) <= 3.0e38f && fabsf(all_hi) <= 3.0e38f)
-          two_sum(all_hi, all_lo, gt);
-        else
-          all_hi += gt;  // an infinite sum has no remainder
-      }
-      if (!(fabsf(hi + gt) <= 4.0f)) {
-        const float e = exp2_fast(kLog2e * (hi + lo)), e2 = exp2_fast(kLog2e * gt);
-        const uint64_t both = pack2(e, e), both2 = pack2(e2, e2);
+    // Lane t: g of token t and its sum from the tile's start.
+    const float own = lane < nt ? raw_g(st)[lane] : 0.f;
+    TwoSum sum = {own, 0.f};
 #pragma unroll
-        for (int i = 0; i < kRows / 2; ++i)
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) s[i][c] = mul2(mul2(s[i][c], both), both2);
-        hi = lo = 0.f;
-      } else {
-        two_sum(hi, lo, gt);
-      }
-      const float up = exp2_fast(-kLog2e * (hi + lo));
-      const float4* kp = reinterpret_cast<const float4*>(f + DK) + r;
-      const float4* vp = reinterpret_cast<const float4*>(f + 2 * DK + col);
-      uint64_t k2[kRows / 2], v2[kCols];
-#pragma unroll
-      for (int i = 0; i < kRows / 4; ++i) {
-        const float4 w = kp[i * R];
-        k2[2 * i] = pack2(w.x, w.y), k2[2 * i + 1] = pack2(w.z, w.w);
-      }
-#pragma unroll
-      for (int i = 0; i < kCols / 4; ++i) {
-        const float4 w = vp[i];
-        const float x[4] = {w.x * up, w.y * up, w.z * up, w.w * up};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v2[4 * i + j] = pack2(x[j], x[j]);
-      }
+    for (int m = 1; m < kStepTokens; m *= 2) {
+      const TwoSum x = sum.from_lane(lane - m);
+      if (lane >= m) sum = x + sum;
+    }
+    const bool lazy = __all_sync(0xFFFFFFFFu, fabsf(sum.hi) <= kLazy);  // not with a NaN either
+    if (pending.hi != 0.f) {
+      const float e = pending.exp(1.f);
+      const uint64_t both = pack2(e, e);
 #pragma unroll
       for (int i = 0; i < kRows / 2; ++i)
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) s[i][c] = fma2(k2[i], v2[c], s[i][c]);
+        for (int c = 0; c < kCols; ++c) s[i][c] = mul2(s[i][c], both);
+    }
+    const float up = lazy ? sum.exp(-1.f) : 1.f, down = lazy ? sum.exp(1.f) * io.scale : io.scale,
+                each = exp2_fast(kLog2e * own);
+    pending = lazy ? sum.from_lane(nt - 1) : TwoSum{0.f, 0.f};
+    if (PASS == kReduce) {
+      if (lazy) {
+        all = all + pending;
+      } else {  // an infinite sum has no remainder
+        for (int t = 0; t < nt; ++t) all.hi += __shfl_sync(0xFFFFFFFFu, own, t);
+      }
+    }
+
+    for (int t = 0; t < nt; ++t, f += lay.row) {
+      const float u = __shfl_sync(0xFFFFFFFFu, up, t);
+      if (!lazy) {
+        const float e = __shfl_sync(0xFFFFFFFFu, each, t);
+        const uint64_t both = pack2(e, e);
+#pragma unroll
+        for (int i = 0; i < kRows / 2; ++i)
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) s[i][c] = mul2(s[i][c], both);
+      }
+      const float4* kp = reinterpret_cast<const float4*>(f + DK) + r;
+      const float4 v = *reinterpret_cast<const float4*>(f + 2 * DK + col);
+      const uint64_t v2[kCols] = {pack2(v.x * u, v.x * u), pack2(v.y * u, v.y * u), pack2(v.z * u, v.z * u),
+                                  pack2(v.w * u, v.w * u)};
+#pragma unroll
+      for (int i = 0; i < kRows / 4; ++i) {
+        const float4 w = kp[i * R];
+        const uint64_t k0 = pack2(w.x, w.y), k1 = pack2(w.z, w.w);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          s[2 * i][c] = fma2(k0, v2[c], s[2 * i][c]);
+          s[2 * i + 1][c] = fma2(k1, v2[c], s[2 * i + 1][c]);
+        }
+      }
       if (PASS == kReduce) continue;
-      const float4* qp = reinterpret_cast<const float4*>(f) + r;
       uint64_t acc[kCols];
+      const float4* qp = reinterpret_cast<const float4*>(f) + r;
 #pragma unroll
       for (int i = 0; i < kRows / 4; ++i) {
         const float4 w = qp[i * R];
@@ -293,9 +321,9 @@ __global__ void __launch_bounds__(128, 2) step_kernel(const __grid_constant__ Li
         }
       }
       constexpr int left = kCols / R < 1 ? 1 : kCols / R;
-      const float down = exp2_fast(kLog2e * (hi + lo)) * io.scale;
+      const float dn = __shfl_sync(0xFFFFFFFFu, down, t);
 #pragma unroll
-      for (int c = 0; c < left; ++c) so[t * lay.vc + col + at + c] = o[c] * down;
+      for (int c = 0; c < left; ++c) so[t * lay.vc + col + at + c] = o[c] * dn;
     }
     if (PASS != kReduce) {
       __syncthreads();
@@ -321,10 +349,10 @@ __global__ void __launch_bounds__(128, 2) step_kernel(const __grid_constant__ Li
     for (int t = max(p.t_end, p.t_lo); t < p.t_hi; ++t)  // no token here
       for (int c = tid; c < nv; c += threads) from_f32(0.f, go + t * ots + c);
   }
-  const float end = exp2_fast(kLog2e * (hi + lo));
+  const float end = pending.exp(1.f);
   if (PASS == kReduce) {
     write_state(a.ws_s + (p.seg * nbh + bh) * sn, end);
-    if (p.vt == 0 && tid == 0) a.ws_g[p.seg * nbh + bh] = all_hi + all_lo;
+    if (p.vt == 0 && tid == 0) a.ws_g[p.seg * nbh + bh] = all.hi + all.lo;
   } else if (p.last && io.state_out && p.slot >= 0) {
     write_state(io.state_out + ((long long)p.slot * io.H + p.h) * sn, end);
   }
@@ -469,7 +497,7 @@ int launch_pass(LinearArgs a, int warps, cudaStream_t s) {
   const StepTile<T, DK> lay(warps);
   static PerDevice ready;
   if (ready.get([&] {
-        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, StepTile<T, DK>(4).bytes) ==
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, StepTile<T, DK>(kStepWarps).bytes) ==
                        cudaSuccess ? 1 : -1;
       }) < 0)
     return SDM_ECUDA;
@@ -491,7 +519,7 @@ int launch_pass(LinearArgs a, int warps, cudaStream_t s) {
 
 template <typename T, int DK>
 int launch_steps(const LinearArgs& a, cudaStream_t s) {
-  const int need = (a.io.dv + Warp<DK>::cols - 1) / Warp<DK>::cols, warps = need < 4 ? need : 4;
+  const int need = (a.io.dv + Warp<DK>::cols - 1) / Warp<DK>::cols, warps = need < kStepWarps ? need : kStepWarps;
   if (a.segments <= 1) return launch_pass<T, DK, kWhole>(a, warps, s);
   int st = launch_pass<T, DK, kReduce>(a, warps, s);
   if (st == SDM_OK) st = launch_front(a, s);
@@ -510,13 +538,13 @@ bool sizes_ok(int dtype, int B, int T, int H, int dk, int dv) {
   return !bad_dtype(dtype) && B >= 1 && T >= 0 && H >= 1 && dk >= 1 && dv >= 1;
 }
 
-// How a sequence is cut for step_kernel: a warp's piece of a state is a unit of work, and the card runs about 8 of
-// them an SM; twice the work pays from some three segments on.
+// How a sequence is cut for step_kernel: a warp's piece of a state is a unit of work, and the card runs 16 of them an
+// SM; twice the work pays from some three segments on.
 void cut_steps(int B, int T, int H, int dk, int dv, int* segments, int* segment) {
-  const int DK = dk <= 32 ? 32 : dk <= 64 ? 64 : dk <= 128 ? 128 : 256, cols = 512 / DK * 8;
+  const int DK = dk <= 32 ? 32 : dk <= 64 ? 64 : dk <= 128 ? 128 : 256, cols = 32 / (DK / kRows) * kCols;
   const long long units = (long long)B * H * ((dv + cols - 1) / cols);
-  long long n = units * 3 > 152 * 8 ? 1 : 152 * 8 / units;
-  n = n < T / 64 ? n : T / 64;
+  long long n = 152 * 16 / units;
+  n = n < T / (2 * kStepTokens) ? n : T / (2 * kStepTokens);
   if (n < 3) n = 1;
   const long long per = ((T + n - 1) / n + kStepTokens - 1) / kStepTokens * kStepTokens;
   *segment = n > 1 ? int(per) : T;
@@ -562,17 +590,31 @@ int launch_front(const LinearArgs& a, cudaStream_t s) {
 
 using namespace sdm;
 
-extern "C" size_t sdm_linear_attention_workspace_size(int dtype, int B, int T, int H, int dk, int dv) {
-  if (!sizes_ok(dtype, B, T, H, dk, dv) || dk > SDM_MAX_LINEAR_D || dv > SDM_MAX_LINEAR_D) return 0;
-  int segments, segment;
-  cut_steps(B, T, H, dk, dv, &segments, &segment);
-  if (dtype == SDM_BF16 && dk <= SDM_LINEAR_TILE_D && dv <= SDM_LINEAR_TILE_D) {  // which form it is, strides decide
-    int n;
-    cut_tiles(B, T, H, &n, &segment);
-    segments = n > segments ? n : segments;
+// What of the workspace a call with these sizes may need: the segments' states and sums of g, then copies of rows that
+// are not multiples of 16 bytes.  Which form is taken, strides and addresses decide too.
+namespace {
+bool tile_sizes(int dtype, int T, int dk) { return dtype == SDM_BF16 && T >= kTileTokens && dk <= SDM_LINEAR_TILE_D; }
+struct LinearSpace {
+  size_t states = 0, pad = 0;
+  LinearSpace(int dtype, int B, int T, int H, int Hk, int dk, int dv) {
+    int segments, segment;
+    cut_steps(B, T, H, dk, dv, &segments, &segment);
+    if (tile_sizes(dtype, T, dk)) {
+      int n;
+      cut_tiles(B, T, H, dv, &n, &segment);
+      segments = n > segments ? n : segments;
+      if (dk % 8 || dv % 8) pad = padded_bytes(B, T, H, Hk, dk, dv);
+    }
+    if (segments > 1) states = (size_t(segments) * B * H * (size_t(dk) * dv + 1) * 4 + 255) / 256 * 256;
   }
-  if (segments <= 1) return 0;
-  return size_t(segments) * B * H * (size_t(dk) * dv + 4) * 4;
+};
+}  // namespace
+
+extern "C" size_t sdm_linear_attention_workspace_size(int dtype, int B, int T, int H, int Hk, int dk, int dv) {
+  if (!sizes_ok(dtype, B, T, H, dk, dv) || Hk < 1 || H % Hk || dk > SDM_MAX_LINEAR_D || dv > SDM_MAX_LINEAR_D || T <= 1)
+    return 0;
+  const LinearSpace space(dtype, B, T, H, Hk, dk, dv);
+  return space.states + space.pad;
 }
 
 extern "C" int sdm_linear_attention(const sdm_linear_args* args, void* workspace, size_t workspace_bytes,
@@ -608,12 +650,13 @@ extern "C" int sdm_linear_attention(const sdm_linear_args* args, void* workspace
   a.vec_v = io.dv % V == 0 && rows16(io.v, io.v_bs, io.v_ts);
   a.vec_o = io.dv % V == 0 && !off(io.o, 15);
   auto steps_on = [&](long long bs, long long ts) { return ts > 0 && (io.B == 1 || bs > 0); };
-  const bool tiles = io.dtype == SDM_BF16 && io.T >= kTileTokens && io.dk <= SDM_LINEAR_TILE_D && io.dv <= SDM_LINEAR_TILE_D &&
-                     a.vec_qk && a.vec_v && a.vec_o && steps_on(io.q_bs, io.q_ts) && steps_on(io.k_bs, io.k_ts) &&
-                     steps_on(io.v_bs, io.v_ts);
-  const size_t need = sdm_linear_attention_workspace_size(io.dtype, io.B, io.T, io.H, io.dk, io.dv);
+  const LinearSpace space(io.dtype, io.B, io.T, io.H, io.Hk, io.dk, io.dv);
+  const size_t need = space.states + space.pad;
+  const bool rows_fit = a.vec_qk && a.vec_v && a.vec_o && steps_on(io.q_bs, io.q_ts) && steps_on(io.k_bs, io.k_ts) &&
+                        steps_on(io.v_bs, io.v_ts);
+  const bool tiles = tile_sizes(io.dtype, io.T, io.dk) && (rows_fit || space.pad);
   if (tiles)
-    cut_tiles(io.B, io.T, io.H, &a.segments, &a.segment);
+    cut_tiles(io.B, io.T, io.H, io.dv, &a.segments, &a.segment);
   else
     cut_steps(io.B, io.T, io.H, io.dk, io.dv, &a.segments, &a.segment);
   if (need) {
@@ -623,6 +666,6 @@ extern "C" int sdm_linear_attention(const sdm_linear_args* args, void* workspace
     a.ws_g = a.ws_s + size_t(a.segments) * io.B * io.H * io.dk * io.dv;
   }
   if (overlap(io, need ? workspace : nullptr, need)) return SDM_EOVERLAP;
-  if (tiles) return launch_tiles(a, s);
+  if (tiles) return launch_tiles(a, rows_fit ? nullptr : static_cast<uint8_t*>(workspace) + space.states, s);
   return io.dtype == SDM_F32 ? launch_type<float>(a, s) : launch_type<__nv_bfloat16>(a, s);
 }

@@ -12,6 +12,7 @@ enum LinearPass { kWhole = 0, kReduce = 1, kJoin = 2 };
 struct LinearArgs {
   sdm_linear_args io;
   int vtiles;            // column tiles of v
+  int o_dv;              // columns of o as it lies in memory (tiles)
   int segments, segment; // segments of a sequence, tokens of a segment
   float* ws_s;           // [segments][B][H][dk][dv]: each segment's end from zero, then the state in front of it
   float* ws_g;           // [segments][B][H]: sum of g over each segment
@@ -52,9 +53,10 @@ __device__ __forceinline__ Place place_of(const LinearArgs& a) {
 // The kernel that turns segments' ends into the states in front of them.
 int launch_front(const LinearArgs& a, cudaStream_t s);
 
-// The tensor cores' form: bf16, dk and dv up to SDM_LINEAR_TILE_D and multiples of 8, rows on 16 bytes, positive strides.
-// Segments of its own.
-void cut_tiles(int B, int T, int H, int* segments, int* segment);
-int launch_tiles(LinearArgs a, cudaStream_t s);
+// The tensor cores' form: bf16, dk up to SDM_LINEAR_TILE_D, and multiples of 8, rows on 16 bytes and positive strides, or
+// else a workspace of padded_bytes at `pad` for copies that have them.  Segments of its own.
+void cut_tiles(int B, int T, int H, int dv, int* segments, int* segment);
+size_t padded_bytes(int B, int T, int H, int Hk, int dk, int dv);
+int launch_tiles(LinearArgs a, void* pad, cudaStream_t s);
 
 }  // namespace sdm

@@ -24,6 +24,7 @@ namespace sdm {
 namespace {
 
 constexpr int kChunk = 128;
+constexpr int kTileColumns = 128;        // of v a CTA takes
 constexpr int kSlot = 32768;             // 128 tokens of 128 columns: two boxes of 64 columns
 constexpr int kBox = kChunk * 128;       // bytes of a box
 constexpr int kSlots = 6;                // two chunks
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   const Place p = place_of<PASS>(a);
   const int tokens = max(p.t_end - p.t_lo, 0), chunks = (tokens + kChunk - 1) / kChunk;
+  const int v0 = p.vt * kTileColumns, dv = min(kTileColumns, io.dv - v0);  // this CTA's columns of v
   const long long bh = (long long)p.b * io.H + p.h, nbh = (long long)io.B * io.H, sn = (long long)io.dk * io.dv;
   if (PASS == kJoin) wait_previous();
 
@@ -287,10 +289,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint32_t dst = place(at), full = bar(kFull + at);
           const bool value = i == kLoads - 1;
           const CUtensorMap* map = value ? &tm.v : i == 0 ? &tm.k : &tm.q;
-          const int boxes = value ? kBoxesV : kBoxesK, head = value ? p.h : p.hk;
+          const int boxes = value ? kBoxesV : kBoxesK, head = value ? p.h : p.hk, x = value ? v0 : 0;
           mbar_expect_tx(full, uint32_t(boxes * kBox));
-          tma_load_4d(dst, map, 0, head, t, p.b, full);
-          if (boxes > 1) tma_load_4d(dst + kBox, map, 64, head, t, p.b, full);
+          tma_load_4d(dst, map, x, head, t, p.b, full);
+          if (boxes > 1) tma_load_4d(dst + kBox, map, x + 64, head, t, p.b, full);
           issued[at] = issued[at] + 1u;
         }
       }
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       total = total + all;
       arrive(kDecayFull);
     }
-    if (PASS == kReduce && lane == 0) a.ws_g[p.seg * nbh + bh] = total.hi + total.lo;
+    if (PASS == kReduce && lane == 0 && p.vt == 0) a.ws_g[p.seg * nbh + bh] = total.hi + total.lo;
   } else if (warp == 1) {
     // ---- MMAs of o ----
     if (PASS != kReduce) {
@@ -543,7 +545,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(kOutEmpty));
-          tma_store_4d(&tm.o, half * (DV / 2), p.h, p.t_lo + c * kChunk + quad * 32, p.b, patch);
+          tma_store_4d(&tm.o, v0 + half * (DV / 2), p.h, p.t_lo + c * kChunk + quad * 32, p.b, patch);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
         __syncwarp();
@@ -562,10 +564,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const float* src = PASS == kJoin ? a.ws_s + (p.seg * nbh + bh) * sn
                        : PASS == kWhole && io.state && p.slot >= 0 ? io.state + ((long long)p.slot * io.H + p.h) * sn
                                                                    : nullptr;
-    if (src && col < io.dv) {
+    if (src && col < dv) {
 #pragma unroll
       for (int i = 0; i < kCols; ++i)
-        if (c0 + i < io.dk) s[i] = src[(c0 + i) * io.dv + col];
+        if (c0 + i < io.dk) s[i] = src[(c0 + i) * io.dv + v0 + col];
     }
     auto show_state = [&] {  // as q reads it
       if (cols) {
@@ -628,19 +630,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float* dst = PASS == kReduce                              ? a.ws_s + (p.seg * nbh + bh) * sn
                  : p.last && io.state_out && p.slot >= 0 ? io.state_out + ((long long)p.slot * io.H + p.h) * sn
                                                               : nullptr;
-    if (dst && col < io.dv) {
+    if (dst && col < dv) {
 #pragma unroll
       for (int i = 0; i < kCols; ++i)
-        if (c0 + i < io.dk) dst[(c0 + i) * io.dv + col] = s[i];
+        if (c0 + i < io.dk) dst[(c0 + i) * io.dv + v0 + col] = s[i];
     }
   }
 
   // No token here: o is 0.
   if (PASS != kReduce) {
-    const int t0 = p.t_lo + chunks * kChunk, pieces = io.dv / 8;
+    const int t0 = p.t_lo + chunks * kChunk, pieces = min(kTileColumns, a.o_dv - v0) / 8;
     for (long long i = threadIdx.x; i < (long long)(p.t_hi - t0) * pieces; i += kTileThreads)
       *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(io.o) +
-                                (((long long)p.b * io.T + t0 + i / pieces) * io.H + p.h) * io.dv + i % pieces * 8) =
+                                (((long long)p.b * io.T + t0 + i / pieces) * io.H + p.h) * a.o_dv + v0 + i % pieces * 8) =
           make_uint4(0, 0, 0, 0);
   }
 
@@ -685,7 +687,7 @@ int launch_pass(const TileMaps& tm, const LinearArgs& a, cudaStream_t s) {
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess ? 1 : -1;
       }) < 0)
     return SDM_ECUDA;
-  const long long blocks = (long long)a.io.H * a.io.B * (PASS == kReduce ? a.segments - 1 : a.segments);
+  const long long blocks = (long long)a.vtiles * a.io.H * a.io.B * (PASS == kReduce ? a.segments - 1 : a.segments);
   if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
   cudaLaunchAttribute attr[1] = {after_previous()};
   cudaLaunchConfig_t cfg = {};
@@ -709,10 +711,68 @@ int launch_sizes(const TileMaps& tm, const LinearArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+// ---- rows off 16 bytes ----
+//
+// Copied to rows of multiples of eight columns first, and o back: 8 x 2048 x 16 heads with dk 100 and dv 128 take 186 us
+// so, and 1,006 token by token.
+
+// q, k and v of the tokens that exist: a block has some tokens of one sequence and one of the three, a warp their heads in
+// turn, four of them at a time, a lane two columns.
+constexpr int kPadThreads = 256, kPadTokens = 16, kPadRows = 4;
+struct PadArgs {
+  sdm_linear_args io;
+  __nv_bfloat16* to[3];
+  int pad[3];  // columns there
+};
+__global__ void __launch_bounds__(kPadThreads) widen_kernel(const __grid_constant__ PadArgs a) {
+  const sdm_linear_args& io = a.io;
+  const int which = blockIdx.y, tiles = (io.T + kPadTokens - 1) / kPadTokens;
+  const int b = int(blockIdx.x / unsigned(tiles)), t0 = int(blockIdx.x % unsigned(tiles)) * kPadTokens;
+  const int n = min(kPadTokens, row_length(io.lengths, b, io.T) - t0);
+  const int heads = which == 2 ? io.H : io.Hk, d = which == 2 ? io.dv : io.dk, dp = a.pad[which];
+  const long long bs = which == 0 ? io.q_bs : which == 1 ? io.k_bs : io.v_bs, ts = which == 0 ? io.q_ts : which == 1 ? io.k_ts : io.v_ts;
+  const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(which == 0 ? io.q : which == 1 ? io.k : io.v) + b * bs + t0 * ts;
+  __nv_bfloat16* to = a.to[which] + ((long long)b * io.T + t0) * heads * dp;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = n * heads;
+  for (int r0 = warp * kPadRows; r0 < rows; r0 += kPadThreads / 32 * kPadRows)
+    for (int c = 2 * lane; c < dp; c += 64) {
+      __nv_bfloat162 v[kPadRows];
+#pragma unroll
+      for (int i = 0; i < kPadRows; ++i) {
+        const int r = r0 + i, t = r / heads;
+        const __nv_bfloat16* row = from + t * ts + (r - t * heads) * d + c;
+        v[i].x = r < rows && c < d ? row[0] : __nv_bfloat16(0.f);
+        v[i].y = r < rows && c + 1 < d ? row[1] : __nv_bfloat16(0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < kPadRows; ++i)
+        if (r0 + i < rows) *reinterpret_cast<__nv_bfloat162*>(to + (long long)(r0 + i) * dp + c) = v[i];
+    }
+}
+// o out of rows of dp columns.
+__global__ void __launch_bounds__(kPadThreads) narrow_kernel(const __nv_bfloat16* from, long long rows, int d, int dp,
+                                                             __nv_bfloat16* o) {
+  wait_previous();
+  const int lane = threadIdx.x & 31;
+  const long long r0 = ((long long)blockIdx.x * (kPadThreads / 32) + (threadIdx.x >> 5)) * kPadRows;
+  for (int c = 2 * lane; c < d; c += 64) {
+    __nv_bfloat162 v[kPadRows];
+#pragma unroll
+    for (int i = 0; i < kPadRows; ++i)
+      if (r0 + i < rows) v[i] = *reinterpret_cast<const __nv_bfloat162*>(from + (r0 + i) * dp + c);
+#pragma unroll
+    for (int i = 0; i < kPadRows; ++i) {
+      if (r0 + i >= rows) break;
+      o[(r0 + i) * d + c] = v[i].x;
+      if (c + 1 < d) o[(r0 + i) * d + c + 1] = v[i].y;
+    }
+  }
+}
+
 // A CTA of the tile kernel fills an SM and takes a chunk in about the time of 64 to 128 KB of HBM traffic of its share, so
 // 152 of them are what the card runs at once.
-void cut_tiles(int B, int T, int H, int* segments, int* segment) {
-  const long long units = (long long)B * H, chunks = (T + kChunk - 1) / kChunk;
+void cut_tiles(int B, int T, int H, int dv, int* segments, int* segment) {
+  const long long units = (long long)B * H * ((dv + kTileColumns - 1) / kTileColumns), chunks = (T + kChunk - 1) / kChunk;
   long long n = units * 2 > 152 ? 1 : 152 / units;
   n = n < chunks / 2 ? n : chunks / 2;
   if (n < 3) n = 1;
@@ -721,18 +781,66 @@ void cut_tiles(int B, int T, int H, int* segments, int* segment) {
   *segment = n > 1 ? int(per * kChunk) : T;
 }
 
-int launch_tiles(LinearArgs a, cudaStream_t s) {
-  const sdm_linear_args& io = a.io;
-  a.vtiles = 1;
+namespace {
+int round8(int d) { return (d + 7) / 8 * 8; }
+size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
+}  // namespace
+
+size_t padded_bytes(int B, int T, int H, int Hk, int dk, int dv) {
+  const size_t tokens = size_t(B) * T * 2;
+  return 2 * pad256(tokens * Hk * round8(dk)) + 2 * pad256(tokens * H * round8(dv));
+}
+
+int launch_tiles(LinearArgs a, void* pad, cudaStream_t s) {
+  const sdm_linear_args given = a.io;
+  sdm_linear_args& io = a.io;
+  a.vtiles = (io.dv + kTileColumns - 1) / kTileColumns;
+  a.o_dv = io.dv;
+  const int dk = round8(io.dk), dv = round8(io.dv);
+  if (pad) {
+    if ((long long)io.B * ((io.T + kPadTokens - 1) / kPadTokens) > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
+    PadArgs w = {};
+    w.io = given;
+    uint8_t* at = static_cast<uint8_t*>(pad);
+    const size_t tokens = size_t(io.B) * io.T * 2;
+    for (int i = 0; i < 3; ++i) {
+      w.pad[i] = i == 2 ? dv : dk;
+      w.to[i] = reinterpret_cast<__nv_bfloat16*>(at);
+      at += pad256(tokens * (i == 2 ? io.H * dv : io.Hk * dk));
+    }
+    widen_kernel<<<dim3(unsigned(io.B) * unsigned((io.T + kPadTokens - 1) / kPadTokens), 3), kPadThreads, 0, s>>>(w);
+    if (last_launch_status() != SDM_OK) return SDM_ECUDA;
+    io.q = w.to[0], io.k = w.to[1], io.v = w.to[2], io.o = at;
+    io.q_ts = io.k_ts = (long long)io.Hk * dk, io.v_ts = (long long)io.H * dv;
+    io.q_bs = io.k_bs = io.q_ts * io.T, io.v_bs = io.v_ts * io.T;
+    a.o_dv = dv;
+  }
   TileMaps tm = {};
-  if (!head_map(&tm.q, io.q, io.B, io.T, io.Hk, io.dk, io.q_bs, io.q_ts) ||
-      !head_map(&tm.k, io.k, io.B, io.T, io.Hk, io.dk, io.k_bs, io.k_ts) ||
-      !head_map(&tm.v, io.v, io.B, io.T, io.H, io.dv, io.v_bs, io.v_ts) ||
-      !head_map(&tm.o, io.o, io.B, io.T, io.H, io.dv, (long long)io.T * io.H * io.dv, (long long)io.H * io.dv, 32,
+  if (!head_map(&tm.q, io.q, io.B, io.T, io.Hk, dk, io.q_bs, io.q_ts) ||
+      !head_map(&tm.k, io.k, io.B, io.T, io.Hk, dk, io.k_bs, io.k_ts) ||
+      !head_map(&tm.v, io.v, io.B, io.T, io.H, dv, io.v_bs, io.v_ts) ||
+      !head_map(&tm.o, io.o, io.B, io.T, io.H, dv, (long long)io.T * io.H * dv, (long long)io.H * dv, 32,
                 io.dv <= 64 ? 32 : 64))
     return SDM_ECUDA;
-  if (io.dk <= 64) return io.dv <= 64 ? launch_sizes<64, 64>(tm, a, s) : launch_sizes<64, 128>(tm, a, s);
-  return io.dv <= 64 ? launch_sizes<128, 64>(tm, a, s) : launch_sizes<128, 128>(tm, a, s);
+  int st;
+  if (io.dk <= 64)
+    st = io.dv <= 64 ? launch_sizes<64, 64>(tm, a, s) : launch_sizes<64, 128>(tm, a, s);
+  else
+    st = io.dv <= 64 ? launch_sizes<128, 64>(tm, a, s) : launch_sizes<128, 128>(tm, a, s);
+  if (!pad || st != SDM_OK) return st;
+  const long long rows = (long long)io.B * io.T * io.H, blocks = (rows + kPadThreads / 32 * kPadRows - 1) / (kPadThreads / 32 * kPadRows);
+  if (blocks > 0x7FFFFFFFLL) return SDM_EUNSUPPORTED;
+  cudaLaunchAttribute attr[1] = {after_previous()};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(kPadThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, narrow_kernel, static_cast<const __nv_bfloat16*>(io.o), rows, io.dv, dv,
+                         static_cast<__nv_bfloat16*>(given.o)) != cudaSuccess)
+    return SDM_ECUDA;
+  return last_launch_status();
 }
 
 }  // namespace sdm

@@ -117,10 +117,10 @@ def project_gated_backward(x, w, dh, activation="silu", dx=None, dw=None, worksp
                                               dev_err)
 
 
-def linear_attention_workspace_size(dtype, B: int, T: int, H: int, dk: int, dv: int) -> int:
+def linear_attention_workspace_size(dtype, B: int, T: int, H: int, Hk: int, dk: int, dv: int) -> int:
     """Bytes of workspace linear_attention needs for q, k, v of torch type `dtype`; 0 where it needs none."""
     code = _api.SDM_BF16 if dtype == torch.bfloat16 else _api.SDM_F32
-    return int(_api.lib().sdm_linear_attention_workspace_size(code, B, T, H, dk, dv))
+    return int(_api.lib().sdm_linear_attention_workspace_size(code, B, T, H, Hk, dk, dv))
 
 
 def linear_attention(q, k, v, decay=None, scale=None, state=None, state_out=None, lengths=None, slots=None, out=None,
