@@ -561,7 +561,8 @@ int sdm_project_gated_backward(const void* x, const void* w, const void* dh, lon
  *   o  [B, T, H, dv] dt, dense;  state, state_out fp32 [n_slots, H, dk, dv].
  * Sums and states are fp32.  bf16 prompts with dk up to SDM_LINEAR_TILE_D go to the tensor cores in chunks of 128
  * tokens: there the masked products of a chunk and the state in front of it are rounded to bf16 as they are read (the
- * state itself is not).  Rows that do not start on 16 bytes are copied for that where dk or dv is no multiple of 8; otherwise they
+ * state itself is not), and a value of v that is not finite makes NaN of its column for every token of its chunk, those
+ * before it among them, and not only from its token on.  Rows that do not start on 16 bytes are copied for that where dk or dv is no multiple of 8; otherwise they
  * are taken token by token.
  * Requires H % Hk == 0, dk <= SDM_MAX_LINEAR_D, dv <= SDM_MAX_LINEAR_D.  o and the workspace overlap nothing else
  * (SDM_EOVERLAP), nor does state_out but for the state itself. */

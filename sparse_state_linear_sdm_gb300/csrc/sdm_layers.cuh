@@ -58,6 +58,9 @@ __device__ __forceinline__ float exp2_fast(float x) {  // at most 2 units in the
   return y;
 }
 
+// The largest float for infinity: a factor that times a state of 0 is 0.  NaN stays.
+__device__ __forceinline__ float at_most_finite(float x) { return x > 3.402823466e38f ? 3.402823466e38f : x; }
+
 __device__ __forceinline__ float rcp_fast(float x) {  // one unit in the last place; 0 for inf
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

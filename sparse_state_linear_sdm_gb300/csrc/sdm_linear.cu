@@ -249,10 +249,10 @@ __global__ void __launch_bounds__(32 * kStepWarps, 2) step_kernel(const __grid_c
         for (int c = 0; c < kCols; ++c) s[i][c] = mul2(s[i][c], both);
     }
     const float up = lazy ? sum.exp(-1.f) : 1.f, down = lazy ? sum.exp(1.f) * io.scale : io.scale,
-                each = exp2_fast(kLog2e * own);
+                each = at_most_finite(exp2_fast(kLog2e * own));
     pending = lazy ? sum.from_lane(nt - 1) : TwoSum{0.f, 0.f};
     if (PASS == kReduce) {
-      if (lazy) {
+      if (lazy && fabsf(all.hi) <= 3.0e38f) {
         all = all + pending;
       } else {  // an infinite sum has no remainder
         for (int t = 0; t < nt; ++t) all.hi += __shfl_sync(0xFFFFFFFFu, own, t);
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
   const T* pv = static_cast<const T*>(io.v) + b * io.v_bs + (long long)h * dv;
 #pragma unroll
   for (int j = 0; j < V; ++j) v[j] = c + j < dv ? to_f32(pv[c + j]) : 0.f;
-  const float e = io.g ? expf(io.g[b * io.g_bs + h]) : 1.0f;
+  const float e = io.g ? at_most_finite(expf(io.g[b * io.g_bs + h])) : 1.0f;
   const int length = row_length(io.lengths, b, 1);
   const int slot = checked_slot(io.slots, asked, io.n_slots, a.dev_err);
   __syncthreads();

@@ -139,12 +139,6 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int x, int 
 }
 __device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// 2^x, at most the largest float: times a state of 0 it is 0.
-__device__ __forceinline__ float finite_exp2(float x) {
-  const float y = exp2f(x);
-  return y > 3.402823466e38f ? 3.402823466e38f : y;
-}
-
 // A sum in two floats: as good as one in 64 bits here, and the card adds few of those.
 struct Sum {
   float hi, lo;
@@ -155,7 +149,7 @@ struct Sum {
   __device__ __forceinline__ Sum from_lane(int lane) const {
     return {__shfl_sync(0xFFFFFFFFu, hi, lane & 31), __shfl_sync(0xFFFFFFFFu, lo, lane & 31)};
   }
-  __device__ __forceinline__ float exp() const { return finite_exp2(fmaf(hi, kLog2e, lo * kLog2e)); }
+  __device__ __forceinline__ float exp() const { return at_most_finite(exp2f(fmaf(hi, kLog2e, lo * kLog2e))); }
 };
 
 // One copy of the loop: the roles' code competes for the instruction cache.
@@ -323,7 +317,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       float each[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) each[i] = exp2_fast(kLog2e * next[i]);
+      for (int i = 0; i < 4; ++i) each[i] = at_most_finite(exp2_fast(kLog2e * next[i]));
       if (c + 1 < chunks) ask(c + 1);
       // Scans over eight lanes, a block of 32 tokens, then over the blocks.
       Sum before = up[3], after = up[3];

@@ -136,8 +136,8 @@ def linear_attention(q, k, v, decay=None, scale=None, state=None, state_out=None
     lengths, slots, an empty batch: as for causal_conv.  out: o's memory; it overlaps no other tensor of the call (nor does
     state_out, but for `state` itself): ValueError.  Returns (o [B, T, H, dv], state written).
 
-    bf16 with dk and dv up to 128 and rows on 16 bytes runs in chunks on the tensor cores, everything else token by
-    token; states are fp32 in both."""
+    bf16 prompts with dk up to 128 run in chunks of 128 tokens on the tensor cores, everything else token by token; states
+    are fp32 in both.  In chunks a value of v that is not finite makes NaN of its column for its whole chunk."""
     return (_module or _binding()).linear(q, k, v, decay, scale, state, state_out, lengths, slots, out, workspace, dev_err,
                                           2)
 
