@@ -124,7 +124,7 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float (*part)[K]) {
     for (int k = 0; k < K; ++k) {
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < W; ++i) s += part[i][k];
+      for (int i = 0; i < W; ++i) s += part[w / W * W + i][k];  // the row's own warps
       v[k] = s;
     }
   }
