@@ -98,11 +98,13 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_dense_kernel(const __nv_bf
   if (parts > 1) cluster_sync_all();  // the sums outlive their readers
 }
 
-// CTAs that share a reduction: enough blocks for four an SM, and at least 512 of D each.
+// CTAs that share a reduction: up to 512 blocks, with at least 1024 of D each.  4 tokens of 8192 x 2048 take 11.8 us with one,
+// 9.6, 8.8 and 12.4 with two, four and eight; 8 of 2048 x 8192 take 7.7, 11.3, 17.4 and 32.4, 4 of 1024 x 1024 2.7, 3.5, 4.0
+// and 4.9.
 int few_parts(int D, int N) {
   const int blocks = ceil_div(N, kFewRows);
   int parts = 1;
-  while (parts < 8 && blocks * parts < 152 * 4 && D / (2 * parts) >= 512) parts *= 2;
+  while (blocks * parts < 512 && D / (2 * parts) >= 1024 && parts < 8) parts *= 2;
   return parts;
 }
 
@@ -138,7 +140,11 @@ int launch_few_act(const void* x, const void* w, const void* bias, const void* r
 
 // A product by itself, its reduction split where its tiles leave pairs of SMs idle: the cut of least time.
 Product plan_dense(int M, int D, int N) {
-  Product p = product(M, N, 2 * kHalf, D), best = p;
+  // Row tiles of a group: with a short reduction the outputs weigh more (16,384 tokens of 2048 x 2048: 101 us in groups
+  // of 4, 111 of 16), with a long one the rows of x that are read again (8192 x 2048: 330 us and 303, 320 of 32).
+  Product p = product(M, N, 2 * kHalf, D);
+  p.group = D <= 2048 ? 4 : 16;
+  Product best = p;
   const Product none = {};
   double least = -1;
   const int most = (long long)p.row_tiles * p.col_tiles < 2 * kPairs ? 32 : 1;
@@ -170,7 +176,7 @@ int launch_dense_act(const Maps& tm, const ProductArgs& a, cudaStream_t s) {
 // MODE's product of x and w with its epilogue into out.
 template <int MODE>
 int launch_dense(const void* x, const void* w, const void* bias, const void* extra, int M, int D, int N, int act, void* out,
-                 void* partial, int* dev_err, cudaStream_t s) {
+                 void* partial, float* sums, int* dev_err, cudaStream_t s) {
   ProductArgs a = {};
   a.p[0] = plan_dense(M, D, N);
   a.p[0].out = static_cast<__nv_bfloat16*>(out);
@@ -178,6 +184,7 @@ int launch_dense(const void* x, const void* w, const void* bias, const void* ext
   a.act = act;
   a.bias = static_cast<const __nv_bfloat16*>(bias);
   a.extra = static_cast<const __nv_bfloat16*>(extra);
+  a.sums = sums;
   a.dev_err = dev_err;
   Maps tm = {};
   if (!bf16_tile_map(&tm.A[0], x, M, D, kHalf) || !bf16_tile_map(&tm.B[0], w, N, D, kHalf) ||
@@ -191,28 +198,25 @@ int launch_dense(const void* x, const void* w, const void* bias, const void* ext
 
 // ---- dbias ----
 
-// Sums of dz over a slice of the tokens: 32 groups of eight columns and eight lanes of tokens a block.
+// Sums of dz over the tokens.  The slope pass leaves them for each 32 rows beside dz (dense_sums); without an activation
+// dz is dy, and they are taken from there: eight columns a thread and eight lanes of tokens a block.
 constexpr int kSumRows = 8;
-int sum_slices(long long M, int N) {
-  const long long blocks = ceil_div(N, 256), most = (M + 63) / 64;
-  const long long n = 608 / blocks < 1 ? 1 : 608 / blocks;
-  return int(n < most ? n : most);
-}
-__global__ void __launch_bounds__(32 * kSumRows) column_sums_kernel(const __nv_bfloat16* dz, int M, int N, int per,
-                                                                    float* part) {
+constexpr int kSumSlice = 256;  // tokens of a block
+__global__ void __launch_bounds__(32 * kSumRows) column_sums_kernel(const __nv_bfloat16* dz, int M, int N, float* part) {
   __shared__ float sums[kSumRows][32][9];
   wait_previous();
   allow_next();
   const int col = blockIdx.x * 256 + int(threadIdx.x) * 8;
-  const int m_end = min(M, (int(blockIdx.y) + 1) * per);
+  const int m0 = int(blockIdx.y) * kSumSlice, m_end = min(M - m0, kSumSlice);
   float s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i] = 0.f;
   if (col < N) {
+    const __nv_bfloat16* p = dz + size_t(m0) * N + col;
 #pragma unroll 8
-    for (int m = int(blockIdx.y) * per + int(threadIdx.y); m < m_end; m += kSumRows) {
+    for (int m = int(threadIdx.y); m < m_end; m += kSumRows) {
       float v[8];
-      Piece<__nv_bfloat16>::load(*reinterpret_cast<const uint4*>(dz + size_t(m) * N + col), v);
+      Piece<__nv_bfloat16>::load(*reinterpret_cast<const uint4*>(p + size_t(m) * N), v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] += v[i];
     }
@@ -227,30 +231,46 @@ __global__ void __launch_bounds__(32 * kSumRows) column_sums_kernel(const __nv_b
   for (int i = 0; i < kSumRows; ++i) t += sums[i][id / 8][id % 8];
   part[size_t(blockIdx.y) * N + c] = t;
 }
-__global__ void __launch_bounds__(256) join_sums_kernel(const float* part, int slices, int N, __nv_bfloat16* out) {
+// The rows' sums: 32 columns and 32 lanes of rows a block, each lane's in their order and then the lanes' in theirs.
+__global__ void __launch_bounds__(1024) join_sums_kernel(const float* part, int rows, int N, __nv_bfloat16* out) {
+  __shared__ float lanes[32][33];
   wait_previous();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= N) return;
+  const int c = blockIdx.x * 32 + threadIdx.x;
   float t = 0.f;
+  if (c < N) {
 #pragma unroll 8
-  for (int i = 0; i < slices; ++i) t += part[size_t(i) * N + c];
+    for (int i = int(threadIdx.y); i < rows; i += 32) t += part[size_t(i) * N + c];
+  }
+  lanes[threadIdx.y][threadIdx.x] = t;
+  __syncthreads();
+  if (threadIdx.y || c >= N) return;
+  t = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) t += lanes[i][threadIdx.x];
   out[c] = __float2bfloat16_rn(t);
 }
-int launch_column_sums(const void* dz, long long M, int N, float* part, void* out, cudaStream_t s) {
-  const int slices = sum_slices(M, N), per = ceil_div(M, slices);
+// Rows of partial sums: where the slope pass leaves them, where it does not.
+int slope_sum_rows(long long M) { return int((M + 31) / 32); }
+int dy_sum_rows(long long M) { return int((M + kSumSlice - 1) / kSumSlice); }
+
+// `rows`: of sums that are there already, or 0.
+int launch_column_sums(const void* dz, long long M, int N, float* part, int rows, void* out, cudaStream_t s) {
   cudaLaunchAttribute attr[1] = {after_previous()};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(ceil_div(N, 256)), unsigned(slices));
-  cfg.blockDim = dim3(32, kSumRows);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, column_sums_kernel, static_cast<const __nv_bfloat16*>(dz), int(M), N, per, part) !=
-      cudaSuccess)
-    return SDM_ECUDA;
-  cfg.gridDim = dim3(unsigned(ceil_div(N, 256)));
-  cfg.blockDim = dim3(256);
-  if (cudaLaunchKernelEx(&cfg, join_sums_kernel, static_cast<const float*>(part), slices, N,
+  if (!rows) {
+    rows = dy_sum_rows(M);
+    cfg.gridDim = dim3(unsigned(ceil_div(N, 256)), unsigned(rows));
+    cfg.blockDim = dim3(32, kSumRows);
+    if (rows > 65535) return SDM_EUNSUPPORTED;
+    if (cudaLaunchKernelEx(&cfg, column_sums_kernel, static_cast<const __nv_bfloat16*>(dz), int(M), N, part) != cudaSuccess)
+      return SDM_ECUDA;
+  }
+  cfg.gridDim = dim3(unsigned(ceil_div(N, 32)));
+  cfg.blockDim = dim3(32, 32);
+  if (cudaLaunchKernelEx(&cfg, join_sums_kernel, static_cast<const float*>(part), rows, N,
                          static_cast<__nv_bfloat16*>(out)) != cudaSuccess)
     return SDM_ECUDA;
   return last_launch_status();
@@ -272,7 +292,7 @@ struct GradSpace {
     Product p[2];
     plan_grads(int(M), D, N, p);
     grads = partial_bytes(p[0]) + partial_bytes(p[1]);
-    bias = round256(size_t(sum_slices(M, N)) * N * 4);
+    bias = round256(size_t(act == SDM_ACT_NONE ? dy_sum_rows(M) : slope_sum_rows(M)) * N * 4);
   }
   size_t total() const { return dz + slope + grads + bias; }
 };
@@ -306,7 +326,7 @@ extern "C" int sdm_project(const void* x, const void* w, const void* bias, const
     if (act == SDM_ACT_GELU) return launch_few_act<SDM_ACT_GELU>(x, w, bias, residual, int(M), D, N, y, s);
     return launch_few_act<SDM_ACT_NONE>(x, w, bias, residual, int(M), D, N, y, s);
   }
-  return launch_dense<kDense>(x, w, bias, residual, int(M), D, N, act, y, workspace, dev_err, s);
+  return launch_dense<kDense>(x, w, bias, residual, int(M), D, N, act, y, workspace, nullptr, dev_err, s);
 }
 
 extern "C" size_t sdm_project_backward_workspace_size(long long M, int D, int N, int act) {
@@ -340,13 +360,16 @@ extern "C" int sdm_project_backward(const void* x, const void* w, const void* bi
   if (meets(dense(x, xn), dx, xn) || meets(dense(dy, yn), dx, xn)) return SDM_EOVERLAP;
   uint8_t* at = static_cast<uint8_t*>(workspace);
   const __nv_bfloat16* dz = static_cast<const __nv_bfloat16*>(dy);
+  uint8_t* grads = at + space.dz + space.slope;
+  float* sums = reinterpret_cast<float*>(grads + space.grads);
+  int rows = 0;
   if (act != SDM_ACT_NONE) {
-    st = launch_dense<kDenseSlope>(x, w, bias, dy, int(M), D, N, act, at, at + space.dz, dev_err, s);
+    st = launch_dense<kDenseSlope>(x, w, bias, dy, int(M), D, N, act, at, at + space.dz, dbias ? sums : nullptr, dev_err, s);
     if (st != SDM_OK) return st;
     dz = reinterpret_cast<const __nv_bfloat16*>(at);
+    if (!space.slope) rows = slope_sum_rows(M);  // a product that is joined leaves none
   }
-  at += space.dz + space.slope;
-  st = launch_grads(dz, x, w, int(M), D, N, dx, dw, at, dev_err, s);
+  st = launch_grads(dz, x, w, int(M), D, N, dx, dw, grads, dev_err, s);
   if (st != SDM_OK || !dbias) return st;
-  return launch_column_sums(dz, M, N, reinterpret_cast<float*>(at + space.grads), dbias, s);
+  return launch_column_sums(dz, M, N, sums, rows, dbias, s);
 }

@@ -46,13 +46,14 @@ struct Layout {
   static constexpr int bytes = off_bars + 512 + 1024 /* alignment slack */;
 };
 constexpr uint32_t kColumns = 512;
-constexpr int kRowGroup = 32;                    // row tiles of a group of the tile order
+constexpr int kRowGroup = 32;                    // row tiles of a group of the tile order, where nothing else is said
 
 // One product: its output [rows, cols], its tiles, and the cut of its reduction (K steps of 64).
 struct Product {
   int rows, cols;
   int row_tiles, col_tiles, splits;
   int kblocks, per_split;
+  int group;               // row tiles of a group of the tile order
   bool a_mn;               // kGrads: A read MN-major (dw)
   __nv_bfloat16* out;      // kGrads: dx or dw
   float* partial;          // [splits][rows][cols] where splits > 1
@@ -63,6 +64,7 @@ struct ProductArgs {
   int act;
   const __nv_bfloat16* bias;   // kDense, kDenseSlope: or null
   const __nv_bfloat16* extra;  // kDense: the residual or null; kDenseSlope: dy
+  float* sums;                 // kDenseSlope: [rows / 32][cols], dz summed over 32 rows each, or null
   int* dev_err;
 };
 
@@ -128,7 +130,7 @@ __device__ __forceinline__ void gate_slope(float g, float& a, float& s) {
   }
 }
 
-// Work unit -> product, row tile, column tile, split: groups of kRowGroup row tiles, row tiles
+// Work unit -> product, row tile, column tile, split: groups of row tiles, row tiles
 // fastest, so that units running at once share a few rows of A and a few column tiles of B in L2.
 struct Unit {
   int which, row, col, k_lo, k_hi, split;
@@ -145,10 +147,10 @@ __device__ __forceinline__ Unit unit_at(int u, const ProductArgs& a) {
   const int tiles = p.row_tiles * p.col_tiles;
   r.split = u / tiles;
   u -= r.split * tiles;
-  const int g = u / (kRowGroup * p.col_tiles), w = u - g * kRowGroup * p.col_tiles;
-  const int gm = min(kRowGroup, p.row_tiles - g * kRowGroup);
+  const int g = u / (p.group * p.col_tiles), w = u - g * p.group * p.col_tiles;
+  const int gm = min(p.group, p.row_tiles - g * p.group);
   r.col = w / gm;
-  r.row = g * kRowGroup + (w - r.col * gm);
+  r.row = g * p.group + (w - r.col * gm);
   r.k_lo = r.split * p.per_split;
   r.k_hi = min(p.kblocks, r.k_lo + p.per_split);
   return r;
@@ -262,6 +264,19 @@ __device__ __forceinline__ void dense_patch(uint32_t taddr, uint32_t patch, int 
                                              has_extra ? patch_load(at) : make_uint4(0, 0, 0, 0)));
     }
   }
+}
+
+// Sums over a patch's rows, two columns a lane; rows past the matrix are 0 (dy is).
+__device__ __forceinline__ void dense_sums(uint32_t patch, int lane, float* out, int cols) {
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r) {
+    uint32_t w;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(patch + patch_at(r, lane / 4) + uint32_t(lane % 4 * 4)));
+    s0 += __uint_as_float(w << 16);
+    s1 += __uint_as_float(w & 0xFFFF0000u);
+  }
+  if (2 * lane < cols) *reinterpret_cast<float2*>(out + 2 * lane) = make_float2(s0, s1);
 }
 
 // Sums of a warp's 32 rows x 128 columns, straight to memory: dx or dw, or partial sums.
@@ -494,6 +509,12 @@ __global__ void __launch_bounds__(kRoles, 1)
             dense_patch<MODE, KIND>(from + 64, patch + kPatch, lane, bias ? bias + 64 : nullptr, loads,
                                     a.p[0].cols - f0 - 64);
           fence_async_proxy();
+          if (MODE == kDenseSlope && a.sums) {
+            __syncwarp();
+            dense_sums(patch, lane, a.sums + size_t(m0 / 32) * a.p[0].cols + f0, a.p[0].cols - f0);
+            if (inside2)
+              dense_sums(patch + kPatch, lane, a.sums + size_t(m0 / 32) * a.p[0].cols + f0 + 64, a.p[0].cols - f0 - 64);
+          }
         } else if (!whole) {
           store_sums(a.p[0], un, m0 + lane, f0, taddr + uint32_t(half * kHalf));
         }
@@ -623,6 +644,7 @@ Product product(int rows, int cols, int tile_cols, long long reduction) {
   p.col_tiles = ceil_div(cols, tile_cols);
   p.kblocks = p.per_split = ceil_div(reduction, kTileK);
   p.splits = 1;
+  p.group = kRowGroup;
   return p;
 }
 
