@@ -57,7 +57,9 @@ int teams_for(int n) {
 }
 int slots_for(long long M, int D, int groups, int kind) {
   const int n = D / groups;
-  const int teams = kind == kStream ? teams_for<kStream>(n) : kind == kInner ? teams_for<kInner>(n) : teams_for<kAll>(n);
+  const int teams = kind == kStream  ? teams_for<kStream>(n)
+                    : kind == kInner ? teams_for<kInner>(n)
+                                     : teams_for<kAll>(n);
   const long long s = teams / groups < 1 ? 1 : teams / groups;
   return int(s < M ? s : M);
 }

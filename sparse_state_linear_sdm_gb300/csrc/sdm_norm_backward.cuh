@@ -31,7 +31,7 @@ struct NormBackward {
 // What of the gradient an instance knows how to do: all of it, or only the norm of the stream (dy, r, dr to
 // dresidual or dx), or only the norm of x and the gate.  The smaller ones need fewer registers.
 enum NormKind { kAll = 0, kStream = 1, kInner = 2 };
-constexpr int sm_threads(int kind, int pieces) { return pieces > 1 || kind == kAll ? 512 : kind == kInner ? 768 : 1024; }  // threads of an SM that the registers allow
+constexpr int sm_threads(int kind, int pieces) { return pieces > 1 || kind == kAll ? 512 : 768; }  // of an SM, by registers
 
 template <typename TX, typename TR>
 int launch_norm_backward(const NormBackward& a, int kind, bool vec, cudaStream_t s);
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_bl
     }
     if (a.dr) rdr.ask(pdr, t, cols), pdr += a.slots * a.dr_rs;
   };
-  constexpr bool kAhead = KIND != kAll || P == 1;  // otherwise it takes more registers than it gains
+  constexpr bool kAhead = P == 1 || (P == 2 && KIND != kAll);  // otherwise it takes more registers than it gains
   if (kAhead) ask(0);
   const long long at = used ? off : 0;
   const int mine = used ? n : 0;
@@ -200,12 +200,24 @@ __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_bl
 #pragma unroll
       for (int e = 0; e < E; ++e) x[e] *= j;  // the norm before its weight
     }
+    float s[E];  // act(gate); z becomes its slope
+    if (gate && io.act == SDM_ACT_SILU) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float p = sigmoid(z[e]);
+        s[e] = z[e] * p;
+        z[e] = fmaf(s[e], 1.f - p, p);
+      }
+    } else if (gate) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[e] = z[e], z[e] = 1.f;
+    }
     if (scale) {
       float o[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         o[e] = after ? x[e] * w[e] : x[e];
-        if (gate) o[e] *= io.act == SDM_ACT_SILU ? silu(z[e]) : z[e];
+        if (gate) o[e] *= s[e];
       }
       sum_scale.add(d, o);
       weights(kScale, io.scale, o);
@@ -213,21 +225,12 @@ __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_bl
       for (int e = 0; e < E; ++e) d[e] *= o[e];
     }
     if (gate) {
-      float dz[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) dz[e] = after ? d[e] * (x[e] * w[e]) : d[e] * x[e];
-      if (io.act == SDM_ACT_SILU) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float p = sigmoid(z[e]), s = z[e] * p;
-          dz[e] *= fmaf(s, 1.f - p, p);
-          d[e] *= s;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) d[e] *= z[e];
+      for (int e = 0; e < E; ++e) {
+        z[e] *= after ? d[e] * (x[e] * w[e]) : d[e] * x[e];
+        d[e] *= s[e];
       }
-      if (a.dgate) R::store(dgate, t, cols, dz), dgate += step;
+      if (a.dgate) R::store(dgate, t, cols, z), dgate += step;
     }
     if (after) {
       float g[1] = {0.f};
