@@ -474,6 +474,8 @@ PyObject* norm(PyObject* const* a) {
   m.s.residual = strided_rows(c, residual, "residual", m.r_type, x.sizes(), &m.s.residual_rs);
   const bool moves = residual.defined() || after.defined() || gate.defined() || scale.defined();
   if (!moves && !weight.defined()) raise(PyExc_ValueError, "nothing to compute: no weight, after, gate, scale or residual");
+  if (!weight.defined() && a[6] != Py_None) raise(PyExc_ValueError, "out is y's memory, which needs a weight");
+  if (!moves && a[7] != Py_None) raise(PyExc_ValueError, "residual_out has no use: r is x itself");
   Held y, r;
   void *py = nullptr, *pr = nullptr;
   if (weight.defined()) py = output(c, a[6], "out", x.sizes(), m.x_type, &y.o);

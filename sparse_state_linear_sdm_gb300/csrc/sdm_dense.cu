@@ -5,6 +5,10 @@
 //
 // Sums are fp32 and y is rounded once.  dz is rounded to bf16 between the products (as the gated projections' dg and
 // du: the tensor cores take nothing wider at that rate), and dbias sums the rounded values; without an activation dz is dy itself.
+//
+// 16,384 tokens of 8192 x 2048 with a residual: 350 us, 1,570 TFLOP/s (0.82 of cuBLAS's burst, 0.92 of its sustained
+// rate).  The gradient of 1000 tokens of 1024 x 2736 with gelu: 39 us, its slope pass 44 tiles on 76 pairs.  4 tokens of
+// 8192 x 2048: 11.4 (0.44 of the HBM floor), of which a launch is 4 to 5.
 #include "sdm_product.cuh"
 
 namespace sdm {
@@ -144,11 +148,11 @@ Product plan_dense(int M, int D, int N) {
   // of 4, 111 of 16), with a long one the rows of x that are read again (8192 x 2048: 330 us and 303, 320 of 32).
   Product p = product(M, N, 2 * kHalf, D);
   p.group = D <= 2048 ? 4 : 16;
+  if ((long long)p.row_tiles * p.col_tiles >= 2 * kPairs) return p;
   Product best = p;
   const Product none = {};
   double least = -1;
-  const int most = (long long)p.row_tiles * p.col_tiles < 2 * kPairs ? 32 : 1;
-  for (int i = 1; i <= most; ++i) {
+  for (int i = 1; i <= 32; ++i) {
     cut(p, i);
     const double t = busiest(p, none) + joining(p);
     if (least < 0 || t < least) {

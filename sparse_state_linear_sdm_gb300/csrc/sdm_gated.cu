@@ -4,10 +4,10 @@
 //   dg = dh * u * act'(g),  du = dh * act(g)
 //   dx = dg Wg + du Wu = [dg | du] w,   dw = [dg | du]^T x
 //
-// Sums are fp32; dg and du are the only rounding between
-// inputs and outputs: the tensor cores take them at full rate as bf16, like x and w beside them, and
-// at half of it or less, with twice the bytes to hold and read, in anything wider.  Each is half a unit of
-// bf16 off, so dx and dw are 0.0023 of their norm off where their own rounding alone makes 0.0017.
+// Sums are fp32; dg and du are the only rounding between inputs and outputs: the tensor cores take them
+// at full rate as bf16, like x and w beside them, and at half of it or less, with twice the bytes to hold
+// and read, in anything wider.  Each is half a unit of bf16 off, so dx and dw are 0.0023 of their norm off
+// where their own rounding alone makes 0.0017.
 //
 // The tensor pipe bounds the large cases, and the card's power: 16,384 tokens of 2048 x 8192 take
 // 0.62 to 0.64 ms back to back (1,720 to 1,780 TFLOP/s), the gradient of 32,768 tokens 4.17 to 4.27 ms

@@ -1,5 +1,5 @@
-// Element access and elementwise functions shared by the convolution, the state space scan
-// and the gated projections (sdm_conv.cu, sdm_ssm.cu, sdm_gated.cu).
+// Element access and elementwise functions shared by the layers beside the memory: convolution, scan, linear attention,
+// norms and projections.
 #pragma once
 
 #include <cuda_bf16.h>

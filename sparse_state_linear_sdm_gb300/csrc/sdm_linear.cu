@@ -4,8 +4,12 @@
 //
 // Three forms.  A single token streams the states through once (token_kernel; HBM bounds it).  Prompts
 // take their tokens one after the other with the state in registers (step_kernel: any type, alignment
-// and size; two multiply-adds a state and token bound it), or, in bf16 with up to 128 columns, in chunks
-// of 128 tokens on the tensor cores (sdm_linear_tiles.cu).
+// and size), or, in bf16 with dk up to 128, in chunks of 128 tokens on the tensor cores (sdm_linear_tiles.cu; rows that
+// TMA cannot take are copied first where dk or dv is at fault, and taken one by one where only strides are).
+//
+// One token of 256 sequences, 16 heads of 128 x 128 in slots: 83 us, 0.96 of the HBM floor.  step_kernel is bound by its two
+// multiply-adds a state and token, which one block an SM leaves at half of their rate (8 x 2048 x 16 heads of 128 in fp32:
+// 690 us, floor 230; two tokens at a time 727).
 //
 // Where sequences and heads leave the card short, a sequence is cut into segments: every segment but the last
 // is reduced to its end state from zero and its sum of g, a small kernel turns those into the state in front of each
@@ -21,7 +25,7 @@ constexpr int kCols = 4;         // and columns
 constexpr int kStepWarps = 8;    // of a block, at most
 
 // A warp holds a DK x cols piece of a state: R lanes share the rows, 32 / R groups of lanes have four columns each.  (With
-// eight, a head of 128 x 128 is four warps, one for each scheduler of an SM: 1.3 times the time.)
+// eight, a head of 128 x 128 is four warps, one for each scheduler of an SM: 779 us instead of 690.)
 template <int DK>
 struct Warp {
   static constexpr int R = DK / kRows;
@@ -539,7 +543,8 @@ bool sizes_ok(int dtype, int B, int T, int H, int dk, int dv) {
 }
 
 // How a sequence is cut for step_kernel: a warp's piece of a state is a unit of work, and the card runs 16 of them an
-// SM; twice the work pays from some three segments on.
+// SM; twice the work pays from some three segments on (4 heads of 64 x 64 in fp32: 95 tokens whole 31 us, 96 in
+// three segments 28; 2048 tokens of 100 heads of 128 x 128 in three 607, 128 heads whole 668).
 void cut_steps(int B, int T, int H, int dk, int dv, int* segments, int* segment) {
   const int DK = dk <= 32 ? 32 : dk <= 64 ? 64 : dk <= 128 ? 128 : 256, cols = 32 / (DK / kRows) * kCols;
   const long long units = (long long)B * H * ((dv + cols - 1) / cols);
@@ -550,8 +555,6 @@ void cut_steps(int B, int T, int H, int dk, int dv, int* segments, int* segment)
   *segment = n > 1 ? int(per) : T;
   *segments = n > 1 ? int((T + per - 1) / per) : 1;
 }
-
-constexpr int kTileTokens = 32;  // tokens of a prompt from which on chunks pay
 
 // What of the output, the new states and the workspace overlaps anything else of the call.
 bool overlap(const sdm_linear_args& io, const void* workspace, size_t workspace_bytes) {
@@ -593,13 +596,20 @@ using namespace sdm;
 // What of the workspace a call with these sizes may need: the segments' states and sums of g, then copies of rows that
 // are not multiples of 16 bytes.  Which form is taken, strides and addresses decide too.
 namespace {
-bool tile_sizes(int dtype, int T, int dk) { return dtype == SDM_BF16 && T >= kTileTokens && dk <= SDM_LINEAR_TILE_D; }
+
+// From 32 tokens on chunks pay: 1024 heads of 128 x 128 take 66 us for 31 tokens one by one and 51 for 32 as a chunk,
+// 128 heads 16 and 12.  Small heads that fill the card several times want 64: 1024 heads of 64 x 64 take 25 us for 31
+// tokens one by one, 47 as a chunk.
+bool tile_sizes(int dtype, int B, int T, int H, int dk, int dv) {
+  const int least = dk * dv <= 64 * 64 && (long long)B * H > 4 * 152 ? 64 : 32;
+  return dtype == SDM_BF16 && T >= least && dk <= SDM_LINEAR_TILE_D;
+}
 struct LinearSpace {
   size_t states = 0, pad = 0;
   LinearSpace(int dtype, int B, int T, int H, int Hk, int dk, int dv) {
     int segments, segment;
     cut_steps(B, T, H, dk, dv, &segments, &segment);
-    if (tile_sizes(dtype, T, dk)) {
+    if (tile_sizes(dtype, B, T, H, dk, dv)) {
       int n;
       cut_tiles(B, T, H, dv, &n, &segment);
       segments = n > segments ? n : segments;
@@ -654,7 +664,7 @@ extern "C" int sdm_linear_attention(const sdm_linear_args* args, void* workspace
   const size_t need = space.states + space.pad;
   const bool rows_fit = a.vec_qk && a.vec_v && a.vec_o && steps_on(io.q_bs, io.q_ts) && steps_on(io.k_bs, io.k_ts) &&
                         steps_on(io.v_bs, io.v_ts);
-  const bool tiles = tile_sizes(io.dtype, io.T, io.dk) && (rows_fit || space.pad);
+  const bool tiles = tile_sizes(io.dtype, io.B, io.T, io.H, io.dk, io.dv) && (rows_fit || space.pad);
   if (tiles)
     cut_tiles(io.B, io.T, io.H, io.dv, &a.segments, &a.segment);
   else

@@ -1,4 +1,4 @@
-// Linear attention over prompts in chunks of 128 tokens on the tcgen05 tensor cores (bf16, up to 128 columns).
+// Linear attention over prompts in chunks of 128 tokens on the tcgen05 tensor cores (bf16, dk up to 128, dv up to 256).
 //
 // With A_ij the product of the decays of tokens j+1 .. i of a chunk, S the state in front of it and G the products from its start:
 //
@@ -6,11 +6,16 @@
 //   S'  = G_last S + sum_j k_j (A_last,j v_j)^T
 //
 // Four products a chunk: q k^T, q S, (A q k^T) v and (A v)^T k, the last one the state transposed.  A CTA takes a
-// sequence's head, its state in registers (fp32, 64 a thread), and walks its chunks.  Warps by role: TMA and
-// decays; MMAs; eight that turn q k^T into the masked bf16 products, scale q S by G and write o; eight that weight
-// v and update the state.  k, q and v of two chunks have a slot of 32 KB each.
-// An MMA of 128 x 128 x 16 whose operands both lie in shared memory waits for them (64 bytes a clock: 128 clocks instead
-// of 64), so the masked products and the weighted v are first operands out of TMEM.
+// sequence's head, its state in registers (fp32, 64 a thread), and walks its chunks.  Warps by role: TMA; the MMAs of
+// o; those of the state; decays; eight that turn q k^T into the masked bf16 products, scale q S by G and write o; eight
+// that update the state; the two eights share the weighting of v.  k, q and v of two chunks have a slot of 32 KB
+// each.  An MMA of 128 x 128 x 16 whose operands both lie in shared memory waits for them (64 bytes a clock: 128
+// clocks instead of 64), so the masked products and the weighted v are first operands out of TMEM.
+//
+// HBM would bound it (128 KB a chunk: 8 prompts of 4096 x 16 heads of 128 in 81 us), the work between the products does:
+// 145 us there, 4.5 us a chunk and SM, 36 % of the issue slots, the tensor pipe at 30 %, a third of the stalls instruction
+// fetches of five roles' code.  One prompt of 32,768 x 8 heads, in 19 segments: 126 us, 45 of them for the segments'
+// ends and 76 for the outputs.  182 and 150 with every operand in shared memory and one group for v and the state.
 //
 // What is rounded to bf16: the masked products and the state as q reads it, as an MMA takes them (each half a unit, as o
 // itself).  The state is not: A v is cut into three bf16 parts whose products are summed in fp32 (two parts
@@ -634,10 +639,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // No token here: o is 0.
   if (PASS != kReduce) {
     const int t0 = p.t_lo + chunks * kChunk, pieces = min(kTileColumns, a.o_dv - v0) / 8;
-    for (long long i = threadIdx.x; i < (long long)(p.t_hi - t0) * pieces; i += kTileThreads)
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(io.o) +
-                                (((long long)p.b * io.T + t0 + i / pieces) * io.H + p.h) * a.o_dv + v0 + i % pieces * 8) =
-          make_uint4(0, 0, 0, 0);
+    __nv_bfloat16* row = static_cast<__nv_bfloat16*>(io.o) + ((long long)p.b * io.T * io.H + p.h) * a.o_dv + v0 + lane * 8;
+    if (lane < pieces)
+      for (int t = t0 + warp; t < p.t_hi; t += kTileThreads / 32)
+        *reinterpret_cast<uint4*>(row + (long long)t * io.H * a.o_dv) = make_uint4(0, 0, 0, 0);
   }
 
   if (warp == 1 || warp == 2) {
@@ -763,14 +768,16 @@ __global__ void __launch_bounds__(kPadThreads) narrow_kernel(const __nv_bfloat16
   }
 }
 
-// A CTA of the tile kernel fills an SM and takes a chunk in about the time of 64 to 128 KB of HBM traffic of its share, so
-// 152 of them are what the card runs at once.
+// A CTA of the tile kernel fills an SM, so 152 of them are what the card runs at once.  A chunk takes one 4.1 us, and 7 over
+// both passes where the sequence is cut, with about 15 us for two more launches and starts.  (50 heads of 4096 tokens in 3
+// segments 116 us and 137 whole, of 1024 tokens 52 and 43; 8 heads of 1024 tokens in 4 segments 32 and 39.  Two
+// segments gain nothing: 64 heads of 4096 tokens 148 us and 139 whole.)
 void cut_tiles(int B, int T, int H, int dv, int* segments, int* segment) {
-  const long long units = (long long)B * H * ((dv + kTileColumns - 1) / kTileColumns), chunks = (T + kChunk - 1) / kChunk;
-  long long n = units * 2 > 152 ? 1 : 152 / units;
+  const long long units = (long long)B * H * ((dv + kTileColumns - 1) / kTileColumns), chunks = ((long long)T + kChunk - 1) / kChunk;
+  long long n = 152 / units;
   n = n < chunks / 2 ? n : chunks / 2;
-  if (n < 3) n = 1;
-  const long long per = (chunks + n - 1) / n;
+  long long per = n > 1 ? (chunks + n - 1) / n : chunks;
+  if (n < 3 || 70 * per + 150 > 41 * chunks) n = 1, per = chunks;
   *segments = n > 1 ? int((chunks + per - 1) / per) : 1;
   *segment = n > 1 ? int(per * kChunk) : T;
 }

@@ -7,7 +7,8 @@
 // any part of which may be absent.  HBM bounds it: a row is read once into registers, and both sums over it are taken there in
 // fp32 (a norm by itself, a gate and a residual addition would each read and write it again).  A row has 8 to 1024 threads
 // of eight channels; a block of 128 threads has several short rows.  Blocks stay and take rows in turn, the next one on its way
-// while one is worked on.
+// while one is worked on.  16,384 rows of 2048 with both norms, scale and an fp32 stream: 66 us, 0.90
+// of the HBM floor; 16,384 x 16 groups of 128 with a gate 37.5 (0.79).  4 rows: 5.9, a launch.
 #include "sdm_norm.cuh"
 
 namespace sdm {

@@ -9,6 +9,11 @@
 // read anyway.  HBM bounds it.  A row is in registers as in the forward pass.  Blocks stay and take rows in turn, so that the sums
 // over rows run in registers as well; each team of threads keeps to one group of channels, writes its sums once, and
 // a second kernel adds the teams' in a fixed order: results do not depend on timing.
+//
+// 16,384 x 16 groups of 128 with a gate: 80 us, 0.61 of the HBM floor, at 53 % of the issue slots and 24 warps an SM;
+// the stream alone, 16,384 x 2048, 70 (0.57).  Rows off 16 bytes are read element by element: everything of 4099 x 1537,
+// bf16 with an fp32 stream, takes 55 (0.37).  Beyond 4096 channels the sums live in shared memory (4096 x 8192
+// with everything 209 us, 282 in registers that spilled).
 #pragma once
 
 #include <type_traits>

@@ -1,5 +1,5 @@
 // Bounded mbarrier waits, TMA copies, tcgen05 descriptors and TMEM access, as the tensor-core
-// kernels use them (sdm_project.cu, sdm_gated.cu).
+// kernels use them (sdm_project.cu, sdm_product.cuh, sdm_linear_tiles.cu).
 #pragma once
 
 #include "sdm_internal.cuh"

@@ -389,3 +389,22 @@ def test_offsets_past_32_bits():
     o2, st2 = sdm.linear_attention(q, odd, v, decay, state_out=torch.empty_like(st), out=o)
     assert torch.allclose(o2[:, n + 5:].float(), tail[:, 5:].float(), rtol=2.0 ** -6, atol=2.0 ** -6)
     assert torch.allclose(st2, ts, rtol=1e-4, atol=1e-5)
+
+
+@pytest.mark.parametrize("c", [
+    ("bf16", 1, 1500, 2, 1, 100, 36, "token", True, (1400,), 3, "wide"),    # copied rows, cut into segments
+    ("bf16", 3, 1290, 2, 2, 64, 128, "token", True, (1290, 1, 700), 0, "wide"),
+    ("bf16", 1, 1152, 3, 3, 128, 64, "head", False, None, 0, "dense"),
+    ("bf16", 160, 40, 4, 4, 32, 16, "token", True, None, 0, "wide"),        # many small heads: one by one below 64
+    ("bf16", 160, 64, 4, 4, 32, 16, "token", True, None, 0, "wide"),        # and a chunk from 64 on
+], ids=lambda c: f"{c[1]}x{c[2]}-H{c[3]}-{c[5]}x{c[6]}")
+def test_linear_where_its_form_changes(c):
+    a = _case(c, seed=11)
+    want, wstate, eo, es = _ref(a)
+    kept = torch.full(wstate.shape, 7.0, device="cuda")
+    o, _ = sdm.linear_attention(**a, state_out=kept)
+    live, _ = _live(a)
+    _check(o, want, eo, "bf16", "o")
+    _check_norm(o, want, "bf16", "o")
+    _check(kept[live], wstate[live], es[live], "f32", "state")
+    _check_norm(kept[live], wstate[live], "f32", "state")

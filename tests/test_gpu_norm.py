@@ -282,3 +282,11 @@ def test_norm_past_32_bit_offsets():
     assert torch.equal(y[M - 300:], sdm.residual_norm(x[M - 300:], weight=w)[0])
     dx = sdm.gated_norm_backward(x, w, y)[0]
     assert torch.equal(dx[M - 300:], sdm.gated_norm_backward(x[M - 300:], w, y[M - 300:])[0])
+
+
+def test_memory_for_an_output_that_there_is_not():
+    x, w = torch.randn(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    with pytest.raises(ValueError):
+        sdm.residual_norm(x, weight=w, residual_out=torch.empty_like(x))
+    with pytest.raises(ValueError):
+        sdm.residual_norm(x, x.clone(), out=torch.empty_like(x))
