@@ -206,12 +206,14 @@ int launch_dense(const void* x, const void* w, const void* bias, const void* ext
 // dz is dy, and they are taken from there: eight columns a thread and eight lanes of tokens a block.
 constexpr int kSumRows = 8;
 constexpr int kSumSlice = 256;  // tokens of a block
-__global__ void __launch_bounds__(32 * kSumRows) column_sums_kernel(const __nv_bfloat16* dz, int M, int N, float* part) {
+__global__ void __launch_bounds__(32 * kSumRows) column_sums_kernel(const __nv_bfloat16* dz, int M, int N, int tiles,
+                                                                    float* part) {
   __shared__ float sums[kSumRows][32][9];
   wait_previous();
   allow_next();
-  const int col = blockIdx.x * 256 + int(threadIdx.x) * 8;
-  const int m0 = int(blockIdx.y) * kSumSlice, m_end = min(M - m0, kSumSlice);
+  const int tile = int(blockIdx.x % unsigned(tiles)), slice = int(blockIdx.x / unsigned(tiles));
+  const int col = tile * 256 + int(threadIdx.x) * 8;
+  const int m0 = slice * kSumSlice, m_end = min(M - m0, kSumSlice);
   float s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i] = 0.f;
@@ -228,12 +230,12 @@ __global__ void __launch_bounds__(32 * kSumRows) column_sums_kernel(const __nv_b
 #pragma unroll
   for (int i = 0; i < 8; ++i) sums[threadIdx.y][threadIdx.x][i] = s[i];
   __syncthreads();
-  const int id = int(threadIdx.y) * 32 + int(threadIdx.x), c = int(blockIdx.x) * 256 + id;
+  const int id = int(threadIdx.y) * 32 + int(threadIdx.x), c = tile * 256 + id;
   if (c >= N) return;
   float t = 0.f;
 #pragma unroll
   for (int i = 0; i < kSumRows; ++i) t += sums[i][id / 8][id % 8];
-  part[size_t(blockIdx.y) * N + c] = t;
+  part[size_t(slice) * N + c] = t;
 }
 // The rows' sums: 32 columns and 32 lanes of rows a block, each lane's in their order and then the lanes' in theirs.
 __global__ void __launch_bounds__(1024) join_sums_kernel(const float* part, int rows, int N, __nv_bfloat16* out) {
@@ -266,10 +268,11 @@ int launch_column_sums(const void* dz, long long M, int N, float* part, int rows
   cfg.numAttrs = 1;
   if (!rows) {
     rows = dy_sum_rows(M);
-    cfg.gridDim = dim3(unsigned(ceil_div(N, 256)), unsigned(rows));
+    const int tiles = ceil_div(N, 256);  // slices * tiles: a block has 64 K of dz's elements, which fit on the card
+    cfg.gridDim = dim3(unsigned(rows) * unsigned(tiles));
     cfg.blockDim = dim3(32, kSumRows);
-    if (rows > 65535) return SDM_EUNSUPPORTED;
-    if (cudaLaunchKernelEx(&cfg, column_sums_kernel, static_cast<const __nv_bfloat16*>(dz), int(M), N, part) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, column_sums_kernel, static_cast<const __nv_bfloat16*>(dz), int(M), N, tiles, part) !=
+        cudaSuccess)
       return SDM_ECUDA;
   }
   cfg.gridDim = dim3(unsigned(ceil_div(N, 32)));

@@ -408,3 +408,11 @@ def test_linear_where_its_form_changes(c):
     _check_norm(o, want, "bf16", "o")
     _check(kept[live], wstate[live], es[live], "f32", "state")
     _check_norm(kept[live], wstate[live], "f32", "state")
+
+
+@pytest.mark.parametrize("dtype, T, dk", [("f32", 20, 64), ("f32", 500, 64), ("bf16", 100, 64), ("bf16", 1500, 128)])
+def test_a_sequence_without_tokens_keeps_its_state_bit_for_bit(dtype, T, dk):
+    a = _case((dtype, 2, T, 2, 2, dk, 64, "token", True, (T, 0), 0, "wide"))
+    kept = torch.empty_like(a["state"])
+    o, _ = sdm.linear_attention(**a, state_out=kept)
+    assert torch.equal(kept[1], a["state"][1]) and (o[1] == 0).all()

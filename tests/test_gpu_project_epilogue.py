@@ -192,3 +192,15 @@ def test_project_past_32_bit_offsets():
     host = lambda t: t[M - 300:].double().cpu().numpy()  # noqa: E731
     want = ref.project_grad(host(x), w.double().cpu().numpy(), None, host(y), "none")
     _check(dx[M - 300:], want[0], want[3], "dx")
+
+
+def test_bias_gradient_of_many_tokens():
+    """65,537 slices of 256 tokens: sums of ones are exact in fp32, and the total is rounded once."""
+    M = 256 * 65536 + 1
+    x = torch.zeros(M, 8, dtype=torch.bfloat16, device="cuda")
+    x[-1] = 1.0
+    w = torch.eye(8, dtype=torch.bfloat16, device="cuda")
+    dy = torch.ones(M, 8, dtype=torch.bfloat16, device="cuda")
+    dx, dw, dbias = sdm.project_backward(x, w, dy, bias=torch.zeros(8, dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(dbias.float(), torch.full((8,), 2.0 ** 24, device="cuda"))
+    assert torch.equal(dx, dy) and torch.equal(dw, torch.ones_like(dw))
