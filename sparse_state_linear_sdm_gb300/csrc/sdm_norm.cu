@@ -26,6 +26,8 @@ template <typename TX, typename TR, int TPR, int P, bool VEC>
 __global__ void __launch_bounds__(norm_block(TPR), kThreads / norm_block(TPR)) norm_kernel(const __grid_constant__ Forward a) {
   typedef Row<TPR, P, VEC> R;
   constexpr int E = R::E, RPB = norm_block(TPR) / TPR, W = norm_block(TPR) / 32;
+  // Rows on 16 bytes are faster with one way through the loop (16,384 x 2048: 66 us and 68).
+  constexpr bool kBreak = R::kAlone && !VEC;
   __shared__ float part[2][2][W][1];
   __shared__ Kept<R, norm_block(TPR), 3> kept;
   const sdm_norm_args& io = a.io;
@@ -47,7 +49,8 @@ __global__ void __launch_bounds__(norm_block(TPR), kThreads / norm_block(TPR)) n
   TX* y = static_cast<TX*>(a.y) + (a.y ? out : 0);
   TR* r = static_cast<TR*>(a.r) + (a.r ? out : 0);
   auto ask = [&](long long m0) {
-    const int cols = used && m0 + slot < io.M ? n : 0;
+    if (kBreak && m0 + slot >= io.M) return;
+    const int cols = kBreak || (used && m0 + slot < io.M) ? n : 0;
     rx.ask(px, t, cols), px += a.slots * io.x_rs;
     if (io.gate) rz.ask(pz, t, cols), pz += a.slots * io.gate_rs;
     if (io.residual) rs.ask(ps, t, cols), ps += a.slots * io.residual_rs;
@@ -59,7 +62,8 @@ __global__ void __launch_bounds__(norm_block(TPR), kThreads / norm_block(TPR)) n
 
   int turn = 0;
   for (long long m0 = 0; m0 < io.M; m0 += a.slots, turn ^= 1) {
-    const int cols = used && m0 + slot < io.M ? n : 0;
+    if (kBreak && m0 + slot >= io.M) break;
+    const int cols = kBreak || (used && m0 + slot < io.M) ? n : 0;
     float v[E], s[E], z[E], w[E];
     rx.get(v);
     if (io.gate) rz.get(z);

@@ -11,9 +11,9 @@
 // a second kernel adds the teams' in a fixed order: results do not depend on timing.
 //
 // 16,384 x 16 groups of 128 with a gate: 80 us, 0.61 of the HBM floor, at 53 % of the issue slots and 24 warps an SM;
-// the stream alone, 16,384 x 2048, 70 (0.57).  Rows off 16 bytes are read element by element: everything of 4099 x 1537,
+// the stream alone, 16,384 x 2048, 68 (0.58).  Rows off 16 bytes are read element by element: everything of 4099 x 1537,
 // bf16 with an fp32 stream, takes 55 (0.37).  Beyond 4096 channels the sums live in shared memory (4096 x 8192
-// with everything 209 us, 282 in registers that spilled).
+// with everything 207 us, 282 in registers that spilled).
 #pragma once
 
 #include <type_traits>
@@ -93,7 +93,9 @@ constexpr int shared_sums_bytes(int kind, int pieces, int block) {
 template <typename TX, typename TR, int TPR, int P, bool VEC, int KIND>
 __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_block(TPR))
     backward_kernel(const __grid_constant__ NormBackward a) {
-  typedef Row<TPR, P, VEC> R;
+  // Everything of long rows off 16 bytes has no registers left to ask for more at a time (4099 x 1537: 55 us, 64 if it
+  // does), short ones have (32768 x 100: 41 and 35).
+  typedef Row<TPR, P, VEC, KIND != kAll || TPR <= 32> R;
   constexpr int E = R::E, RPB = norm_block(TPR) / TPR, W = norm_block(TPR) / 32;
   constexpr int K = KIND == kAll ? 3 : KIND == kStream ? 2 : 1;  // sums of the first round; the last one is of x
   constexpr int kWeights = KIND == kAll ? 3 : 1;
@@ -127,7 +129,8 @@ __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_bl
   TX* dgate = static_cast<TX*>(a.dgate) + (a.dgate ? out : 0);
   TR* dres = static_cast<TR*>(a.dres) + (a.dres ? out : 0);
   auto ask = [&](long long m0) {
-    const int cols = used && m0 + slot < io.M ? n : 0;
+    if (R::kAlone && m0 + slot >= io.M) return;
+    const int cols = R::kAlone || (used && m0 + slot < io.M) ? n : 0;
     if (after || gate || scale) rx.ask(px, t, cols), px += a.slots * io.x_rs;
     if (gate) rz.ask(pz, t, cols), pz += a.slots * io.gate_rs;
     if (weight) {
@@ -149,7 +152,8 @@ __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_bl
 
   int turn = 0;
   for (long long m0 = 0; m0 < io.M; m0 += a.slots, turn ^= 1) {
-    const bool live = used && m0 + slot < io.M;
+    if (R::kAlone && m0 + slot >= io.M) break;
+    const bool live = R::kAlone || (used && m0 + slot < io.M);
     const int cols = live ? n : 0;
     float x[E], z[E], r[E], d[E], dr[E], w[E];
     if (!kAhead) ask(m0);
