@@ -55,11 +55,8 @@ int teams_for(int n) {
     return 152 * (sm_threads(KIND, pieces) / block) * (block / int(tpr));
   });
 }
-int slots_for(long long M, int D, int groups, int kind) {
-  const int n = D / groups;
-  const int teams = kind == kStream  ? teams_for<kStream>(n)
-                    : kind == kInner ? teams_for<kInner>(n)
-                                     : teams_for<kAll>(n);
+int slots_for(long long M, int D, int groups, int parts) {
+  const int teams = norm_instance(parts, [&](auto kind) { return teams_for<kind>(D / groups); });
   const long long s = teams / groups < 1 ? 1 : teams / groups;
   return int(s < M ? s : M);
 }
@@ -95,8 +92,8 @@ using namespace sdm;
 extern "C" size_t sdm_residual_norm_backward_workspace_size(long long M, int D, int groups) {
   if (M < 1 || D < 1 || groups < 1 || D % groups || D / groups > kNormMax) return 0;
   int most = 0;
-  for (int kind : {kAll, kStream, kInner}) {
-    const int s = slots_for(M, D, groups, kind);
+  for (int parts = 0; parts <= kAny; ++parts) {
+    const int s = slots_for(M, D, groups, parts);
     most = s > most ? s : most;
   }
   return size_t(most) * 3 * D * 4;
@@ -172,11 +169,12 @@ extern "C" int sdm_residual_norm_backward(const sdm_norm_args* args, const sdm_n
                    rows16(g.dy, g.dy_rs) && rows16(g.r, g.r_rs) && rows16(g.dr, g.dr_rs) && !misaligned(g.dx, 15) &&
                    !misaligned(g.dgate, 15) && !misaligned(g.dresidual, 15) && !misaligned(io.after, 15) &&
                    !misaligned(io.scale, 15) && !misaligned(io.weight, 15);
-  const bool inner_only = !g.dy && !io.scale, stream_only = !(io.after || io.gate || io.scale);
-  const int kind = inner_only ? kInner : stream_only ? kStream : kAll;
-  a.slots = slots_for(io.M, io.D, io.groups, kind);
-  const int r = io.x_dtype == SDM_F32   ? launch_norm_backward<float, float>(a, kind, vec, s)
-                : io.r_dtype == SDM_F32 ? launch_norm_backward<__nv_bfloat16, float>(a, kind, vec, s)
-                                        : launch_norm_backward<__nv_bfloat16, __nv_bfloat16>(a, kind, vec, s);
+  const bool gated = io.gate && io.act == SDM_ACT_SILU;
+  const int parts = (g.dy ? kStream : 0) | (io.after ? kAfter : 0) | (gated ? kGate : 0) | (io.scale ? kScale : 0) |
+                    (io.gate && !gated ? kAny : 0);
+  a.slots = slots_for(io.M, io.D, io.groups, parts);
+  const int r = io.x_dtype == SDM_F32   ? launch_norm_backward<float, float>(a, parts, vec, s)
+                : io.r_dtype == SDM_F32 ? launch_norm_backward<__nv_bfloat16, float>(a, parts, vec, s)
+                                        : launch_norm_backward<__nv_bfloat16, __nv_bfloat16>(a, parts, vec, s);
   return r != SDM_OK ? r : launch_sums(a, s);
 }

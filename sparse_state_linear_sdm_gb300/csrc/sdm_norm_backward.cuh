@@ -10,10 +10,9 @@
 // over rows run in registers as well; each team of threads keeps to one group of channels, writes its sums once, and
 // a second kernel adds the teams' in a fixed order: results do not depend on timing.
 //
-// 16,384 x 16 groups of 128 with a gate: 80 us, 0.61 of the HBM floor, at 53 % of the issue slots and 24 warps an SM;
-// the stream alone, 16,384 x 2048, 68 (0.58).  Rows off 16 bytes are read element by element: everything of 4099 x 1537,
-// bf16 with an fp32 stream, takes 55 (0.37).  Beyond 4096 channels the sums live in shared memory (4096 x 8192
-// with everything 207 us, 282 in registers that spilled).
+// 16,384 x 16 groups of 128 with a gate: 61 us, 0.81 of the HBM floor; the stream alone, 16,384 x 2048, 55 (0.72).  Rows
+// off 16 bytes are read element by element: everything of 4099 x 1537, bf16 with an fp32 stream, takes 41 (0.50).
+// Beyond 4096 channels the sums live in shared memory (4096 x 8192 with everything 174 us, 282 in registers that spilled).
 #pragma once
 
 #include <type_traits>
@@ -33,13 +32,30 @@ struct NormBackward {
   int kinds;    // sums wanted
 };
 
-// What of the gradient an instance knows how to do: all of it, or only the norm of the stream (dy, r, dr to
-// dresidual or dx), or only the norm of x and the gate.  The smaller ones need fewer registers.
-enum NormKind { kAll = 0, kStream = 1, kInner = 2 };
-constexpr int sm_threads(int kind, int pieces) { return pieces > 1 || kind == kAll ? 512 : 768; }  // of an SM, by registers
+// What a call has of the gradient: bits, known where an instance is compiled.  Decided at run time, every one of them costs
+// branches and registers: 32,768 x 1000 with all of them takes 169 us so and 97 as its own instance, the norm and gate over
+// heads 82 and 61, the stream alone 68 and 55.  The sets that models use have an instance, the rest kAny.
+enum NormParts { kStream = 1, kAfter = 2, kGate = 4, kScale = 8, kAny = 16 };  // kGate: silu
+constexpr bool norm_has(int kind, int part) { return kind == kAny || (kind & part); }
+constexpr bool norm_small(int kind) { return kind == kStream || kind == kAfter || kind == (kAfter | kGate); }
+constexpr int sm_threads(int kind, int pieces) { return pieces > 1 || !norm_small(kind) ? 512 : 768; }  // of an SM, by registers
+
+// f(kind) of the instance for a set of parts.
+template <typename F>
+auto norm_instance(int parts, F f) {
+  switch (parts) {
+    case kStream: return f(std::integral_constant<int, kStream>());
+    case kAfter: return f(std::integral_constant<int, kAfter>());
+    case kAfter | kGate: return f(std::integral_constant<int, kAfter | kGate>());
+    case kStream | kAfter: return f(std::integral_constant<int, kStream | kAfter>());
+    case kStream | kAfter | kScale: return f(std::integral_constant<int, kStream | kAfter | kScale>());
+    case kStream | kAfter | kGate | kScale: return f(std::integral_constant<int, kStream | kAfter | kGate | kScale>());
+    default: return f(std::integral_constant<int, kAny>());
+  }
+}
 
 template <typename TX, typename TR>
-int launch_norm_backward(const NormBackward& a, int kind, bool vec, cudaStream_t s);
+int launch_norm_backward(const NormBackward& a, int parts, bool vec, cudaStream_t s);
 
 namespace {
 
@@ -85,7 +101,7 @@ struct Sum {
     }
   }
 };
-constexpr bool shared_sums(int kind, int pieces) { return kind == kAll && pieces > 1; }
+constexpr bool shared_sums(int kind, int pieces) { return !norm_small(kind) && pieces > 1; }
 constexpr int shared_sums_bytes(int kind, int pieces, int block) {
   return shared_sums(kind, pieces) ? 3 * 8 * pieces * 4 * block : 0;
 }
@@ -93,12 +109,11 @@ constexpr int shared_sums_bytes(int kind, int pieces, int block) {
 template <typename TX, typename TR, int TPR, int P, bool VEC, int KIND>
 __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_block(TPR))
     backward_kernel(const __grid_constant__ NormBackward a) {
-  // Everything of long rows off 16 bytes has no registers left to ask for more at a time (4099 x 1537: 55 us, 64 if it
-  // does), short ones have (32768 x 100: 41 and 35).
-  typedef Row<TPR, P, VEC, KIND != kAll || TPR <= 32> R;
+  // kAny's long rows have no registers left to ask for more at a time (4099 x 1537: 55 us, 64 if they do).
+  typedef Row<TPR, P, VEC, KIND != kAny || TPR <= 32> R;
   constexpr int E = R::E, RPB = norm_block(TPR) / TPR, W = norm_block(TPR) / 32;
-  constexpr int K = KIND == kAll ? 3 : KIND == kStream ? 2 : 1;  // sums of the first round; the last one is of x
-  constexpr int kWeights = KIND == kAll ? 3 : 1;
+  constexpr int A = norm_has(KIND, kAfter), S = norm_has(KIND, kStream), K = 2 * S + A;  // sums of the first round
+  constexpr int kWeights = A + S + norm_has(KIND, kScale);
   __shared__ float part1[2][W][K], part2[2][W][1];
   __shared__ Kept<R, norm_block(TPR), kWeights> kept;
   const sdm_norm_args& io = a.io;
@@ -108,13 +123,15 @@ __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_bl
   const bool used = slot < unsigned(a.slots);
   const long long off = (long long)group * n;
   const float rn = 1.0f / float(n);
-  const bool weight = KIND != kInner && a.dy, after = KIND != kStream && io.after, gate = KIND != kStream && io.gate,
-             scale = KIND == kAll && io.scale;
+  auto has = [](int part, bool asked) { return KIND == kAny ? asked : (KIND & part) != 0; };
+  const bool weight = has(kStream, a.dy), after = has(kAfter, io.after), gate = has(kGate, io.gate),
+             scale = has(kScale, io.scale), silu_gate = KIND != kAny || io.act == SDM_ACT_SILU;
+  const bool from_r = !weight || a.dr;  // dr comes in
   allow_next();
 
   extern __shared__ float4 sums_at[];
-  typedef Sum<E, norm_block(TPR), shared_sums(KIND, P)> S;
-  S sum_after(sums_at), sum_scale(sums_at + E / 4 * norm_block(TPR)), sum_weight(sums_at + E / 2 * norm_block(TPR));
+  typedef Sum<E, norm_block(TPR), shared_sums(KIND, P)> Sums;
+  Sums sum_after(sums_at), sum_scale(sums_at + E / 4 * norm_block(TPR)), sum_weight(sums_at + E / 2 * norm_block(TPR));
 
   // A row as it lies in memory; the next one is asked for while this one is worked on.
   typename R::template Raw<TX> rx, rz, rdy;
@@ -123,7 +140,7 @@ __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_bl
   const TX* pz = static_cast<const TX*>(io.gate) + (gate ? slot * io.gate_rs + off : 0);
   const TX* pdy = static_cast<const TX*>(a.dy) + (weight ? slot * a.dy_rs + off : 0);
   const TR* pr = static_cast<const TR*>(a.r) + (weight ? slot * a.r_rs + off : 0);
-  const TR* pdr = static_cast<const TR*>(a.dr) + (a.dr ? slot * a.dr_rs + off : 0);
+  const TR* pdr = static_cast<const TR*>(a.dr) + (from_r ? slot * a.dr_rs + off : 0);
   const long long out = slot * (long long)io.D + off, step = a.slots * (long long)io.D;
   TX* dx = static_cast<TX*>(a.dx) + (a.dx ? out : 0);
   TX* dgate = static_cast<TX*>(a.dgate) + (a.dgate ? out : 0);
@@ -137,18 +154,17 @@ __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_bl
       rdy.ask(pdy, t, cols), pdy += a.slots * a.dy_rs;
       rr.ask(pr, t, cols), pr += a.slots * a.r_rs;
     }
-    if (a.dr) rdr.ask(pdr, t, cols), pdr += a.slots * a.dr_rs;
+    if (from_r) rdr.ask(pdr, t, cols), pdr += a.slots * a.dr_rs;
   };
-  constexpr bool kAhead = P == 1 || (P == 2 && KIND != kAll);  // otherwise it takes more registers than it gains
+  constexpr bool kAhead = P == 1 || (P == 2 && norm_small(KIND));  // otherwise it takes more registers than it gains
   if (kAhead) ask(0);
   const long long at = used ? off : 0;
   const int mine = used ? n : 0;
   auto keep = [&](int which, const void* p) { kept.put(which, p, io.w_dtype, at, t, mine); };
   auto weights = [&](int which, const void* p, float (&w)[E]) { kept.get(which, p, io.w_dtype, at, t, mine, w); };
-  constexpr int kAfter = 0, kWeight = KIND == kAll ? 1 : 0, kScale = 2;
-  if (after) keep(kAfter, io.after);
-  if (weight) keep(kWeight, io.weight);
-  if (KIND == kAll && scale) keep(kScale, io.scale);
+  if (after) keep(0, io.after);
+  if (weight) keep(A, io.weight);
+  if (scale) keep(A + S, io.scale);
 
   int turn = 0;
   for (long long m0 = 0; m0 < io.M; m0 += a.slots, turn ^= 1) {
@@ -160,27 +176,27 @@ __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_bl
     if (after || gate || scale) rx.get(x);
     if (gate) rz.get(z);
     if (weight) rdy.get(d), rr.get(r);
-    if (a.dr) rdr.get(dr);
+    if (from_r) rdr.get(dr);
     if (kAhead && m0 + a.slots < io.M) ask(m0 + a.slots);
 
     float q[K] = {};
-    if constexpr (KIND != kInner) if (weight) {
-      weights(kWeight, io.weight, w);
+    if constexpr (S > 0) if (weight) {
+      weights(A, io.weight, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         q[0] = fmaf(r[e], r[e], q[0]);
         q[1] = fmaf(d[e] * w[e], r[e], q[1]);
       }
     }
-    if (after) {
+    if constexpr (A > 0) if (after) {
 #pragma unroll
       for (int e = 0; e < E; ++e) q[K - 1] = fmaf(x[e], x[e], q[K - 1]);
     }
     if (weight || after) row_sums<TPR>(q, part1[turn]);
-    if (KIND == kInner || !weight) {
+    if (!weight) {
 #pragma unroll
       for (int e = 0; e < E; ++e) d[e] = dr[e];
-    } else if constexpr (KIND != kInner) {
+    } else if constexpr (S > 0) {
       const float i = live ? rsqrtf(fmaf(q[0], rn, io.eps)) : 0.f, c = i * (q[1] * rn);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -189,7 +205,7 @@ __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_bl
       sum_weight.add(d, r);
 #pragma unroll
       for (int e = 0; e < E; ++e) d[e] = i * fmaf(d[e], w[e], -(r[e] * c));
-      if (a.dr) {
+      if (from_r) {
 #pragma unroll
         for (int e = 0; e < E; ++e) d[e] += dr[e];
       }
@@ -203,14 +219,14 @@ __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_bl
     float j = 1.f;
     if (after) {
       j = live ? rsqrtf(fmaf(q[K - 1], rn, io.eps)) : 0.f;
-      weights(kAfter, io.after, w);
+      weights(0, io.after, w);
     }
     if (after) {
 #pragma unroll
       for (int e = 0; e < E; ++e) x[e] *= j;  // the norm before its weight
     }
     float s[E];  // act(gate); z becomes its slope
-    if (gate && io.act == SDM_ACT_SILU) {
+    if (gate && silu_gate) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float p = sigmoid(z[e]);
@@ -229,7 +245,7 @@ __global__ void __launch_bounds__(norm_block(TPR), sm_threads(KIND, P) / norm_bl
         if (gate) o[e] *= s[e];
       }
       sum_scale.add(d, o);
-      weights(kScale, io.scale, o);
+      weights(A + S, io.scale, o);
 #pragma unroll
       for (int e = 0; e < E; ++e) d[e] *= o[e];
     }
@@ -286,10 +302,10 @@ int launch_rows(const NormBackward& a, cudaStream_t s) {
 }  // namespace
 
 template <typename TX, typename TR>
-int launch_norm_backward(const NormBackward& a, int kind, bool vec, cudaStream_t s) {
-  if (kind == kStream) return vec ? launch_rows<TX, TR, true, kStream>(a, s) : launch_rows<TX, TR, false, kStream>(a, s);
-  if (kind == kInner) return vec ? launch_rows<TX, TR, true, kInner>(a, s) : launch_rows<TX, TR, false, kInner>(a, s);
-  return vec ? launch_rows<TX, TR, true, kAll>(a, s) : launch_rows<TX, TR, false, kAll>(a, s);
+int launch_norm_backward(const NormBackward& a, int parts, bool vec, cudaStream_t s) {
+  return norm_instance(parts, [&](auto kind) {
+    return vec ? launch_rows<TX, TR, true, kind>(a, s) : launch_rows<TX, TR, false, kind>(a, s);
+  });
 }
 
 }  // namespace sdm
