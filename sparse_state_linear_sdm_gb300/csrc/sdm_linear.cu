@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(32 * kStepWarps, 2) step_kernel(const __grid_c
   const Place p = place_of<PASS>(a);
   const int c0 = p.vt * lay.vc;              // first column of the block
   const int nv = min(lay.vc, io.dv - c0);
-  const int lane = tid & 31, r = lane % R;
-  const int col = (tid >> 5) * CW + lane / R * kCols;  // this lane's first column in the block
+  const int warp = tid >> 5, lane = tid & 31, r = lane % R;
+  const int col = warp * CW + lane / R * kCols;  // this lane's first column in the block
   const int dk = io.dk;
 
   const T* gq = static_cast<const T*>(io.q) + p.b * io.q_bs + (long long)p.hk * dk;
@@ -110,13 +110,18 @@ __global__ void __launch_bounds__(32 * kStepWarps, 2) step_kernel(const __grid_c
           copy16(dst + t * lay.row + (key ? DK : 0) + c,
                  (key ? gk : gq) + (in ? (t0 + t) * (key ? io.k_ts : io.q_ts) + c : 0), in);
       }
-    } else {
-#pragma unroll 4
-      for (int e = tid; e < kStepTokens * 2 * DK; e += threads) {
-        const int t = e / (2 * DK), w = e % (2 * DK), c = w % DK;
-        const bool in = t < nt && c < dk, key = w >= DK;
-        if (key || PASS != kReduce)
-          copy1(dst + t * lay.row + w, (key ? gk : gq) + (in ? (t0 + t) * (key ? io.k_ts : io.q_ts) + c : 0), in);
+    } else {  // a token a warp
+#pragma unroll 2
+      for (int t = warp; t < kStepTokens; t += warps) {
+        const int row = t0 + min(t, nt - 1);
+        const T *rq = gq + row * io.q_ts, *rk = gk + row * io.k_ts;
+#pragma unroll
+        for (int c = lane; c < DK; c += 32) {
+          const bool in = t < nt && c < dk;
+          const int at = in ? c : 0;
+          if (PASS != kReduce) copy1(dst + t * lay.row + c, rq + at, in);
+          copy1(dst + t * lay.row + DK + c, rk + at, in);
+        }
       }
     }
     if (a.vec_v) {
@@ -127,11 +132,13 @@ __global__ void __launch_bounds__(32 * kStepWarps, 2) step_kernel(const __grid_c
         copy16(dst + t * lay.row + 2 * DK + c, gv + (in ? (t0 + t) * io.v_ts + c : 0), in);
       }
     } else {
-#pragma unroll 4
-      for (int e = tid; e < kStepTokens * lay.vc; e += threads) {
-        const int t = e / lay.vc, c = e % lay.vc;
-        const bool in = t < nt && c < nv;
-        copy1(dst + t * lay.row + 2 * DK + c, gv + (in ? (t0 + t) * io.v_ts + c : 0), in);
+#pragma unroll 2
+      for (int t = warp; t < kStepTokens; t += warps) {
+        const T* rv = gv + (t0 + min(t, nt - 1)) * io.v_ts;
+        for (int c = lane; c < lay.vc; c += 32) {
+          const bool in = t < nt && c < nv;
+          copy1(dst + t * lay.row + 2 * DK + c, rv + (in ? c : 0), in);
+        }
       }
     }
     if (tid < kStepTokens) {
@@ -342,10 +349,8 @@ __global__ void __launch_bounds__(32 * kStepWarps, 2) step_kernel(const __grid_c
           *reinterpret_cast<uint4*>(go + (t0 + t) * ots + c) = Piece<T>::pack(x);
         }
       } else {
-        for (int e = tid; e < nt * lay.vc; e += threads) {
-          const int t = e / lay.vc, c = e % lay.vc;
-          if (c < nv) from_f32(so[t * lay.vc + c], go + (t0 + t) * ots + c);
-        }
+        for (int t = warp; t < nt; t += warps)
+          for (int c = lane; c < nv; c += 32) from_f32(so[t * lay.vc + c], go + (t0 + t) * ots + c);
       }
     }
   }
