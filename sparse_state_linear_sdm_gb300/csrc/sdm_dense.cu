@@ -8,7 +8,7 @@
 //
 // 16,384 tokens of 8192 x 2048 with a residual: 350 us, 1,570 TFLOP/s (0.82 of cuBLAS's burst, 0.92 of its sustained
 // rate).  The gradient of 1000 tokens of 1024 x 2736 with gelu: 39 us, its slope pass 44 tiles on 76 pairs.  4 tokens of
-// 8192 x 2048: 11.4 (0.44 of the HBM floor), of which a launch is 4 to 5.
+// 8192 x 2048: 9.6 (0.52 of the HBM floor), of which a launch is 3 to 4.
 #include "sdm_product.cuh"
 
 namespace sdm {
@@ -18,28 +18,24 @@ namespace {
 //
 // HBM bounds a decode step's product: all of w for a handful of tokens.  A block takes 16 rows of w, the rows of one
 // mma.m16n8k16 with tokens as its columns, in 16-byte words straight from global memory as sdm_gated.cu's kernel does.
-// Where N is short of blocks the reduction is cut over the CTAs of a cluster, whose sums meet in the first
-// one's shared memory in their order.
-constexpr int kFewWarps = 4;
+// Where N is short of blocks a block has more warps for its reduction; their sums meet in shared memory in their order.
 constexpr int kFewRows = 16;
 
-template <int ACT, int NT>
-__global__ void __launch_bounds__(kFewWarps * 32) few_dense_kernel(const __nv_bfloat16* __restrict__ x,
-                                                                   const __nv_bfloat16* __restrict__ w,
-                                                                   const __nv_bfloat16* __restrict__ bias,
-                                                                   const __nv_bfloat16* residual, int M, int D, int N, int per,
-                                                                   int parts, __nv_bfloat16* y) {
+template <int ACT, int NT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) few_dense_kernel(const __nv_bfloat16* __restrict__ x,
+                                                               const __nv_bfloat16* __restrict__ w,
+                                                               const __nv_bfloat16* __restrict__ bias,
+                                                               const __nv_bfloat16* residual, int M, int D, int N,
+                                                               __nv_bfloat16* y) {
   constexpr int kAhead = 8 / NT;
-  __shared__ float4 part[kFewWarps][NT][32];
-  __shared__ float4 sums[NT][32];
+  __shared__ float4 part[WARPS][NT][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int rank = blockIdx.x % unsigned(parts), n0 = int(blockIdx.x / unsigned(parts)) * kFewRows + g;
+  const int n0 = int(blockIdx.x) * kFewRows + g;
   const bool second = n0 + 8 < N;  // N % 8 == 0: the first row is always inside
   const __nv_bfloat16* wa = w + size_t(n0) * D + c * 8;
   const __nv_bfloat16* wb = wa + size_t(8) * D;
   const __nv_bfloat16* xr = x + size_t(g) * D + c * 8;
-  const int k_end = min(D, (rank + 1) * per);
 
   float acc[NT][4];
 #pragma unroll
@@ -47,12 +43,12 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_dense_kernel(const __nv_bf
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int k0 = rank * per + warp * 32 * kAhead; k0 < k_end; k0 += kFewWarps * 32 * kAhead) {
+  for (int k0 = warp * 32 * kAhead; k0 < D; k0 += WARPS * 32 * kAhead) {
     uint4 va[kAhead], vb[kAhead], vx[kAhead][NT];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int k = k0 + j * 32;
-      const bool in = k + c * 8 < k_end;  // D % 8 == 0 and per % 8 == 0
+      const bool in = k + c * 8 < D;  // D % 8 == 0
       va[j] = in ? load_stream(wa + k) : zero;
       vb[j] = in && second ? load_stream(wb + k) : zero;
 #pragma unroll
@@ -70,22 +66,12 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_dense_kernel(const __nv_bf
 #pragma unroll
   for (int t = 0; t < NT; ++t) part[warp][t][lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
   __syncthreads();
-  if (warp < NT) {
+  if (warp < NT) {  // row n0 of tokens m, m + 1 in x, y; row n0 + 8 in z, w
     float4 s = part[0][warp][lane];
 #pragma unroll
-    for (int i = 1; i < kFewWarps; ++i) {
+    for (int i = 1; i < WARPS; ++i) {
       const float4 p = part[i][warp][lane];
       s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
-    }
-    sums[warp][lane] = s;
-  }
-  if (parts > 1) cluster_sync_all();
-  if (rank == 0 && warp < NT) {  // row n0 of tokens m, m + 1 in x, y; row n0 + 8 in z, w
-    float4 s = sums[warp][lane];
-    for (int i = 1; i < parts; ++i) {
-      const uint32_t at = cluster_addr(smem_u32(&sums[warp][lane]), uint32_t(i));
-      s.x += __uint_as_float(ld_cluster_u32(at)), s.y += __uint_as_float(ld_cluster_u32(at + 4));
-      s.z += __uint_as_float(ld_cluster_u32(at + 8)), s.w += __uint_as_float(ld_cluster_u32(at + 12));
     }
     const int m = warp * 8 + 2 * c;
     const float z[4] = {s.x, s.y, s.z, s.w};
@@ -99,39 +85,27 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_dense_kernel(const __nv_bf
       y[at] = __float2bfloat16_rn(v);
     }
   }
-  if (parts > 1) cluster_sync_all();  // the sums outlive their readers
 }
 
-// CTAs that share a reduction: up to 512 blocks, with at least 1024 of D each.  4 tokens of 8192 x 2048 take 11.8 us with one,
-// 9.6, 8.8 and 12.4 with two, four and eight; 8 of 2048 x 8192 take 7.7, 11.3, 17.4 and 32.4, 4 of 1024 x 1024 2.7, 3.5, 4.0
-// and 4.9.
-int few_parts(int D, int N) {
-  const int blocks = ceil_div(N, kFewRows);
-  int parts = 1;
-  while (blocks * parts < 512 && D / (2 * parts) >= 1024 && parts < 8) parts *= 2;
-  return parts;
-}
-
-template <int ACT, int NT>
+template <int ACT, int NT, int WARPS>
 int launch_few_dense(const void* x, const void* w, const void* bias, const void* residual, int M, int D, int N, void* y,
                      cudaStream_t s) {
   typedef const __nv_bfloat16* P;
-  const int parts = few_parts(D, N), per = ceil_div(ceil_div(D, parts), 32) * 32;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(parts);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(ceil_div(N, kFewRows)) * unsigned(parts));
-  cfg.blockDim = dim3(kFewWarps * 32);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, few_dense_kernel<ACT, NT>, static_cast<P>(x), static_cast<P>(w), static_cast<P>(bias),
-                         static_cast<P>(residual), M, D, N, per, parts, static_cast<__nv_bfloat16*>(y)) != cudaSuccess)
-    return SDM_ECUDA;
+  few_dense_kernel<ACT, NT, WARPS><<<unsigned(ceil_div(N, kFewRows)), WARPS * 32, 0, s>>>(
+      static_cast<P>(x), static_cast<P>(w), static_cast<P>(bias), static_cast<P>(residual), M, D, N,
+      static_cast<__nv_bfloat16*>(y));
   return last_launch_status();
+}
+// Warps of a block: enough of them on the card where its blocks are few and their reductions long.  4 tokens of 8192 x 2048 take
+// 11.7 us with 4 warps, 8.8 with 8 and 8.2 with 16, of 4096 x 4096 8.8, 7.8 and 9.8, of 2048 x 2048 3.9, 3.3 and 3.4; 8 of
+// 2048 x 8192 8.0, 9.4 and 12.7.  (The reduction over a cluster's CTAs took 8.9, 9.5, 4.2 and 7.7.)
+template <int ACT, int NT>
+int launch_few_dense(const void* x, const void* w, const void* bias, const void* residual, int M, int D, int N, void* y,
+                     cudaStream_t s) {
+  const int blocks = ceil_div(N, kFewRows);
+  if (blocks <= 128 && D >= 4096) return launch_few_dense<ACT, NT, 16>(x, w, bias, residual, M, D, N, y, s);
+  if (blocks <= 256 && D >= 2048) return launch_few_dense<ACT, NT, 8>(x, w, bias, residual, M, D, N, y, s);
+  return launch_few_dense<ACT, NT, 4>(x, w, bias, residual, M, D, N, y, s);
 }
 template <int ACT>
 int launch_few_act(const void* x, const void* w, const void* bias, const void* residual, int M, int D, int N, void* y,
