@@ -33,7 +33,7 @@ def _check(got, want, bound, label):
 
 
 SIZES = [
-    # M, D, N: few tokens (whole and in clusters), tiles, tiles with a split reduction
+    # M, D, N: few tokens, tiles, tiles with a split reduction
     (1, 8, 8), (1, 64, 136), (3, 72, 40), (8, 2048, 264), (9, 1032, 72), (16, 4096, 24), (16, 520, 2000),
     (17, 128, 136), (33, 1024, 64), (64, 200, 256), (100, 72, 136), (129, 128, 256), (257, 96, 520), (300, 640, 88),
     (20, 4096, 264), (130, 2056, 520), (600, 1000, 1000),
@@ -204,3 +204,11 @@ def test_bias_gradient_of_many_tokens():
     dx, dw, dbias = sdm.project_backward(x, w, dy, bias=torch.zeros(8, dtype=torch.bfloat16, device="cuda"))
     assert torch.equal(dbias.float(), torch.full((8,), 2.0 ** 24, device="cuda"))
     assert torch.equal(dx, dy) and torch.equal(dw, torch.ones_like(dw))
+
+
+@pytest.mark.parametrize("M,D,N", [(5, 4104, 2008), (2, 2056, 4080), (11, 8192, 48), (16, 6000, 2048)])
+def test_few_tokens_of_long_reductions(M, D, N):
+    """Blocks of 8 and 16 warps, whose shares of D end anywhere."""
+    x, w, bias, residual, _ = _inputs(M, D, N, seed=5)
+    want, bound = ref.project(*(_host(t) for t in (x, w, bias, residual)), "gelu")
+    _check(sdm.project(x, w, bias, residual, activation="gelu"), want, bound, "y")
