@@ -9,7 +9,7 @@
 //
 // One token of 256 sequences, 16 heads of 128 x 128 in slots: 83 us, 0.96 of the HBM floor.  step_kernel is bound by its two
 // multiply-adds a state and token, which one block an SM leaves at half of their rate (8 x 2048 x 16 heads of 128 in fp32:
-// 690 us, floor 230; two tokens at a time 727).
+// 665 us, floor 230; two tokens at a time 727 of 690).
 //
 // Where sequences and heads leave the card short, a sequence is cut into segments: every segment but the last
 // is reduced to its end state from zero and its sum of g, a small kernel turns those into the state in front of each
