@@ -13,9 +13,9 @@
 // clocks instead of 64), so the masked products and the weighted v are first operands out of TMEM.
 //
 // HBM would bound it (128 KB a chunk: 8 prompts of 4096 x 16 heads of 128 in 81 us), the work between the products does:
-// 145 us there, 4.5 us a chunk and SM, 36 % of the issue slots, the tensor pipe at 30 %, a third of the stalls instruction
-// fetches of five roles' code.  One prompt of 32,768 x 8 heads, in 19 segments: 126 us, 45 of them for the segments'
-// ends and 76 for the outputs.  182 and 150 with every operand in shared memory and one group for v and the state.
+// 123 us there, 3.8 us a chunk and SM.  (182 with every operand in shared memory and one group for v and the state; 145 with
+// the first slices of v weighed by the state's group in the chunk itself: 36 % of the issue slots then, a third of the
+// stalls instruction fetches of five roles' code.)  One prompt of 32,768 x 8 heads, in 19 segments: 114 us.
 //
 // What is rounded to bf16: the masked products and the state as q reads it, as an MMA takes them (each half a unit, as o
 // itself).  The state is not: A v is cut into three bf16 parts whose products are summed in fp32 (two parts
@@ -37,7 +37,10 @@ constexpr int kSlice = 32;               // tokens of a weighted slice of v: two
 // Warps: copies; the MMAs of o; those of the state; decays; and two groups of eight.
 constexpr int kTileThreads = 32 * 20;
 constexpr int kMaskWarp = 4, kStateWarp = 12;
-constexpr int kStateSlices = 2;          // slices of a chunk that the state's group weighs; the other group has the rest
+// Slices of a chunk that the group of o weighs, the first ones, while the tensor cores make o of the chunk before; the
+// state's group has the rest.
+constexpr int kEarlySlices = 2;
+static_assert(kChunk / kSlice == 4 && kEarlySlices == 2, "two buffers, each group's slices in either");
 
 enum Bar {
   kFull = 0, kEmpty = kSlots,     // slots
@@ -46,22 +49,24 @@ enum Bar {
   kMaskFull,                      // the masked products, in the place of q k^T
   kOutFull, kOutEmpty,            // o
   kStateFull, kStateEmpty,        // the state as q reads it
-  kPartFull, kPartEmpty = kPartFull + 2,  // weighted slices
-  kSumFull = kPartEmpty + 2, kSumEmpty,   // k^T (A v)
+  kPartFull, kPartEmpty = kPartFull + 2,  // weighted slices: the buffer's, and those of a chunk one by one
+  kSumFull = kPartEmpty + kChunk / kSlice, kSumEmpty,  // k^T (A v)
   kStaged,                        // o has left the slot of q, of even and of odd chunks: the copies may be late by two
   kDone = kStaged + 2,            // the MMAs of o, of even and of odd chunks
-  kDecayFull = kDone + 2, kDecayEmpty,
+  kDecayFull = kDone + 2, kDecayEmpty = kDecayFull + 2,  // of even and of odd chunks
+  kEachEmpty = kDecayEmpty + 2,
   kCut,                // tokens past the end cleared
   kDrain, kBars = kDrain + 2
 };
 
-struct Decays {  // of a chunk
-  float each[kChunk];  // e^g
-  float from[kChunk];  // products from the chunk's start up to each token
-  float to[kChunk];    // products after each token up to the chunk's end; 0 past the sequence's
-  float block[kChunk]; // products from the start of each token's block of 32 up to it
-  float rest[kChunk];  // and those after it up to the block's end
-  float all, pad[3];
+struct Decays {
+  float each[kChunk];  // e^g of a chunk
+  struct Chunk {
+    float block[kChunk];       // products from the start of each token's block of 32 up to it
+    float rest[kChunk];        // and those after it up to the block's end; 0 past the sequence's
+    float before[4], after[4]; // products of the blocks before and after each
+    float all, pad[3];
+  } of[2];  // even chunks, odd ones
 };
 
 template <int DK, int DV>
@@ -69,7 +74,8 @@ struct Tiles {
   static constexpr int off_state = kSlots * kSlot;
   static constexpr int off_decays = off_state + DK * DV * 2;
   static constexpr int off_bars = off_decays + int(sizeof(Decays));
-  static constexpr int bytes = off_bars + 448;
+  static constexpr int bytes = off_bars + (kBars * 8 + 32 + 15) / 16 * 16;
+  static_assert(bytes <= 227 * 1024, "shared memory of a block");
 };
 
 // TMEM columns.  Of each 32 of q k^T the masked products take 16; a slice's three parts are 16 columns each.
@@ -186,7 +192,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (i == kMaskFull || i == kStaged || i == kStaged + 1 || i == kOutEmpty || i == kStateFull || i == kPartFull || i == kPartFull + 1 ||
           i == kSumEmpty || i == kCut)
         n = 8;  // the warps of a group
-      if (i == kDecayEmpty) n = 16;
+      if (i == kEachEmpty) n = 8;
+      if (i == kDecayEmpty || i == kDecayEmpty + 1) n = 16;
       mbar_init(bar(i), uint32_t(n));
     }
     *stop = (base & 1023u) != 0;
@@ -228,10 +235,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int col = quad * 32 + lane;
   const uint32_t lanes = uint32_t(quad * 32) << 16;
   auto weigh = [&](int c, int s, uint32_t sv) {
-    const int slice = c * (kChunk / kSlice) + s, b = slice & 1;
-    if (!wait_all(kPartEmpty + b, uint32_t(slice >> 1) + 1)) return false;
+    // Before it the buffer had slice s - 2, or s + 2 of the chunk before.  A wait sees one phase ahead and one behind, and either
+    // group may be a whole chunk away from the other's slices, so each slice has a barrier of its own.
+    const int b = s & 1;
+    if (!(s < 2 ? wait_all(kPartEmpty + s + 2, uint32_t(c) + 1) : wait_all(kPartEmpty + s - 2, uint32_t(c)))) return false;
     tc_fence_after();
     if (quad * 32 < DV) {  // half of the slice's tokens, eight at a time
+      const Decays::Chunk& dc = d.of[c & 1];
+      const uint64_t after = pack2(dc.after[s], dc.after[s]);  // a slice is a block
 #pragma unroll 1
       for (int j = 0; j < kSlice / 2; j += 8) {
         const int t1 = s * kSlice + half * (kSlice / 2) + j;
@@ -243,8 +254,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h[k]) : "r"(at + swizzled(2 * i + k, col / 8 % 8)) : "memory");
-          const float2 w = *reinterpret_cast<const float2*>(&d.to[t1 + 2 * i]);
-          x[i] = mul2(pack2(__uint_as_float(uint32_t(h[0]) << 16), __uint_as_float(uint32_t(h[1]) << 16)), pack2(w.x, w.y));
+          const float2 w = *reinterpret_cast<const float2*>(&dc.rest[t1 + 2 * i]);
+          x[i] = mul2(pack2(__uint_as_float(uint32_t(h[0]) << 16), __uint_as_float(uint32_t(h[1]) << 16)),
+                      mul2(pack2(w.x, w.y), after));
         }
         // The first two parts are the upper halves of what is left, so what they leave is exact.
         const uint64_t minus = pack2(-1.f, -1.f);
@@ -280,8 +292,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bool ok = true;
       for (int c = 0; c < chunks && ok; ++c) {
         const int t = p.t_lo + c * kChunk;
-        for (int i = 0; i < kLoads; ++i) {
-          const int at = slot(c, i);
+        for (int j = 0; j < kLoads; ++j) {  // v, which is weighed early, then k, then q, whose place is free last
+          const int i = j == 0 ? kLoads - 1 : j - 1, at = slot(c, i);
           // The slot's last load: q's is free when o has left its place, the others' when their MMAs are done.
           if (c > 1) ok = PASS != kReduce && i == 1 ? wait(kStaged + (c & 1), turn(c) + 1) : wait(kEmpty + at, turn(c) + 1);
           if (!ok) break;
@@ -344,26 +356,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       Sum left = before.from_lane(lane - 1), right = after.from_lane(lane + 1);
       if (lane % 8 == 0) left = zero;
       if (lane % 8 == 7) right = zero;
-      float block[4], rest[4], from[4], to[4];
+      float block[4], rest[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const Sum x = left + up[i], y = right + down[i];
         block[i] = x.exp();
-        rest[i] = y.exp();
-        from[i] = (earlier + x).exp();
-        to[i] = c * kChunk + lane * 4 + i < tokens ? (later + y).exp() : 0.f;
+        rest[i] = c * kChunk + lane * 4 + i < tokens ? y.exp() : 0.f;
       }
-      const float last = all.exp();
+      const float last = all.exp(), start = earlier.exp(), end = later.exp();
       // All of it is computed here and not behind the wait, after which the other warps wait for it.
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        asm volatile("" ::"f"(each[i]), "f"(block[i]), "f"(rest[i]), "f"(from[i]), "f"(to[i]), "f"(last));
-      if (!wait_all(kDecayEmpty, uint32_t(c) + 1)) break;
+        asm volatile("" ::"f"(each[i]), "f"(block[i]), "f"(rest[i]), "f"(start), "f"(end), "f"(last));
+      if (!wait_all(kDecayEmpty + (c & 1), turn(c) + 1)) break;
+      if (PASS != kReduce && !wait_all(kEachEmpty, uint32_t(c) + 1)) break;
+      Decays::Chunk& dc = d.of[c & 1];
       auto put = [&](float* at, const float (&v)[4]) { reinterpret_cast<float4*>(at)[lane] = make_float4(v[0], v[1], v[2], v[3]); };
-      put(d.each, each), put(d.block, block), put(d.rest, rest), put(d.from, from), put(d.to, to);
-      if (lane == 0) d.all = last;
+      put(d.each, each), put(dc.block, block), put(dc.rest, rest);
+      if (lane % 8 == 0) dc.before[lane / 8] = start, dc.after[lane / 8] = end;
+      if (lane == 0) dc.all = last;
       total = total + all;
-      arrive(kDecayFull);
+      arrive(kDecayFull + (c & 1));
     }
     if (PASS == kReduce && lane == 0 && p.vt == 0) a.ws_g[p.seg * nbh + bh] = total.hi + total.lo;
   } else if (warp == 1) {
@@ -419,7 +432,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int i = 0; i < 3; ++i)
             mma1_tmem(tmem + kSum, tmem + kParts + uint32_t(b * 3 + i) * kPartCols + uint32_t(kk * 8),
                       k_rows + uint64_t((t0 + kk * 16) * 128 >> 4), t0 > 0 || kk > 0 || i > 0, tile_idesc(DK, false, true));
-        commit1(bar(kPartEmpty + b));
+        commit1(bar(kPartEmpty + t0 / kSlice));
       }
       if (!ok) break;
       commit1(bar(kSumFull));
@@ -430,18 +443,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp < kStateWarp) {
     // ---- masked products, some of weighted v, then o ----
-    auto weigh_rest = [&](int c, int n) {
-      const int iv = slot(c, kLoads - 1);
-      if (n <= kStateSlices * kSlice) return true;
-      bool ok = wait_all(kFull + iv, turn(c)) && (n == kChunk || wait_all(kCut, 0));
+    auto weigh_first = [&](int c) {
+      const int n = min(kChunk, tokens - c * kChunk), iv = slot(c, kLoads - 1);
+      bool ok = wait_all(kDecayFull + (c & 1), turn(c)) && wait_all(kFull + iv, turn(c)) && (n == kChunk || wait_all(kCut, 0));
 #pragma unroll 1
-      for (int i = kStateSlices; i * kSlice < n && ok; ++i) ok = weigh(c, i, place(iv));
+      for (int i = 0; i < kEarlySlices && i * kSlice < n && ok; ++i) ok = weigh(c, i, place(iv));
       return ok;
     };
     if (PASS == kReduce) {
       for (int c = 0; c < chunks; ++c) {
-        if (!wait_all(kDecayFull, uint32_t(c)) || !weigh_rest(c, min(kChunk, tokens - c * kChunk))) break;
-        arrive(kDecayEmpty);
+        if (!weigh_first(c)) break;
+        arrive(kDecayEmpty + (c & 1));
       }
     } else {
       const int row = col;
@@ -453,74 +465,78 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       auto staged = [&](int piece) {
         return DV == 128 ? swizzled(lane, piece) : uint32_t(lane * 64 + ((piece ^ (lane >> 1 & 3)) << 4));
       };
-      for (int c = 0; c < chunks; ++c) {
+      for (int c = -1; c < chunks; ++c) {  // the first round only weighs
         const int n = min(kChunk, tokens - c * kChunk);
-        if (!wait_all(kDecayFull, uint32_t(c))) break;
-        if (!wait_all(kScoreFull, uint32_t(c))) break;
-        tc_fence_after();
-        float f = io.scale * d.block[row];  // scale A of this row and the last column of the block that is next
-        for (int b = quad - 1; b > b_hi; --b) f *= d.block[b * 32 + 31];
+        if (c >= 0) {
+          const Decays::Chunk& dc = d.of[c & 1];
+          if (!wait_all(kScoreFull, uint32_t(c))) break;
+          tc_fence_after();
+          float f = io.scale * dc.block[row];  // scale A of this row and the last column of the block that is next
+          for (int b = quad - 1; b > b_hi; --b) f *= dc.block[b * 32 + 31];
 #pragma unroll 1
-        for (int b = b_hi; b >= b_lo; --b) {
-          uint32_t r[32], pairs[16];
-          tmem_load32(tmem + lanes + kScore + uint32_t(b * 32), r);
-          if (b == quad) {  // the diagonal's: from there on a product after the other
-            const float* each = d.each + b * 32;
-            float e = io.scale;
+          for (int b = b_hi; b >= b_lo; --b) {
+            uint32_t r[32], pairs[16];
+            tmem_load32(tmem + lanes + kScore + uint32_t(b * 32), r);
+            if (b == quad) {  // the diagonal's: from there on a product after the other
+              const float* each = d.each + b * 32;
+              float e = io.scale;
 #pragma unroll
-            for (int j = 30; j >= 0; j -= 2) {  // columns j, j + 1 of the block
-              const float2 w = *reinterpret_cast<const float2*>(each + j);
-              const float hi = j + 1 > lane ? 0.f : e * __uint_as_float(r[j + 1]);
-              e = j + 1 > lane ? e : e * w.y;
-              const float lo = j > lane ? 0.f : e * __uint_as_float(r[j]);
-              e = j > lane ? e : e * w.x;
-              pairs[j / 2] = pack_bf16(__float_as_uint(lo), __float_as_uint(hi));
-            }
-          } else {
-            const uint64_t both = pack2(f, f);
+              for (int j = 30; j >= 0; j -= 2) {  // columns j, j + 1 of the block
+                const float2 w = *reinterpret_cast<const float2*>(each + j);
+                const float hi = j + 1 > lane ? 0.f : e * __uint_as_float(r[j + 1]);
+                e = j + 1 > lane ? e : e * w.y;
+                const float lo = j > lane ? 0.f : e * __uint_as_float(r[j]);
+                e = j > lane ? e : e * w.x;
+                pairs[j / 2] = pack_bf16(__float_as_uint(lo), __float_as_uint(hi));
+              }
+            } else {
+              const uint64_t both = pack2(f, f);
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 w = *reinterpret_cast<const float4*>(d.rest + b * 32 + j);
-              float x0, x1;
-              unpack2(mul2(mul2(pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), pack2(w.x, w.y)), both), x0, x1);
-              pairs[j / 2] = pack_bf16(__float_as_uint(x0), __float_as_uint(x1));
-              unpack2(mul2(mul2(pack2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), pack2(w.z, w.w)), both), x0, x1);
-              pairs[j / 2 + 1] = pack_bf16(__float_as_uint(x0), __float_as_uint(x1));
+              for (int j = 0; j < 32; j += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(dc.rest + b * 32 + j);
+                float x0, x1;
+                unpack2(mul2(mul2(pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), pack2(w.x, w.y)), both), x0, x1);
+                pairs[j / 2] = pack_bf16(__float_as_uint(x0), __float_as_uint(x1));
+                unpack2(mul2(mul2(pack2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), pack2(w.z, w.w)), both), x0, x1);
+                pairs[j / 2 + 1] = pack_bf16(__float_as_uint(x0), __float_as_uint(x1));
+              }
+              f *= dc.block[b * 32 + 31];
             }
-            f *= d.block[b * 32 + 31];
+            tmem_store16(tmem + lanes + kScore + uint32_t(b * 32), pairs);
           }
-          tmem_store16(tmem + lanes + kScore + uint32_t(b * 32), pairs);
-        }
-        if (!weigh_rest(c, n)) break;
-        if (!half) {  // nothing above the diagonal
-          const uint32_t zeros[16] = {};
-          for (int b = quad + 1; b < 4; ++b) tmem_store16(tmem + lanes + kScore + uint32_t(b * 32), zeros);
-        }
-        // o of the chunk before has long left for memory
-        if (c > 0 && lane == 0) {
-          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          mbar_arrive(bar(kStaged + ((c - 1) & 1)));
-        }
-        __syncwarp();
-        // q S, on which the chunk's own products are added, takes the decays from the chunk's start.
-        const float from = d.from[row] * io.scale;
-        if (!wait_all(kReadFull, uint32_t(c))) break;
-        tc_fence_after();
+          arrive(kEachEmpty);
+          if (!half) {  // nothing above the diagonal
+            const uint32_t zeros[16] = {};
+            for (int b = quad + 1; b < 4; ++b) tmem_store16(tmem + lanes + kScore + uint32_t(b * 32), zeros);
+          }
+          // o of the chunk before has long left for memory
+          if (c > 0 && lane == 0) {
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            mbar_arrive(bar(kStaged + ((c - 1) & 1)));
+          }
+          __syncwarp();
+          // q S, on which the chunk's own products are added, takes the decays from the chunk's start.
+          const float from = dc.before[quad] * dc.block[row] * io.scale;
+          if (!wait_all(kReadFull, uint32_t(c))) break;
+          tc_fence_after();
 #pragma unroll 1
-        for (int x = 0; x < DV / 2; x += 16) {
-          uint32_t r[16];
-          tmem_load16(out_at + uint32_t(x), r);
+          for (int x = 0; x < DV / 2; x += 16) {
+            uint32_t r[16];
+            tmem_load16(out_at + uint32_t(x), r);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(from * __uint_as_float(r[i]));
-          tmem_store16(out_at + uint32_t(x), r);
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(from * __uint_as_float(r[i]));
+            tmem_store16(out_at + uint32_t(x), r);
+          }
+          tmem_stored();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(kMaskFull));
+            mbar_arrive(bar(kDecayEmpty + (c & 1)));
+          }
         }
-        tmem_stored();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kMaskFull));
-          mbar_arrive(bar(kDecayEmpty));
-        }
+        if (c + 1 < chunks && !weigh_first(c + 1)) break;
+        if (c < 0) continue;
         if (!wait_all(kOutFull, uint32_t(c))) break;
         tc_fence_after();
         const uint32_t patch = place(slot(c, 1)) + uint32_t((half * 4 + quad) * 32 * kRowBytes);
@@ -601,13 +617,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         arrive(kCut);
         if (!wait_all(kCut, 0)) break;  // the others of this group, whose rows are read below
       }
-      if (!wait_all(kDecayFull, uint32_t(c))) break;
+      if (!wait_all(kDecayFull + (c & 1), turn(c))) break;
       bool ok = true;
 #pragma unroll 1
-      for (int i = 0; i < kStateSlices && i * kSlice < n && ok; ++i) ok = weigh(c, i, sv);
+      for (int i = kEarlySlices; i * kSlice < n && ok; ++i) ok = weigh(c, i, sv);
       if (!ok) break;
-      const float all = d.all;
-      arrive(kDecayEmpty);
+      const float all = d.of[c & 1].all;
+      arrive(kDecayEmpty + (c & 1));
       if (!wait_all(kSumFull, uint32_t(c))) break;
       tc_fence_after();
       if (cols) {

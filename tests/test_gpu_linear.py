@@ -416,3 +416,16 @@ def test_a_sequence_without_tokens_keeps_its_state_bit_for_bit(dtype, T, dk):
     kept = torch.empty_like(a["state"])
     o, _ = sdm.linear_attention(**a, state_out=kept)
     assert torch.equal(kept[1], a["state"][1]) and (o[1] == 0).all()
+
+
+@pytest.mark.parametrize("B,T,H,d", [(1, 16384, 8, 128), (4, 1024, 16, 128), (2, 4096, 16, 64)])
+def test_long_prompts_many_times(B, T, H, d):
+    """The chunks' warps meet in any order; results and errors do not depend on it."""
+    a = _case(("bf16", B, T, H, H, d, d, "token", True, None, 0, "wide"))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kept, again = torch.empty_like(a["state"]), torch.empty_like(a["state"])
+    o, _ = sdm.linear_attention(**a, state_out=kept, dev_err=err)
+    for i in range(200):
+        o2, _ = sdm.linear_attention(**a, state_out=again, dev_err=err)
+        assert torch.equal(o2, o) and torch.equal(again, kept), i
+    assert err.item() == 0
