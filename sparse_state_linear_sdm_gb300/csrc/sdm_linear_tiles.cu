@@ -784,8 +784,8 @@ __global__ void __launch_bounds__(kPadThreads) narrow_kernel(const __nv_bfloat16
   }
 }
 
-// A CTA of the tile kernel fills an SM, so 152 of them are what the card runs at once.  A chunk takes one 4.1 us, and 7 over
-// both passes where the sequence is cut, with about 15 us for two more launches and starts.  (50 heads of 4096 tokens in 3
+// A CTA of the tile kernel fills an SM, so 152 of them are what the card runs at once.  A chunk takes one about 4 us, and
+// 7 over both passes where the sequence is cut, with about 15 us for two more launches and starts.  (50 heads of 4096 tokens in 3
 // segments 116 us and 137 whole, of 1024 tokens 52 and 43; 8 heads of 1024 tokens in 4 segments 32 and 39.  Two
 // segments gain nothing: 64 heads of 4096 tokens 148 us and 139 whole.)
 void cut_tiles(int B, int T, int H, int dv, int* segments, int* segment) {
