@@ -44,7 +44,7 @@ __device__ __forceinline__ Place place_of(const LinearArgs& a) {
   p.slot = row_slot(io.slots, p.b, io.n_slots, a.dev_err);
   const int len = p.slot < 0 ? 0 : row_length(io.lengths, p.b, io.T);
   p.t_lo = PASS == kWhole ? 0 : p.seg * a.segment;
-  p.t_hi = PASS == kWhole ? io.T : min(p.t_lo + a.segment, io.T);
+  p.t_hi = PASS == kWhole || io.T - p.t_lo < a.segment ? io.T : p.t_lo + a.segment;  // t_lo + segment may pass 2^31
   p.t_end = min(len, p.t_hi);
   p.last = PASS == kWhole || p.seg == a.segments - 1;
   return p;
