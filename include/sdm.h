@@ -561,8 +561,8 @@ int sdm_project_gated_backward(const void* x, const void* w, const void* dh, lon
  *   o  [B, T, H, dv] dt, dense;  state, state_out fp32 [n_slots, H, dk, dv].
  * Sums and states are fp32.  bf16 prompts with dk up to SDM_LINEAR_TILE_D go to the tensor cores in chunks of 128
  * tokens: there the masked products of a chunk and the state in front of it are rounded to bf16 as they are read (the
- * state itself is not), and a value of v that is not finite makes NaN of its column for every token of its chunk, those
- * before it among them, and not only from its token on.  Rows that do not start on 16 bytes are copied for that where
+ * state itself is not), and an infinity in v makes NaN of its column in the state, where token by token it may stay one
+ * (a head with such values takes several times as long).  Rows that do not start on 16 bytes are copied for that where
  * dk or dv is no multiple of 8; otherwise they are taken token by token.  Token by token, a prompt's products k v are kept
  * up to e^30 larger than they are for 16 tokens: beyond 3e25 they may overflow.
  * Requires H % Hk == 0, dk <= SDM_MAX_LINEAR_D, dv <= SDM_MAX_LINEAR_D.  o and the workspace overlap nothing else

@@ -166,6 +166,112 @@ struct Sum {
 // One copy of the loop: the roles' code competes for the instruction cache.
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* stop) { return mbar_wait(bar, parity, stop); }
 
+// ---- values of v that are not finite ----
+//
+// 0 times one is not 0, so the masked products carry it to the tokens of its chunk that come before it.  Its column of the
+// state is NaN from then on, which shows at the end, and those tokens' outputs are then formed again, token by token from the
+// state that the sequence (the segment) begins with: 820 us instead of 127 where each of 8 prompts of 4096 x 16 heads of 128
+// has such a token.  Looking every chunk over for one took a tenth of the time of all the others (121 us -> 129 to 137 on one
+// GPU, by which warp looks).
+
+// The state in front of the first token.
+template <int PASS>
+__device__ __forceinline__ const float* front_state(const LinearArgs& a, const Place& p) {
+  const sdm_linear_args& io = a.io;
+  const long long sn = (long long)io.dk * io.dv;
+  if (PASS == kJoin) return a.ws_s + (((long long)p.seg * io.B + p.b) * io.H + p.h) * sn;
+  return PASS == kWhole && io.state && p.slot >= 0 ? io.state + ((long long)p.slot * io.H + p.h) * sn : nullptr;
+}
+// A warp's eight columns, the c0-th on.  A lane has rows lane, lane + 32 ...
+template <int DK, int PASS>
+__device__ void form_columns(const LinearArgs& a, const Place& p, int c0) {
+  constexpr int N = DK / 32, kAhead = 4;  // tokens asked for at a time
+  const sdm_linear_args& io = a.io;
+  const float* src = front_state<PASS>(a, p);
+  const int lane = threadIdx.x & 31, tokens = p.t_end - p.t_lo, dk8 = (io.dk + 7) / 8 * 8;
+  typedef const __nv_bfloat16* In;
+  const In q = In(io.q) + p.b * io.q_bs + p.t_lo * io.q_ts + (long long)p.hk * dk8;
+  const In k = In(io.k) + p.b * io.k_bs + p.t_lo * io.k_ts + (long long)p.hk * dk8;
+  const In v = In(io.v) + p.b * io.v_bs + p.t_lo * io.v_ts + (long long)p.h * a.o_dv + c0;
+  const float* g = io.g ? io.g + p.b * io.g_bs + p.t_lo * io.g_ts + p.h : nullptr;
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(io.o) + (((long long)p.b * io.T + p.t_lo) * io.H + p.h) * a.o_dv + c0;
+  const long long os = (long long)io.H * a.o_dv;
+
+  int first[8];  // of each column, or the tokens' number
+#pragma unroll
+  for (int j = 0; j < 8; ++j) first[j] = tokens;
+  for (int t0 = 0; t0 < tokens; t0 += 32) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (t0 + lane < tokens) w = *reinterpret_cast<const uint4*>(v + (t0 + lane) * io.v_ts);
+    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const unsigned hit = __ballot_sync(0xFFFFFFFFu, (r[j / 2] >> (j % 2 * 16) & 0x7F80u) == 0x7F80u);
+      if (hit && first[j] == tokens) first[j] = t0 + __ffs(hit) - 1;
+    }
+  }
+  int from = tokens, to = 0;  // tokens whose outputs are formed again
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (first[j] == tokens) first[j] = 0;
+    if (first[j] % kChunk) from = min(from, first[j] / kChunk * kChunk), to = max(to, first[j]);
+  }
+
+  float s[N][8];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = lane + 32 * i;
+      s[i][j] = src && r < io.dk && c0 + j < io.dv ? src[(long long)r * io.dv + c0 + j] : 0.f;
+    }
+  for (int t0 = 0; t0 < to; t0 += kAhead) {
+    __nv_bfloat16 kr[kAhead][N];
+    uint4 vr[kAhead];
+    float gr[kAhead];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const int t = min(t0 + x, tokens - 1);
+      vr[x] = *reinterpret_cast<const uint4*>(v + t * io.v_ts);
+      gr[x] = g ? g[t * io.g_ts] : 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) kr[x][i] = lane + 32 * i < io.dk ? k[t * io.k_ts + lane + 32 * i] : __nv_bfloat16(0.f);
+    }
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const int t = t0 + x;
+      if (t >= to) break;
+      const float e = at_most_finite(expf(gr[x]));
+      float f[8];
+      Piece<__nv_bfloat16>::load(vr[x], f);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] = fmaf(e, s[i][j], to_f32(kr[x][i]) * f[j]);
+      if (t < from) continue;
+      float qr[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) qr[i] = lane + 32 * i < io.dk ? to_f32(q[t * io.q_ts + lane + 32 * i]) : 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) y = fmaf(qr[i], s[i][j], y);
+#pragma unroll
+        for (int m = 16; m > 0; m /= 2) y += __shfl_xor_sync(0xFFFFFFFFu, y, m);
+        if (lane == j && t >= first[j] / kChunk * kChunk && t < first[j]) from_f32(y * io.scale, o + t * os + j);
+      }
+    }
+  }
+}
+
+template <int DK, int PASS>
+__device__ __noinline__ void form_again(const LinearArgs& a) {
+  const Place p = place_of<PASS>(a);
+  const int c0 = p.vt * kTileColumns, warp = threadIdx.x >> 5;
+  for (int c = warp * 8; c < min(kTileColumns, a.o_dv - c0); c += kStateWarp * 8) form_columns<DK, PASS>(a, p, c0 + c);
+}
+
 // Every wait is bounded; one that runs out stops the CTA, which waits for the copies and MMAs in flight, frees TMEM and
 // reports SDM_DEV_TIMEOUT.
 template <int DK, int DV, int PASS>
@@ -576,9 +682,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float s[kCols];  // the state
 #pragma unroll
     for (int i = 0; i < kCols; ++i) s[i] = 0.f;
-    const float* src = PASS == kJoin ? a.ws_s + (p.seg * nbh + bh) * sn
-                       : PASS == kWhole && io.state && p.slot >= 0 ? io.state + ((long long)p.slot * io.H + p.h) * sn
-                                                                   : nullptr;
+    const float* src = front_state<PASS>(a, p);
     if (src && col < dv) {
 #pragma unroll
       for (int i = 0; i < kCols; ++i)
@@ -642,6 +746,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         show_state();
       }
     }
+    float zero = 0.f;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) zero = fmaf(0.f, s[i], zero);
+    if (PASS != kReduce && __syncthreads_or(zero != 0.f)) __syncthreads();  // the new state may lie over the old one
     float* dst = PASS == kReduce                              ? a.ws_s + (p.seg * nbh + bh) * sn
                  : p.last && io.state_out && p.slot >= 0 ? io.state_out + ((long long)p.slot * io.H + p.h) * sn
                                                               : nullptr;
@@ -650,6 +758,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int i = 0; i < kCols; ++i)
         if (c0 + i < io.dk) dst[(c0 + i) * io.dv + v0 + col] = s[i];
     }
+  }
+
+  if (PASS != kReduce && warp < kStateWarp && __syncthreads_or(0)) {  // a state is not finite
+    asm volatile("fence.proxy.async;" ::: "memory");  // o has left by copies
+    if (!*stop) form_again<DK, PASS>(a);
+    __syncthreads();
   }
 
   // No token here: o is 0.
