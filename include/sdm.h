@@ -485,7 +485,12 @@ int sdm_gen_M0(unsigned long long seed, int H, long long N, int d_v, float scale
  *            SDM_DEV_INDEX_RANGE.  Live slots of one call are distinct.
  *   state    read (NULL: zeros); state_out written (NULL: not kept); the same buffer updates it
  *            in place.  n_slots: rows of either.  Otherwise state_out overlaps nothing that the
- *            call reads (SDM_EOVERLAP). */
+ *            call reads (SDM_EOVERLAP).
+ *   dev_err  int on the device, or NULL: SDM_DEV_* bits are OR-ed in.  The kernels on the tensor
+ *            cores (linear attention, the projections and their gradients) give a wait up after
+ *            two seconds: SDM_DEV_TIMEOUT, after which the outputs are unspecified.  A new state is
+ *            then written whole, for a head and up to 128 of its columns, or left as it was; without
+ *            dev_err nothing tells that it was left. */
 typedef enum { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1, SDM_ACT_GELU = 2 } sdm_activation;
 
 /* B * T <= 2^31 - 1, and T short of 2^31 by the last strip's or chunk's rounding
@@ -585,6 +590,14 @@ typedef struct {
 size_t sdm_linear_attention_workspace_size(int dtype, int B, int T, int H, int Hk, int dk, int dv);
 int sdm_linear_attention(const sdm_linear_args* args, void* workspace, size_t workspace_bytes,
                          int* dev_err, void* stream);
+
+/* sdm_test_linear_stall - test of the tensor cores' stop path: sdm_linear_attention in which the copies of one block
+ * (of the pass 0: a sequence in one piece, 1: the segments' ends, 2: the segments) stop in front of a chunk's copy of k (load 0),
+ * q (1) or v (2; of pass 1 it is load 1), and every wait gives up after wait_ns, 10^5 to 10^9 (SDM_EINVAL otherwise).  The block
+ * stops, waits for its copies and MMAs in flight and ORs SDM_DEV_TIMEOUT into *dev_err (required).
+ * SDM_EUNSUPPORTED where the call goes token by token. */
+int sdm_test_linear_stall(const sdm_linear_args* args, void* workspace, size_t workspace_bytes, int pass, int block, int chunk,
+                          int load, unsigned long long wait_ns, int* dev_err, void* stream);
 
 /* sdm_residual_norm - the norms after and before a block with its gate, residual scale and residual, in one pass:
  *   a = x / rms(x) * after * act(gate)        rms over each of `groups` groups of D / groups channels

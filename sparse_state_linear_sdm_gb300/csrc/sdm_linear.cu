@@ -620,7 +620,7 @@ struct LinearSpace {
       segments = n > segments ? n : segments;
       if (dk % 8 || dv % 8) pad = padded_bytes(B, T, H, Hk, dk, dv);
     }
-    if (segments > 1) states = (size_t(segments) * B * H * (size_t(dk) * dv + 1) * 4 + 255) / 256 * 256;
+    if (segments > 1) states = (size_t(segments) * B * H * (size_t(dk) * dv + 1 + tile_columns(dv)) * 4 + 255) / 256 * 256;
   }
 };
 }  // namespace
@@ -632,8 +632,8 @@ extern "C" size_t sdm_linear_attention_workspace_size(int dtype, int B, int T, i
   return space.states + space.pad;
 }
 
-extern "C" int sdm_linear_attention(const sdm_linear_args* args, void* workspace, size_t workspace_bytes,
-                                    int* dev_err, void* stream) {
+static int linear_attention(const sdm_linear_args* args, void* workspace, size_t workspace_bytes, int* dev_err, void* stream,
+                            const LinearStall* stall) {
   if (!args) return SDM_EINVAL;
   const sdm_linear_args& io = *args;
   if (!sizes_ok(io.dtype, io.B, io.T, io.H, io.dk, io.dv) || io.Hk < 1 || io.H % io.Hk) return SDM_EINVAL;
@@ -653,9 +653,11 @@ extern "C" int sdm_linear_attention(const sdm_linear_args* args, void* workspace
   LinearArgs a = {};
   a.io = io;
   a.dev_err = dev_err;
+  if (stall) a.stall = *stall;
   cudaStream_t s = as_stream(stream);
   a.vec_s = io.dv % 4 == 0 && !off(io.state, 15) && !off(io.state_out, 15);
   if (io.T == 1) {
+    if (stall) return SDM_EUNSUPPORTED;
     if (overlap(io, nullptr, 0)) return SDM_EOVERLAP;
     return io.dtype == SDM_F32 ? launch_token<float>(a, s) : launch_token<__nv_bfloat16>(a, s);
   }
@@ -670,6 +672,7 @@ extern "C" int sdm_linear_attention(const sdm_linear_args* args, void* workspace
   const bool rows_fit = a.vec_qk && a.vec_v && a.vec_o && steps_on(io.q_bs, io.q_ts) && steps_on(io.k_bs, io.k_ts) &&
                         steps_on(io.v_bs, io.v_ts);
   const bool tiles = tile_sizes(io.dtype, io.B, io.T, io.H, io.dk, io.dv) && (rows_fit || space.pad);
+  if (stall && !tiles) return SDM_EUNSUPPORTED;
   if (tiles)
     cut_tiles(io.B, io.T, io.H, io.dv, &a.segments, &a.segment);
   else
@@ -679,8 +682,24 @@ extern "C" int sdm_linear_attention(const sdm_linear_args* args, void* workspace
     if (workspace_bytes < need) return SDM_ENOSPACE;
     a.ws_s = static_cast<float*>(workspace);
     a.ws_g = a.ws_s + size_t(a.segments) * io.B * io.H * io.dk * io.dv;
+    a.ws_stop = reinterpret_cast<int*>(a.ws_g + size_t(a.segments) * io.B * io.H);
   }
   if (overlap(io, need ? workspace : nullptr, need)) return SDM_EOVERLAP;
   if (tiles) return launch_tiles(a, rows_fit ? nullptr : static_cast<uint8_t*>(workspace) + space.states, s);
   return io.dtype == SDM_F32 ? launch_type<float>(a, s) : launch_type<__nv_bfloat16>(a, s);
+}
+
+extern "C" int sdm_linear_attention(const sdm_linear_args* args, void* workspace, size_t workspace_bytes, int* dev_err,
+                                    void* stream) {
+  return linear_attention(args, workspace, workspace_bytes, dev_err, stream, nullptr);
+}
+
+extern "C" int sdm_test_linear_stall(const sdm_linear_args* args, void* workspace, size_t workspace_bytes, int pass, int block,
+                                     int chunk, int load, unsigned long long wait_ns, int* dev_err, void* stream) {
+  if (pass < kWhole || pass > kJoin || block < 0 || chunk < 0 || load < 0 || load > 2 || wait_ns < 100000ull ||
+      wait_ns > 1000000000ull || !dev_err)
+    return SDM_EINVAL;
+  LinearStall stall;
+  stall.pass = pass, stall.block = block, stall.chunk = chunk, stall.load = load, stall.wait_ns = wait_ns;
+  return linear_attention(args, workspace, workspace_bytes, dev_err, stream, &stall);
 }

@@ -9,6 +9,13 @@ namespace sdm {
 // (kReduce), then each run from the state in front of it (kJoin).
 enum LinearPass { kWhole = 0, kReduce = 1, kJoin = 2 };
 
+// The time limit of the tiles' waits.  Tests only: in this pass and block the copies stop in front of this chunk's load (of the
+// slots' order).
+struct LinearStall {
+  unsigned long long wait_ns = 0;
+  int pass = -1, block = 0, chunk = 0, load = 0;
+};
+
 struct LinearArgs {
   sdm_linear_args io;
   int vtiles;            // column tiles of v
@@ -18,7 +25,9 @@ struct LinearArgs {
   float* ws_g;           // [segments][B][H]: sum of g over each segment
   bool vec_qk, vec_v, vec_o; // rows of 16-byte pieces
   bool vec_s;            // rows of the states start on 16 bytes
+  int* ws_stop;          // [segments][B][H][vtiles]: whether a wait ran out before the segment's end was known (tiles)
   int* dev_err;
+  LinearStall stall;
 };
 
 struct Place {
@@ -55,6 +64,8 @@ int launch_front(const LinearArgs& a, cudaStream_t s);
 
 // The tensor cores' form: bf16, dk up to SDM_LINEAR_TILE_D, and multiples of 8, rows on 16 bytes and positive strides, or
 // else a workspace of padded_bytes at `pad` for copies that have them.  Segments of its own.
+constexpr int kTileColumns = 128;  // of v a CTA takes
+inline int tile_columns(int dv) { return (dv + kTileColumns - 1) / kTileColumns; }
 void cut_tiles(int B, int T, int H, int dv, int* segments, int* segment);
 size_t padded_bytes(int B, int T, int H, int Hk, int dk, int dv);
 int launch_tiles(LinearArgs a, void* pad, cudaStream_t s);

@@ -29,7 +29,6 @@ namespace sdm {
 namespace {
 
 constexpr int kChunk = 128;
-constexpr int kTileColumns = 128;        // of v a CTA takes
 constexpr int kSlot = 32768;             // 128 tokens of 128 columns: two boxes of 64 columns
 constexpr int kBox = kChunk * 128;       // bytes of a box
 constexpr int kSlots = 6;                // two chunks
@@ -164,7 +163,9 @@ struct Sum {
 };
 
 // One copy of the loop: the roles' code competes for the instruction cache.
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* stop) { return mbar_wait(bar, parity, stop); }
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* stop, unsigned long long limit_ns) {
+  return mbar_wait(bar, parity, stop, limit_ns);
+}
 
 // ---- values of v that are not finite ----
 //
@@ -273,7 +274,7 @@ __device__ __noinline__ void form_again(const LinearArgs& a) {
 }
 
 // Every wait is bounded; one that runs out stops the CTA, which waits for the copies and MMAs in flight, frees TMEM and
-// reports SDM_DEV_TIMEOUT.
+// reports SDM_DEV_TIMEOUT.  A new state is written whole or not at all.
 template <int DK, int DV, int PASS>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ TileMaps tm, const __grid_constant__ LinearArgs a) {
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (PASS == kJoin) wait_previous();
 
   auto wait = [&](int i, uint32_t parity) {
-    return mbar_test(bar(i), parity & 1u) || wait_on(bar(i), parity & 1u, stop);
+    return mbar_test(bar(i), parity & 1u) || wait_on(bar(i), parity & 1u, stop, a.stall.wait_ns);
   };
   auto wait_all = [&](int i, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(i, parity)); };
   auto arrive = [&](int i) {  // once for the warp
@@ -400,8 +401,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int t = p.t_lo + c * kChunk;
         for (int j = 0; j < kLoads; ++j) {  // v, which is weighed early, then k, then q, whose place is free last
           const int i = j == 0 ? kLoads - 1 : j - 1, at = slot(c, i);
+          if (a.stall.pass == PASS && int(blockIdx.x) == a.stall.block && c == a.stall.chunk && i == a.stall.load) ok = false;
           // The slot's last load: q's is free when o has left its place, the others' when their MMAs are done.
-          if (c > 1) ok = PASS != kReduce && i == 1 ? wait(kStaged + (c & 1), turn(c) + 1) : wait(kEmpty + at, turn(c) + 1);
+          if (ok && c > 1) ok = PASS != kReduce && i == 1 ? wait(kStaged + (c & 1), turn(c) + 1) : wait(kEmpty + at, turn(c) + 1);
           if (!ok) break;
           const uint32_t dst = place(at), full = bar(kFull + at);
           const bool value = i == kLoads - 1;
@@ -688,6 +690,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int i = 0; i < kCols; ++i)
         if (c0 + i < io.dk) s[i] = src[(c0 + i) * io.dv + v0 + col];
     }
+    bool lost = false;  // the end of a segment before this one
+    if (PASS == kJoin && p.last) {
+      for (int i = lane; i < p.seg * a.vtiles; i += 32)
+        lost |= a.ws_stop[(i / a.vtiles * nbh + bh) * a.vtiles + i % a.vtiles] != 0;
+      lost = __any_sync(0xFFFFFFFFu, lost);
+    }
     auto show_state = [&] {  // as q reads it
       if (cols) {
 #pragma unroll
@@ -704,7 +712,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       arrive(kStateFull);
     };
     if (PASS != kReduce && chunks > 0) show_state();
-    for (int c = 0; c < chunks; ++c) {
+    int c = 0;
+    for (; c < chunks; ++c) {
       const int n = min(kChunk, tokens - c * kChunk), ik = slot(c, 0), iv = slot(c, kLoads - 1);
       const uint32_t sk = place(ik), sv = place(iv);
       if (!wait_all(kFull + iv, turn(c))) break;
@@ -753,13 +762,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float* dst = PASS == kReduce                              ? a.ws_s + (p.seg * nbh + bh) * sn
                  : p.last && io.state_out && p.slot >= 0 ? io.state_out + ((long long)p.slot * io.H + p.h) * sn
                                                               : nullptr;
-    if (dst && col < dv) {
+    // After a wait that ran out the state is that of some chunk on the way: the old one stays.
+    if (dst && c == chunks && !lost && col < dv) {
 #pragma unroll
       for (int i = 0; i < kCols; ++i)
         if (c0 + i < io.dk) dst[(c0 + i) * io.dv + v0 + col] = s[i];
     }
   }
 
+  __syncwarp();
   if (PASS != kReduce && warp < kStateWarp && __syncthreads_or(0)) {  // a state is not finite
     asm volatile("fence.proxy.async;" ::: "memory");  // o has left by copies
     if (!*stop) form_again<DK, PASS>(a);
@@ -785,6 +796,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_after();
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  if (PASS == kReduce && threadIdx.x == 0) a.ws_stop[(p.seg * nbh + bh) * a.vtiles + p.vt] = *stop;
   if (threadIdx.x == 0 && *stop) {
     for (int i = 0; i < kSlots; ++i)
       if (issued[i] > 0) mbar_wait_teardown(bar(kFull + i), (issued[i] - 1u) & 1u);
@@ -903,7 +915,7 @@ __global__ void __launch_bounds__(kPadThreads) narrow_kernel(const __nv_bfloat16
 // segments 116 us and 137 whole, of 1024 tokens 52 and 43; 8 heads of 1024 tokens in 4 segments 32 and 39.  Two
 // segments gain nothing: 64 heads of 4096 tokens 148 us and 139 whole.)
 void cut_tiles(int B, int T, int H, int dv, int* segments, int* segment) {
-  const long long units = (long long)B * H * ((dv + kTileColumns - 1) / kTileColumns), chunks = ((long long)T + kChunk - 1) / kChunk;
+  const long long units = (long long)B * H * tile_columns(dv), chunks = ((long long)T + kChunk - 1) / kChunk;
   long long n = 152 / units;
   n = n < chunks / 2 ? n : chunks / 2;
   long long per = n > 1 ? (chunks + n - 1) / n : chunks;
@@ -925,7 +937,8 @@ size_t padded_bytes(int B, int T, int H, int Hk, int dk, int dv) {
 int launch_tiles(LinearArgs a, void* pad, cudaStream_t s) {
   const sdm_linear_args given = a.io;
   sdm_linear_args& io = a.io;
-  a.vtiles = (io.dv + kTileColumns - 1) / kTileColumns;
+  a.vtiles = tile_columns(io.dv);
+  if (a.stall.pass < 0) a.stall.wait_ns = kWaitNs;
   a.o_dv = io.dv;
   const int dk = round8(io.dk), dv = round8(io.dv);
   if (pad) {

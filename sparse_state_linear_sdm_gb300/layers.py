@@ -5,6 +5,10 @@ residuals and projections with an epilogue (include/sdm.h, second half).
 As in ``api``, every step runs in libsdm.so's CUDA kernels on the current stream, and a tensor that is not on a CUDA
 device is refused.  The tensors are checked and the outputs allocated in ``csrc/sdm_binding.cpp``: these calls are on a
 decode step's path.
+
+dev_err, where a call takes it, is an int32 [1] tensor that error bits (SDM_DEV_*) are OR-ed into.  After SDM_DEV_TIMEOUT, when
+a wait inside a kernel ran out, outputs are unspecified and a state may still be the one from before the call, which nothing
+else tells a caller that updates states in place.
 """
 from __future__ import annotations
 
