@@ -171,9 +171,9 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int
 //
 // 0 times one is not 0, so the masked products carry it to the tokens of its chunk that come before it.  Its column of the
 // state is NaN from then on, which shows at the end, and those tokens' outputs are then formed again, token by token from the
-// state that the sequence (the segment) begins with: 820 us instead of 127 where each of 8 prompts of 4096 x 16 heads of 128
-// has such a token.  Looking every chunk over for one took a tenth of the time of all the others (121 us -> 129 to 137 on one
-// GPU, by which warp looks).
+// state that the sequence (the segment) begins with: 870 us instead of 125 where each of 8 prompts of 4096 x 16 heads of 128
+// has such a token.  Calls without one take what they took without this (121 us then and 123 now on one GPU; 129 to 137
+// where a warp looks every chunk over).
 
 // The state in front of the first token.
 template <int PASS>
@@ -183,7 +183,8 @@ __device__ __forceinline__ const float* front_state(const LinearArgs& a, const P
   if (PASS == kJoin) return a.ws_s + (((long long)p.seg * io.B + p.b) * io.H + p.h) * sn;
   return PASS == kWhole && io.state && p.slot >= 0 ? io.state + ((long long)p.slot * io.H + p.h) * sn : nullptr;
 }
-// A warp's eight columns, the c0-th on.  A lane has rows lane, lane + 32 ...
+// A warp's four columns, the c0-th on (with eight, whose registers spill, the kernel's other code came out slower too: 128 us).
+// A lane has rows lane, lane + 32 ...
 template <int DK, int PASS>
 __device__ void form_columns(const LinearArgs& a, const Place& p, int c0) {
   constexpr int N = DK / 32, kAhead = 4;  // tokens asked for at a time
@@ -198,42 +199,42 @@ __device__ void form_columns(const LinearArgs& a, const Place& p, int c0) {
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(io.o) + (((long long)p.b * io.T + p.t_lo) * io.H + p.h) * a.o_dv + c0;
   const long long os = (long long)io.H * a.o_dv;
 
-  int first[8];  // of each column, or the tokens' number
+  int first[4];  // of each column, or the tokens' number
 #pragma unroll
-  for (int j = 0; j < 8; ++j) first[j] = tokens;
+  for (int j = 0; j < 4; ++j) first[j] = tokens;
   for (int t0 = 0; t0 < tokens; t0 += 32) {
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (t0 + lane < tokens) w = *reinterpret_cast<const uint4*>(v + (t0 + lane) * io.v_ts);
-    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+    uint2 w = make_uint2(0, 0);
+    if (t0 + lane < tokens) w = *reinterpret_cast<const uint2*>(v + (t0 + lane) * io.v_ts);
+    const uint32_t r[2] = {w.x, w.y};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const unsigned hit = __ballot_sync(0xFFFFFFFFu, (r[j / 2] >> (j % 2 * 16) & 0x7F80u) == 0x7F80u);
       if (hit && first[j] == tokens) first[j] = t0 + __ffs(hit) - 1;
     }
   }
   int from = tokens, to = 0;  // tokens whose outputs are formed again
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     if (first[j] == tokens) first[j] = 0;
     if (first[j] % kChunk) from = min(from, first[j] / kChunk * kChunk), to = max(to, first[j]);
   }
 
-  float s[N][8];
+  float s[N][4];
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const int r = lane + 32 * i;
       s[i][j] = src && r < io.dk && c0 + j < io.dv ? src[(long long)r * io.dv + c0 + j] : 0.f;
     }
   for (int t0 = 0; t0 < to; t0 += kAhead) {
     __nv_bfloat16 kr[kAhead][N];
-    uint4 vr[kAhead];
+    uint2 vr[kAhead];
     float gr[kAhead];
 #pragma unroll
     for (int x = 0; x < kAhead; ++x) {
       const int t = min(t0 + x, tokens - 1);
-      vr[x] = *reinterpret_cast<const uint4*>(v + t * io.v_ts);
+      vr[x] = *reinterpret_cast<const uint2*>(v + t * io.v_ts);
       gr[x] = g ? g[t * io.g_ts] : 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) kr[x][i] = lane + 32 * i < io.dk ? k[t * io.k_ts + lane + 32 * i] : __nv_bfloat16(0.f);
@@ -243,18 +244,18 @@ __device__ void form_columns(const LinearArgs& a, const Place& p, int c0) {
       const int t = t0 + x;
       if (t >= to) break;
       const float e = at_most_finite(expf(gr[x]));
-      float f[8];
-      Piece<__nv_bfloat16>::load(vr[x], f);
+      const float f[4] = {__uint_as_float(vr[x].x << 16), __uint_as_float(vr[x].x & 0xFFFF0000u), __uint_as_float(vr[x].y << 16),
+                          __uint_as_float(vr[x].y & 0xFFFF0000u)};
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[i][j] = fmaf(e, s[i][j], to_f32(kr[x][i]) * f[j]);
+        for (int j = 0; j < 4; ++j) s[i][j] = fmaf(e, s[i][j], to_f32(kr[x][i]) * f[j]);
       if (t < from) continue;
       float qr[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) qr[i] = lane + 32 * i < io.dk ? to_f32(q[t * io.q_ts + lane + 32 * i]) : 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         float y = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) y = fmaf(qr[i], s[i][j], y);
@@ -270,7 +271,7 @@ template <int DK, int PASS>
 __device__ __noinline__ void form_again(const LinearArgs& a) {
   const Place p = place_of<PASS>(a);
   const int c0 = p.vt * kTileColumns, warp = threadIdx.x >> 5;
-  for (int c = warp * 8; c < min(kTileColumns, a.o_dv - c0); c += kStateWarp * 8) form_columns<DK, PASS>(a, p, c0 + c);
+  for (int c = warp * 4; c < min(kTileColumns, a.o_dv - c0); c += kStateWarp * 4) form_columns<DK, PASS>(a, p, c0 + c);
 }
 
 // Every wait is bounded; one that runs out stops the CTA, which waits for the copies and MMAs in flight, frees TMEM and
