@@ -117,6 +117,14 @@ struct Row {
   }
 };
 
+// Sum of N warps' parts, in log2 N roundings.
+template <int N, int K>
+__device__ __forceinline__ float tree_sum(const float (*part)[K], int k) {
+  if constexpr (N == 1)
+    return part[0][k];
+  else
+    return tree_sum<N / 2, K>(part, k) + tree_sum<N / 2, K>(part + N / 2, k);
+}
 // Sums of K values over the TPR threads of a row; every thread of the block calls it.  `part` is this call's own.
 template <int TPR, int K>
 __device__ __forceinline__ void row_sums(float (&v)[K], float (*part)[K]) {
@@ -132,12 +140,7 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float (*part)[K]) {
       for (int k = 0; k < K; ++k) part[w][k] = v[k];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < W; ++i) s += part[w / W * W + i][k];  // the row's own warps
-      v[k] = s;
-    }
+    for (int k = 0; k < K; ++k) v[k] = tree_sum<W, K>(part + w / W * W, k);  // the row's own warps
   }
 }
 
