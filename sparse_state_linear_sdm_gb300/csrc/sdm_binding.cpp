@@ -456,11 +456,12 @@ Norm norm_operands(const Call& c, PyObject* const* a, const at::Tensor& x, const
   m.s.weight = c.dense(weight, "weight", m.w_type, {m.D});
   m.s.M = m.D ? x.numel() / m.D : 0;
   m.s.D = as_int(m.D, "D");
-  m.s.groups = int(PyLong_AsLong(a[0]));
+  const long groups = PyLong_AsLong(a[0]);
   m.s.eps = float(PyFloat_AsDouble(a[1]));
   m.s.act = int(PyLong_AsLong(a[2]));
   if (PyErr_Occurred()) throw Raised();
-  if (m.s.groups < 1 || m.D % m.s.groups) raise(PyExc_ValueError, "groups must divide the channels");
+  if (groups < 1 || m.D % groups) raise(PyExc_ValueError, "groups must divide the channels");
+  m.s.groups = as_int(groups, "groups");
   if (weight.defined() && m.s.groups > 1) raise(PyExc_ValueError, "groups are those of `after`: weight's norm is over whole rows");
   return m;
 }
