@@ -6,8 +6,8 @@
 // Sums are fp32 and y is rounded once.  dz is rounded to bf16 between the products (as the gated projections' dg and
 // du: the tensor cores take nothing wider at that rate), and dbias sums the rounded values; without an activation dz is dy itself.
 //
-// 16,384 tokens of 8192 x 2048 with a residual: 350 us, 1,570 TFLOP/s (0.82 of cuBLAS's burst, 0.92 of its sustained
-// rate).  The gradient of 1000 tokens of 1024 x 2736 with gelu: 39 us, its slope pass 44 tiles on 76 pairs.  4 tokens of
+// 16,384 tokens of 8192 x 2048 with a residual: 350 to 356 us by GPU, 1,545 to 1,570 TFLOP/s (0.81 of cuBLAS's burst, 0.91
+// of its sustained rate).  The gradient of 1000 tokens of 1024 x 2736 with gelu: 39 us, its slope pass 44 tiles on 76 pairs.  4 tokens of
 // 8192 x 2048: 9.6 (0.52 of the HBM floor), of which a launch is 3 to 4.
 #include "sdm_product.cuh"
 

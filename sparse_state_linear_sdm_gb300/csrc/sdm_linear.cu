@@ -64,6 +64,7 @@ struct TwoSum {
   }
   // e^(hi + lo): what the argument's rounding leaves is multiplied on.
   __device__ __forceinline__ float exp(float sign) const {
+    // 1.9259630e-8: what kLog2e leaves of log2 e.
     const float x = hi * kLog2e, rest = fmaf(hi, kLog2e, -x) + fmaf(hi, 1.925963033500e-8f, lo * kLog2e);
     const float e = exp2_fast(sign * x);
     return fmaf(e, sign * 0.69314718f * rest, e);

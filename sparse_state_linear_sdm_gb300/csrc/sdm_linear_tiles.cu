@@ -13,9 +13,10 @@
 // clocks instead of 64), so the masked products and the weighted v are first operands out of TMEM.
 //
 // HBM would bound it (128 KB a chunk: 8 prompts of 4096 x 16 heads of 128 in 81 us), the work between the products does:
-// 123 us there, 3.8 us a chunk and SM.  (182 with every operand in shared memory and one group for v and the state; 145 with
-// the first slices of v weighed by the state's group in the chunk itself: 36 % of the issue slots then, a third of the
-// stalls instruction fetches of five roles' code.)  One prompt of 32,768 x 8 heads, in 19 segments: 114 us.
+// 122 to 133 us there, by GPU (the same build), 3.8 us a chunk and SM.  (182 with every operand in shared memory and one
+// group for v and the state; 145 with the first slices of v weighed by the state's group in the chunk itself: 36 % of the
+// issue slots then, a third of the stalls instruction fetches of five roles' code.)  One prompt of 32,768 x 8 heads, in 19
+// segments: 114 to 119 us.
 //
 // What is rounded to bf16: the masked products and the state as q reads it, as an MMA takes them (each half a unit, as o
 // itself).  The state is not: A v is cut into three bf16 parts whose products are summed in fp32 (two parts
@@ -855,7 +856,7 @@ int launch_sizes(const TileMaps& tm, const LinearArgs& a, cudaStream_t s) {
 
 // ---- rows off 16 bytes ----
 //
-// Copied to rows of multiples of eight columns first, and o back: 8 x 2048 x 16 heads with dk 100 and dv 128 take 186 us
+// Copied to rows of multiples of eight columns first, and o back: 8 x 2048 x 16 heads with dk 100 and dv 128 take 172 us
 // so, and 1,006 token by token.
 
 // q, k and v of the tokens that exist: a block has some tokens of one sequence and one of the three, a warp their heads in
@@ -913,8 +914,9 @@ __global__ void __launch_bounds__(kPadThreads) narrow_kernel(const __nv_bfloat16
 
 // A CTA of the tile kernel fills an SM, so 152 of them are what the card runs at once.  A chunk takes one about 4 us, and
 // 7 over both passes where the sequence is cut, with about 15 us for two more launches and starts.  (50 heads of 4096 tokens in 3
-// segments 116 us and 137 whole, of 1024 tokens 52 and 43; 8 heads of 1024 tokens in 4 segments 32 and 39.  Two
-// segments gain nothing: 64 heads of 4096 tokens 148 us and 139 whole.)
+// segments 102 us and 119 whole, of 1024 tokens 44 and 35; 8 heads of 1024 tokens in 4 segments 27 and 35.  Two
+// segments gain nothing: 64 heads of 4096 tokens 135 us and 119 whole, in 3 segments 146.  Whole, 51 to 128 heads leave SMs
+// idle and take what 51 do.)
 void cut_tiles(int B, int T, int H, int dv, int* segments, int* segment) {
   const long long units = (long long)B * H * tile_columns(dv), chunks = ((long long)T + kChunk - 1) / kChunk;
   long long n = 152 / units;

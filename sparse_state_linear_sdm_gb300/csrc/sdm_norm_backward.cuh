@@ -34,7 +34,8 @@ struct NormBackward {
 
 // What a call has of the gradient: bits, known where an instance is compiled.  Decided at run time, every one of them costs
 // branches and registers: 32,768 x 1000 with all of them takes 169 us so and 97 as its own instance, the norm and gate over
-// heads 82 and 61, the stream alone 68 and 55.  The sets that models use have an instance, the rest kAny.
+// heads 82 and 61, the stream alone 68 and 55.  The sets below have an instance; the rest share kAny, among them the stream
+// with a scale or a gate and no inner norm.
 enum NormParts { kStream = 1, kAfter = 2, kGate = 4, kScale = 8, kAny = 16 };  // kGate: silu
 constexpr bool norm_has(int kind, int part) { return kind == kAny || (kind & part); }
 constexpr bool norm_small(int kind) { return kind == kStream || kind == kAfter || kind == (kAfter | kGate); }

@@ -141,7 +141,8 @@ def linear_attention(q, k, v, decay=None, scale=None, state=None, state_out=None
     state_out, but for `state` itself): ValueError.  Returns (o [B, T, H, dv], state written).
 
     bf16 prompts with dk up to 128 run in chunks of 128 tokens on the tensor cores, everything else token by token; states
-    are fp32 in both.  In chunks an infinity in v makes NaN of its column of the state."""
+    are fp32 in both.  In chunks an infinity in v makes NaN of its column of the state.  There is no gradient: outputs require
+    none, whatever the inputs require (as for the convolution and the scan)."""
     return (_module or _binding()).linear(q, k, v, decay, scale, state, state_out, lengths, slots, out, workspace, dev_err,
                                           2)
 
