@@ -13,7 +13,7 @@
 // clocks instead of 64), so the masked products and the weighted v are first operands out of TMEM.
 //
 // HBM would bound it (128 KB a chunk: 8 prompts of 4096 x 16 heads of 128 in 81 us), the work between the products does:
-// 122 to 133 us there, by GPU (the same build), 3.8 us a chunk and SM.  (182 with every operand in shared memory and one
+// 122 to 133 us there, by GPU (the same code), 3.8 us a chunk and SM.  (182 with every operand in shared memory and one
 // group for v and the state; 145 with the first slices of v weighed by the state's group in the chunk itself: 36 % of the
 // issue slots then, a third of the stalls instruction fetches of five roles' code.)  One prompt of 32,768 x 8 heads, in 19
 // segments: 114 to 119 us.
